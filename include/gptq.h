@@ -353,6 +353,156 @@ gptq_status gptq_dequant_matmul(const void* X, gptq_dtype x_dtype, int64_t n_tok
                                 const int32_t* g_idx, const int32_t* perm, int32_t group_size,
                                 int64_t d_out, float* Y, int64_t ld_y, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled values (the element and scale formats of the OCP Microscaling
+ * Formats specification, v1.0): blocks of 32 consecutive values of a row
+ * share one power of two, and each value is a 4- or 8-bit float times it.
+ *
+ *   a = max |v_i| over the block;  e = floor(log2 a) - E, at least -127, with
+ *   E = 2 (e2m1) or 8 (e4m3); e = -127 for a block of zeros;
+ *   code_i = v_i 2^-e rounded to the element grid, ties to the even code,
+ *            magnitudes above the largest element (6, 448) taken to it;
+ *   scale byte = e + 127;  value_i = element(code_i) * 2^e.
+ * A block that holds a NaN or an infinity gets scale byte 255 and zero codes
+ * and reads back as NaN.  Signs of zeros are kept.
+ *
+ * Storage of n_rows x n_cols values: codes, gptq_mx_codes_per_row(n_cols,
+ * format) bytes per row (e2m1: two codes per byte, the even column in the
+ * low half), and scales, gptq_mx_scales_per_row(n_cols) bytes per row.  Rows
+ * are padded to a multiple of 128 columns with zero codes and zero scale
+ * bytes; the products rely on that padding.  Codes are 16-byte aligned
+ * (GPTQ_ERR_INVALID_ARG otherwise), scales 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    GPTQ_MX_NONE = 0,  /* 16-bit values, no scales (KV caches only) */
+    GPTQ_MX_FP8 = 1,   /* e4m3 */
+    GPTQ_MX_FP4 = 2    /* e2m1 */
+} gptq_mx_format;
+
+/* Bytes per row; -1 for n_cols < 0 or a format other than FP8 and FP4. */
+int64_t gptq_mx_codes_per_row(int64_t n_cols, gptq_mx_format format);
+int64_t gptq_mx_scales_per_row(int64_t n_cols);
+
+/* X: n_rows x n_cols of x_dtype, row stride ld_x, any alignment.  Every byte
+ * of codes and scales, the padding's included, is written.  Sizes in
+ * [0, 2^20] (n_cols >= 1).  n_rows == 0: nothing is launched.  Asynchronous. */
+gptq_status gptq_mx_quantize(const void* X, gptq_dtype x_dtype, int64_t n_rows, int64_t n_cols, int64_t ld_x,
+                             gptq_mx_format format, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* Y[r][c] = element(code) * 2^e, rounded to y_dtype (exact for float32 and
+ * bfloat16 within their range, and for float16 where the value came from a
+ * float16).  Y: n_rows x n_cols, row stride ld_y.  Asynchronous. */
+gptq_status gptq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, gptq_mx_format format, int64_t n_rows,
+                               int64_t n_cols, void* Y, gptq_dtype y_dtype, int64_t ld_y, hipStream_t stream);
+
+/* Y[t][r] = sum_{k < d_in} X[t][k] w[r][k], w the d_out x d_in e2m1 values of
+ * (codes, scales).  X: n_tok x d_in of x_dtype, row stride ld_x; Y: float32,
+ * n_tok x d_out, row stride ld_y, overwritten.  The weights enter the
+ * matrix cores as bfloat16, which holds every one of them exactly; float16
+ * and float32 activations enter as two and three bfloat16 parts that sum to
+ * them, so no product is rounded; sums are float32.  An infinity or NaN in X
+ * reaches its token's outputs as in float32 arithmetic.
+ * Errors: GPTQ_ERR_INVALID_ARG for a bad dtype, sizes outside [0, 2^20]
+ * (d_in >= 1), ld_x < d_in, ld_y < d_out, misaligned codes or a null pointer.
+ * n_tok == 0 or d_out == 0: nothing is launched.  Asynchronous, no workspace. */
+gptq_status gptq_mx_matmul(const void* X, gptq_dtype x_dtype, int64_t n_tok, int64_t d_in, int64_t ld_x,
+                           const uint8_t* codes, const uint8_t* scales, int64_t d_out, float* Y, int64_t ld_y,
+                           hipStream_t stream);
+
+/* The same product with activations that are microscaled too (x_codes,
+ * x_scales: n_tok x d_in as gptq_mx_quantize writes them, x_format e2m1 or
+ * e4m3): e2m1 on the block-scaled matrix instructions, e4m3 as bfloat16
+ * (which holds every value).  Errors as above, and GPTQ_ERR_INVALID_ARG for
+ * x_format GPTQ_MX_NONE. */
+gptq_status gptq_mx_matmul_quantized(const uint8_t* x_codes, const uint8_t* x_scales, gptq_mx_format x_format,
+                                     int64_t n_tok, int64_t d_in, const uint8_t* codes, const uint8_t* scales,
+                                     int64_t d_out, float* Y, int64_t ld_y, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache of keys and values.
+ *
+ * k and v: [n_pages][n_kv_heads][page_size] rows of head_dim values: 16-bit
+ * values of `dtype` (GPTQ_MX_NONE), or codes of `format` without padding
+ * (head_dim or head_dim / 2 bytes), with k_scales and v_scales
+ * [n_pages][n_kv_heads][page_size] rows of head_dim / 32 scale bytes.
+ * head_dim: 32, 64, 96 or 128.  page_size: any, at least 1.  k, v 16-byte
+ * aligned; n_pages * n_kv_heads * page_size at most 2^31 - 1.
+ * Position p of a sequence lives in page table[p / page_size] at offset
+ * p % page_size.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scales;       /* NULL for GPTQ_MX_NONE */
+    uint8_t* v_scales;
+    int64_t n_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    gptq_mx_format format;
+    gptq_dtype dtype;        /* element type of a GPTQ_MX_NONE cache (F16 or BF16); ignored otherwise */
+} gptq_kv_cache;
+
+/* Writes token t's keys and values (K + t * ld_k, V + t * ld_v: n_kv_heads x
+ * head_dim of x_dtype, each head quantised in blocks of 32 channels as by
+ * gptq_mx_quantize) to slot slots[t] = page * page_size + offset.  Slots
+ * outside [0, n_pages * page_size) are skipped (a padded batch uses -1).
+ * Two tokens of one call must not name the same slot: its content is then
+ * unspecified.  A GPTQ_MX_NONE cache takes x_dtype == dtype only.
+ * Asynchronous. */
+gptq_status gptq_cache_write(const gptq_kv_cache* cache, const void* K, const void* V, gptq_dtype x_dtype,
+                             int64_t n_tok, int64_t ld_k, int64_t ld_v, const int64_t* slots, hipStream_t stream);
+
+/* Reads sequences back: row row_start[s] + j of K and V (n_rows rows of
+ * n_kv_heads x head_dim values of y_dtype, row strides ld_k and ld_v) gets
+ * position j of sequence s, for 0 <= j < row_start[s + 1] - row_start[s].
+ * row_start: device int32[n_seq + 1], ascending.  table: device
+ * int32[n_seq][max_pages].  Rows behind row_start[n_seq] (and before
+ * row_start[0]) are left as they were; positions whose page is outside
+ * [0, n_pages), or past the table, read as NaN.  Asynchronous. */
+gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, int64_t max_pages, int64_t n_seq,
+                            const int32_t* row_start, int64_t n_rows, void* K, void* V, gptq_dtype y_dtype,
+                            int64_t ld_k, int64_t ld_v, hipStream_t stream);
+
+/* Attention of new tokens over the cache (which already holds their own keys
+ * and values).  Sequence s has the tokens q_start[s] .. q_start[s + 1] - 1 of
+ * Q and kv_len[s] positions in all, the last of them its newest token; token
+ * i of its n stands at position p = kv_len[s] - n + i and attends to the
+ * positions j <= p, with window > 0 only to j > p - window:
+ *
+ *   O[t][h] = sum_j softmax_j(scale * Q[t][h] . K[j][h'])  V[j][h'],
+ *   h' = h / (n_heads / n_kv_heads)
+ *
+ * Q, O: n_tok tokens of n_heads x head_dim values of q_dtype (F16 or BF16;
+ * the dtype of a GPTQ_MX_NONE cache), token strides ld_q and ld_o, any
+ * alignment.  Microscaled keys and values are rounded to q_dtype as they are
+ * read (exact for bfloat16, and for float16 where they came from a float16).
+ * Scores, maxima, sums and outputs are held in float32; the weights of the
+ * value sum are rounded to q_dtype.
+ * A token that attends to nothing (p < 0, or weights that are all zero) gets
+ * zeros.  Keys and values at positions that a token does not attend to have
+ * no influence on it, whatever they hold.  A page outside [0, n_pages), or a
+ * position past the table, is not read and makes the tokens that attend to
+ * it NaN.  Tokens outside q_start[0] .. q_start[n_seq] - 1 are left as they
+ * were in O.
+ * q_start: device int32[n_seq + 1], ascending; kv_len: device int32[n_seq];
+ * table: device int32[n_seq][max_pages].
+ * max_q: the largest number of new tokens of one sequence (a hint for the
+ * choice of kernels; results do not depend on it).
+ * workspace: gptq_cache_attention_workspace(...) bytes (may be 0), for parts
+ * of long sequences.  Asynchronous.
+ * Errors: GPTQ_ERR_INVALID_ARG for a bad cache, dtype, size, stride or
+ * pointer, n_heads not a multiple of n_kv_heads, a scale that is not a
+ * positive number, or a window outside [0, 2^30];
+ * GPTQ_ERR_UNSUPPORTED for another head_dim; GPTQ_ERR_WORKSPACE. */
+size_t gptq_cache_attention_workspace(const gptq_kv_cache* cache, int64_t n_tok, int64_t n_heads, int64_t n_seq,
+                                      int64_t max_pages, int64_t max_q, int64_t window);
+gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq_dtype q_dtype, int64_t n_tok,
+                                 int64_t n_heads, int64_t ld_q, const int32_t* q_start, const int32_t* kv_len,
+                                 const int32_t* table, int64_t max_pages, int64_t n_seq, int64_t max_q,
+                                 float scale, int64_t window, void* O, int64_t ld_o, void* workspace,
+                                 size_t ws_bytes, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* gptq_status_string(gptq_status status);
 

@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(HERE, "libgptq_mi355x.so")
 OK, ERR_INVALID_ARG, ERR_NOT_PD, ERR_NONFINITE, ERR_WORKSPACE, ERR_HIP, ERR_UNSUPPORTED = range(7)
 # gptq_dtype
 F32, F16, BF16 = 0, 1, 2
+# gptq_mx_format
+MX_NONE, MX_FP8, MX_FP4 = 0, 1, 2
 
 # Every symbol include/gptq.h declares.
 EXPORTS = (
@@ -26,8 +28,10 @@ EXPORTS = (
     "gptq_quantize_layer", "gptq_prepare_hinv_factored_workspace", "gptq_prepare_hinv_factored",
     "gptq_quantize_layer_factored_workspace", "gptq_quantize_layer_factored",
     "gptq_packed_words_per_row", "gptq_pack", "gptq_pack_permuted",
-    "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns", "gptq_status_string",
-    "gptq_version",
+    "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
+    "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
+    "gptq_mx_matmul_quantized", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
+    "gptq_cache_attention", "gptq_status_string", "gptq_version",
 )
 
 
@@ -66,6 +70,14 @@ class Config(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("group_size", ctypes.c_int32), ("sym", ctypes.c_int32),
                 ("act_order", ctypes.c_int32), ("block_size", ctypes.c_int32), ("static_groups", ctypes.c_int32),
                 ("damp", ctypes.c_double)]
+
+
+class Cache(ctypes.Structure):
+    """gptq_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
 
 
 def make_config(bits=4, group_size=128, sym=False, act_order=False, block=128, damp=0.01,
@@ -134,6 +146,28 @@ def load(path: str | None = None):
     lib.gptq_dequant_matmul.restype = ctypes.c_int
     lib.gptq_gather_columns.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, i64, vp]
     lib.gptq_gather_columns.restype = ctypes.c_int
+    cachep, ci = ctypes.POINTER(Cache), ctypes.c_int
+    lib.gptq_mx_codes_per_row.argtypes = [i64, ci]
+    lib.gptq_mx_codes_per_row.restype = i64
+    lib.gptq_mx_scales_per_row.argtypes = [i64]
+    lib.gptq_mx_scales_per_row.restype = i64
+    lib.gptq_mx_quantize.argtypes = [vp, ci, i64, i64, i64, ci, vp, vp, vp]
+    lib.gptq_mx_quantize.restype = ci
+    lib.gptq_mx_dequantize.argtypes = [vp, vp, ci, i64, i64, vp, ci, i64, vp]
+    lib.gptq_mx_dequantize.restype = ci
+    lib.gptq_mx_matmul.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, i64, vp]
+    lib.gptq_mx_matmul.restype = ci
+    lib.gptq_mx_matmul_quantized.argtypes = [vp, vp, ci, i64, i64, vp, vp, i64, vp, i64, vp]
+    lib.gptq_mx_matmul_quantized.restype = ci
+    lib.gptq_cache_write.argtypes = [cachep, vp, vp, ci, i64, i64, i64, vp, vp]
+    lib.gptq_cache_write.restype = ci
+    lib.gptq_cache_read.argtypes = [cachep, vp, i64, i64, vp, i64, vp, vp, ci, i64, i64, vp]
+    lib.gptq_cache_read.restype = ci
+    lib.gptq_cache_attention_workspace.argtypes = [cachep, i64, i64, i64, i64, i64, i64]
+    lib.gptq_cache_attention_workspace.restype = sz
+    lib.gptq_cache_attention.argtypes = [cachep, vp, ci, i64, i64, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, i64,
+                                         vp, i64, vp, sz, vp]
+    lib.gptq_cache_attention.restype = ci
     _lib = lib
     return lib
 

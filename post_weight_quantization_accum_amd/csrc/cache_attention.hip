@@ -1,0 +1,890 @@
+// Attention of new tokens over a paged cache (include/gptq.h,
+// gptq_cache_attention).
+//
+// The rows of one sequence and key-value head are its tokens times the heads
+// of the group, r = token * G + head, so that grouped heads share every key
+// they read.  Scores are computed transposed, S^T = K Q^T: the matrix
+// instruction then leaves each lane with one row's scores for a few keys,
+// which is the layout in which the same lane supplies P^T to O^T = V^T P^T
+// once the keys are taken in that order.  P never leaves the registers; V
+// goes through LDS and comes back transposed by ds_read_b64_tr_b16.
+//
+// Two kernels.  cache_few_kernel: tiles of 16 rows, each wave with keys of
+// its own, for sequences of few rows (decoding), which are bound by the
+// cache's bytes.  cache_many_kernel: tiles of 128 rows that share tiles of 64
+// keys in LDS, for chunks of a prompt, which are bound by the matrix cores
+// and the exponentials.  Both can cut a tile's keys into parts (a float32
+// output, a maximum and a sum per row and part) that cache_join_kernel joins.
+//
+// Softmax runs over the keys with a running maximum that is raised only when
+// a score exceeds it by 2^8 (powers of two): until then the weights are at
+// most 2^8, far from any overflow, and nothing has to be rescaled.
+#include <algorithm>
+
+#include "mx.hpp"
+
+namespace gptq {
+namespace {
+
+constexpr int FEW_ROWS = 16, MANY_ROWS = 128;
+// Sequences of at most this many rows go to the few-row kernel.
+constexpr int FEW_MOST = 64;
+constexpr int FEW_KEYS = 32, MANY_KEYS = 64;      // keys per step
+constexpr int FEW_MIN = 8, MANY_MIN = 8;          // least steps per part
+constexpr float RAISE = 8.0f;
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+struct AttnArgs {
+    const uint8_t *K, *V, *KS, *VS;
+    int64_t n_pages;
+    FastDiv page;
+    int n_kv, d;
+    const uint16_t* Q;
+    uint16_t* O;
+    int64_t ld_q, ld_o;
+    bool q_aligned, o_aligned;     // rows of 16 bytes, of 8 bytes
+    const int32_t *q_start, *kv_len, *table;
+    int64_t max_pages;
+    int cap;                       // positions that the table reaches
+    int n_seq, n_tok;
+    FastDiv group;                 // heads per key-value head
+    float scale;                   // times log2(e)
+    float raise;                   // 2^8 in scores before scaling
+    int window;                    // 0: none
+    uint32_t span;                 // keys that a token sees, itself the last
+    int n_slots, per_seq;          // tiles in the grid; > 0: slots s * per_seq + t, else packed
+    int n_split;
+    int64_t rows_min, rows_max;    // of the sequences this launch takes
+    float* part_o;                 // [part][token][head][D]
+    float* part_ml;                // [part][token][head][2]
+    int64_t n_rows;                // tokens * heads
+};
+
+// A tile of rows of one sequence, and the keys that any of them attends to.
+struct Tile {
+    int seq, q0, row0, rows;       // first token; first row of the tile; rows of the sequence
+    int first;                     // position of the sequence's first new token
+    int lo, hi;                    // keys
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+__device__ __forceinline__ int first_slot(const AttnArgs& a, int s, int rt) {
+    const int64_t q0 = clampi(a.q_start[s], 0, a.n_tok);
+    return (int)(q0 * a.group.d / rt) + s;
+}
+
+// The last of n ascending values f(i) that is at most x (-1: none), by the
+// 64 lanes of a wave.
+template <class Fn>
+__device__ __forceinline__ int last_at_most(int n, int x, Fn f) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    while (true) {
+        const int step = (n + 63) >> 6, i = lane * step;
+        const uint64_t ok = __ballot(i < n && f(lo + min(i, n - 1)) <= x);
+        const int c = __popcll(ok);
+        if (c == 0) return -1;       // only at the first step
+        lo += (c - 1) * step;
+        n = min(step, n - (c - 1) * step);
+        if (step == 1) return lo;
+    }
+}
+
+__device__ __forceinline__ void tile_keys(const AttnArgs& a, Tile& t, int rt) {
+    const int last = t.first + (int)div_by((uint32_t)min(t.row0 + rt, t.rows) - 1u, a.group);
+    const int from = t.first + (int)div_by((uint32_t)t.row0, a.group);
+    t.hi = clampi(last + 1, 0, a.cap);
+    t.lo = a.window ? clampi(from - a.window + 1, 0, t.hi) : 0;
+}
+
+// Fills in sequence s; false where it is not this launch's.
+__device__ __forceinline__ bool sequence(const AttnArgs& a, int s, Tile& t) {
+    t.seq = s;
+    t.q0 = clampi(a.q_start[s], 0, a.n_tok);
+    const int n = clampi(a.q_start[s + 1], t.q0, a.n_tok) - t.q0;
+    const int64_t rows = (int64_t)n * a.group.d;
+    t.rows = (int)rows;
+    t.first = max(a.kv_len[s], 0) - n;
+    return rows > a.rows_min && rows <= a.rows_max;
+}
+
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int slot, int rt, Tile& t) {
+    int s, k;
+    if (a.per_seq > 0) {
+        s = slot / a.per_seq;
+        k = slot - s * a.per_seq;
+    } else {
+        s = last_at_most(a.n_seq, slot, [&](int i) { return first_slot(a, i, rt); });
+        if (s < 0) return false;
+        k = slot - first_slot(a, s, rt);
+    }
+    s = __builtin_amdgcn_readfirstlane(s);
+    k = __builtin_amdgcn_readfirstlane(k);
+    if (!sequence(a, s, t) || (int64_t)k * rt >= t.rows) return false;
+    t.row0 = k * rt;
+    tile_keys(a, t, rt);
+    return true;
+}
+
+// Parts of a tile, and the steps of one part.
+__device__ __forceinline__ int parts_of(const Tile& t, int keys, int least, int n_split, int& first, int& steps,
+                                        int& per) {
+    first = t.lo / keys;
+    steps = t.hi > t.lo ? (t.hi + keys - 1) / keys - first : 0;
+    const int n = clampi(steps / least, 1, n_split);
+    per = (steps + n - 1) / n;
+    return per ? (steps + per - 1) / per : 1;
+}
+
+// Row of the cache that holds a position: -1 outside [lo, hi), -2 on a bad
+// page.
+__device__ __forceinline__ int cache_row(const AttnArgs& a, const Tile& t, int head, int key) {
+    if (key < t.lo || key >= t.hi) return -1;
+    const uint32_t n = div_by((uint32_t)key, a.page);
+    const int p = a.table[t.seq * a.max_pages + n];
+    if (p < 0 || p >= a.n_pages) return -2;
+    return (p * a.n_kv + head) * (int)a.page.d + (int)((uint32_t)key - n * a.page.d);
+}
+
+// Eight elements of Q from channel c of a row of head_dim d.
+__device__ __forceinline__ u32x4_t load_q(const AttnArgs& a, int64_t at, int c) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (c < a.d) {
+        const uint16_t* p = a.Q + at + c;
+        if (a.q_aligned) {
+            v = *(const u32x4_t*)p;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+        }
+    }
+    return v;
+}
+
+// 16 bytes of a row of values, and the scale of its block.
+template <gptq_mx_format F>
+struct Chunk {
+    u32x4_t w;
+    uint32_t s;
+    // i-th group of eight as 16-bit values
+    template <bool BF>
+    __device__ __forceinline__ u32x4_t eight(int i) const {
+        if constexpr (F == GPTQ_MX_FP4) return fp4x8<BF>(w[i], mx_scale(s));
+        else if constexpr (F == GPTQ_MX_FP8) return fp8x8<BF>(w[2 * i], w[2 * i + 1], mx_scale(s));
+        else return w;
+    }
+};
+
+// Chunk ci of cache row `row` (negative: nothing, all zeros; -2 with `nan`:
+// NaN).
+template <gptq_mx_format F, bool BF>
+__device__ __forceinline__ Chunk<F> load_chunk(const AttnArgs& a, const uint8_t* rows, const uint8_t* scales, int row,
+                                               int ci, bool nan) {
+    Chunk<F> c;
+    c.w = u32x4_t{0u, 0u, 0u, 0u};
+    c.s = nan && row == -2 ? 255u : 0u;
+    const int bytes = F == GPTQ_MX_FP4 ? a.d / 2 : F == GPTQ_MX_FP8 ? a.d : 2 * a.d;
+    if (row >= 0) {
+        if (16 * ci < bytes) {
+            c.w = *(const u32x4_t*)(rows + (int64_t)row * bytes + 16 * ci);
+            if constexpr (F != GPTQ_MX_NONE)
+                c.s = scales[(int64_t)row * (a.d >> 5) + (F == GPTQ_MX_FP4 ? ci : ci >> 1)];
+        }
+    } else if (F == GPTQ_MX_NONE && nan && row == -2) {
+        c.w = u32x4_t{H16<BF>::NAN2, H16<BF>::NAN2, H16<BF>::NAN2, H16<BF>::NAN2};
+    }
+    return c;
+}
+
+template <gptq_mx_format F>
+constexpr int chunks_of(int D) { return F == GPTQ_MX_FP4 ? D / 32 : F == GPTQ_MX_FP8 ? D / 16 : D / 8; }
+// groups of eight per chunk
+template <gptq_mx_format F>
+constexpr int eights() { return F == GPTQ_MX_FP4 ? 4 : F == GPTQ_MX_FP8 ? 2 : 1; }
+
+__device__ __forceinline__ s16x4_t tr_read(const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(void*)p);
+}
+
+// Two transposed reads as one operand.
+__device__ __forceinline__ u32x4_t tr_pair(const char* p, const char* q) {
+    const u32x2_t x = __builtin_bit_cast(u32x2_t, tr_read(p)), y = __builtin_bit_cast(u32x2_t, tr_read(q));
+    return u32x4_t{x.x, x.y, y.x, y.y};
+}
+
+// LDS written by some lanes of a wave and read by others of the same wave:
+// the LDS unit keeps a wave's order, the compiler must too.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Infinities and NaN in V.  A weight of 0 does not keep them from a token
+// that must not see their key (0 * inf).  So in the steps whose keys some
+// tokens of a tile see and others do not ("mixed": at the diagonal, and at
+// the window's far edge) they are taken out of V on its way to LDS, and where
+// that happened patch() adds them to the outputs of the tokens that do see
+// them, after those are written.
+template <bool BF>
+__device__ __forceinline__ bool take_out(u32x4_t& v) {
+    constexpr uint32_t LO = BF ? 0x7F80u : 0x7C00u, HI = LO << 16;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool lo = (v[i] & LO) == LO, hi = (v[i] & HI) == HI;
+        any |= lo || hi;
+        v[i] = (lo ? 0u : v[i] & 0xFFFFu) | (hi ? 0u : v[i] & 0xFFFF0000u);
+    }
+    return any;
+}
+
+__device__ __forceinline__ bool mixed_step(const AttnArgs& a, int key0, int keys, int pos0, int pos1) {
+    return pos1 > pos0 && (key0 + keys > pos0 + 1 || (a.window != 0 && key0 <= pos1 - a.window));
+}
+
+template <gptq_mx_format F, bool BF>
+__device__ float v_value(const AttnArgs& a, int row, int ch) {
+    if constexpr (F == GPTQ_MX_NONE) {
+        return H16<BF>::to_f32(((const uint16_t*)a.V)[(int64_t)row * a.d + ch]);
+    } else {
+        const float s = mx_scale(a.VS[(int64_t)row * (a.d >> 5) + (ch >> 5)]);
+        uint32_t w;
+        if constexpr (F == GPTQ_MX_FP8) w = H16<BF>::template fp8<false>(a.V[(int64_t)row * a.d + ch], s);
+        else w = H16<BF>::template fp4<0>(a.V[(int64_t)row * (a.d >> 1) + (ch >> 1)] >> (4 * (ch & 1)), s);
+        return H16<BF>::to_f32((uint16_t)w);
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ void store_out(const AttnArgs& a, uint16_t* p, float v0, float v1, float v2, float v3) {
+    const uint32_t x = H16<BF>::pack(v0, v1), y = H16<BF>::pack(v2, v3);
+    if (a.o_aligned) {
+        *(u32x2_t*)p = u32x2_t{x, y};
+    } else {
+        p[0] = (uint16_t)x;
+        p[1] = (uint16_t)(x >> 16);
+        p[2] = (uint16_t)y;
+        p[3] = (uint16_t)(y >> 16);
+    }
+}
+
+// Where a row's outputs are: in O, or in the part's float32 rows.
+struct Out {
+    uint16_t* o;
+    float* f;
+};
+__device__ __forceinline__ Out out_of(const AttnArgs& a, const Tile& t, int head, int row, int part, bool direct, int D) {
+    const int tok = (int)div_by((uint32_t)row, a.group), g = (int)a.group.d, hd = head * g + row - tok * g;
+    Out r = {nullptr, nullptr};
+    if (direct) r.o = a.O + (int64_t)(t.q0 + tok) * a.ld_o + (int64_t)hd * a.d;
+    else r.f = a.part_o + ((int64_t)part * a.n_rows + (int64_t)(t.q0 + tok) * (a.n_kv * g) + hd) * D;
+    return r;
+}
+
+// The workgroup's rows rt from row0 on, steps [begin, end).
+template <gptq_mx_format F, bool BF, int D>
+__device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head, int part, bool direct, int rt, int keys,
+                                   int begin, int end, int pos0, int pos1) {
+    __threadfence_block();
+    __syncthreads();
+    for (int e = threadIdx.x; e < rt * D; e += 256) {
+        const int row = t.row0 + e / D, ch = e % D;
+        if (row >= t.rows || ch >= a.d) continue;
+        const int pos = t.first + (int)div_by((uint32_t)row, a.group);
+        float add = 0.0f;
+        for (int step = begin; step < end; ++step) {
+            if (!mixed_step(a, step * keys, keys, pos0, pos1)) continue;
+            for (int key = step * keys; key < (step + 1) * keys; ++key) {
+                if ((uint32_t)(pos - key) >= a.span) continue;
+                const int r = cache_row(a, t, head, key);
+                const float v = r >= 0 ? v_value<F, BF>(a, r, ch) : 0.0f;
+                if (!__builtin_isfinite(v)) add += v;
+            }
+        }
+        if (add != 0.0f) {       // an infinity or NaN
+            const Out o = out_of(a, t, head, row, part, direct, D);
+            if (direct) o.o[ch] = (uint16_t)H16<BF>::pack(H16<BF>::to_f32(o.o[ch]) + add, 0.0f);
+            else o.f[ch] += add;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows.
+// ---------------------------------------------------------------------------
+template <gptq_mx_format F, bool BF, int D>
+__global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
+    constexpr int NC = chunks_of<F>(D), E8 = eights<F>();
+    constexpr int KC = NC > 4 ? NC / 4 : 1;         // 16-byte chunks of K per lane and 16 keys (D = 64, e2m1: half of one)
+    constexpr int QC = D / 32;                      // k-steps of 32 channels
+    constexpr int VP = NC / 2;                      // V chunks per lane and step
+    constexpr int CT = D / 16;
+    constexpr int V_ROW = 2 * D + 32;               // rows 32 bytes further in the banks: transposed reads hit all
+    constexpr int WAVE_B = FEW_KEYS * V_ROW;
+    constexpr int O_ROW = D + 4;
+    static_assert(FEW_ROWS * O_ROW * 4 <= WAVE_B, "a wave's outputs fit where its V tile was");
+    __shared__ __attribute__((aligned(16))) char lds[4 * WAVE_B];
+    __shared__ float ml[4][FEW_ROWS][2];
+
+    const int head = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv;
+    const int part = rest % a.n_split, slot = rest / a.n_split;
+    Tile t;
+    if (!find_tile(a, slot, FEW_ROWS, t)) return;
+    int step0, steps, per;
+    const int n_parts = parts_of(t, FEW_KEYS, FEW_MIN, a.n_split, step0, steps, per);
+    if (part >= n_parts) return;
+    const int end = step0 + min(steps, (part + 1) * per);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int row = t.row0 + n;
+    const bool live = row < t.rows;
+    const int tok = (int)div_by((uint32_t)row, a.group);
+    const int pos = live ? t.first + tok : -1;
+    const int pos0 = t.first + (int)div_by((uint32_t)t.row0, a.group);
+    const int pos1 = t.first + (int)div_by((uint32_t)min(t.row0 + FEW_ROWS, t.rows) - 1u, a.group);
+
+    // channel of element j of k-step c in lane group g
+    const auto chan = [&](int c) {
+        if constexpr (F == GPTQ_MX_NONE) return 32 * c + 8 * g;
+        else return D == 128 ? 32 * g + 8 * c : 16 * g + 8 * c;
+    };
+    u32x4_t q[QC];
+    {
+        const int64_t at = (int64_t)(t.q0 + tok) * a.ld_q + (int64_t)(head * (int)a.group.d + row - tok * (int)a.group.d) * a.d;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) q[c] = live ? load_q(a, at, chan(c)) : u32x4_t{0u, 0u, 0u, 0u};
+    }
+
+    f32x4_t acc[CT];
+#pragma unroll
+    for (int i = 0; i < CT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    float m = NEG_INF, l = 0.0f;
+    bool taken = false;
+    char* const vt = lds + wave * WAVE_B;
+
+    // Keys of one step: K chunks of keys n and 16 + n, V chunks of VP keys.
+    struct Step {
+        Chunk<F> k[2][KC];
+        Chunk<F> v[VP];
+    };
+    const auto load = [&](Step& s, int rows) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = __shfl(rows, 16 * h + n, 64);
+#pragma unroll
+            for (int i = 0; i < KC; ++i) {
+                int ci;
+                if constexpr (F == GPTQ_MX_NONE) ci = 4 * i + g;
+                else if constexpr (D == 128) ci = KC * g + i;
+                else ci = F == GPTQ_MX_FP8 ? g : g >> 1;
+                s.k[h][i] = load_chunk<F, BF>(a, a.K, a.KS, r, ci, true);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int r = __shfl(rows, i * (64 / NC) + lane / NC, 64);
+            s.v[i] = load_chunk<F, BF>(a, a.V, a.VS, r, lane % NC, false);
+        }
+    };
+    const auto rows_of = [&](int step) { return step < end ? cache_row(a, t, head, step * FEW_KEYS + (lane & 31)) : -1; };
+
+    int step = step0 + part * per + wave;
+    Step cur;
+    int rows = rows_of(step);
+    load(cur, rows);
+    rows = rows_of(step + 4);
+    for (; step < end; step += 4) {
+        Step nxt;
+        load(nxt, rows);
+        rows = rows_of(step + 8);
+        const int key0 = step * FEW_KEYS;
+
+        // S^T: this lane gets row n, keys key0 + 16 h + 4 g + r
+        f32x4_t s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+                u32x4_t k;
+                if constexpr (F == GPTQ_MX_NONE) k = cur.k[h][c].template eight<BF>(0);
+                else if constexpr (D == 128) k = cur.k[h][c / E8].template eight<BF>(c % E8);
+                else if constexpr (F == GPTQ_MX_FP8) k = cur.k[h][0].template eight<BF>(c);
+                else {
+                    // half of a 16-byte chunk per lane group
+                    const uint32_t w = (g & 1) ? cur.k[h][0].w[2 + c] : cur.k[h][0].w[c];
+                    k = fp4x8<BF>(w, mx_scale(cur.k[h][0].s));
+                }
+                s[h] = H16<BF>::mfma16(k, q[c], s[h]);
+            }
+        }
+        // V to LDS, rows of keys
+        const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            char* p = vt + (i * (64 / NC) + lane / NC) * V_ROW + (lane % NC) * (16 * E8);
+#pragma unroll
+            for (int e = 0; e < E8; ++e) {
+                u32x4_t v = cur.v[i].template eight<BF>(e);
+                if (mixed) taken |= take_out<BF>(v);
+                *(u32x4_t*)(p + 16 * e) = v;
+            }
+        }
+        wave_sync();
+
+        float x[8], mx = NEG_INF;
+        const int rel = pos - key0 - 4 * g;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = (uint32_t)(rel - (16 * (e >> 2) + (e & 3))) < a.span ? s[e >> 2][e & 3] : NEG_INF;
+            mx = fmaxf(mx, x[e]);
+        }
+        if (__any(mx > m + a.raise)) {
+            mx = fmaxf(mx, m);
+            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float f = mx == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f((m - mx) * a.scale);
+#pragma unroll
+            for (int i = 0; i < CT; ++i) acc[i] *= f;
+            l *= f;
+            m = mx;
+        }
+        const float base = m == NEG_INF ? 0.0f : m * a.scale;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
+            l += x[e];
+        }
+        // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
+        const u32x4_t p = {H16<BF>::pack(x[0], x[1]), H16<BF>::pack(x[2], x[3]), H16<BF>::pack(x[4], x[5]),
+                           H16<BF>::pack(x[6], x[7])};
+        const char* vr = vt + (4 * g + (n >> 2)) * V_ROW + 8 * (n & 3);
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            acc[i] = H16<BF>::mfma16(tr_pair(vr + 32 * i, vr + 16 * V_ROW + 32 * i), p, acc[i]);
+        wave_sync();
+        cur = nxt;
+    }
+
+    // join the four waves
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    float* const ow = (float*)vt;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) *(f32x4_t*)(ow + n * O_ROW + 16 * i + 4 * g) = acc[i];
+    if (g == 0) {
+        ml[wave][n][0] = m * a.scale;
+        ml[wave][n][1] = l;
+    }
+    taken = __syncthreads_or(taken);
+    constexpr int CH = D / 16;                      // channels per thread
+    const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * CH;
+    float mj = NEG_INF;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mj = fmaxf(mj, ml[w][r][0]);
+    const float bj = mj == NEG_INF ? 0.0f : mj;
+    float lj = 0.0f, o[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - bj);
+        lj += f * ml[w][r][1];
+        const float* p = (const float*)(lds + w * WAVE_B) + r * O_ROW + c0;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[i] += f * p[i];
+    }
+    if (t.row0 + r < t.rows) {
+        const int tk = (int)div_by((uint32_t)(t.row0 + r), a.group);
+        if (t.first + tk >= a.cap) {                // the table does not reach this token
+            lj = __builtin_nanf("");
+            mj = 0.0f;
+        }
+        const Out out = out_of(a, t, head, t.row0 + r, part, n_parts == 1, D);
+        if (n_parts == 1) {
+            const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
+#pragma unroll
+            for (int i = 0; i < CH; i += 4)
+                if (c0 + i < a.d) store_out<BF>(a, out.o + c0 + i, o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH; i += 4)
+                *(float4*)(out.f + c0 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            if ((threadIdx.x & 15) == 0) {
+                const int64_t at = (out.f - a.part_o) / D;
+                a.part_ml[2 * at] = mj;
+                a.part_ml[2 * at + 1] = lj;
+            }
+        }
+    }
+    if (taken)
+        patch<F, BF, D>(a, t, head, part, n_parts == 1, FEW_ROWS, FEW_KEYS, step0 + part * per, end, pos0, pos1);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows.
+// ---------------------------------------------------------------------------
+template <gptq_mx_format F, bool BF, int D>
+__global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
+    constexpr int NC = chunks_of<F>(D), E8 = eights<F>();
+    constexpr int PER = MANY_KEYS * NC;             // chunks of a tile of keys
+    constexpr int CPT = 2 * PER / 256;              // chunks of K and V per thread
+    constexpr int KPT = CPT > 1 ? CPT / 2 : 1;      // keys per thread
+    constexpr int QC = D / 16, CT = D / 32;
+    constexpr int K_ROW = 2 * D + 16, V_ROW = 2 * D + 64;
+    constexpr int BUF = MANY_KEYS * (K_ROW + V_ROW);
+    __shared__ __attribute__((aligned(16))) char lds[2 * BUF];
+
+    const int head = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv;
+    const int part = rest % a.n_split, slot = a.n_slots - 1 - rest / a.n_split;   // the longest tiles first
+    Tile t;
+    if (!find_tile(a, slot, MANY_ROWS, t)) return;
+    int step0, steps, per;
+    const int n_parts = parts_of(t, MANY_KEYS, MANY_MIN, a.n_split, step0, steps, per);
+    if (part >= n_parts) return;
+    const int begin = step0 + part * per, end = step0 + min(steps, (part + 1) * per);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, h = lane >> 5;
+    const int w0 = t.row0 + 32 * wave, row = w0 + n;
+    const bool live = row < t.rows;
+    const int tok = (int)div_by((uint32_t)row, a.group);
+    const int hd = head * (int)a.group.d + row - tok * (int)a.group.d;
+    const int pos = live ? t.first + tok : -1;
+    const int tile0 = t.first + (int)div_by((uint32_t)t.row0, a.group);
+    const int tile1 = t.first + (int)div_by((uint32_t)min(t.row0 + MANY_ROWS, t.rows) - 1u, a.group);
+    bool taken = false;
+    // positions of the wave's first and last row (none: pos1 < pos0)
+    const int pos0 = t.first + (int)div_by((uint32_t)w0, a.group);
+    const int pos1 = w0 < t.rows ? t.first + (int)div_by((uint32_t)min(w0 + 32, t.rows) - 1u, a.group) : -1;
+
+    u32x4_t q[QC];
+    {
+        const int64_t at = (int64_t)(t.q0 + tok) * a.ld_q + (int64_t)hd * a.d;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) q[c] = live ? load_q(a, at, 16 * c + 8 * h) : u32x4_t{0u, 0u, 0u, 0u};
+    }
+    f16_t acc[CT];
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+    float m = NEG_INF, l = 0.0f;
+
+    const auto rows_of = [&](int (&r)[KPT], int step) {
+#pragma unroll
+        for (int i = 0; i < KPT; ++i)
+            r[i] = step < end ? cache_row(a, t, head, step * MANY_KEYS + (tid + 256 * i) % PER / NC) : -1;
+    };
+    const auto load = [&](Chunk<F> (&c)[CPT], const int (&r)[KPT]) {
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const bool v = tid + 256 * i >= PER;
+            c[i] = load_chunk<F, BF>(a, v ? a.V : a.K, v ? a.VS : a.KS, r[i % KPT], (tid + 256 * i) % NC, !v);
+        }
+    };
+    const auto store = [&](const Chunk<F> (&c)[CPT], int b, int step) {
+        const bool mixed = mixed_step(a, step * MANY_KEYS, MANY_KEYS, tile0, tile1);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int e = tid + 256 * i, key = e % PER / NC, ci = e % NC;
+            const bool v = e >= PER;
+            char* p = lds + b * BUF + (v ? MANY_KEYS * K_ROW + key * V_ROW : key * K_ROW) + ci * (16 * E8);
+#pragma unroll
+            for (int j = 0; j < E8; ++j) {
+                u32x4_t x = c[i].template eight<BF>(j);
+                if (mixed && v) taken |= take_out<BF>(x);
+                *(u32x4_t*)(p + 16 * j) = x;
+            }
+        }
+    };
+
+    Chunk<F> c[CPT];
+    int rows[KPT];
+    rows_of(rows, begin);
+    load(c, rows);
+    rows_of(rows, begin + 1);
+    store(c, 0, begin);
+    __syncthreads();
+    for (int step = begin; step < end; ++step) {
+        const int b = (step - begin) & 1, key0 = step * MANY_KEYS;
+        load(c, rows);
+        rows_of(rows, step + 2);
+        const bool none = key0 > pos1 || (a.window && key0 + MANY_KEYS - 1 <= pos0 - a.window);
+        if (!none) {
+            const char* kt = lds + b * BUF;
+            const char* vt = kt + MANY_KEYS * K_ROW;
+            // S^T: this lane gets row n, keys key0 + 32 i + 8 (e / 4) + 4 h + e % 4
+            f16_t s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < QC; ++k)
+                    s[i] = H16<BF>::mfma32(*(const u32x4_t*)(kt + (32 * i + n) * K_ROW + 32 * k + 16 * h), q[k], s[i]);
+            }
+            const bool whole = key0 + MANY_KEYS <= pos0 + 1 && (a.window == 0 || key0 > pos1 - a.window);
+            float x[32], mx = NEG_INF;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = s[e >> 4][e & 15];
+            if (!whole) {
+                const int rel = pos - key0 - 4 * h;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    // selected, not assigned under a condition: hipcc (ROCm 7.2) loses the other
+                    // elements of a matrix result when one of them is set in a divergent branch
+                    const int o = 8 * (e >> 2) + (e & 3);
+                    x[e] = (uint32_t)(rel - o) < a.span ? x[e] : NEG_INF;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
+            if (__any(mx > m + a.raise)) {
+                mx = fmaxf(mx, m);
+                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                const float f = mx == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f((m - mx) * a.scale);
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+                l *= f;
+                m = mx;
+            }
+            const float base = m == NEG_INF ? 0.0f : m * a.scale;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
+                l += x[e];
+            }
+            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
+            u32x4_t p[4];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e >> 2][e & 3] = H16<BF>::pack(x[2 * e], x[2 * e + 1]);
+            const char* vr = vt + (4 * h + ((lane & 15) >> 2)) * V_ROW + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    const char* v = vr + 16 * k * V_ROW + 64 * i;
+                    acc[i] = H16<BF>::mfma32(tr_pair(v, v + 8 * V_ROW), p[k], acc[i]);
+                }
+        }
+        store(c, b ^ 1, step + 1);
+        __syncthreads();
+    }
+    taken = __syncthreads_or(taken);
+    l += __shfl_xor(l, 32, 64);
+    if (live) {
+        if (pos >= a.cap) {                         // the table does not reach this token
+            l = __builtin_nanf("");
+            m = 0.0f;
+        }
+        const Out out = out_of(a, t, head, row, part, n_parts == 1, D);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int ch = 32 * i + 2 * e + 4 * h;
+                if (n_parts != 1)
+                    *(float4*)(out.f + ch) = make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
+                else if (ch < a.d)
+                    store_out<BF>(a, out.o + ch, acc[i][e] * inv, acc[i][e + 1] * inv, acc[i][e + 2] * inv, acc[i][e + 3] * inv);
+            }
+        if (n_parts != 1 && h == 0) {
+            const int64_t at = (out.f - a.part_o) / D;
+            a.part_ml[2 * at] = m * a.scale;
+            a.part_ml[2 * at + 1] = l;
+        }
+    }
+    if (taken) patch<F, BF, D>(a, t, head, part, n_parts == 1, MANY_ROWS, MANY_KEYS, begin, end, tile0, tile1);
+}
+
+// ---------------------------------------------------------------------------
+// The parts of a row joined: a wave per token and head, O = sum_p 2^(m_p - m)
+// O_p / sum_p 2^(m_p - m) l_p.
+// ---------------------------------------------------------------------------
+struct JoinArgs {
+    AttnArgs a;
+    int64_t few_max;               // sequences of at most this many rows were the few-row kernel's
+    int few_split, many_split;
+};
+
+template <bool BF, int D>
+__global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
+    const AttnArgs& a = j.a;
+    const int lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (id >= a.n_rows) return;
+    const int heads = a.n_kv * (int)a.group.d;
+    const int tok = (int)(id / heads), hd = (int)(id - (int64_t)tok * heads);
+    const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, tok, [&](int i) { return a.q_start[i]; }));
+    if (s < 0) return;
+    Tile t;
+    sequence(a, s, t);
+    const int64_t row = (int64_t)(tok - t.q0) * a.group.d + hd % a.group.d;
+    if (tok < t.q0 || row >= t.rows) return;
+    const bool few = t.rows <= j.few_max;
+    const int rt = few ? FEW_ROWS : MANY_ROWS;
+    t.row0 = (int)row / rt * rt;
+    tile_keys(a, t, rt);
+    int first, steps, per;
+    const int n = parts_of(t, few ? FEW_KEYS : MANY_KEYS, few ? FEW_MIN : MANY_MIN, few ? j.few_split : j.many_split,
+                           first, steps, per);
+    if (n == 1) return;
+    float m = NEG_INF;
+    for (int p = lane; p < n; p += 64) m = fmaxf(m, a.part_ml[2 * (p * a.n_rows + id)]);
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
+    const float base = m == NEG_INF ? 0.0f : m;
+    constexpr int CH = D / 64;
+    float l = 0.0f, o[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) o[i] = 0.0f;
+    for (int p = 0; p < n; ++p) {
+        const int64_t at = p * a.n_rows + id;
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - base);
+        l += f * a.part_ml[2 * at + 1];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[at * D + CH * lane + i];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* out = a.O + (int64_t)tok * a.ld_o + (int64_t)hd * a.d;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+        if (CH * lane + i < a.d) out[CH * lane + i] = (uint16_t)H16<BF>::pack(o[i] * inv, 0.0f);
+}
+
+// What is launched: which sequences go to which kernel, and in how many parts.
+struct Plan {
+    bool few, many;
+    int64_t few_max;
+    int64_t few_slots, many_slots;
+    int few_per_seq, few_split, many_split;
+    int D;
+};
+
+Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
+    Plan p;
+    const int64_t g = s.n_heads / c.n_kv_heads, rows = s.n_tok * g;
+    p.D = c.head_dim <= 64 ? 64 : 128;
+    // The hint decides only between kernels: each launch takes every sequence
+    // that no other one does, however many rows it has.
+    p.few = true;
+    p.many = s.max_q * g > FEW_MOST;
+    if (p.many && s.n_seq == 1) p.few = false;
+    p.few_max = !p.many ? INT64_MAX : p.few ? FEW_MOST : -1;
+    p.few_per_seq = p.few && p.many ? FEW_MOST / FEW_ROWS : 0;
+    p.few_slots = !p.few ? 0 : p.many ? s.n_seq * p.few_per_seq : rows / FEW_ROWS + s.n_seq;
+    p.many_slots = p.many ? rows / MANY_ROWS + s.n_seq : 0;
+    // Enough workgroups to fill the chip (four of the few-row kernel's to a
+    // compute unit, two of the other's), parts no shorter than the least.
+    int64_t keys = (int64_t)c.page_size * s.max_pages;
+    if (s.window) keys = std::min(keys, s.window + s.max_q);
+    const auto split = [&](int64_t slots, int64_t target, int64_t most, int64_t least) {
+        if (slots == 0) return (int64_t)1;
+        return std::max<int64_t>(1, std::min({most, target / (slots * c.n_kv_heads), keys / least}));
+    };
+    p.few_split = (int)split(p.few_slots, 1024, 128, FEW_KEYS * FEW_MIN);
+    p.many_split = (int)split(p.many_slots, 512, 32, MANY_KEYS * MANY_MIN);
+    return p;
+}
+
+template <gptq_mx_format F, bool BF, int D>
+void launch(AttnArgs& a, const Plan& p, hipStream_t s) {
+    if (p.many) {
+        a.n_slots = (int)p.many_slots;
+        a.per_seq = 0;
+        a.n_split = p.many_split;
+        a.rows_min = p.few ? FEW_MOST : 0;
+        a.rows_max = INT64_MAX;
+        hipLaunchKernelGGL((cache_many_kernel<F, BF, D>), dim3((unsigned)(p.many_slots * a.n_kv * p.many_split)),
+                           dim3(256), 0, s, a);
+    }
+    if (p.few) {
+        a.n_slots = (int)p.few_slots;
+        a.per_seq = p.few_per_seq;
+        a.n_split = p.few_split;
+        a.rows_min = 0;
+        a.rows_max = p.few_max;
+        hipLaunchKernelGGL((cache_few_kernel<F, BF, D>), dim3((unsigned)(p.few_slots * a.n_kv * p.few_split)), dim3(256),
+                           0, s, a);
+    }
+}
+
+template <bool BF, int D>
+void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) {
+    switch (f) {
+        case GPTQ_MX_FP4: launch<GPTQ_MX_FP4, BF, D>(a, p, s); break;
+        case GPTQ_MX_FP8: launch<GPTQ_MX_FP8, BF, D>(a, p, s); break;
+        default: launch<GPTQ_MX_NONE, BF, D>(a, p, s); break;
+    }
+    if (p.few_split > 1 || p.many_split > 1) {
+        JoinArgs j{a, p.few_max, p.few_split, p.many_split};
+        hipLaunchKernelGGL((cache_join_kernel<BF, D>), dim3((unsigned)ceil_div(a.n_rows, 4)), dim3(256), 0, s, j);
+    }
+}
+
+}  // namespace
+
+size_t cache_attention_ws(const gptq_kv_cache& c, const AttentionShape& s) {
+    const Plan p = plan_of(c, s);
+    const int parts = std::max(p.few_split, p.many_split);
+    return parts > 1 ? (size_t)parts * (size_t)(s.n_tok * s.n_heads) * (size_t)(p.D + 2) * sizeof(float) : 0;
+}
+
+gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape& s, const void* Q, gptq_dtype dt,
+                                   int64_t ld_q, const int32_t* q_start, const int32_t* kv_len, const int32_t* table,
+                                   float scale, void* O, int64_t ld_o, void* ws, hipStream_t stream) {
+    const Plan p = plan_of(c, s);
+    AttnArgs a;
+    a.K = (const uint8_t*)c.k;
+    a.V = (const uint8_t*)c.v;
+    a.KS = c.k_scales;
+    a.VS = c.v_scales;
+    a.n_pages = c.n_pages;
+    a.page = fast_div((uint32_t)c.page_size);
+    a.n_kv = c.n_kv_heads;
+    a.d = c.head_dim;
+    a.Q = (const uint16_t*)Q;
+    a.O = (uint16_t*)O;
+    a.ld_q = ld_q;
+    a.ld_o = ld_o;
+    a.q_aligned = ((uintptr_t)Q | (uintptr_t)(2 * ld_q)) % 16 == 0;
+    a.o_aligned = ((uintptr_t)O | (uintptr_t)(2 * ld_o)) % 8 == 0;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.table = table;
+    a.max_pages = s.max_pages;
+    a.cap = (int)std::min<int64_t>((int64_t)c.page_size * s.max_pages, INT32_MAX - MANY_KEYS);
+    a.n_seq = (int)s.n_seq;
+    a.n_tok = (int)s.n_tok;
+    a.group = fast_div((uint32_t)(s.n_heads / c.n_kv_heads));
+    a.scale = scale * 1.44269504088896340736f;
+    a.raise = RAISE / a.scale;
+    a.window = (int)s.window;
+    a.span = s.window ? (uint32_t)s.window : 0x80000000u;
+    a.n_rows = s.n_tok * s.n_heads;
+    const int parts = std::max(p.few_split, p.many_split);
+    a.part_o = (float*)ws;
+    a.part_ml = parts > 1 ? a.part_o + (int64_t)parts * a.n_rows * p.D : nullptr;
+    // tiles, rows of a sequence and workgroups are counted in 32 bits
+    if (a.n_rows > INT32_MAX || p.few_slots * a.n_kv * p.few_split > INT32_MAX ||
+        p.many_slots * a.n_kv * p.many_split > INT32_MAX || ceil_div(a.n_rows, 4) > INT32_MAX)
+        return GPTQ_ERR_UNSUPPORTED;
+    const bool bf = dt == GPTQ_BF16;
+    if (p.D == 64) {
+        if (bf) launch_format<true, 64>(a, p, c.format, stream);
+        else launch_format<false, 64>(a, p, c.format, stream);
+    } else {
+        if (bf) launch_format<true, 128>(a, p, c.format, stream);
+        else launch_format<false, 128>(a, p, c.format, stream);
+    }
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+}  // namespace gptq

@@ -1,0 +1,216 @@
+// Writing keys and values into the pages of a cache, and reading sequences
+// back (include/gptq.h, "A paged cache of keys and values").
+//
+// Both move rows of head_dim values in units of eight, a lane each, keys in
+// the first half of the grid and values in the second; a block of 32 channels
+// is a quad of lanes (head_dim is a multiple of 32), quantised as by
+// mx_quantize_kernel.  Both are bound by memory, or by their launch for a
+// handful of tokens.
+#include "mx.hpp"
+
+namespace gptq {
+namespace {
+
+struct Store {
+    uint8_t* rows[2];      // keys, values
+    uint8_t* scales[2];
+    int64_t n_pages;
+    FastDiv page;          // page_size
+    int n_kv, d;
+};
+
+// Row number of (page, head, offset).
+__device__ __forceinline__ int64_t row_of(const Store& c, int64_t page, int head, int off) {
+    return (page * c.n_kv + head) * c.page.d + off;
+}
+
+struct WriteArgs {
+    Store c;
+    const void* X[2];
+    int64_t ld[2];
+    bool aligned[2];
+    gptq_dtype dt;
+    const int64_t* slots;
+    int64_t n_units;       // tokens * units per token
+    FastDiv upt, uph;      // units per token, per head
+    uint32_t half;         // workgroups per matrix
+};
+
+template <gptq_mx_format F>
+__global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
+    const int m = blockIdx.x >= a.half;
+    const int64_t u = (int64_t)(blockIdx.x - (m ? a.half : 0)) * 256 + threadIdx.x;
+    if (u >= a.n_units) return;
+    const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
+    const uint32_t k = (uint32_t)(u - t * a.upt.d);
+    const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
+    const int64_t slot = a.slots[t];
+    // a quad shares its token: it leaves or stays as one
+    if (slot < 0 || slot >= a.c.n_pages * a.c.page.d) return;
+    const int64_t page = slot <= (int64_t)UINT32_MAX ? div_by((uint32_t)slot, a.c.page) : slot / a.c.page.d;
+    const int64_t row = row_of(a.c, page, (int)head, (int)(slot - page * a.c.page.d));
+    const int64_t at = row * (a.c.d / 8) + c;
+    if constexpr (F == GPTQ_MX_NONE) {
+        const uint16_t* p = (const uint16_t*)a.X[m] + t * a.ld[m] + 8 * k;
+        uint4 w;
+        if (a.aligned[m]) {
+            w = *(const uint4*)p;
+        } else {
+            w = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16,
+                           p[6] | (uint32_t)p[7] << 16);
+        }
+        ((uint4*)a.c.rows[m])[at] = w;
+    } else {
+        float v[8];
+        load8_f32(a.X[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v);
+        uint32_t byte;
+        u32x2_t w;
+        quantize_block8<F>(v, byte, w);
+        if constexpr (F == GPTQ_MX_FP4) ((uint32_t*)a.c.rows[m])[at] = w.x;
+        else ((u32x2_t*)a.c.rows[m])[at] = w;
+        if ((c & 3) == 0) a.c.scales[m][at >> 2] = (uint8_t)byte;
+    }
+}
+
+struct ReadArgs {
+    Store c;
+    gptq_dtype held;       // of 16-bit rows
+    const int32_t* table;
+    const int32_t* row_start;
+    int64_t max_pages;
+    int n_seq;
+    void* Y[2];
+    int64_t ld[2];
+    bool aligned[2];
+    gptq_dtype dt;
+    int64_t n_units;
+    FastDiv upt, uph;
+    uint32_t half;
+};
+
+template <gptq_mx_format F>
+__global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
+    const int m = blockIdx.x >= a.half;
+    const int64_t u = (int64_t)(blockIdx.x - (m ? a.half : 0)) * 256 + threadIdx.x;
+    if (u >= a.n_units) return;
+    const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
+    const uint32_t k = (uint32_t)(u - t * a.upt.d);
+    const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
+    // the last sequence that starts at or before row t
+    if (t < a.row_start[0] || t >= a.row_start[a.n_seq]) return;
+    int lo = 0, hi = a.n_seq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.row_start[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const uint32_t pos = (uint32_t)(t - a.row_start[lo]);
+    const uint32_t slot = div_by(pos, a.c.page);
+    const int64_t page = slot < a.max_pages ? a.table[(int64_t)lo * a.max_pages + slot] : -1;
+    float v[8];
+    if (page < 0 || page >= a.c.n_pages) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7FC00000u);
+    } else {
+        const int64_t row = row_of(a.c, page, (int)head, (int)(pos - slot * a.c.page.d));
+        const int64_t at = row * (a.c.d / 8) + c;
+        if constexpr (F == GPTQ_MX_NONE) {
+            load8_f32(a.c.rows[m], a.held, 8 * at, 8, true, v);
+        } else {
+            u32x2_t w = {0u, 0u};
+            if constexpr (F == GPTQ_MX_FP4) w.x = ((const uint32_t*)a.c.rows[m])[at];
+            else w = ((const u32x2_t*)a.c.rows[m])[at];
+            values8<F>(w.x, w.y, a.c.scales[m][at >> 2], v);
+        }
+    }
+    store8(a.Y[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v);
+}
+
+Store store_of(const gptq_kv_cache& c) {
+    Store s;
+    s.rows[0] = (uint8_t*)c.k;
+    s.rows[1] = (uint8_t*)c.v;
+    s.scales[0] = c.k_scales;
+    s.scales[1] = c.v_scales;
+    s.n_pages = c.n_pages;
+    s.page = fast_div((uint32_t)c.page_size);
+    s.n_kv = c.n_kv_heads;
+    s.d = c.head_dim;
+    return s;
+}
+
+bool rows_aligned(const void* p, int64_t ld, gptq_dtype dt) {
+    return ((uintptr_t)p | (uintptr_t)(ld * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
+}
+
+template <class A>
+gptq_status units(A& a, const gptq_kv_cache& c, int64_t n_rows, dim3& grid) {
+    const int uph = c.head_dim / 8;
+    a.upt = fast_div((uint32_t)(uph * c.n_kv_heads));
+    a.uph = fast_div((uint32_t)uph);
+    a.n_units = n_rows * a.upt.d;
+    const int64_t half = ceil_div(a.n_units, 256);
+    if (2 * half > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+    a.half = (uint32_t)half;
+    grid = dim3((unsigned)(2 * half));
+    return GPTQ_OK;
+}
+
+}  // namespace
+
+gptq_status cache_write_launch(const gptq_kv_cache& c, const void* K, const void* V, gptq_dtype dt, int64_t n_tok,
+                               int64_t ld_k, int64_t ld_v, const int64_t* slots, hipStream_t s) {
+    WriteArgs a;
+    a.c = store_of(c);
+    a.X[0] = K;
+    a.X[1] = V;
+    a.ld[0] = ld_k;
+    a.ld[1] = ld_v;
+    a.aligned[0] = rows_aligned(K, ld_k, dt);
+    a.aligned[1] = rows_aligned(V, ld_v, dt);
+    a.dt = dt;
+    a.slots = slots;
+    dim3 grid;
+    const gptq_status st = units(a, c, n_tok, grid);
+    if (st != GPTQ_OK) return st;
+    const dim3 block(256);
+    switch (c.format) {
+        case GPTQ_MX_FP4: hipLaunchKernelGGL(cache_write_kernel<GPTQ_MX_FP4>, grid, block, 0, s, a); break;
+        case GPTQ_MX_FP8: hipLaunchKernelGGL(cache_write_kernel<GPTQ_MX_FP8>, grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL(cache_write_kernel<GPTQ_MX_NONE>, grid, block, 0, s, a); break;
+    }
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+gptq_status cache_read_launch(const gptq_kv_cache& c, const int32_t* table, int64_t max_pages, int64_t n_seq,
+                              const int32_t* row_start, int64_t n_rows, void* K, void* V, gptq_dtype dt, int64_t ld_k,
+                              int64_t ld_v, hipStream_t s) {
+    ReadArgs a;
+    a.c = store_of(c);
+    a.held = c.dtype;
+    a.table = table;
+    a.row_start = row_start;
+    a.max_pages = max_pages;
+    a.n_seq = (int)n_seq;
+    a.Y[0] = K;
+    a.Y[1] = V;
+    a.ld[0] = ld_k;
+    a.ld[1] = ld_v;
+    a.aligned[0] = rows_aligned(K, ld_k, dt);
+    a.aligned[1] = rows_aligned(V, ld_v, dt);
+    a.dt = dt;
+    dim3 grid;
+    const gptq_status st = units(a, c, n_rows, grid);
+    if (st != GPTQ_OK) return st;
+    const dim3 block(256);
+    switch (c.format) {
+        case GPTQ_MX_FP4: hipLaunchKernelGGL(cache_read_kernel<GPTQ_MX_FP4>, grid, block, 0, s, a); break;
+        case GPTQ_MX_FP8: hipLaunchKernelGGL(cache_read_kernel<GPTQ_MX_FP8>, grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL(cache_read_kernel<GPTQ_MX_NONE>, grid, block, 0, s, a); break;
+    }
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+}  // namespace gptq
