@@ -1,15 +1,18 @@
 // Products with e2m1 weights: Y = X W^T (include/gptq.h, gptq_mx_matmul and
 // gptq_mx_matmul_quantized).
+#include <cmath>
+#include <type_traits>
+
 #include "mx.hpp"
 
 namespace gptq {
 namespace {
 
-// Kinds of activations that enter as bfloat16 parts.
-enum Act : int { ACT_F32 = GPTQ_F32, ACT_F16 = GPTQ_F16, ACT_BF16 = GPTQ_BF16, ACT_FP8 };
+// Kinds of activations.
+enum Act : int { ACT_F32 = GPTQ_F32, ACT_F16 = GPTQ_F16, ACT_BF16 = GPTQ_BF16, ACT_FP8, ACT_FP4 };
 
 struct MatArgs {
-    const void* X;         // values, or e4m3 codes
+    const void* X;         // values, or codes
     const uint8_t* XS;     // scale bytes of the codes
     int64_t n_tok, d_in, ld_x;
     bool aligned;          // X rows start on 16 bytes
@@ -17,212 +20,426 @@ struct MatArgs {
     const uint8_t* S;      // scale bytes
     int64_t w_row, s_row;  // bytes per row
     int steps;             // padded 128-column steps
+    int full;              // the first of them whose activations are read in whole 16-byte pieces
     int64_t d_out, ld_y;
     float* Y;
+    bool y_aligned;        // Y rows start on 16 bytes
 };
 
 // ---------------------------------------------------------------------------
 // Activations as bfloat16 parts.  A float32 is the sum of three bfloat16 cut
 // off its top (8 + 8 + 8 of its 24 bits), a float16 of two: no rounding, and
-// no overflow.  The parts below an infinity or NaN are 0.  A microscaled e4m3
-// value is a bfloat16 as it is.  (v_mfma_scale_f32_32x32x64_f8f6f4 would take
-// its codes directly, at twice the rate, but with an e4m3 operand it cuts
-// products off some 16 bits below the largest one of an instruction: an
-// error of 1e-5 of sum |x w| and more, measured, where these sums keep 1e-7.)
+// no overflow.  The parts below an infinity or NaN are 0.  A microscaled value
+// is a bfloat16 as it is.  (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3
+// codes directly, at twice the rate, but with an e4m3 operand it cuts products
+// off some 16 bits below the largest one of an instruction: an error of 1e-5
+// of sum |x w| and more, measured, where these sums keep 1e-7.)
+//
+// Float16 activations enter as they are, with weights as float16, for blocks
+// whose scale leaves them in float16's range (byte 104 .. 140: 2^-24 ..
+// 6 * 2^13), which those of trained weights do.  Other blocks count as zeros
+// there, and a wave that met one adds theirs in a loop of its own afterwards,
+// with activations in two parts.
 // ---------------------------------------------------------------------------
 template <Act DT>
 constexpr int parts_of() { return DT == ACT_F16 ? 2 : DT == ACT_F32 ? 3 : 1; }
 
-// Eight activations from (t, k): n of them exist.
+__device__ __forceinline__ bool scale_fits_f16(uint32_t byte) { return byte - 104u <= 36u; }
+// codes if `keep`, else zeros
+__device__ __forceinline__ u32x4_t codes_if(bool keep, u32x4_t w) {
+    const uint32_t m = keep ? 0xFFFFFFFFu : 0u;
+    return w & u32x4_t{m, m, m, m};
+}
+// codes that are not all zero
+__device__ __forceinline__ bool some(u32x4_t w) { return (w.x | w.y | w.z | w.w) != 0u; }
+
+// 16-byte pieces of 32 activations (one block of a token)
 template <Act DT>
-__device__ __forceinline__ void load_parts(const MatArgs& a, int64_t t, int64_t k, u32x4_t (&p)[parts_of<DT>()]) {
-    if constexpr (DT == ACT_FP8) {
-        const u32x2_t w = *(const u32x2_t*)((const uint8_t*)a.X + t * a.ld_x + k);
-        p[0] = fp8x8<true>(w.x, w.y, mx_scale(a.XS[t * a.s_row + (k >> 5)]));
-        return;
-    }
-    const int n = (int)max((int64_t)0, min((int64_t)8, a.d_in - k));
-    const bool vec = a.aligned && n == 8;
-    if constexpr (DT == ACT_BF16) {
-        const uint16_t* q = (const uint16_t*)a.X + t * a.ld_x + k;
-        if (vec) {
-            p[0] = *(const u32x4_t*)q;
+constexpr int pieces_of() { return DT == ACT_F32 ? 8 : DT == ACT_FP8 ? 2 : DT == ACT_FP4 ? 1 : 4; }
+
+// Some consecutive activations of a token as they are in memory: N groups of
+// eight (N = 4, a block, for the microscaled kinds).
+template <Act DT, int N = 4>
+struct Raw {
+    static constexpr int W = DT == ACT_F32 ? 2 * N : DT == ACT_FP8 ? (N + 1) / 2 : DT == ACT_FP4 ? 1 : N;
+    u32x4_t w[W];
+    uint32_t s;
+
+    // whole: aligned, and every column exists
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const MatArgs& a, int64_t t, int64_t k) {
+        if constexpr (DT == ACT_FP4) {
+            const uint8_t* p = (const uint8_t*)a.X + t * a.ld_x + (k >> 1);
+            if constexpr (N == 4) w[0] = *(const u32x4_t*)p;
+            else w[0].x = *(const uint32_t*)p;
+            s = a.XS[t * a.s_row + (k >> 5)];
+        } else if constexpr (DT == ACT_FP8) {
+            const uint8_t* p = (const uint8_t*)a.X + t * a.ld_x + k;
+            if constexpr (N == 4) {
+                w[0] = *(const u32x4_t*)p;
+                w[1] = *(const u32x4_t*)(p + 16);
+            } else {
+                const u32x2_t v = *(const u32x2_t*)p;
+                w[0].x = v.x;
+                w[0].y = v.y;
+            }
+            s = a.XS[t * a.s_row + (k >> 5)];
+        } else if constexpr (WHOLE) {
+            const u32x4_t* p = (const u32x4_t*)((const char*)a.X + (t * a.ld_x + k) * (DT == ACT_F32 ? 4 : 2));
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = p[i];
         } else {
+            const int n = (int)max((int64_t)0, min((int64_t)(8 * N), a.d_in - k));
+            if constexpr (DT == ACT_F32) {
+                const uint32_t* p = (const uint32_t*)a.X + t * a.ld_x + k;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = 2 * i < n ? q[2 * i] : 0, hi = 2 * i + 1 < n ? q[2 * i + 1] : 0;
-                p[0][i] = lo | hi << 16;
+                for (int i = 0; i < 8 * N; ++i) w[i >> 2][i & 3] = i < n ? p[i] : 0u;
+            } else {
+                const uint16_t* p = (const uint16_t*)a.X + t * a.ld_x + k;
+#pragma unroll
+                for (int i = 0; i < 4 * N; ++i) {
+                    const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+                    w[i >> 2][i & 3] = lo | hi << 16;
+                }
             }
         }
-    } else if constexpr (DT != ACT_FP8) {
+    }
+
+    // Group c as 16-bit values (not for float32).
+    __device__ __forceinline__ u32x4_t eight(int c) const {
+        if constexpr (DT == ACT_FP4) return fp4x8<true>(w[0][c], mx_scale(s));
+        else if constexpr (DT == ACT_FP8) return fp8x8<true>(w[c >> 1][2 * (c & 1)], w[c >> 1][2 * (c & 1) + 1], mx_scale(s));
+        else return w[c];
+    }
+};
+
+// bfloat16 parts of eight float32 values.
+template <int NP>
+__device__ __forceinline__ void split(float (&v)[8], u32x4_t (&p)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint(v[i]);
+            const bool fin = (b & 0x7F800000u) != 0x7F800000u;
+            // a NaN whose top bits are an infinity's keeps a quiet bit
+            w[i] = b | ((b & 0x7FFFFFFFu) > 0x7F800000u ? 0x00400000u : 0u);
+            v[i] = fin ? v[i] - __uint_as_float(b & 0xFFFF0000u) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[j][i] = w[2 * i] >> 16 | (w[2 * i + 1] & 0xFFFF0000u);
+    }
+}
+// The same of eight float16.
+__device__ __forceinline__ void split_f16(u32x4_t h, u32x4_t (&p)[2]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = H16<false>::to_f32((uint16_t)h[i]);
+        v[2 * i + 1] = H16<false>::to_f32((uint16_t)(h[i] >> 16));
+    }
+    split<2>(v, p);
+}
+template <Act DT, int N>
+__device__ __forceinline__ void parts(const Raw<DT, N>& x, int c, u32x4_t (&p)[parts_of<DT>()]) {
+    if constexpr (DT == ACT_F32) {
         float v[8];
-        load8_f32(a.X, (gptq_dtype)DT, t * a.ld_x + k, n, vec, v);
 #pragma unroll
-        for (int j = 0; j < parts_of<DT>(); ++j) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t b = __float_as_uint(v[i]);
-                const bool fin = (b & 0x7F800000u) != 0x7F800000u;
-                // a NaN whose top bits are an infinity's keeps a quiet bit
-                w[i] = (b & 0xFFFF0000u) | ((b & 0x7FFFFFFFu) > 0x7F800000u ? 0x00400000u : 0u);
-                v[i] = fin ? v[i] - __uint_as_float(b & 0xFFFF0000u) : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[j][i] = w[2 * i] >> 16 | (w[2 * i + 1] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x.w[2 * c + (i >> 2)][i & 3]);
+        split<3>(v, p);
+    } else if constexpr (DT == ACT_F16) {
+        split_f16(x.w[c], p);
+    } else {
+        p[0] = x.eight(c);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: 16 weight rows per workgroup, its eight waves share the
-// 128-column steps, and their sums meet in LDS.  v_mfma_f32_16x16x32_bf16
-// with a lane's four k-groups of eight chosen as one block of 32 columns:
-// lane l holds row l % 16, block l / 16 of the step (16 bytes of codes, one
-// scale), and activations of token l % 16 in the same columns.
+// Few tokens: a workgroup computes 16 RT weight rows x 16 TT tokens; its eight
+// waves share the 128-column steps, and their sums meet in LDS.
+// v_mfma_f32_16x16x32 with a lane's four k-groups of eight chosen as one block
+// of 32 columns: lane l holds row l % 16, block l / 16 of the step (16 bytes
+// of codes, one scale), and activations of token l % 16 in the same columns.
+// Everything goes straight from memory to the lanes that multiply it.  Rows
+// and tokens past the end are read from the last one and not stored.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8;
 
-template <Act DT, int TT>
+template <Act DT, int RT, int TT>
 __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
     constexpr int NP = parts_of<DT>();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i16 = lane & 15, g = lane >> 4;
-    const int64_t r0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (16 * TT);
-    const int64_t row = min(r0 + i16, a.d_out - 1);
-    const uint8_t* wp = a.W + row * a.w_row + 16 * g;
-    const uint8_t* sp = a.S + row * a.s_row + g;
-    f32x4_t acc[TT];
+    const int64_t r0 = (int64_t)blockIdx.x * (16 * RT), t0 = (int64_t)blockIdx.y * (16 * TT);
+    const uint8_t *wp[RT], *sp[RT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int PF = 4;
-    u32x4_t w[PF];
-    uint32_t s[PF];
-    const int last = a.steps - 1;
-#pragma unroll
-    for (int i = 0; i < PF; ++i) {
-        const int st = min(wave + FEW_WAVES * i, last);
-        w[i] = *(const u32x4_t*)(wp + 64 * (int64_t)st);
-        s[i] = sp[4 * (int64_t)st];
+    for (int i = 0; i < RT; ++i) {
+        const int64_t row = min(r0 + 16 * i + i16, a.d_out - 1);
+        wp[i] = a.W + row * a.w_row + 16 * g;
+        sp[i] = a.S + row * a.s_row + g;
     }
-    for (int s0 = wave; s0 < a.steps; s0 += FEW_WAVES * PF) {
+    int64_t tok[TT];
 #pragma unroll
-        for (int i = 0; i < PF; ++i) {
-            const int st = s0 + FEW_WAVES * i;
-            if (st < a.steps) {
-                const int64_t k = 128 * (int64_t)st + 32 * g;
-                const float sc = mx_scale(s[i]);
-                u32x4_t aw[4];
+    for (int i = 0; i < TT; ++i) tok[i] = min(t0 + 16 * i + i16, a.n_tok - 1);
+    f32x4_t acc[RT][TT];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) aw[c] = fp4x8<true>(w[i][c], sc);
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const int64_t tok = t0 + 16 * t + i16;
+        for (int j = 0; j < TT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    struct Step {
+        u32x4_t w[RT];
+        uint32_t s[RT];
+        Raw<DT> x[TT];
+    };
+    const auto load = [&](Step& d, int st, auto whole) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        u32x4_t p[NP];
-                        if (tok < a.n_tok) {
-                            load_parts<DT>(a, tok, k + 8 * c, p);
-                        } else {
+        for (int i = 0; i < RT; ++i) {
+            d.w[i] = *(const u32x4_t*)(wp[i] + 64 * (int64_t)st);
+            d.s[i] = sp[i][4 * (int64_t)st];
+        }
 #pragma unroll
-                            for (int j = 0; j < NP; ++j) p[j] = u32x4_t{0u, 0u, 0u, 0u};
-                        }
+        for (int j = 0; j < TT; ++j) d.x[j].template load<decltype(whole)::value>(a, tok[j], 128 * (int64_t)st + 32 * g);
+    };
+    bool left = false;       // float16: a block was left out
+    // REST: the blocks that were
+    const auto multiply = [&](const Step& d, auto rest) {
+        constexpr bool REST = decltype(rest)::value, HALF = DT == ACT_F16 && !REST;
+        u32x4_t codes[RT];
+        uint32_t sc[RT];
 #pragma unroll
-                        for (int j = 0; j < NP; ++j) acc[t] = H16<true>::mfma16(aw[c], p[j], acc[t]);
-                    }
+        for (int i = 0; i < RT; ++i) {
+            codes[i] = d.w[i];
+            sc[i] = d.s[i];
+            if constexpr (DT == ACT_F16) {
+                const bool fits = scale_fits_f16(sc[i]);
+                if constexpr (HALF) left |= !fits && (some(codes[i]) || sc[i] == 255u);
+                codes[i] = codes_if(fits == HALF, codes[i]);
+                if (fits != HALF) sc[i] = 127u;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            u32x4_t w[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) w[i] = fp4x8<!HALF>(codes[i][c], mx_scale(sc[i]));
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) acc[i][j] = H16<false>::mfma16(w[i], d.x[j].eight(c), acc[i][j]);
+                } else {
+                    u32x4_t p[NP];
+                    parts(d.x[j], c, p);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) acc[i][j] = H16<true>::mfma16(w[i], p[q], acc[i][j]);
                 }
             }
-            const int nx = min(st + FEW_WAVES * PF, last);
-            w[i] = *(const u32x4_t*)(wp + 64 * (int64_t)nx);
-            s[i] = sp[4 * (int64_t)nx];
+        }
+    };
+
+    // Steps in flight: enough for about 32 KiB of weights per compute unit.
+    constexpr int PF = RT * TT > 4 || (DT == ACT_F32 && TT > 1) ? 1 : RT * TT > 1 || DT == ACT_F32 ? 2 : 4;
+    const int mine = (a.full - wave + FEW_WAVES - 1) / FEW_WAVES;    // whole steps of this wave
+    if (mine > 0) {
+        Step d[PF];
+#pragma unroll
+        for (int i = 0; i < PF; ++i) load(d[i], wave + FEW_WAVES * min(i, mine - 1), std::true_type{});
+        for (int s0 = 0; s0 < mine; s0 += PF) {
+#pragma unroll
+            for (int i = 0; i < PF; ++i) {
+                Step cur = d[i];
+                load(d[i], wave + FEW_WAVES * min(s0 + i + PF, mine - 1), std::true_type{});
+                if (s0 + i < mine) multiply(cur, std::false_type{});
+            }
         }
     }
-    __shared__ f32x4_t part[FEW_WAVES][TT][64];
+    for (int st = a.full + wave; st < a.steps; st += FEW_WAVES) {
+        Step d;
+        load(d, st, std::false_type{});
+        multiply(d, std::false_type{});
+    }
+    if constexpr (DT == ACT_F16) {
+        for (int st = __any(left) ? wave : a.steps; st < a.steps; st += FEW_WAVES) {
+            Step d;
+            load(d, st, std::false_type{});
+            multiply(d, std::true_type{});
+        }
+    }
+
+    // the waves' sums, in the order of the waves, four tiles at a time
+    constexpr int TILES = RT * TT, AT = TILES < 4 ? TILES : 4;
+    __shared__ f32x4_t part[FEW_WAVES][AT][64];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) part[wave][t][lane] = acc[t];
-    __syncthreads();
-    for (int e = threadIdx.x; e < TT * 64; e += 64 * FEW_WAVES) {
-        const int t = e >> 6, l = e & 63;
-        f32x4_t v = part[0][t][l];
+    for (int b = 0; b < TILES; b += AT) {
+        if (b) __syncthreads();
 #pragma unroll
-        for (int q = 1; q < FEW_WAVES; ++q) v += part[q][t][l];
-        const int64_t tok = t0 + 16 * t + (l & 15), r = r0 + 4 * (l >> 4);
-        if (tok < a.n_tok) {
+        for (int e = 0; e < AT; ++e) part[wave][e][lane] = acc[(b + e) / TT][(b + e) % TT];
+        __syncthreads();
+        for (int e = threadIdx.x; e < AT * 64; e += 64 * FEW_WAVES) {
+            const int tile = b + (e >> 6), l = e & 63;
+            f32x4_t v = part[0][e >> 6][l];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r + j < a.d_out) a.Y[tok * a.ld_y + r + j] = v[j];
+            for (int q = 1; q < FEW_WAVES; ++q) v += part[q][e >> 6][l];
+            const int64_t t = t0 + 16 * (tile % TT) + (l & 15), r = r0 + 16 * (tile / TT) + 4 * (l >> 4);
+            if (t < a.n_tok) {
+                float* y = a.Y + t * a.ld_y + r;
+                if (a.y_aligned && r + 4 <= a.d_out) {
+                    *(f32x4_t*)y = v;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (r + j < a.d_out) y[j] = v[j];
+                }
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 128 weight rows x 128 tokens per workgroup of four waves, each
-// 64 x 64 of v_mfma_f32_32x32x16_bf16.  Activations go through LDS (split
-// into their parts on the way), weights straight from memory into the lanes
-// that multiply them: lane l holds row l % 32 and, of every 64 columns, block
-// l / 32.
+// Many tokens: 64 RW weight rows x 128 tokens per workgroup of 2 x 2 waves,
+// each 32 RW x 64 in v_mfma_f32_32x32x16.  Activations go through two LDS
+// buffers of 64 columns (float32 ones as their three parts), weights straight
+// from memory into the lanes that multiply them: lane l holds row l % 32 and,
+// of every 64 columns, block l / 32.  Both are fetched a step ahead.
 // ---------------------------------------------------------------------------
-constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;
+constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
-template <Act DT>
-__global__ __launch_bounds__(256) void mx_many_kernel(MatArgs a) {
-    constexpr int NP = parts_of<DT>();
-    __shared__ __attribute__((aligned(16))) char xs[NP * MT * X_ROW];
+template <Act DT, int RW>
+__global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
+    constexpr int NP = DT == ACT_F32 ? 3 : 1;           // planes in LDS
+    constexpr int BUF = NP * MT * X_ROW;
+    extern __shared__ __attribute__((aligned(16))) char xs[];   // two buffers
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i32 = lane & 31, h = lane >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * MT + 64 * (wave >> 1), t0 = (int64_t)blockIdx.y * MT;
+    // consecutive workgroups go to different dies: give each die a run of
+    // tiles that share weight rows
+    const uint32_t nt = (uint32_t)((a.n_tok + MT - 1) / MT), n = gridDim.x, per = n / 8;
+    const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
+    const int64_t r0 = (int64_t)(id / nt) * (64 * RW) + 32 * RW * (wave >> 1), t0 = (int64_t)(id % nt) * MT;
     const int tw = 64 * (wave & 1);
-    const uint8_t* wp[2];
-    const uint8_t* sp[2];
+    const uint8_t *wp[RW], *sp[RW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RW; ++i) {
         const int64_t row = min(r0 + 32 * i + i32, a.d_out - 1);
         wp[i] = a.W + row * a.w_row + 16 * h;
         sp[i] = a.S + row * a.s_row + h;
     }
-    f16_t acc[2][2];
+    f16_t acc[RW][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < RW; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    for (int st = 0; st < 2 * a.steps; ++st) {
-        __syncthreads();
-        // 128 tokens x 8 groups of eight columns, four per thread
+
+    // this thread's four pieces of eight columns
+    Raw<DT, 1> x[4];
+    const auto load_x = [&](int st) {
+        if (st < 2 * a.full) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = threadIdx.x + 256 * q;
+                x[q].template load<true>(a, min(t0 + (e >> 3), a.n_tok - 1), (int64_t)MK * st + 8 * (e & 7));
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = threadIdx.x + 256 * q;
+                x[q].template load<false>(a, min(t0 + (e >> 3), a.n_tok - 1), (int64_t)MK * st + 8 * (e & 7));
+            }
+        }
+    };
+    const auto store_x = [&](int b) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int e = threadIdx.x + 256 * q, t = e >> 3, c = e & 7;
-            u32x4_t p[NP];
-            if (t0 + t < a.n_tok) {
-                load_parts<DT>(a, t0 + t, (int64_t)MK * st + 8 * c, p);
+            const int e = threadIdx.x + 256 * q;
+            char* p = xs + b * BUF + (e >> 3) * X_ROW + 16 * (e & 7);
+            if constexpr (DT == ACT_F32) {
+                u32x4_t v[3];
+                parts(x[q], 0, v);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) *(u32x4_t*)(p + j * MT * X_ROW) = v[j];
             } else {
-#pragma unroll
-                for (int j = 0; j < NP; ++j) p[j] = u32x4_t{0u, 0u, 0u, 0u};
+                *(u32x4_t*)p = x[q].eight(0);
             }
-#pragma unroll
-            for (int j = 0; j < NP; ++j) *(u32x4_t*)(xs + (j * MT + t) * X_ROW + 16 * c) = p[j];
         }
-        u32x4_t w[2];
-        float sc[2];
+    };
+    bool left = false;       // float16: a block was left out
+    u32x4_t w[RW];
+    uint32_t sc[RW];
+    const auto load_w = [&](int st) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < RW; ++i) {
             w[i] = *(const u32x4_t*)(wp[i] + 32 * (int64_t)st);
-            sc[i] = mx_scale(sp[i][2 * (int64_t)st]);
+            sc[i] = sp[i][2 * (int64_t)st];
         }
+    };
+    const int last = 2 * a.steps - 1;
+    load_x(0);
+    load_w(0);
+    store_x(0);
+    __syncthreads();
+    for (int st = 0; st <= last; ++st) {
+        const char* xb = xs + (st & 1) * BUF + (tw + i32) * X_ROW + 64 * h;
+        u32x4_t cw[RW];
+        uint32_t cs[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            cw[i] = w[i];
+            cs[i] = sc[i];
+        }
+        const int nx = min(st + 1, last);
+        load_x(nx);
+        load_w(nx);
+        if constexpr (DT == ACT_F16) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const bool fits = scale_fits_f16(cs[i]);
+                left |= !fits && (some(cw[i]) || cs[i] == 255u);
+                cw[i] = codes_if(fits, cw[i]);
+                if (!fits) cs[i] = 127u;
+            }
+        }
+        constexpr bool HALF = DT == ACT_F16;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                u32x4_t b[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) b[j] = *(const u32x4_t*)(xb + (p * MT + 32 * j) * X_ROW + 16 * c);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const u32x4_t v = fp4x8<!HALF>(cw[i][c], mx_scale(cs[i]));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[i][j] = H16<!HALF>::mfma32(v, b[j], acc[i][j]);
+                }
+            }
+        store_x((st & 1) ^ 1);
         __syncthreads();
+    }
+    if constexpr (DT == ACT_F16) {
+        for (int st = __any(left) ? 0 : last + 1; st <= last; ++st) {
+            load_w(st);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            u32x4_t aw[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) aw[i] = fp4x8<true>(w[i][c], sc[i]);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const u32x4_t b = *(const u32x4_t*)(xs + (p * MT + tw + 32 * j + i32) * X_ROW + 64 * h + 16 * c);
+                    Raw<DT, 1> y;
+                    y.template load<false>(a, min(t0 + tw + 32 * j + i32, a.n_tok - 1), (int64_t)MK * st + 32 * h + 8 * c);
+                    u32x4_t p[2];
+                    split_f16(y.w[0], p);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) acc[i][j] = H16<true>::mfma32(aw[i], b, acc[i][j]);
+                    for (int i = 0; i < RW; ++i) {
+                        const bool fits = scale_fits_f16(sc[i]);
+                        const u32x4_t v = fp4x8<true>(fits ? 0u : w[i][c], mx_scale(fits ? 127u : sc[i]));
+                        acc[i][j] = H16<true>::mfma32(v, p[0], acc[i][j]);
+                        acc[i][j] = H16<true>::mfma32(v, p[1], acc[i][j]);
+                    }
                 }
         }
     }
@@ -231,11 +448,18 @@ __global__ __launch_bounds__(256) void mx_many_kernel(MatArgs a) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < RW; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int64_t r = r0 + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3);
-                if (r < a.d_out) a.Y[t * a.ld_y + r] = acc[i][j][e];
+            for (int e = 0; e < 16; e += 4) {
+                const int64_t r = r0 + 32 * i + 2 * e + 4 * h;
+                float* y = a.Y + t * a.ld_y + r;
+                if (a.y_aligned && r + 4 <= a.d_out) {
+                    *(f32x4_t*)y = f32x4_t{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (r + q < a.d_out) y[q] = acc[i][j][e + q];
+                }
             }
     }
 }
@@ -315,17 +539,53 @@ __global__ __launch_bounds__(256) void mx_mx_kernel(MxArgs a) {
     }
 }
 
+// The few-token kernel's tile: the least bytes through a compute unit, where
+// a workgroup reads 16 RT rows of codes and 16 TT tokens for every column and
+// 256 of them run at a time.
+template <Act DT, int RT, int TT>
+void launch_few(const MatArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
+                       dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
+                       dim3(64 * FEW_WAVES), 0, s, a);
+}
+
+template <Act DT, int RW>
+gptq_status launch_many(const MatArgs& a, hipStream_t s) {
+    constexpr int lds = 2 * (DT == ACT_F32 ? 3 : 1) * MT * X_ROW;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_many_kernel<DT, RW>, lds));
+    hipLaunchKernelGGL((mx_many_kernel<DT, RW>), dim3((unsigned)(ceil_div(a.d_out, 64 * RW) * ceil_div(a.n_tok, MT))),
+                       dim3(256), lds, s, a);
+    return GPTQ_OK;
+}
+
 template <Act DT>
-void launch_16bit(const MatArgs& a, hipStream_t s) {
-    if (a.n_tok <= 16) {
-        hipLaunchKernelGGL((mx_few_kernel<DT, 1>), dim3((unsigned)ceil_div(a.d_out, 16)), dim3(64 * FEW_WAVES), 0, s, a);
-    } else if (a.n_tok <= 64) {
-        hipLaunchKernelGGL((mx_few_kernel<DT, 2>), dim3((unsigned)ceil_div(a.d_out, 16), (unsigned)ceil_div(a.n_tok, 32)),
-                           dim3(64 * FEW_WAVES), 0, s, a);
-    } else {
-        hipLaunchKernelGGL(mx_many_kernel<DT>, dim3((unsigned)ceil_div(a.d_out, MT), (unsigned)ceil_div(a.n_tok, MT)),
-                           dim3(256), 0, s, a);
+gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
+    if (a.n_tok <= 256) {
+        const double xb = DT == ACT_F32 ? 4.0 : DT == ACT_FP8 ? 1.03 : DT == ACT_FP4 ? 0.53 : 2.0;
+        const int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
+        int best = 0;
+        double least = 1e30;
+        for (int i = 0; i < 6; ++i) {
+            const double wg = (double)(ceil_div(a.d_out, 16 * rt[i]) * ceil_div(a.n_tok, 16 * tt[i]));
+            const double cost = std::ceil(wg / 256.0) * (0.53 * rt[i] + xb * tt[i]);
+            if (cost < least) {
+                least = cost;
+                best = i;
+            }
+        }
+        switch (best) {
+            case 0: launch_few<DT, 1, 1>(a, s); break;
+            case 1: launch_few<DT, 2, 1>(a, s); break;
+            case 2: launch_few<DT, 4, 1>(a, s); break;
+            case 3: launch_few<DT, 2, 2>(a, s); break;
+            case 4: launch_few<DT, 4, 2>(a, s); break;
+            default: launch_few<DT, 4, 4>(a, s); break;
+        }
+        return GPTQ_OK;
     }
+    // tiles of 256 rows where they fill the chip twice, else of 128
+    if (ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
+    return launch_many<DT, 2>(a, s);
 }
 
 MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int64_t d_in, int64_t d_out, float* Y,
@@ -335,6 +595,8 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
     a.XS = nullptr;
     a.ld_x = 0;
     a.aligned = false;
+    a.full = (int)ceil_div(d_in, MX_PAD);
+    a.y_aligned = ((uintptr_t)Y | (uintptr_t)(4 * ld_y)) % 16 == 0;
     a.n_tok = n_tok;
     a.d_in = d_in;
     a.W = codes;
@@ -357,11 +619,14 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
     a.X = X;
     a.ld_x = ld_x;
     a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
+    a.full = a.aligned ? (int)(d_in / MX_PAD) : 0;
+    gptq_status st;
     switch (dt) {
-        case GPTQ_BF16: launch_16bit<ACT_BF16>(a, s); break;
-        case GPTQ_F16: launch_16bit<ACT_F16>(a, s); break;
-        default: launch_16bit<ACT_F32>(a, s); break;
+        case GPTQ_BF16: st = launch_parts<ACT_BF16>(a, s); break;
+        case GPTQ_F16: st = launch_parts<ACT_F16>(a, s); break;
+        default: st = launch_parts<ACT_F32>(a, s); break;
     }
+    if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -370,16 +635,20 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
                                        int64_t d_in, const uint8_t* codes, const uint8_t* scales, int64_t d_out,
                                        float* Y, int64_t ld_y, hipStream_t s) {
     MatArgs m = mat_args(codes, scales, n_tok, d_in, d_out, Y, ld_y);
+    m.X = xc;
+    m.XS = xs;
+    m.ld_x = mx_code_bytes(d_in, xf);
+    gptq_status st = GPTQ_OK;
     if (xf == GPTQ_MX_FP8) {
-        m.X = xc;
-        m.XS = xs;
-        m.ld_x = mx_code_bytes(d_in, xf);
-        launch_16bit<ACT_FP8>(m, s);
+        st = launch_parts<ACT_FP8>(m, s);
+    } else if (n_tok <= 64) {
+        st = launch_parts<ACT_FP4>(m, s);
     } else {
         const MxArgs a{xc, xs, m};
         hipLaunchKernelGGL(mx_mx_kernel, dim3((unsigned)ceil_div(d_out, 128), (unsigned)ceil_div(n_tok, 128)), dim3(256),
                            0, s, a);
     }
+    if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }

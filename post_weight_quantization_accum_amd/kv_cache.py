@@ -9,7 +9,7 @@ import dataclasses
 
 from . import _lib
 from ._lib import load
-from .mx import _base, _same_device
+from .mx import _current, _dtype_code, _gpu, _on, _torch
 
 FORMATS = {"16bit": _lib.MX_NONE, "fp8": _lib.MX_FP8, "fp4": _lib.MX_FP4}
 
@@ -42,7 +42,7 @@ class KVCache:
 def new_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt: str = "fp8", dtype=None,
               device="cuda") -> KVCache:
     """An empty cache (all zeros); dtype: of a "16bit" cache's values (bfloat16)."""
-    torch = _base()._torch()
+    torch = _torch()
     if fmt not in FORMATS:
         raise ValueError(f"fmt must be one of {', '.join(FORMATS)}")
     if head_dim % 32:
@@ -58,62 +58,75 @@ def new_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt:
 
 
 def _cache(c: KVCache):
-    """(gptq_kv_cache, device) of c, with its tensors checked."""
-    base = _base()
-    torch = base._torch()
-    if c.fmt not in FORMATS:
+    """(reference to gptq_kv_cache, GPU, kv heads, head_dim) of c, with its tensors checked."""
+    torch = _torch()
+    f = FORMATS.get(c.fmt)
+    if f is None:
         raise ValueError(f"cache.fmt must be one of {', '.join(FORMATS)}")
-    mx = c.fmt != "16bit"
-    for name, t in (("k", c.k), ("v", c.v)):
-        if t.dim() != 4 or not t.is_contiguous() or t.shape != c.k.shape:
-            raise TypeError(f"cache.{name} must be a contiguous [page][kv head][offset][...] tensor, k and v alike")
-        if t.dtype not in ((torch.uint8,) if mx else (torch.bfloat16, torch.float16)) or t.dtype != c.k.dtype:
-            raise TypeError(f"cache.{name} has the wrong dtype for a {c.fmt} cache")
-    if c.head_dim % 32:
+    k, v = c.k, c.v
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or not k.is_contiguous() or not v.is_contiguous():
+        raise TypeError("cache.k and cache.v must be contiguous [page][kv head][offset][...] tensors, both alike")
+    n_pages, heads, page, d = shape
+    dt = k.dtype
+    if v.dtype != dt or (dt != torch.uint8 if f else dt != torch.bfloat16 and dt != torch.float16):
+        raise TypeError(f"cache.k and cache.v have the wrong dtype for a {c.fmt} cache")
+    if f == _lib.MX_FP4:
+        d *= 2
+    if d % 32:
         raise ValueError("the cache's head_dim must be a multiple of 32")
-    if mx:
-        want = (*c.k.shape[:3], c.head_dim // 32)
-        for name, t in (("k_scales", c.k_scales), ("v_scales", c.v_scales)):
-            if t is None or t.dtype != torch.uint8 or tuple(t.shape) != want or not t.is_contiguous():
-                raise TypeError(f"cache.{name} must be a contiguous uint8 tensor of shape {want}")
-    dev = _same_device(c.k, c.v, *((c.k_scales, c.v_scales) if mx else ()))
-    p = lambda t: t.data_ptr() if t is not None and mx else None  # noqa: E731
-    return _lib.Cache(c.k.data_ptr(), c.v.data_ptr(), p(c.k_scales), p(c.v_scales), c.k.shape[0], c.page_size,
-                      c.n_kv_heads, c.head_dim, FORMATS[c.fmt], 0 if mx else base._dtype_code(c.k)), dev
+    if not f:
+        return ctypes.byref(_lib.Cache(k.data_ptr(), v.data_ptr(), None, None, n_pages, page, heads, d, f,
+                                       _dtype_code(k))), _gpu(k, v), heads, d
+    ks, vs = c.k_scales, c.v_scales
+    want = (n_pages, heads, page, d // 32)
+    for t in (ks, vs):
+        if t is None or t.dtype != torch.uint8 or t.shape != want or not t.is_contiguous():
+            raise TypeError(f"cache.k_scales and cache.v_scales must be contiguous uint8 tensors of shape {want}")
+    return ctypes.byref(_lib.Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page, heads, d, f,
+                                   0)), _gpu(k, v, ks, vs), heads, d
 
 
 def _heads(X, name, n_heads, head_dim):
-    """(tokens, token stride) of a tokens x heads x head_dim tensor whose tokens are contiguous."""
-    if X.dim() != 3 or (n_heads is not None and X.shape[1] != n_heads) or X.shape[2] != head_dim:
+    """(tokens, token stride, heads) of a tokens x heads x head_dim tensor whose tokens are contiguous."""
+    shape = X.shape
+    if len(shape) != 3 or (n_heads is not None and shape[1] != n_heads) or shape[2] != head_dim:
         raise ValueError(f"{name} must be tokens x heads x head_dim of the cache")
-    if X.stride(2) != 1 or (X.shape[1] > 1 and X.stride(1) != head_dim):
+    n, h, _ = shape
+    ld, by, one = X.stride()
+    if one != 1 or (h > 1 and by != head_dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return X.shape[0], X.stride(0) if X.shape[0] > 1 else X.shape[1] * head_dim
+    return n, ld if n > 1 else h * head_dim, h
 
 
 def _int32(name, t, shape):
-    torch = _base()._torch()
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != _torch().int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+
+
+def _table(table):
+    if table.dim() != 2 or table.dtype != _torch().int32 or not table.is_contiguous():
+        raise TypeError("table must be a contiguous 2-D int32 tensor")
+    return table.shape
 
 
 def cache_write(cache: KVCache, K, V, slots, stream=None):
     """Token t's keys and values (tokens x kv heads x head_dim) to slot
     slots[t] (int64: page * page_size + offset; outside the cache: skipped)."""
-    lib, base = load(), _base()
-    torch = base._torch()
-    c, dev = _cache(cache)
-    _same_device(cache.k, K, V, slots)
-    n, ld_k = _heads(K, "K", cache.n_kv_heads, cache.head_dim)
-    n_v, ld_v = _heads(V, "V", cache.n_kv_heads, cache.head_dim)
+    lib, torch = load(), _torch()
+    c, dev, heads, d = _cache(cache)
+    _gpu(cache.k, K, V, slots)
+    n, ld_k, _ = _heads(K, "K", heads, d)
+    n_v, ld_v, _ = _heads(V, "V", heads, d)
     if n != n_v or K.dtype != V.dtype:
         raise ValueError("K and V must match in tokens and dtype")
-    if slots.dtype != torch.int64 or tuple(slots.shape) != (n,) or not slots.is_contiguous():
+    if slots.dtype != torch.int64 or slots.shape != (n,) or not slots.is_contiguous():
         raise TypeError("slots must be contiguous int64, one per token")
-    with torch.cuda.device(dev):
-        st = lib.gptq_cache_write(ctypes.byref(c), base._ptr(K), base._ptr(V), base._dtype_code(K), n, ld_k, ld_v,
-                                  base._ptr(slots), base._stream(stream))
-    _lib.check(st, "gptq_cache_write")
+    with _on(dev, stream):
+        st = lib.gptq_cache_write(c, K.data_ptr(), V.data_ptr(), _dtype_code(K), n, ld_k, ld_v, slots.data_ptr(),
+                                  _current(dev))
+    if st:
+        _lib.check(st, "gptq_cache_write")
     return cache
 
 
@@ -122,31 +135,28 @@ def cache_read(cache: KVCache, table, row_start, n_rows: int, dtype=None, out=No
     of sequence s (int32 row_start[n_seq + 1], table[n_seq][max_pages]); rows
     outside row_start[0] .. row_start[n_seq] - 1 are not written.  dtype:
     bfloat16 unless given (a "16bit" cache's own)."""
-    lib, base = load(), _base()
-    torch = base._torch()
-    c, dev = _cache(cache)
-    _same_device(cache.k, table, row_start)
-    if table.dim() != 2:
-        raise TypeError("table must be 2-D")
-    n_seq, max_pages = table.shape
-    _int32("table", table, (n_seq, max_pages))
+    lib, torch = load(), _torch()
+    c, dev, heads, d = _cache(cache)
+    _gpu(cache.k, table, row_start)
+    n_seq, max_pages = _table(table)
     _int32("row_start", row_start, (n_seq + 1,))
     if dtype is None:
         dtype = out[0].dtype if out is not None else cache.k.dtype if cache.fmt == "16bit" else torch.bfloat16
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
         if out is None:
-            with base._alloc_on(stream):
-                out = tuple(torch.empty((n_rows, cache.n_kv_heads, cache.head_dim), dtype=dtype, device=dev)
-                            for _ in range(2))
-        K, V = out
-        _same_device(cache.k, K, V)
-        n_k, ld_k = _heads(K, "out", cache.n_kv_heads, cache.head_dim)
-        n_v, ld_v = _heads(V, "out", cache.n_kv_heads, cache.head_dim)
+            K = torch.empty((n_rows, heads, d), dtype=dtype, device=table.device)
+            V = torch.empty((n_rows, heads, d), dtype=dtype, device=table.device)
+        else:
+            K, V = out
+            _gpu(table, K, V)
+        n_k, ld_k, _ = _heads(K, "out", heads, d)
+        n_v, ld_v, _ = _heads(V, "out", heads, d)
         if n_k != n_rows or n_v != n_rows or K.dtype != dtype or V.dtype != dtype:
             raise TypeError("out must be two tensors of n_rows rows and dtype")
-        st = lib.gptq_cache_read(ctypes.byref(c), base._ptr(table), max_pages, n_seq, base._ptr(row_start), n_rows,
-                                 base._ptr(K), base._ptr(V), base._dtype_code(K), ld_k, ld_v, base._stream(stream))
-    _lib.check(st, "gptq_cache_read")
+        st = lib.gptq_cache_read(c, table.data_ptr(), max_pages, n_seq, row_start.data_ptr(), n_rows, K.data_ptr(),
+                                 V.data_ptr(), _dtype_code(K), ld_k, ld_v, _current(dev))
+    if st:
+        _lib.check(st, "gptq_cache_read")
     return K, V
 
 
@@ -162,35 +172,34 @@ def cache_attention(Q, cache: KVCache, q_start, kv_len, table, *, max_q: int | N
     1); it only chooses between kernels.  scale: head_dim ** -0.5 unless
     given.  window > 0: only the last `window` positions.
     """
-    lib, base = load(), _base()
-    torch = base._torch()
-    c, dev = _cache(cache)
-    _same_device(cache.k, Q, q_start, kv_len, table)
-    n, ld_q = _heads(Q, "Q", None, cache.head_dim)
-    n_heads = Q.shape[1]
-    if table.dim() != 2:
-        raise TypeError("table must be 2-D")
-    n_seq, max_pages = table.shape
-    _int32("table", table, (n_seq, max_pages))
+    lib, torch = load(), _torch()
+    c, dev, _, d = _cache(cache)
+    _gpu(cache.k, Q, q_start, kv_len, table)
+    n, ld_q, n_heads = _heads(Q, "Q", None, d)
+    n_seq, max_pages = _table(table)
     _int32("q_start", q_start, (n_seq + 1,))
     _int32("kv_len", kv_len, (n_seq,))
-    most = n if max_q is None else int(max_q)
-    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        nws = lib.gptq_cache_attention_workspace(ctypes.byref(c), n, n_heads, n_seq, max_pages, most, int(window))
-        with base._alloc_on(stream):
-            if out is None:
-                out = torch.empty((n, n_heads, cache.head_dim), dtype=Q.dtype, device=dev)
-            ws = workspace if workspace is not None else base._workspace(nws, dev)
-        _same_device(cache.k, out, ws)
-        n_o, ld_o = _heads(out, "out", n_heads, cache.head_dim)
-        if n_o != n or out.dtype != Q.dtype:
-            raise TypeError("out must match Q in tokens and dtype")
-        st = lib.gptq_cache_attention(ctypes.byref(c), base._ptr(Q), base._dtype_code(Q), n, n_heads, ld_q,
-                                      base._ptr(q_start), base._ptr(kv_len), base._ptr(table), max_pages, n_seq, most,
-                                      scale, int(window), base._ptr(out), ld_o, base._ptr(ws),
-                                      ws.numel() * ws.element_size() if ws is not None else 0, base._stream(stream))
-    _lib.check(st, "gptq_cache_attention")
+    max_q = n if max_q is None else int(max_q)
+    with _on(dev, stream):
+        nws = lib.gptq_cache_attention_workspace(c, n, n_heads, n_seq, max_pages, max_q, window)
+        if out is None:
+            out, ld_o = torch.empty((n, n_heads, d), dtype=Q.dtype, device=Q.device), n_heads * d
+        else:
+            _gpu(Q, out)
+            n_o, ld_o, _ = _heads(out, "out", n_heads, d)
+            if n_o != n or out.dtype != Q.dtype:
+                raise TypeError("out must match Q in tokens and dtype")
+        if workspace is not None:
+            _gpu(Q, workspace)
+            nws = workspace.numel() * workspace.element_size()
+        elif nws:
+            workspace = torch.empty(nws, dtype=torch.uint8, device=Q.device)
+        st = lib.gptq_cache_attention(c, Q.data_ptr(), _dtype_code(Q), n, n_heads, ld_q, q_start.data_ptr(),
+                                      kv_len.data_ptr(), table.data_ptr(), max_pages, n_seq, max_q,
+                                      d ** -0.5 if scale is None else scale, window, out.data_ptr(), ld_o,
+                                      workspace.data_ptr() if workspace is not None else None, nws, _current(dev))
+    if st:
+        _lib.check(st, "gptq_cache_attention")
     return out
 
 

@@ -280,3 +280,19 @@ def test_rows_past_4_gib():
         xq = M.mx_values(q[0].cpu().numpy(), q[1].cpu().numpy(), "fp4", d_in)
         _check(Y[:, -64:].contiguous(), xq, M.mx_values(c, s, "fp4", d_in))
         assert (Y[:, :-64] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 300, 20), (13, 1100, 40), (40, 260, 200), (300, 200, 300), (600, 130, 70)])
+def test_weights_of_every_size(n, d_in, d_out, dtype):
+    """Blocks of weights from 2^-60 to 2^40, among them scales just inside and outside float16's range."""
+    rng = np.random.default_rng(d_in)
+    e = np.repeat(rng.integers(-60, 40, (d_out, -(-d_in // 32))), 32, 1)[:, :d_in].astype(np.float64)
+    e[0], e[1, :64], e[2], e[3] = -24.0 + 2, 15.0, -23.0 + 2, 13.0 + 2
+    e[4::3] = -5.0
+    w, ws = M.mx_quantize(np.clip(rng.standard_normal((d_out, d_in)), -1.9, 1.9) * 2.0 ** e, "fp4")
+    X = torch.from_numpy(rng.standard_normal((n, d_in))).to(TYPES[dtype])
+    Y = P.mx_matmul(X.to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV)).double().cpu().numpy()
+    x, wv = X.double().numpy(), M.mx_values(w, ws, "fp4", d_in)
+    bound = (4 * d_in + 64) * 2.0 ** -23 * (np.abs(x) @ np.abs(wv).T)
+    assert (np.abs(Y - x @ wv.T) <= bound).all()
