@@ -27,16 +27,17 @@ namespace gptq {
 namespace {
 
 constexpr int FEW_ROWS = 16, MANY_ROWS = 128;
+constexpr int FEW_WAVES = 8;                      // of a few-row workgroup, each with steps of its own
 // Sequences of at most this many rows go to the few-row kernel.
 constexpr int FEW_MOST = 64;
-constexpr int FEW_KEYS = 32, MANY_KEYS = 64;      // keys per step
-constexpr int FEW_MIN = 8, MANY_MIN = 8;          // least steps per part
+constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
+constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
 constexpr float RAISE = 8.0f;
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 struct AttnArgs {
     const uint8_t *K, *V, *KS, *VS;
-    int64_t n_pages;
+    uint32_t n_pages;
     FastDiv page;
     int n_kv, d;
     const uint16_t* Q;
@@ -52,7 +53,8 @@ struct AttnArgs {
     float raise;                   // 2^8 in scores before scaling
     int window;                    // 0: none
     uint32_t span;                 // keys that a token sees, itself the last
-    int n_slots, per_seq;          // tiles in the grid; > 0: slots s * per_seq + t, else packed
+    int n_slots;                   // of the many-row kernel's tiles
+    int per_seq;                   // of the few-row kernel's workgroups per sequence
     int n_split;
     int64_t rows_min, rows_max;    // of the sequences this launch takes
     float* part_o;                 // [part][token][head][D]
@@ -109,42 +111,58 @@ __device__ __forceinline__ bool sequence(const AttnArgs& a, int s, Tile& t) {
     return rows > a.rows_min && rows <= a.rows_max;
 }
 
+// Tile of the many-row kernel's slot.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int slot, int rt, Tile& t) {
-    int s, k;
-    if (a.per_seq > 0) {
-        s = slot / a.per_seq;
-        k = slot - s * a.per_seq;
-    } else {
-        s = last_at_most(a.n_seq, slot, [&](int i) { return first_slot(a, i, rt); });
-        if (s < 0) return false;
-        k = slot - first_slot(a, s, rt);
-    }
-    s = __builtin_amdgcn_readfirstlane(s);
-    k = __builtin_amdgcn_readfirstlane(k);
+    const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, slot, [&](int i) { return first_slot(a, i, rt); }));
+    if (s < 0) return false;
+    const int k = __builtin_amdgcn_readfirstlane(slot - first_slot(a, s, rt));
     if (!sequence(a, s, t) || (int64_t)k * rt >= t.rows) return false;
     t.row0 = k * rt;
     tile_keys(a, t, rt);
     return true;
 }
 
-// Parts of a tile, and the steps of one part.
-__device__ __forceinline__ int parts_of(const Tile& t, int keys, int least, int n_split, int& first, int& steps,
-                                        int& per) {
-    first = t.lo / keys;
-    steps = t.hi > t.lo ? (t.hi + keys - 1) / keys - first : 0;
-    const int n = clampi(steps / least, 1, n_split);
-    per = (steps + n - 1) / n;
-    return per ? (steps + per - 1) / per : 1;
+// Steps in one part: the longest sequence's over the number of parts that the
+// grid has room for, so that all parts of a ragged batch are equally long and
+// a shorter sequence has fewer.
+__device__ __forceinline__ int part_steps(const AttnArgs& a, int rt, int keys, int least, int n_split) {
+    if (n_split == 1) return INT32_MAX;
+    int most = 0;
+    for (int i = threadIdx.x & 63; i < a.n_seq; i += 64) most = max(most, a.kv_len[i]);
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) most = max(most, __shfl_xor(most, i, 64));
+    most = min(most, a.cap);
+    if (a.window) most = min(most, a.window + rt);      // a tile has at most rt tokens
+    const int steps = most / keys + 2;                  // at least any tile's
+    return max(least, (steps + n_split - 1) / n_split);
 }
 
-// Row of the cache that holds a position: -1 outside [lo, hi), -2 on a bad
-// page.
-__device__ __forceinline__ int cache_row(const AttnArgs& a, const Tile& t, int head, int key) {
-    if (key < t.lo || key >= t.hi) return -1;
-    const uint32_t n = div_by((uint32_t)key, a.page);
-    const int p = a.table[t.seq * a.max_pages + n];
-    if (p < 0 || p >= a.n_pages) return -2;
-    return (p * a.n_kv + head) * (int)a.page.d + (int)((uint32_t)key - n * a.page.d);
+// Parts of a tile.
+__device__ __forceinline__ int parts_of(const Tile& t, int keys, int per, int& first, int& steps) {
+    first = t.lo / keys;
+    steps = t.hi > t.lo ? (t.hi + keys - 1) / keys - first : 0;
+    return steps > per ? (steps - 1) / per + 1 : 1;
+}
+__device__ __forceinline__ int part_begin(int first, int steps, int per, int part) {
+    return per > steps ? first : first + part * per;
+}
+__device__ __forceinline__ int part_end(int first, int steps, int per, int part) {
+    return per > steps || (part + 1) * per > steps ? first + steps : first + (part + 1) * per;
+}
+
+// The table's entry for a position, as it is: what it says is looked at a
+// step later, when it has arrived.  (Only where the tile has keys at all.)
+__device__ __forceinline__ int table_entry(const AttnArgs& a, const Tile& t, int key) {
+    const uint32_t n = div_by((uint32_t)clampi(key, 0, a.cap - 1), a.page);
+    return a.table[t.seq * a.max_pages + n];
+}
+
+// Row of the cache that holds a position, given its entry: -1 outside
+// [lo, hi), -2 on a bad page.
+__device__ __forceinline__ int cache_row(const AttnArgs& a, const Tile& t, int head, int key, int entry) {
+    const uint32_t off = (uint32_t)key - div_by((uint32_t)key, a.page) * a.page.d;
+    const int row = (entry * a.n_kv + head) * (int)a.page.d + (int)off;
+    return key < t.lo || key >= t.hi ? -1 : (uint32_t)entry >= a.n_pages ? -2 : row;
 }
 
 // Eight elements of Q from channel c of a row of head_dim d.
@@ -176,25 +194,29 @@ struct Chunk {
     }
 };
 
-// Chunk ci of cache row `row` (negative: nothing, all zeros; -2 with `nan`:
-// NaN).
-template <gptq_mx_format F, bool BF>
-__device__ __forceinline__ Chunk<F> load_chunk(const AttnArgs& a, const uint8_t* rows, const uint8_t* scales, int row,
-                                               int ci, bool nan) {
-    Chunk<F> c;
-    c.w = u32x4_t{0u, 0u, 0u, 0u};
-    c.s = nan && row == -2 ? 255u : 0u;
+// Chunk ci of cache row `row`.  Always reads: row 0 for a negative row, the
+// row's first chunk where it has none of that number.  Such a chunk is put
+// right by mend() when it is used, so that nothing waits for it before.
+template <gptq_mx_format F>
+__device__ __forceinline__ void load_chunk(const AttnArgs& a, Chunk<F>& c, const uint8_t* rows, const uint8_t* scales,
+                                           int row, int ci) {
     const int bytes = F == GPTQ_MX_FP4 ? a.d / 2 : F == GPTQ_MX_FP8 ? a.d : 2 * a.d;
-    if (row >= 0) {
-        if (16 * ci < bytes) {
-            c.w = *(const u32x4_t*)(rows + (int64_t)row * bytes + 16 * ci);
-            if constexpr (F != GPTQ_MX_NONE)
-                c.s = scales[(int64_t)row * (a.d >> 5) + (F == GPTQ_MX_FP4 ? ci : ci >> 1)];
-        }
-    } else if (F == GPTQ_MX_NONE && nan && row == -2) {
-        c.w = u32x4_t{H16<BF>::NAN2, H16<BF>::NAN2, H16<BF>::NAN2, H16<BF>::NAN2};
+    const uint32_t r = (uint32_t)max(row, 0), at = 16 * ci < bytes ? 16 * ci : 0;
+    c.w = *(const u32x4_t*)(rows + (uint64_t)r * (uint32_t)bytes + at);
+    if constexpr (F != GPTQ_MX_NONE) c.s = scales[(uint64_t)r * (uint32_t)(a.d >> 5) + (at >> (F == GPTQ_MX_FP4 ? 4 : 5))];
+    else c.s = 0;
+}
+
+// Zeros for a chunk that is not there; for K (`nan`) NaN on a bad page.
+template <gptq_mx_format F, bool BF>
+__device__ __forceinline__ void mend(const AttnArgs& a, Chunk<F>& c, int row, int ci, bool nan) {
+    const int bytes = F == GPTQ_MX_FP4 ? a.d / 2 : F == GPTQ_MX_FP8 ? a.d : 2 * a.d;
+    if (row < 0 || 16 * ci >= bytes) {
+        const bool bad = nan && row == -2;
+        const uint32_t w = F == GPTQ_MX_NONE && bad ? H16<BF>::NAN2 : 0u;
+        c.w = u32x4_t{w, w, w, w};
+        c.s = bad ? 255u : 0u;
     }
-    return c;
 }
 
 template <gptq_mx_format F>
@@ -257,6 +279,16 @@ __device__ float v_value(const AttnArgs& a, int row, int ch) {
 }
 
 template <bool BF>
+__device__ __forceinline__ void store_pair(const AttnArgs& a, uint16_t* p, float v0, float v1) {
+    const uint32_t x = H16<BF>::pack(v0, v1);
+    if (a.o_aligned) {
+        *(uint32_t*)p = x;
+    } else {
+        p[0] = (uint16_t)x;
+        p[1] = (uint16_t)(x >> 16);
+    }
+}
+template <bool BF>
 __device__ __forceinline__ void store_out(const AttnArgs& a, uint16_t* p, float v0, float v1, float v2, float v3) {
     const uint32_t x = H16<BF>::pack(v0, v1), y = H16<BF>::pack(v2, v3);
     if (a.o_aligned) {
@@ -288,7 +320,7 @@ __device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head
                                    int begin, int end, int pos0, int pos1) {
     __threadfence_block();
     __syncthreads();
-    for (int e = threadIdx.x; e < rt * D; e += 256) {
+    for (int e = threadIdx.x; e < rt * D; e += blockDim.x) {
         const int row = t.row0 + e / D, ch = e % D;
         if (row >= t.rows || ch >= a.d) continue;
         const int pos = t.first + (int)div_by((uint32_t)row, a.group);
@@ -296,8 +328,8 @@ __device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head
         for (int step = begin; step < end; ++step) {
             if (!mixed_step(a, step * keys, keys, pos0, pos1)) continue;
             for (int key = step * keys; key < (step + 1) * keys; ++key) {
-                if ((uint32_t)(pos - key) >= a.span) continue;
-                const int r = cache_row(a, t, head, key);
+                if ((uint32_t)(pos - key) >= a.span || key < t.lo || key >= t.hi) continue;
+                const int r = cache_row(a, t, head, key, table_entry(a, t, key));
                 const float v = r >= 0 ? v_value<F, BF>(a, r, ch) : 0.0f;
                 if (!__builtin_isfinite(v)) add += v;
             }
@@ -313,30 +345,38 @@ __device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head
 // ---------------------------------------------------------------------------
 // Few rows.
 // ---------------------------------------------------------------------------
+// Waves per SIMD that the registers are kept for: 16-bit rows take four times
+// those of e2m1.
+template <gptq_mx_format F, int D>
+constexpr int few_waves() { return D == 128 || F == GPTQ_MX_NONE ? 2 : 3; }
+
 template <gptq_mx_format F, bool BF, int D>
-__global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few_kernel(AttnArgs a) {
     constexpr int NC = chunks_of<F>(D), E8 = eights<F>();
-    constexpr int KC = NC > 4 ? NC / 4 : 1;         // 16-byte chunks of K per lane and 16 keys (D = 64, e2m1: half of one)
+    constexpr int KC = NC > 4 ? NC / 4 : 1;         // 16-byte chunks per lane and key (D = 64, e2m1: half of one)
     constexpr int QC = D / 32;                      // k-steps of 32 channels
-    constexpr int VP = NC / 2;                      // V chunks per lane and step
     constexpr int CT = D / 16;
     constexpr int V_ROW = 2 * D + 32;               // rows 32 bytes further in the banks: transposed reads hit all
-    constexpr int WAVE_B = FEW_KEYS * V_ROW;
+    constexpr int WAVE_B = 32 * V_ROW;              // half a step's values at a time
     constexpr int O_ROW = D + 4;
     static_assert(FEW_ROWS * O_ROW * 4 <= WAVE_B, "a wave's outputs fit where its V tile was");
-    __shared__ __attribute__((aligned(16))) char lds[4 * WAVE_B];
-    __shared__ float ml[4][FEW_ROWS][2];
+    __shared__ __attribute__((aligned(16))) char lds[FEW_WAVES * WAVE_B];
+    __shared__ float ml[FEW_WAVES][FEW_ROWS][2];
 
     const int head = blockIdx.x % a.n_kv, rest = blockIdx.x / a.n_kv;
     const int part = rest % a.n_split, slot = rest / a.n_split;
     Tile t;
-    if (!find_tile(a, slot, FEW_ROWS, t)) return;
-    int step0, steps, per;
-    const int n_parts = parts_of(t, FEW_KEYS, FEW_MIN, a.n_split, step0, steps, per);
-    if (part >= n_parts) return;
-    const int end = step0 + min(steps, (part + 1) * per);
+    const int per = part_steps(a, FEW_ROWS, FEW_KEYS, FEW_MIN, a.n_split);
+    if (!sequence(a, slot / a.per_seq, t)) return;
+    // a sequence of more rows than the caller's hint said has several tiles to a workgroup
+    for (t.row0 = slot % a.per_seq * FEW_ROWS; t.row0 < t.rows; t.row0 += a.per_seq * FEW_ROWS) {
+    tile_keys(a, t, FEW_ROWS);
+    int step0, steps;
+    const int n_parts = parts_of(t, FEW_KEYS, per, step0, steps);
+    if (part >= n_parts) continue;
+    const int begin = part_begin(step0, steps, per, part), end = part_end(step0, steps, per, part);
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int n = lane & 15, g = lane >> 4;
     const int row = t.row0 + n;
     const bool live = row < t.rows;
@@ -345,10 +385,20 @@ __global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
     const int pos0 = t.first + (int)div_by((uint32_t)t.row0, a.group);
     const int pos1 = t.first + (int)div_by((uint32_t)min(t.row0 + FEW_ROWS, t.rows) - 1u, a.group);
 
-    // channel of element j of k-step c in lane group g
+    // A lane holds, of keys n, 16 + n, 32 + n and 48 + n of a step, D / 4
+    // channels of K and of V: element j of k-step c is channel chan(c) + j.
     const auto chan = [&](int c) {
         if constexpr (F == GPTQ_MX_NONE) return 32 * c + 8 * g;
         else return D == 128 ? 32 * g + 8 * c : 16 * g + 8 * c;
+    };
+    const auto chunk = [&](int i) {                 // its i-th 16 bytes
+        if constexpr (F == GPTQ_MX_NONE) return 4 * i + g;
+        else if constexpr (D == 64 && F == GPTQ_MX_FP4) return g >> 1;
+        else return KC * g + i;
+    };
+    const auto piece = [&](const Chunk<F>(&x)[KC], int c) {
+        if constexpr (D == 64 && F == GPTQ_MX_FP4) return fp4x8<BF>((g & 1) ? x[0].w[2 + c] : x[0].w[c], mx_scale(x[0].s));
+        else return x[c / E8].template eight<BF>(c % E8);
     };
     u32x4_t q[QC];
     {
@@ -364,83 +414,71 @@ __global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
     bool taken = false;
     char* const vt = lds + wave * WAVE_B;
 
-    // Keys of one step: K chunks of keys n and 16 + n, V chunks of VP keys.
-    struct Step {
-        Chunk<F> k[2][KC];
-        Chunk<F> v[VP];
+    // Keys and values of a step, fetched while the one before is worked on: K
+    // again as soon as the scores are there, V as soon as it is in LDS.
+    Chunk<F> kc[4][KC], vc[4][KC];
+    int row4[4];
+    bool edge = false;                              // some of it is not there
+    const auto entry_of = [&](int step) { return table_entry(a, t, step * FEW_KEYS + lane); };
+    const auto rows_of = [&](int (&r)[4], int step, int entry) {
+        const int mine = step < end ? cache_row(a, t, head, step * FEW_KEYS + lane, entry) : -1;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) r[h] = __shfl(mine, 16 * h + n, 64);
+        return a.d != D || __any(mine < 0);
     };
-    const auto load = [&](Step& s, int rows) {
+    const auto load = [&](Chunk<F>(&c)[KC], const uint8_t* rows, const uint8_t* scales, int r) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = __shfl(rows, 16 * h + n, 64);
-#pragma unroll
-            for (int i = 0; i < KC; ++i) {
-                int ci;
-                if constexpr (F == GPTQ_MX_NONE) ci = 4 * i + g;
-                else if constexpr (D == 128) ci = KC * g + i;
-                else ci = F == GPTQ_MX_FP8 ? g : g >> 1;
-                s.k[h][i] = load_chunk<F, BF>(a, a.K, a.KS, r, ci, true);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int r = __shfl(rows, i * (64 / NC) + lane / NC, 64);
-            s.v[i] = load_chunk<F, BF>(a, a.V, a.VS, r, lane % NC, false);
+        for (int i = 0; i < KC; ++i) {
+            load_chunk<F>(a, c[i], rows, scales, r, chunk(i));
+            if (F == GPTQ_MX_FP8 && i > 0) c[i].s = c[0].s;   // the lane's channels lie in one block
         }
     };
-    const auto rows_of = [&](int step) { return step < end ? cache_row(a, t, head, step * FEW_KEYS + (lane & 31)) : -1; };
 
-    int step = step0 + part * per + wave;
-    Step cur;
-    int rows = rows_of(step);
-    load(cur, rows);
-    rows = rows_of(step + 4);
-    for (; step < end; step += 4) {
-        Step nxt;
-        load(nxt, rows);
-        rows = rows_of(step + 8);
+    int step = begin + wave, entry = 0;
+    if (begin < end) {
+        const int e = entry_of(step);
+        entry = entry_of(step + FEW_WAVES);
+        edge = rows_of(row4, step, e);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) load(kc[h], a.K, a.KS, row4[h]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) load(vc[h], a.V, a.VS, row4[h]);
+    }
+    for (; step < end; step += FEW_WAVES) {
         const int key0 = step * FEW_KEYS;
-
-        // S^T: this lane gets row n, keys key0 + 16 h + 4 g + r
-        f32x4_t s[2];
+        // the next step's rows; the table's entries for the one after it are
+        // asked for first, since loads arrive in order
+        int rown[4];
+        const int e = entry;
+        entry = entry_of(step + 2 * FEW_WAVES);
+        const bool edgen = rows_of(rown, step + FEW_WAVES, e);
+        if (edge) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int i = 0; i < KC; ++i) mend<F, BF>(a, kc[h][i], row4[h], chunk(i), true);
+        }
+        // S^T: this lane gets row n, keys key0 + 16 h + 4 g + r
+        f32x4_t s[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
             s[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < QC; ++c) {
-                u32x4_t k;
-                if constexpr (F == GPTQ_MX_NONE) k = cur.k[h][c].template eight<BF>(0);
-                else if constexpr (D == 128) k = cur.k[h][c / E8].template eight<BF>(c % E8);
-                else if constexpr (F == GPTQ_MX_FP8) k = cur.k[h][0].template eight<BF>(c);
-                else {
-                    // half of a 16-byte chunk per lane group
-                    const uint32_t w = (g & 1) ? cur.k[h][0].w[2 + c] : cur.k[h][0].w[c];
-                    k = fp4x8<BF>(w, mx_scale(cur.k[h][0].s));
-                }
-                s[h] = H16<BF>::mfma16(k, q[c], s[h]);
-            }
+            for (int c = 0; c < QC; ++c) s[h] = H16<BF>::mfma16(piece(kc[h], c), q[c], s[h]);
         }
-        // V to LDS, rows of keys
-        const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
 #pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            char* p = vt + (i * (64 / NC) + lane / NC) * V_ROW + (lane % NC) * (16 * E8);
-#pragma unroll
-            for (int e = 0; e < E8; ++e) {
-                u32x4_t v = cur.v[i].template eight<BF>(e);
-                if (mixed) taken |= take_out<BF>(v);
-                *(u32x4_t*)(p + 16 * e) = v;
-            }
-        }
-        wave_sync();
+        for (int h = 0; h < 4; ++h) load(kc[h], a.K, a.KS, rown[h]);
 
-        float x[8], mx = NEG_INF;
-        const int rel = pos - key0 - 4 * g;
+        float x[16], mx = NEG_INF;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = (uint32_t)(rel - (16 * (e >> 2) + (e & 3))) < a.span ? s[e >> 2][e & 3] : NEG_INF;
-            mx = fmaxf(mx, x[e]);
+        for (int e2 = 0; e2 < 16; ++e2) x[e2] = s[e2 >> 2][e2 & 3];
+        if (key0 < t.lo || key0 + FEW_KEYS > pos0 + 1 || (a.window != 0 && key0 <= pos1 - a.window)) {
+            const int rel = pos - key0 - 4 * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = (uint32_t)(rel - (16 * (i >> 2) + (i & 3))) < a.span ? x[i] : NEG_INF;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
         if (__any(mx > m + a.raise)) {
             mx = fmaxf(mx, m);
             mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
@@ -453,22 +491,46 @@ __global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
         }
         const float base = m == NEG_INF ? 0.0f : m * a.scale;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
-            l += x[e];
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
+            l += x[i];
         }
-        // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
-        const u32x4_t p = {H16<BF>::pack(x[0], x[1]), H16<BF>::pack(x[2], x[3]), H16<BF>::pack(x[4], x[5]),
-                           H16<BF>::pack(x[6], x[7])};
+        const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
         const char* vr = vt + (4 * g + (n >> 2)) * V_ROW + 8 * (n & 3);
 #pragma unroll
-        for (int i = 0; i < CT; ++i)
-            acc[i] = H16<BF>::mfma16(tr_pair(vr + 32 * i, vr + 16 * V_ROW + 32 * i), p, acc[i]);
-        wave_sync();
-        cur = nxt;
+        for (int f = 0; f < 2; ++f) {
+            // V to LDS, rows of keys
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                auto& c4 = vc[2 * f + h];
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < KC; ++i) mend<F, BF>(a, c4[i], row4[2 * f + h], chunk(i), false);
+                }
+#pragma unroll
+                for (int c = 0; c < QC; ++c) {
+                    u32x4_t y = piece(c4, c);
+                    if (mixed) taken |= take_out<BF>(y);
+                    *(u32x4_t*)(vt + (16 * h + n) * V_ROW + 2 * chan(c)) = y;
+                }
+                load(c4, a.V, a.VS, rown[2 * f + h]);
+            }
+            wave_sync();
+            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
+            const float* w = x + 8 * f;
+            const u32x4_t p = {H16<BF>::pack(w[0], w[1]), H16<BF>::pack(w[2], w[3]), H16<BF>::pack(w[4], w[5]),
+                               H16<BF>::pack(w[6], w[7])};
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+                acc[i] = H16<BF>::mfma16(tr_pair(vr + 32 * i, vr + 16 * V_ROW + 32 * i), p, acc[i]);
+            wave_sync();
+        }
+        edge = edgen;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) row4[h] = rown[h];
     }
 
-    // join the four waves
+    // join the waves
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     float* const ow = (float*)vt;
@@ -479,17 +541,17 @@ __global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
         ml[wave][n][1] = l;
     }
     taken = __syncthreads_or(taken);
-    constexpr int CH = D / 16;                      // channels per thread
-    const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * CH;
+    constexpr int TPR = 64 * FEW_WAVES / FEW_ROWS, CH = D / TPR;   // threads of a row, channels of a thread
+    const int r = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CH;
     float mj = NEG_INF;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mj = fmaxf(mj, ml[w][r][0]);
+    for (int w = 0; w < FEW_WAVES; ++w) mj = fmaxf(mj, ml[w][r][0]);
     const float bj = mj == NEG_INF ? 0.0f : mj;
     float lj = 0.0f, o[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) o[i] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < FEW_WAVES; ++w) {
         const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - bj);
         lj += f * ml[w][r][1];
         const float* p = (const float*)(lds + w * WAVE_B) + r * O_ROW + c0;
@@ -506,21 +568,21 @@ __global__ __launch_bounds__(256) void cache_few_kernel(AttnArgs a) {
         if (n_parts == 1) {
             const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
 #pragma unroll
-            for (int i = 0; i < CH; i += 4)
-                if (c0 + i < a.d) store_out<BF>(a, out.o + c0 + i, o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+            for (int i = 0; i < CH; i += 2)
+                if (c0 + i < a.d) store_pair<BF>(a, out.o + c0 + i, o[i] * inv, o[i + 1] * inv);
         } else {
 #pragma unroll
-            for (int i = 0; i < CH; i += 4)
-                *(float4*)(out.f + c0 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            if ((threadIdx.x & 15) == 0) {
+            for (int i = 0; i < CH; i += 2) *(float2*)(out.f + c0 + i) = make_float2(o[i], o[i + 1]);
+            if (threadIdx.x % TPR == 0) {
                 const int64_t at = (out.f - a.part_o) / D;
                 a.part_ml[2 * at] = mj;
                 a.part_ml[2 * at + 1] = lj;
             }
         }
     }
-    if (taken)
-        patch<F, BF, D>(a, t, head, part, n_parts == 1, FEW_ROWS, FEW_KEYS, step0 + part * per, end, pos0, pos1);
+    if (taken) patch<F, BF, D>(a, t, head, part, n_parts == 1, FEW_ROWS, FEW_KEYS, begin, end, pos0, pos1);
+    __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -541,10 +603,11 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
     const int part = rest % a.n_split, slot = a.n_slots - 1 - rest / a.n_split;   // the longest tiles first
     Tile t;
     if (!find_tile(a, slot, MANY_ROWS, t)) return;
-    int step0, steps, per;
-    const int n_parts = parts_of(t, MANY_KEYS, MANY_MIN, a.n_split, step0, steps, per);
+    const int per = part_steps(a, MANY_ROWS, MANY_KEYS, MANY_MIN, a.n_split);
+    int step0, steps;
+    const int n_parts = parts_of(t, MANY_KEYS, per, step0, steps);
     if (part >= n_parts) return;
-    const int begin = step0 + part * per, end = step0 + min(steps, (part + 1) * per);
+    const int begin = part_begin(step0, steps, per, part), end = part_end(step0, steps, per, part);
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, h = lane >> 5;
@@ -573,19 +636,34 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
         for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
     float m = NEG_INF, l = 0.0f;
 
-    const auto rows_of = [&](int (&r)[KPT], int step) {
+    const auto key_of = [&](int step, int i) { return step * MANY_KEYS + (tid + 256 * i) % PER / NC; };
+    const auto entries_of = [&](int (&e)[KPT], int step) {
 #pragma unroll
-        for (int i = 0; i < KPT; ++i)
-            r[i] = step < end ? cache_row(a, t, head, step * MANY_KEYS + (tid + 256 * i) % PER / NC) : -1;
+        for (int i = 0; i < KPT; ++i) e[i] = table_entry(a, t, key_of(step, i));
     };
-    const auto load = [&](Chunk<F> (&c)[CPT], const int (&r)[KPT]) {
+    Chunk<F> c[CPT];
+    int rows[KPT];
+    bool edge = false;
+    const auto load = [&](int step, const int (&e)[KPT]) {
+        edge = a.d != D;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            rows[i] = step < end ? cache_row(a, t, head, key_of(step, i), e[i]) : -1;
+            edge |= rows[i] < 0;
+        }
+        edge = __any(edge);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const bool v = tid + 256 * i >= PER;
-            c[i] = load_chunk<F, BF>(a, v ? a.V : a.K, v ? a.VS : a.KS, r[i % KPT], (tid + 256 * i) % NC, !v);
+            load_chunk<F>(a, c[i], v ? a.V : a.K, v ? a.VS : a.KS, rows[i % KPT], (tid + 256 * i) % NC);
         }
     };
-    const auto store = [&](const Chunk<F> (&c)[CPT], int b, int step) {
+    const auto store = [&](int b, int step) {
+        if (edge) {
+#pragma unroll
+            for (int i = 0; i < CPT; ++i)
+                mend<F, BF>(a, c[i], rows[i % KPT], (tid + 256 * i) % NC, tid + 256 * i < PER);
+        }
         const bool mixed = mixed_step(a, step * MANY_KEYS, MANY_KEYS, tile0, tile1);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
@@ -601,17 +679,25 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
         }
     };
 
-    Chunk<F> c[CPT];
-    int rows[KPT];
-    rows_of(rows, begin);
-    load(c, rows);
-    rows_of(rows, begin + 1);
-    store(c, 0, begin);
+    int entries[KPT];
+    if (begin < end) {
+        entries_of(entries, begin);
+        int first[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) first[i] = entries[i];
+        entries_of(entries, begin + 1);
+        load(begin, first);
+        store(0, begin);
+    }
     __syncthreads();
     for (int step = begin; step < end; ++step) {
         const int b = (step - begin) & 1, key0 = step * MANY_KEYS;
-        load(c, rows);
-        rows_of(rows, step + 2);
+        // the table's entries first: loads arrive in order, and they are wanted before the rest
+        int next[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) next[i] = entries[i];
+        entries_of(entries, step + 2);
+        load(step + 1, next);
         const bool none = key0 > pos1 || (a.window && key0 + MANY_KEYS - 1 <= pos0 - a.window);
         if (!none) {
             const char* kt = lds + b * BUF;
@@ -672,7 +758,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                     acc[i] = H16<BF>::mfma32(tr_pair(v, v + 8 * V_ROW), p[k], acc[i]);
                 }
         }
-        store(c, b ^ 1, step + 1);
+        store(b ^ 1, step + 1);
         __syncthreads();
     }
     taken = __syncthreads_or(taken);
@@ -704,58 +790,99 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The parts of a row joined: a wave per token and head, O = sum_p 2^(m_p - m)
-// O_p / sum_p 2^(m_p - m) l_p.
+// The parts of a row joined: a workgroup per token and head, O = sum_p
+// 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p, each wave with every fourth part.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
     AttnArgs a;
     int64_t few_max;               // sequences of at most this many rows were the few-row kernel's
     int few_split, many_split;
+    int rows_per_seq;              // > 0: only the first so many rows of each sequence and head, none of longer ones
 };
 
-template <bool BF, int D>
+// WAVES waves to a row, 4 / WAVES rows to a workgroup.
+template <bool BF, int D, int WAVES>
 __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
     const AttnArgs& a = j.a;
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    if (id >= a.n_rows) return;
+    constexpr int CH = D / 64;
+    __shared__ float ow[4][D + 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t id = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;
     const int heads = a.n_kv * (int)a.group.d;
-    const int tok = (int)(id / heads), hd = (int)(id - (int64_t)tok * heads);
-    const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, tok, [&](int i) { return a.q_start[i]; }));
-    if (s < 0) return;
     Tile t;
-    sequence(a, s, t);
-    const int64_t row = (int64_t)(tok - t.q0) * a.group.d + hd % a.group.d;
-    if (tok < t.q0 || row >= t.rows) return;
-    const bool few = t.rows <= j.few_max;
-    const int rt = few ? FEW_ROWS : MANY_ROWS;
-    t.row0 = (int)row / rt * rt;
-    tile_keys(a, t, rt);
-    int first, steps, per;
-    const int n = parts_of(t, few ? FEW_KEYS : MANY_KEYS, few ? FEW_MIN : MANY_MIN, few ? j.few_split : j.many_split,
-                           first, steps, per);
+    int row = -1, tok = 0, hd = 0;
+    if (j.rows_per_seq) {
+        const int64_t sh = id / j.rows_per_seq;
+        row = (int)(id - sh * j.rows_per_seq);
+        const int s = (int)(sh / a.n_kv), kv = (int)(sh - (int64_t)s * a.n_kv);
+        if (s >= a.n_seq) row = -1;
+        else {
+            sequence(a, s, t);
+            if (t.rows > j.rows_per_seq || row >= t.rows) row = -1;
+            else {
+                const int i = (int)div_by((uint32_t)row, a.group);
+                tok = t.q0 + i;
+                hd = kv * (int)a.group.d + row - i * (int)a.group.d;
+            }
+        }
+    } else if (id < a.n_rows) {
+        tok = (int)(id / heads);
+        hd = (int)(id - (int64_t)tok * heads);
+        const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, tok, [&](int i) { return a.q_start[i]; }));
+        if (s >= 0) {
+            sequence(a, s, t);
+            const int64_t r = (int64_t)(tok - t.q0) * a.group.d + hd % a.group.d;
+            if (tok >= t.q0 && r < t.rows) row = (int)r;
+        }
+    }
+    int n = 1;
+    if (row >= 0) {
+        const bool few = t.rows <= j.few_max;
+        const int rt = few ? FEW_ROWS : MANY_ROWS, keys = few ? FEW_KEYS : MANY_KEYS;
+        t.row0 = row / rt * rt;
+        tile_keys(a, t, rt);
+        int first, steps;
+        n = parts_of(t, keys, part_steps(a, rt, keys, few ? FEW_MIN : MANY_MIN, few ? j.few_split : j.many_split), first, steps);
+    }
+    // the same for all waves of a row, and of the workgroup where they meet
     if (n == 1) return;
+    const int64_t at0 = (int64_t)tok * heads + hd;
+    const float2* ml = (const float2*)a.part_ml + at0;
     float m = NEG_INF;
-    for (int p = lane; p < n; p += 64) m = fmaxf(m, a.part_ml[2 * (p * a.n_rows + id)]);
+    for (int p = lane; p < n; p += 64) m = fmaxf(m, ml[p * a.n_rows].x);
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
     const float base = m == NEG_INF ? 0.0f : m;
-    constexpr int CH = D / 64;
     float l = 0.0f, o[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) o[i] = 0.0f;
-    for (int p = 0; p < n; ++p) {
-        const int64_t at = p * a.n_rows + id;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - base);
-        l += f * a.part_ml[2 * at + 1];
+#pragma unroll 8
+    for (int p = wave % WAVES; p < n; p += WAVES) {
+        const int64_t at = p * a.n_rows;
+        const float2 v = ml[at];
+        const float f = __builtin_amdgcn_exp2f(v.x - base);
+        l += f * v.y;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[at * D + CH * lane + i];
+        for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[(at + at0) * D + CH * lane + i];
+    }
+    if constexpr (WAVES > 1) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) ow[wave][CH * lane + i] = o[i];
+        if (lane == 0) ow[wave][D] = l;
+        __syncthreads();
+        if (wave) return;
+        l = ow[0][D] + ow[1][D] + ow[2][D] + ow[3][D];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = CH * lane + i;
+            o[i] = ow[0][c] + ow[1][c] + ow[2][c] + ow[3][c];
+        }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* out = a.O + (int64_t)tok * a.ld_o + (int64_t)hd * a.d;
+    uint16_t* out = a.O + (int64_t)tok * a.ld_o + (int64_t)hd * a.d + CH * lane;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
-        if (CH * lane + i < a.d) out[CH * lane + i] = (uint16_t)H16<BF>::pack(o[i] * inv, 0.0f);
+        if (CH * lane + i < a.d) out[i] = (uint16_t)H16<BF>::pack(o[i] * inv, 0.0f);
 }
 
 // What is launched: which sequences go to which kernel, and in how many parts.
@@ -763,32 +890,31 @@ struct Plan {
     bool few, many;
     int64_t few_max;
     int64_t few_slots, many_slots;
-    int few_per_seq, few_split, many_split;
+    int per_seq, few_split, many_split;
     int D;
 };
 
 Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
     Plan p;
-    const int64_t g = s.n_heads / c.n_kv_heads, rows = s.n_tok * g;
+    const int64_t g = s.n_heads / c.n_kv_heads, rows = s.n_tok * g, most = std::max<int64_t>(1, s.max_q * g);
     p.D = c.head_dim <= 64 ? 64 : 128;
     // The hint decides only between kernels: each launch takes every sequence
     // that no other one does, however many rows it has.
-    p.few = true;
-    p.many = s.max_q * g > FEW_MOST;
-    if (p.many && s.n_seq == 1) p.few = false;
+    p.many = most > FEW_MOST;
+    p.few = !(p.many && s.n_seq == 1);
     p.few_max = !p.many ? INT64_MAX : p.few ? FEW_MOST : -1;
-    p.few_per_seq = p.few && p.many ? FEW_MOST / FEW_ROWS : 0;
-    p.few_slots = !p.few ? 0 : p.many ? s.n_seq * p.few_per_seq : rows / FEW_ROWS + s.n_seq;
+    p.per_seq = (int)ceil_div(std::min<int64_t>(most, FEW_MOST), FEW_ROWS);
+    p.few_slots = p.few ? s.n_seq * p.per_seq : 0;
     p.many_slots = p.many ? rows / MANY_ROWS + s.n_seq : 0;
-    // Enough workgroups to fill the chip (four of the few-row kernel's to a
-    // compute unit, two of the other's), parts no shorter than the least.
+    // Parts: where there are fewer workgroups than fill the chip once (one of
+    // the few-row kernel's to a compute unit, two of the other's), and none
+    // shorter than the least.
     int64_t keys = (int64_t)c.page_size * s.max_pages;
     if (s.window) keys = std::min(keys, s.window + s.max_q);
-    const auto split = [&](int64_t slots, int64_t target, int64_t most, int64_t least) {
-        if (slots == 0) return (int64_t)1;
-        return std::max<int64_t>(1, std::min({most, target / (slots * c.n_kv_heads), keys / least}));
+    const auto split = [&](int64_t slots, int64_t room, int64_t limit, int64_t least) {
+        return slots == 0 ? 1 : std::max<int64_t>(1, std::min({limit, room / (slots * c.n_kv_heads), keys / least}));
     };
-    p.few_split = (int)split(p.few_slots, 1024, 128, FEW_KEYS * FEW_MIN);
+    p.few_split = (int)split(p.few_slots, 256, 64, FEW_KEYS * FEW_MIN);
     p.many_split = (int)split(p.many_slots, 512, 32, MANY_KEYS * MANY_MIN);
     return p;
 }
@@ -797,7 +923,6 @@ template <gptq_mx_format F, bool BF, int D>
 void launch(AttnArgs& a, const Plan& p, hipStream_t s) {
     if (p.many) {
         a.n_slots = (int)p.many_slots;
-        a.per_seq = 0;
         a.n_split = p.many_split;
         a.rows_min = p.few ? FEW_MOST : 0;
         a.rows_max = INT64_MAX;
@@ -805,13 +930,12 @@ void launch(AttnArgs& a, const Plan& p, hipStream_t s) {
                            dim3(256), 0, s, a);
     }
     if (p.few) {
-        a.n_slots = (int)p.few_slots;
-        a.per_seq = p.few_per_seq;
+        a.per_seq = p.per_seq;
         a.n_split = p.few_split;
         a.rows_min = 0;
         a.rows_max = p.few_max;
-        hipLaunchKernelGGL((cache_few_kernel<F, BF, D>), dim3((unsigned)(p.few_slots * a.n_kv * p.few_split)), dim3(256),
-                           0, s, a);
+        hipLaunchKernelGGL((cache_few_kernel<F, BF, D>), dim3((unsigned)(p.few_slots * a.n_kv * p.few_split)),
+                           dim3(64 * FEW_WAVES), 0, s, a);
     }
 }
 
@@ -823,8 +947,14 @@ void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) 
         default: launch<GPTQ_MX_NONE, BF, D>(a, p, s); break;
     }
     if (p.few_split > 1 || p.many_split > 1) {
-        JoinArgs j{a, p.few_max, p.few_split, p.many_split};
-        hipLaunchKernelGGL((cache_join_kernel<BF, D>), dim3((unsigned)ceil_div(a.n_rows, 4)), dim3(256), 0, s, j);
+        JoinArgs j{a, p.few_max, p.few_split, p.many_split, 0};
+        if (p.many && p.many_split == 1) j.rows_per_seq = FEW_MOST;   // only the few-row kernel made parts
+        const int64_t rows = j.rows_per_seq ? (int64_t)a.n_seq * a.n_kv * FEW_MOST : a.n_rows;
+        // one wave walks a few parts as fast as four do, and four rows share its workgroup
+        if (std::max(p.few_split, p.many_split) > 8)
+            hipLaunchKernelGGL((cache_join_kernel<BF, D, 4>), dim3((unsigned)rows), dim3(256), 0, s, j);
+        else
+            hipLaunchKernelGGL((cache_join_kernel<BF, D, 1>), dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, s, j);
     }
 }
 
@@ -845,7 +975,7 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     a.V = (const uint8_t*)c.v;
     a.KS = c.k_scales;
     a.VS = c.v_scales;
-    a.n_pages = c.n_pages;
+    a.n_pages = (uint32_t)c.n_pages;
     a.page = fast_div((uint32_t)c.page_size);
     a.n_kv = c.n_kv_heads;
     a.d = c.head_dim;
@@ -871,9 +1001,11 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     const int parts = std::max(p.few_split, p.many_split);
     a.part_o = (float*)ws;
     a.part_ml = parts > 1 ? a.part_o + (int64_t)parts * a.n_rows * p.D : nullptr;
+    a.n_slots = a.per_seq = a.n_split = 1;
+    a.rows_min = a.rows_max = 0;
     // tiles, rows of a sequence and workgroups are counted in 32 bits
     if (a.n_rows > INT32_MAX || p.few_slots * a.n_kv * p.few_split > INT32_MAX ||
-        p.many_slots * a.n_kv * p.many_split > INT32_MAX || ceil_div(a.n_rows, 4) > INT32_MAX)
+        p.many_slots * a.n_kv * p.many_split > INT32_MAX || s.n_seq * a.n_kv * FEW_MOST > INT32_MAX)
         return GPTQ_ERR_UNSUPPORTED;
     const bool bf = dt == GPTQ_BF16;
     if (p.D == 64) {
