@@ -491,10 +491,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
         }
         const float base = m == NEG_INF ? 0.0f : m * a.scale;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
-            l += x[i];
-        }
+        for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
         const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
         const char* vr = vt + (4 * g + (n >> 2)) * V_ROW + 8 * (n & 3);
 #pragma unroll
@@ -516,10 +513,13 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
                 load(c4, a.V, a.VS, rown[2 * f + h]);
             }
             wave_sync();
-            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
+            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it,
+            // and so rounded in their sum
             const float* w = x + 8 * f;
             const u32x4_t p = {H16<BF>::pack(w[0], w[1]), H16<BF>::pack(w[2], w[3]), H16<BF>::pack(w[4], w[5]),
                                H16<BF>::pack(w[6], w[7])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l = H16<BF>::add2(p[i], l);
 #pragma unroll
             for (int i = 0; i < CT; ++i)
                 acc[i] = H16<BF>::mfma16(tr_pair(vr + 32 * i, vr + 16 * V_ROW + 32 * i), p, acc[i]);
@@ -636,22 +636,16 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
         for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
     float m = NEG_INF, l = 0.0f;
 
-    const auto key_of = [&](int step, int i) { return step * MANY_KEYS + (tid + 256 * i) % PER / NC; };
-    const auto entries_of = [&](int (&e)[KPT], int step) {
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) e[i] = table_entry(a, t, key_of(step, i));
-    };
+    // lane l looks after key l of a step
+    const auto entry_of = [&](int step) { return table_entry(a, t, step * MANY_KEYS + lane); };
     Chunk<F> c[CPT];
     int rows[KPT];
     bool edge = false;
-    const auto load = [&](int step, const int (&e)[KPT]) {
-        edge = a.d != D;
+    const auto load = [&](int step, int entry) {
+        const int mine = step < end ? cache_row(a, t, head, step * MANY_KEYS + lane, entry) : -1;
+        edge = a.d != D || __any(mine < 0);
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            rows[i] = step < end ? cache_row(a, t, head, key_of(step, i), e[i]) : -1;
-            edge |= rows[i] < 0;
-        }
-        edge = __any(edge);
+        for (int i = 0; i < KPT; ++i) rows[i] = __shfl(mine, (tid + 256 * i) % PER / NC, 64);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
             const bool v = tid + 256 * i >= PER;
@@ -679,13 +673,10 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
         }
     };
 
-    int entries[KPT];
+    int entry = 0;
     if (begin < end) {
-        entries_of(entries, begin);
-        int first[KPT];
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) first[i] = entries[i];
-        entries_of(entries, begin + 1);
+        const int first = entry_of(begin);
+        entry = entry_of(begin + 1);
         load(begin, first);
         store(0, begin);
     }
@@ -693,10 +684,8 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
     for (int step = begin; step < end; ++step) {
         const int b = (step - begin) & 1, key0 = step * MANY_KEYS;
         // the table's entries first: loads arrive in order, and they are wanted before the rest
-        int next[KPT];
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) next[i] = entries[i];
-        entries_of(entries, step + 2);
+        const int next = entry;
+        entry = entry_of(step + 2);
         load(step + 1, next);
         const bool none = key0 > pos1 || (a.window && key0 + MANY_KEYS - 1 <= pos0 - a.window);
         if (!none) {
@@ -741,14 +730,15 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
             }
             const float base = m == NEG_INF ? 0.0f : m * a.scale;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
-                l += x[e];
-            }
-            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it
+            for (int e = 0; e < 32; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
+            // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it, and
+            // so rounded in their sum (two at a time)
             u32x4_t p[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p[e >> 2][e & 3] = H16<BF>::pack(x[2 * e], x[2 * e + 1]);
+            for (int e = 0; e < 16; ++e) {
+                p[e >> 2][e & 3] = H16<BF>::pack(x[2 * e], x[2 * e + 1]);
+                l = H16<BF>::add2(p[e >> 2][e & 3], l);
+            }
             const char* vr = vt + (4 * h + ((lane & 15) >> 2)) * V_ROW + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k)

@@ -53,6 +53,10 @@ struct H16<true> {
     static __device__ __forceinline__ uint32_t fp8(uint32_t w, float s) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, HI));
     }
+    // c + the two values of w
+    static __device__ __forceinline__ float add2(uint32_t w, float c) {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(s16x2_t, w), __builtin_bit_cast(s16x2_t, 0x3F803F80u), c, false);
+    }
     static __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
@@ -79,6 +83,9 @@ struct H16<false> {
     template <bool HI>
     static __device__ __forceinline__ uint32_t fp8(uint32_t w, float s) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, HI));
+    }
+    static __device__ __forceinline__ float add2(uint32_t w, float c) {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(h16x2_t, w), __builtin_bit_cast(h16x2_t, 0x3C003C00u), c, false);
     }
     static __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h16x8_t, a),
