@@ -155,6 +155,19 @@ __device__ __forceinline__ void parts(const Raw<DT, N>& x, int c, u32x4_t (&p)[p
     }
 }
 
+// Four neighbouring outputs of a token.
+__device__ __forceinline__ void store4(const MatArgs& a, int64_t t, int64_t r, float v0, float v1, float v2, float v3) {
+    float* y = a.Y + t * a.ld_y + r;
+    if (a.y_aligned && r + 4 <= a.d_out) {
+        *(f32x4_t*)y = f32x4_t{v0, v1, v2, v3};
+    } else {
+        if (r < a.d_out) y[0] = v0;
+        if (r + 1 < a.d_out) y[1] = v1;
+        if (r + 2 < a.d_out) y[2] = v2;
+        if (r + 3 < a.d_out) y[3] = v3;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Few tokens: a workgroup computes 16 RT weight rows x 16 TT tokens; its eight
 // waves share the 128-column steps, and their sums meet in LDS.
@@ -285,16 +298,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
 #pragma unroll
             for (int q = 1; q < FEW_WAVES; ++q) v += part[q][e >> 6][l];
             const int64_t t = t0 + 16 * (tile % TT) + (l & 15), r = r0 + 16 * (tile / TT) + 4 * (l >> 4);
-            if (t < a.n_tok) {
-                float* y = a.Y + t * a.ld_y + r;
-                if (a.y_aligned && r + 4 <= a.d_out) {
-                    *(f32x4_t*)y = v;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (r + j < a.d_out) y[j] = v[j];
-                }
-            }
+            if (t < a.n_tok) store4(a, t, r, v[0], v[1], v[2], v[3]);
         }
     }
 }
@@ -450,17 +454,8 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const int64_t r = r0 + 32 * i + 2 * e + 4 * h;
-                float* y = a.Y + t * a.ld_y + r;
-                if (a.y_aligned && r + 4 <= a.d_out) {
-                    *(f32x4_t*)y = f32x4_t{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (r + q < a.d_out) y[q] = acc[i][j][e + q];
-                }
-            }
+            for (int e = 0; e < 16; e += 4)
+                store4(a, t, r0 + 32 * i + 2 * e + 4 * h, acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
     }
 }
 
@@ -468,74 +463,134 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
 // Both operands e2m1: v_mfma_scale_f32_32x32x64_f8f6f4.  Lane l holds row
 // (token) l % 32 and block l / 32 of the 64 columns, 16 bytes, with that
 // block's scale.  (Checked on the GPU against float64.)
+//
+// 64 RW weight rows x 128 tokens per workgroup of 2 x 2 waves, each 32 RW x
+// 64: at four bits a matrix instruction consumes its operands so fast that
+// LDS feeds it only if each is used RW (or two) times.  Stages of 256 columns
+// go through registers into two LDS buffers, a stage ahead; scales come
+// straight from memory, a stage ahead too.
 // ---------------------------------------------------------------------------
 struct MxArgs {
     const uint8_t* X;
     const uint8_t* XS;
-    MatArgs m;             // X, XS, ld_x, aligned unused
+    MatArgs m;             // X, XS, ld_x, aligned, full unused
 };
 
-__global__ __launch_bounds__(256) void mx_mx_kernel(MxArgs a) {
+constexpr int MX_STAGE = 128;                       // bytes of a row per stage
+constexpr int MX_ROW = MX_STAGE + 16;               // 16 bytes further in the banks with each row
+
+template <int Q>
+__device__ __forceinline__ f16_t mfma_fp4(u32x4_t w, u32x4_t x, f16_t c, uint32_t ws, uint32_t xs) {
+    const i32x8_t a = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+    const i32x8_t b = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2 * (Q & 1), (int)ws, 2 * (Q & 1), (int)xs);
+}
+
+template <int RW>
+__global__ __launch_bounds__(256, RW == 4 ? 1 : 2) void mx_mx_kernel(MxArgs a) {
+    constexpr int WR = 64 * RW, ROWS = WR + 128, PER = ROWS / 32;   // rows of a stage; pieces of 16 bytes per thread
+    constexpr int BUF = ROWS * MX_ROW;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i32 = lane & 31, h = lane >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * 128 + 64 * (wave >> 1), t0 = (int64_t)blockIdx.y * 128 + 64 * (wave & 1);
-    const uint8_t *wp[2], *sp[2], *xp[2], *xsp[2];
+    const uint32_t nt = (uint32_t)((a.m.n_tok + 127) / 128), n = gridDim.x, per = n / 8;
+    const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
+    const int64_t r0 = (int64_t)(id / nt) * WR, t0 = (int64_t)(id % nt) * 128;
+    const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
+
+    // this thread's pieces: column 16 (t % 8) of rows t / 8 + 32 j
+    const int pc = 16 * (threadIdx.x & 7), pr = threadIdx.x >> 3;
+    const uint8_t* src[PER];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t row = min(r0 + 32 * i + i32, a.m.d_out - 1), tok = min(t0 + 32 * i + i32, a.m.n_tok - 1);
-        wp[i] = a.m.W + row * a.m.w_row + 16 * h;
-        sp[i] = a.m.S + row * a.m.s_row;
-        xp[i] = a.X + tok * a.m.w_row + 16 * h;
-        xsp[i] = a.XS + tok * a.m.s_row;
+    for (int j = 0; j < PER; ++j) {
+        const int r = pr + 32 * j;
+        src[j] = r < WR ? a.m.W + min(r0 + r, a.m.d_out - 1) * a.m.w_row : a.X + min(t0 + r - WR, a.m.n_tok - 1) * a.m.w_row;
     }
-    f16_t acc[2][2];
+    const uint8_t *ws[RW], *xs[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < RW; ++i) ws[i] = a.m.S + min(r0 + rw + 32 * i + i32, a.m.d_out - 1) * a.m.s_row;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) xs[j] = a.XS + min(t0 + tw + 32 * j + i32, a.m.n_tok - 1) * a.m.s_row;
+
+    u32x4_t piece[PER];
+    uint32_t sw[RW][2], sx[2][2];
+    const int stages = (a.m.steps + 1) / 2;
+    const auto load = [&](int st) {
+        // the last stage can be half a one: nothing is read past a row
+        const bool in = (int64_t)MX_STAGE * st + pc < a.m.w_row, two = 2 * st + 1 < a.m.steps;
+        const int64_t at = in ? (int64_t)MX_STAGE * st + pc : 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            piece[j] = *(const u32x4_t*)(src[j] + at);
+            if (!in) piece[j] = u32x4_t{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const uint32_t* p = (const uint32_t*)(ws[i] + 8 * (int64_t)st);
+            sw[i][0] = p[0];
+            sw[i][1] = two ? p[two ? 1 : 0] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t* p = (const uint32_t*)(xs[j] + 8 * (int64_t)st);
+            sx[j][0] = p[0];
+            sx[j][1] = two ? p[two ? 1 : 0] : 0u;
+        }
+    };
+    const auto store = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) *(u32x4_t*)(lds + b * BUF + (pr + 32 * j) * MX_ROW + pc) = piece[j];
+    };
+    f16_t acc[RW][2];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    for (int st = 0; st < a.m.steps; ++st) {
-        int ws[2], xs[2];
+    load(0);
+    store(0);
+    __syncthreads();
+    for (int st = 0; st < stages; ++st) {
+        uint32_t cw[RW][2], cx[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ws[i] = (int)(*(const uint32_t*)(sp[i] + 4 * (int64_t)st) >> (8 * h));
-            xs[i] = (int)(*(const uint32_t*)(xsp[i] + 4 * (int64_t)st) >> (8 * h));
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i) cw[i][k] = sw[i][k] >> (8 * h);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) cx[j][k] = sx[j][k] >> (8 * h);
         }
+        load(min(st + 1, stages - 1));
+        const char* wb = lds + (st & 1) * BUF + (rw + i32) * MX_ROW + 16 * h;
+        const char* xb = lds + (st & 1) * BUF + (WR + tw + i32) * MX_ROW + 16 * h;
+        const auto step = [&](auto q) {
+            constexpr int Q = decltype(q)::value;
+            u32x4_t x[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            i32x8_t w[2], x[2];
+            for (int j = 0; j < 2; ++j) x[j] = *(const u32x4_t*)(xb + 32 * j * MX_ROW + 32 * Q);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const u32x4_t v = *(const u32x4_t*)(wp[i] + 64 * (int64_t)st + 32 * q);
-                const u32x4_t u = *(const u32x4_t*)(xp[i] + 64 * (int64_t)st + 32 * q);
-                w[i] = i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-                x[i] = i32x8_t{(int)u.x, (int)u.y, (int)u.z, (int)u.w, 0, 0, 0, 0};
+            for (int i = 0; i < RW; ++i) {
+                const u32x4_t w = *(const u32x4_t*)(wb + 32 * i * MX_ROW + 32 * Q);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4<Q>(w, x[j], acc[i][j], cw[i][Q >> 1], cx[j][Q >> 1]);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (q == 0)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], x[j], acc[i][j], 4, 4, 0,
-                                                                                   ws[i], 0, xs[j]);
-                    else
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], x[j], acc[i][j], 4, 4, 2,
-                                                                                   ws[i], 2, xs[j]);
-                }
-        }
+        };
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
+        store((st & 1) ^ 1);
+        __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int64_t t = t0 + 32 * j + i32;
+        const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.m.n_tok) continue;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < RW; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int64_t r = r0 + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3);
-                if (r < a.m.d_out) a.m.Y[t * a.m.ld_y + r] = acc[i][j][e];
-            }
+            for (int e = 0; e < 16; e += 4)
+                store4(a.m, t, r0 + rw + 32 * i + 2 * e + 4 * h, acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
     }
 }
 
@@ -586,6 +641,15 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
     // tiles of 256 rows where they fill the chip twice, else of 128
     if (ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
     return launch_many<DT, 2>(a, s);
+}
+
+template <int RW>
+gptq_status launch_mx(const MxArgs& a, hipStream_t s) {
+    constexpr int lds = 2 * (64 * RW + 128) * MX_ROW;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW>, lds));
+    hipLaunchKernelGGL(mx_mx_kernel<RW>, dim3((unsigned)(ceil_div(a.m.d_out, 64 * RW) * ceil_div(a.m.n_tok, 128))),
+                       dim3(256), lds, s, a);
+    return GPTQ_OK;
 }
 
 MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int64_t d_in, int64_t d_out, float* Y,
@@ -644,9 +708,10 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
     } else if (n_tok <= 64) {
         st = launch_parts<ACT_FP4>(m, s);
     } else {
+        // tiles of 256 rows where they fill the chip, else of 128
         const MxArgs a{xc, xs, m};
-        hipLaunchKernelGGL(mx_mx_kernel, dim3((unsigned)ceil_div(d_out, 128), (unsigned)ceil_div(n_tok, 128)), dim3(256),
-                           0, s, a);
+        if (ceil_div(d_out, 256) * ceil_div(n_tok, 128) >= 256) st = launch_mx<4>(a, s);
+        else st = launch_mx<2>(a, s);
     }
     if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();
