@@ -252,6 +252,43 @@ __device__ __forceinline__ void values8(uint32_t w0, uint32_t w1, uint32_t byte,
 }
 
 // ---------------------------------------------------------------------------
+// Memory to LDS without registers.
+// ---------------------------------------------------------------------------
+// Raw buffer over `bytes` bytes from p (wave-uniform); reads past them give 0.
+__device__ __forceinline__ u32x4_t buffer_of(const void* p, int64_t bytes) {
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    u32x4_t r;
+    r.x = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    r.y = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
+    r.z = __builtin_amdgcn_readfirstlane((uint32_t)min(bytes, (int64_t)0xFFFFFFFF));
+    r.w = 0x00020000u;
+    return r;
+}
+// Lane l's 16 (4) bytes at buffer offset `off` land at LDS address `to` + 16 l
+// (4 l).  Written as inline asm so that the compiler does not make every later
+// LDS read wait for it; the kernel waits itself (wait_vmem, then a barrier).
+// No register receives data.
+__device__ __forceinline__ void dma_16(uint32_t to, uint32_t off, u32x4_t buf) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
+}
+__device__ __forceinline__ void dma_4(uint32_t to, uint32_t off, u32x4_t buf) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
+}
+// At most N of this wave's memory loads still under way.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+// All waves here, with their LDS reads done.
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Launchers (arguments validated in mx_api.hip).
 // ---------------------------------------------------------------------------
 gptq_status mx_quantize_launch(const void* X, gptq_dtype dt, int64_t n_rows, int64_t n_cols, int64_t ld_x,

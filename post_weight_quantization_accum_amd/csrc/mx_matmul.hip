@@ -1,6 +1,7 @@
 // Products with e2m1 weights: Y = X W^T (include/gptq.h, gptq_mx_matmul and
 // gptq_mx_matmul_quantized).
 #include <cmath>
+#include <cstdlib>
 #include <type_traits>
 
 #include "mx.hpp"
@@ -467,8 +468,12 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
 // 64 RW weight rows x 128 tokens per workgroup of 2 x 2 waves, each 32 RW x
 // 64: at four bits a matrix instruction consumes its operands so fast that
 // LDS feeds it only if each is used RW (or two) times.  Stages of 256 columns
-// go through registers into two LDS buffers, a stage ahead; scales come
-// straight from memory, a stage ahead too.
+// of codes go from memory to a ring of three LDS slots, two stages ahead.  Of
+// a row's eight 16-byte chunks number c sits at slot c ^ (row / 2 % 8), so
+// that sixteen rows' reads of one chunk hit all banks.  Scales are fetched for
+// two stages at once (16 bytes of a row by four lanes: a request to the cache
+// per row, where a word per lane was 64 of them and took as long as the
+// codes), half of the rows with each stage, and held in registers from there.
 // ---------------------------------------------------------------------------
 struct MxArgs {
     const uint8_t* X;
@@ -476,8 +481,13 @@ struct MxArgs {
     MatArgs m;             // X, XS, ld_x, aligned, full unused
 };
 
-constexpr int MX_STAGE = 128;                       // bytes of a row per stage
-constexpr int MX_ROW = MX_STAGE + 16;               // 16 bytes further in the banks with each row
+template <int RW>
+struct MxTile {
+    static constexpr int WR = 64 * RW, ROWS = WR + 128;
+    static constexpr int STAGE = 128 * ROWS, RING = 3, SCALES = 16 * ROWS;
+    static constexpr int C_DMA = ROWS / 32, S_DMA = ROWS / 128;   // per wave and stage: 8 rows of codes, 16 of scales
+    static constexpr int LDS = RING * STAGE + 2 * SCALES;
+};
 
 template <int Q>
 __device__ __forceinline__ f16_t mfma_fp4(u32x4_t w, u32x4_t x, f16_t c, uint32_t ws, uint32_t xs) {
@@ -487,60 +497,60 @@ __device__ __forceinline__ f16_t mfma_fp4(u32x4_t w, u32x4_t x, f16_t c, uint32_
 }
 
 template <int RW>
-__global__ __launch_bounds__(256, RW == 4 ? 1 : 2) void mx_mx_kernel(MxArgs a) {
-    constexpr int WR = 64 * RW, ROWS = WR + 128, PER = ROWS / 32;   // rows of a stage; pieces of 16 bytes per thread
-    constexpr int BUF = ROWS * MX_ROW;
+__global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
+    using T = MxTile<RW>;
+    constexpr int DMA = T::C_DMA + T::S_DMA;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i32 = lane & 31, h = lane >> 5;
     const uint32_t nt = (uint32_t)((a.m.n_tok + 127) / 128), n = gridDim.x, per = n / 8;
     const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
-    const int64_t r0 = (int64_t)(id / nt) * WR, t0 = (int64_t)(id % nt) * 128;
+    const int64_t r0 = (int64_t)(id / nt) * T::WR, t0 = (int64_t)(id % nt) * 128;
     const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
 
-    // this thread's pieces: column 16 (t % 8) of rows t / 8 + 32 j
-    const int pc = 16 * (threadIdx.x & 7), pr = threadIdx.x >> 3;
-    const uint8_t* src[PER];
+    // Buffers over the tile's rows (they end with the matrix; the last stage
+    // may read past a row's end, into columns that are not multiplied).
+    const int64_t wn = min((int64_t)T::WR, a.m.d_out - r0), xn = min((int64_t)128, a.m.n_tok - t0);
+    const u32x4_t wb = buffer_of(a.m.W + r0 * a.m.w_row, wn * a.m.w_row), xb = buffer_of(a.X + t0 * a.m.w_row, xn * a.m.w_row);
+    const u32x4_t wsb = buffer_of(a.m.S + r0 * a.m.s_row, wn * a.m.s_row), xsb = buffer_of(a.XS + t0 * a.m.s_row, xn * a.m.s_row);
+    // Codes: instruction j of wave w takes rows 8 (w + 4 j) .. + 7, lane l row
+    // l / 8 and slot l % 8 of them.
+    uint32_t coff[T::C_DMA];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int r = pr + 32 * j;
-        src[j] = r < WR ? a.m.W + min(r0 + r, a.m.d_out - 1) * a.m.w_row : a.X + min(t0 + r - WR, a.m.n_tok - 1) * a.m.w_row;
+    for (int j = 0; j < T::C_DMA; ++j) {
+        const int r = 8 * (wave + 4 * j) + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
+        const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
+        coff[j] = (uint32_t)(row * a.m.w_row + 16 * c);
     }
-    const uint8_t *ws[RW], *xs[2];
+    // Scales of two stages: instruction j of wave w takes rows 16 (w + 4 j) ..
+    // + 15, lane l word l % 4 of row l / 4; the first S_DMA of them make one
+    // half, the others the other.
+    uint32_t soff[2 * T::S_DMA];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) ws[i] = a.m.S + min(r0 + rw + 32 * i + i32, a.m.d_out - 1) * a.m.s_row;
+    for (int j = 0; j < 2 * T::S_DMA; ++j) {
+        const int r = 16 * (wave + 4 * j) + (lane >> 2);
+        const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
+        soff[j] = (uint32_t)(row * a.m.s_row + 4 * (lane & 3));
+    }
+    const uint32_t base = (uint32_t)(uintptr_t)lds;
+    const int stages = (a.m.steps + 1) / 2, pairs = (stages + 1) / 2;
+    const auto fetch = [&](int st, int slot) {
+        const uint32_t at = base + slot * T::STAGE, co = __builtin_amdgcn_readfirstlane(128 * st);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) xs[j] = a.XS + min(t0 + tw + 32 * j + i32, a.m.n_tok - 1) * a.m.s_row;
+        for (int j = 0; j < T::C_DMA; ++j)
+            dma_16(at + 1024 * (wave + 4 * j), coff[j] + co, 32 * j < T::WR ? wb : xb);
+    };
+    const auto fetch_scales = [&](int pair, auto half) {
+        const uint32_t at = base + T::RING * T::STAGE + (pair & 1) * T::SCALES;
+        const uint32_t so = __builtin_amdgcn_readfirstlane(16 * min(pair, pairs - 1));
+#pragma unroll
+        for (int i = 0; i < T::S_DMA; ++i) {
+            constexpr int H = decltype(half)::value;
+            const int j = H * T::S_DMA + i;
+            dma_4(at + 256 * (wave + 4 * j), soff[j] + so, 64 * j + 16 * wave < T::WR ? wsb : xsb);
+        }
+    };
 
-    u32x4_t piece[PER];
-    uint32_t sw[RW][2], sx[2][2];
-    const int stages = (a.m.steps + 1) / 2;
-    const auto load = [&](int st) {
-        // the last stage can be half a one: nothing is read past a row
-        const bool in = (int64_t)MX_STAGE * st + pc < a.m.w_row, two = 2 * st + 1 < a.m.steps;
-        const int64_t at = in ? (int64_t)MX_STAGE * st + pc : 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            piece[j] = *(const u32x4_t*)(src[j] + at);
-            if (!in) piece[j] = u32x4_t{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-            const uint32_t* p = (const uint32_t*)(ws[i] + 8 * (int64_t)st);
-            sw[i][0] = p[0];
-            sw[i][1] = two ? p[two ? 1 : 0] : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t* p = (const uint32_t*)(xs[j] + 8 * (int64_t)st);
-            sx[j][0] = p[0];
-            sx[j][1] = two ? p[two ? 1 : 0] : 0u;
-        }
-    };
-    const auto store = [&](int b) {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) *(u32x4_t*)(lds + b * BUF + (pr + 32 * j) * MX_ROW + pc) = piece[j];
-    };
     f16_t acc[RW][2];
 #pragma unroll
     for (int i = 0; i < RW; ++i)
@@ -548,40 +558,62 @@ __global__ __launch_bounds__(256, RW == 4 ? 1 : 2) void mx_mx_kernel(MxArgs a) {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int st = 0; st < stages; ++st) {
-        uint32_t cw[RW][2], cx[2][2];
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
+    fetch_scales(0, First{});
+    fetch_scales(0, Second{});
+    fetch(0, 0);
+    fetch(min(1, stages - 1), 1);
+    fetch_scales(1, First{});
+    int slot = 0;
+    u32x4_t ws[RW], xs[2];
+    // Stage 2 p + k: PAIR k of the scales of pair p.
+    const auto multiply = [&](int st, auto k) {
+        constexpr int K = decltype(k)::value;
+        wait_vmem<DMA>();                               // this stage has landed, the next may be under way
+        meet();
+        // the slot of the stage before is free: the stage after next goes there
+        fetch(min(st + 2, stages - 1), slot == 0 ? 2 : slot - 1);
+        if constexpr (K == 0) {
+            fetch_scales((st >> 1) + 1, Second{});
+            const u32x4_t* sb = (const u32x4_t*)(lds + T::RING * T::STAGE + (st >> 1 & 1) * T::SCALES) + i32;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+            for (int i = 0; i < RW; ++i) ws[i] = sb[rw + 32 * i];
 #pragma unroll
-            for (int i = 0; i < RW; ++i) cw[i][k] = sw[i][k] >> (8 * h);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) cx[j][k] = sx[j][k] >> (8 * h);
+            for (int j = 0; j < 2; ++j) xs[j] = sb[T::WR + tw + 32 * j];
+        } else {
+            fetch_scales((st >> 1) + 2, First{});       // this pair's scales are in registers
         }
-        load(min(st + 1, stages - 1));
-        const char* wb = lds + (st & 1) * BUF + (rw + i32) * MX_ROW + 16 * h;
-        const char* xb = lds + (st & 1) * BUF + (WR + tw + i32) * MX_ROW + 16 * h;
+        const char* cb = lds + slot * T::STAGE;
+        const char* wp = cb + (rw + i32) * 128;
+        const char* xp = cb + (T::WR + tw + i32) * 128;
         const auto step = [&](auto q) {
-            constexpr int Q = decltype(q)::value;
+            constexpr int Q = decltype(q)::value, W = 2 * K + (Q >> 1);
+            const int c = 16 * ((2 * Q + h) ^ (i32 >> 1 & 7));
             u32x4_t x[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) x[j] = *(const u32x4_t*)(xb + 32 * j * MX_ROW + 32 * Q);
+            for (int j = 0; j < 2; ++j) x[j] = *(const u32x4_t*)(xp + 32 * 128 * j + c);
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
-                const u32x4_t w = *(const u32x4_t*)(wb + 32 * i * MX_ROW + 32 * Q);
+                const u32x4_t w = *(const u32x4_t*)(wp + 32 * 128 * i + c);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4<Q>(w, x[j], acc[i][j], cw[i][Q >> 1], cx[j][Q >> 1]);
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = mfma_fp4<Q>(w, x[j], acc[i][j], ws[i][W] >> (8 * h), xs[j][W] >> (8 * h));
             }
         };
         step(std::integral_constant<int, 0>{});
         step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 3>{});
-        store((st & 1) ^ 1);
-        __syncthreads();
+        if (2 * st + 1 < a.m.steps) {
+            step(std::integral_constant<int, 2>{});
+            step(std::integral_constant<int, 3>{});
+        }
+        slot = slot == 2 ? 0 : slot + 1;
+    };
+    for (int st = 0; st < stages; st += 2) {
+        multiply(st, First{});
+        if (st + 1 < stages) multiply(st + 1, Second{});
     }
+    wait_vmem<0>();                                     // nothing lands in LDS that is another's by then
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
@@ -639,13 +671,13 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
         return GPTQ_OK;
     }
     // tiles of 256 rows where they fill the chip twice, else of 128
-    if (ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
+    if (getenv("XR") ? atoi(getenv("XR")) == 4 : ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
     return launch_many<DT, 2>(a, s);
 }
 
 template <int RW>
 gptq_status launch_mx(const MxArgs& a, hipStream_t s) {
-    constexpr int lds = 2 * (64 * RW + 128) * MX_ROW;
+    constexpr int lds = MxTile<RW>::LDS;
     GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW>, lds));
     hipLaunchKernelGGL(mx_mx_kernel<RW>, dim3((unsigned)(ceil_div(a.m.d_out, 64 * RW) * ceil_div(a.m.n_tok, 128))),
                        dim3(256), lds, s, a);
