@@ -461,6 +461,203 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Many tokens of 16 bits whose rows start on 16 bytes: 64 RG weight rows x 128
+// tokens per workgroup of RG x 2 waves of 64 x 64, with both operands
+// brought from memory to a ring of three LDS slots of 128 columns, two stages
+// ahead and without registers.  16-byte chunk c of a row sits at slot c ^
+// (row % 16) (activations: 16 chunks) or c ^ (row / 4 % 4) (codes: 4), so that
+// sixteen rows' reads of one chunk hit all banks.  Scales are fetched for four
+// stages at once, a quarter of the rows with each stage (four lanes to the 16
+// bytes of a row), and held in registers from there.  Columns after the last
+// whole 128 come from memory directly, at the end.
+// ---------------------------------------------------------------------------
+template <int RG>
+struct WideTile {
+    static constexpr int WAVES = 2 * RG, WR = 64 * RG;
+    static constexpr int W_BYTES = 64 * WR, X_BYTES = 256 * MT, STAGE = W_BYTES + X_BYTES, RING = 3, SCALES = 16 * WR;
+    static constexpr int W_DMA = WR / 16 / WAVES, X_DMA = MT / 4 / WAVES;   // per wave and stage: 16 rows of codes, 4 tokens
+    static constexpr int LDS = RING * STAGE + 2 * SCALES;
+};
+
+template <Act DT, int RG>
+__global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
+    using T = WideTile<RG>;
+    constexpr int RW = 2, NW = T::WAVES;
+    constexpr int DMA = T::W_DMA + T::X_DMA + 1;
+    constexpr bool HALF = DT == ACT_F16;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int i32 = lane & 31, h = lane >> 5;
+    const uint32_t nt = (uint32_t)((a.n_tok + MT - 1) / MT), n = gridDim.x, per = n / 8;
+    const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
+    const int64_t r0 = (int64_t)(id / nt) * T::WR, t0 = (int64_t)(id % nt) * MT;
+    const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
+
+    // buffers over the tile's rows: they end with the matrix
+    const int64_t wn = min((int64_t)T::WR, a.d_out - r0), xn = min((int64_t)MT, a.n_tok - t0);
+    const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), sb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row);
+    const u32x4_t xb = buffer_of((const uint16_t*)a.X + t0 * a.ld_x, 2 * ((xn - 1) * a.ld_x + a.d_in));
+    uint32_t woff[T::W_DMA], xoff[T::X_DMA], soff[4];
+#pragma unroll
+    for (int j = 0; j < T::W_DMA; ++j) {
+        const int r = 16 * (wave + NW * j) + (lane >> 2), c = (lane & 3) ^ (r >> 2 & 3);
+        woff[j] = (uint32_t)(min((int64_t)r, wn - 1) * a.w_row + 16 * c);
+    }
+#pragma unroll
+    for (int j = 0; j < T::X_DMA; ++j) {
+        const int r = 4 * (wave + NW * j) + (lane >> 4), c = (lane & 15) ^ (r & 15);
+        xoff[j] = (uint32_t)(min((int64_t)r, xn - 1) * 2 * a.ld_x + 16 * c);
+    }
+    // the waves bring some scales twice
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        soff[k] = (uint32_t)(min((int64_t)(16 * ((wave + NW * k) % (T::WR / 16)) + (lane >> 2)), wn - 1) * a.s_row + 4 * (lane & 3));
+    const uint32_t base = (uint32_t)(uintptr_t)lds;
+    const int stages = a.full, quads = (stages + 3) / 4;
+    // stage f's codes and activations, and a quarter of the scales of the four
+    // stages after its own four
+    const auto fetch_scales = [&](int quad, int k) {
+        dma_4(base + T::RING * T::STAGE + (quad & 1) * T::SCALES + 256 * ((wave + NW * k) % (T::WR / 16)),
+              soff[k] + __builtin_amdgcn_readfirstlane(16 * min(quad, quads - 1)), sb);
+    };
+    // every eighth of a stage's pieces from e on
+    constexpr int PIECES = T::W_DMA + T::X_DMA;
+    const auto fetch = [&](int f, int slot, int e) {
+        const int st = min(f, stages - 1);
+        const uint32_t at = base + slot * T::STAGE;
+#pragma unroll
+        for (int j = e; j < PIECES; j += 8) {
+            if (j < T::X_DMA)
+                dma_16(at + T::W_BYTES + 1024 * (wave + NW * j), xoff[j] + __builtin_amdgcn_readfirstlane(256 * st), xb);
+            else
+                dma_16(at + 1024 * (wave + NW * (j - T::X_DMA)), woff[j - T::X_DMA] + __builtin_amdgcn_readfirstlane(64 * st), wb);
+        }
+    };
+
+    f16_t acc[RW][2];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    bool left = false;       // float16: a block was left out
+    int slot = 0;
+    u32x4_t ws[RW];
+    const auto multiply = [&](int st, auto kk) {
+        constexpr int K = decltype(kk)::value;              // st % 4
+        wait_vmem<DMA>();                                   // this stage has landed, the next may be under way
+        meet();
+        // The slot of the stage before is free: the stage after next goes there,
+        // a few pieces with each step, so that the products need not wait until
+        // all of it is asked for.
+        const int fslot = slot == 0 ? 2 : slot - 1;
+        if constexpr (K == 0) {
+            const u32x4_t* p = (const u32x4_t*)(lds + T::RING * T::STAGE + (st >> 2 & 1) * T::SCALES) + rw + i32;
+#pragma unroll
+            for (int i = 0; i < RW; ++i) ws[i] = p[32 * i];
+        }
+        const char* wp = lds + slot * T::STAGE + (rw + i32) * 64;
+        const char* xp = lds + slot * T::STAGE + T::W_BYTES + (tw + i32) * 256;
+        u32x4_t w[2][RW], x[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < RW; ++i)
+                w[q][i] = *(const u32x4_t*)(wp + 32 * 64 * i + 16 * ((2 * q + h) ^ (i32 >> 2 & 3)));
+        // a step's activations are read while the one before multiplies
+        const auto read = [&](int e) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[e & 1][j] = *(const u32x4_t*)(xp + 32 * 256 * j + 16 * ((8 * (e >> 2) + 4 * h + (e & 3)) ^ (i32 & 15)));
+        };
+        read(0);
+        float sc[RW];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int q = e >> 2, c = e & 3;
+            if (e < 7) read(e + 1);
+            if (c == 0) {
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    uint32_t byte = ws[i][K] >> (16 * q + 8 * h) & 255u;
+                    if constexpr (HALF) {
+                        const bool fits = scale_fits_f16(byte);
+                        left |= !fits && (some(w[q][i]) || byte == 255u);
+                        w[q][i] = codes_if(fits, w[q][i]);
+                        byte = fits ? byte : 127u;
+                    }
+                    sc[i] = mx_scale(byte);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const u32x4_t v = fp4x8<!HALF>(w[q][i][c], sc[i]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = H16<!HALF>::mfma32(v, x[e & 1][j], acc[i][j]);
+            }
+            fetch(st + 2, fslot, e);
+            if (e == 7) fetch_scales(((st + 2) >> 2) + 1, (K + 2) & 3);
+        }
+        slot = slot == 2 ? 0 : slot + 1;
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) fetch_scales(0, k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) fetch(0, 0, e);
+    fetch_scales(1, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) fetch(1, 1, e);
+    fetch_scales(1, 1);
+    for (int st = 0; st < stages; st += 4) {
+        multiply(st, std::integral_constant<int, 0>{});
+        if (st + 1 < stages) multiply(st + 1, std::integral_constant<int, 1>{});
+        if (st + 2 < stages) multiply(st + 2, std::integral_constant<int, 2>{});
+        if (st + 3 < stages) multiply(st + 3, std::integral_constant<int, 3>{});
+    }
+    wait_vmem<0>();                                         // nothing lands in LDS that is another's by then
+
+    // the columns after the last whole stage, and for float16 the blocks that
+    // were left out before it
+    const int last = 2 * a.steps;
+    for (int st = DT == ACT_F16 && __any(left) ? 0 : 2 * stages; st < last; ++st) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                Raw<DT, 1> y;
+                y.template load<false>(a, min(t0 + tw + 32 * j + i32, a.n_tok - 1), (int64_t)MK * st + 32 * h + 8 * c);
+                u32x4_t p[parts_of<DT>()];
+                parts(y, 0, p);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int64_t row = min(r0 + rw + 32 * i + i32, a.d_out - 1);
+                    uint32_t code = *(const uint32_t*)(a.W + row * a.w_row + 32 * (int64_t)st + 16 * h + 4 * c);
+                    uint32_t byte = a.S[row * a.s_row + 2 * (int64_t)st + h];
+                    if (st < 2 * stages && scale_fits_f16(byte)) {
+                        code = 0u;
+                        byte = 127u;
+                    }
+                    const u32x4_t v = fp4x8<true>(code, mx_scale(byte));
+#pragma unroll
+                    for (int k = 0; k < parts_of<DT>(); ++k) acc[i][j] = H16<true>::mfma32(v, p[k], acc[i][j]);
+                }
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t t = t0 + tw + 32 * j + i32;
+        if (t >= a.n_tok) continue;
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                store4(a, t, r0 + rw + 32 * i + 2 * e + 4 * h, acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Both operands e2m1: v_mfma_scale_f32_32x32x64_f8f6f4.  Lane l holds row
 // (token) l % 32 and block l / 32 of the 64 columns, 16 bytes, with that
 // block's scale.  (Checked on the GPU against float64.)
@@ -534,11 +731,14 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
     }
     const uint32_t base = (uint32_t)(uintptr_t)lds;
     const int stages = (a.m.steps + 1) / 2, pairs = (stages + 1) / 2;
-    const auto fetch = [&](int st, int slot) {
+    // quarter q of a stage's codes
+    const auto fetch = [&](int st, int slot, int q) {
         const uint32_t at = base + slot * T::STAGE, co = __builtin_amdgcn_readfirstlane(128 * st);
 #pragma unroll
-        for (int j = 0; j < T::C_DMA; ++j)
+        for (int i = 0; i < T::C_DMA / 4; ++i) {
+            const int j = q * (T::C_DMA / 4) + i;
             dma_16(at + 1024 * (wave + 4 * j), coff[j] + co, 32 * j < T::WR ? wb : xb);
+        }
     };
     const auto fetch_scales = [&](int pair, auto half) {
         const uint32_t at = base + T::RING * T::STAGE + (pair & 1) * T::SCALES;
@@ -562,8 +762,10 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
     using Second = std::integral_constant<int, 1>;
     fetch_scales(0, First{});
     fetch_scales(0, Second{});
-    fetch(0, 0);
-    fetch(min(1, stages - 1), 1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) fetch(0, 0, q);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) fetch(min(1, stages - 1), 1, q);
     fetch_scales(1, First{});
     int slot = 0;
     u32x4_t ws[RW], xs[2];
@@ -572,41 +774,60 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
         constexpr int K = decltype(k)::value;
         wait_vmem<DMA>();                               // this stage has landed, the next may be under way
         meet();
-        // the slot of the stage before is free: the stage after next goes there
-        fetch(min(st + 2, stages - 1), slot == 0 ? 2 : slot - 1);
+        // The slot of the stage before is free: the stage after next goes there,
+        // a quarter with each step, so that the products need not wait until
+        // all of it is asked for.
+        const int far = min(st + 2, stages - 1), fslot = slot == 0 ? 2 : slot - 1;
         if constexpr (K == 0) {
-            fetch_scales((st >> 1) + 1, Second{});
             const u32x4_t* sb = (const u32x4_t*)(lds + T::RING * T::STAGE + (st >> 1 & 1) * T::SCALES) + i32;
 #pragma unroll
             for (int i = 0; i < RW; ++i) ws[i] = sb[rw + 32 * i];
 #pragma unroll
             for (int j = 0; j < 2; ++j) xs[j] = sb[T::WR + tw + 32 * j];
-        } else {
-            fetch_scales((st >> 1) + 2, First{});       // this pair's scales are in registers
         }
         const char* cb = lds + slot * T::STAGE;
         const char* wp = cb + (rw + i32) * 128;
         const char* xp = cb + (T::WR + tw + i32) * 128;
+        // a step's operands are read while the one before multiplies
+        u32x4_t x[2][2], w[2][RW];
+        const auto read = [&](auto q) {
+            constexpr int Q = decltype(q)::value;
+            const int c = 16 * ((2 * Q + h) ^ (i32 >> 1 & 7));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) x[Q & 1][j] = *(const u32x4_t*)(xp + 32 * 128 * j + c);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) w[Q & 1][i] = *(const u32x4_t*)(wp + 32 * 128 * i + c);
+            __builtin_amdgcn_sched_barrier(0);
+        };
         const auto step = [&](auto q) {
             constexpr int Q = decltype(q)::value, W = 2 * K + (Q >> 1);
-            const int c = 16 * ((2 * Q + h) ^ (i32 >> 1 & 7));
-            u32x4_t x[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) x[j] = *(const u32x4_t*)(xp + 32 * 128 * j + c);
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                const u32x4_t w = *(const u32x4_t*)(wp + 32 * 128 * i + c);
+            for (int i = 0; i < RW; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    acc[i][j] = mfma_fp4<Q>(w, x[j], acc[i][j], ws[i][W] >> (8 * h), xs[j][W] >> (8 * h));
-            }
+                    acc[i][j] = mfma_fp4<Q>(w[Q & 1][i], x[Q & 1][j], acc[i][j], ws[i][W] >> (8 * h), xs[j][W] >> (8 * h));
         };
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-        if (2 * st + 1 < a.m.steps) {
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
+        using Q0 = std::integral_constant<int, 0>;
+        using Q1 = std::integral_constant<int, 1>;
+        using Q2 = std::integral_constant<int, 2>;
+        using Q3 = std::integral_constant<int, 3>;
+        const bool both = 2 * st + 1 < a.m.steps;       // uniform: the last stage can be half a one
+        read(Q0{});
+        read(Q1{});
+        step(Q0{});
+        fetch(far, fslot, 0);
+        if (both) read(Q2{});
+        step(Q1{});
+        fetch(far, fslot, 1);
+        if constexpr (K == 0) fetch_scales((st >> 1) + 1, Second{});
+        else fetch_scales((st >> 1) + 2, First{});      // this pair's scales are in registers
+        if (both) {
+            read(Q3{});
+            step(Q2{});
         }
+        fetch(far, fslot, 2);
+        if (both) step(Q3{});
+        fetch(far, fslot, 3);
         slot = slot == 2 ? 0 : slot + 1;
     };
     for (int st = 0; st < stages; st += 2) {
@@ -645,9 +866,19 @@ gptq_status launch_many(const MatArgs& a, hipStream_t s) {
     return GPTQ_OK;
 }
 
+template <Act DT, int RG>
+gptq_status launch_wide(const MatArgs& a, hipStream_t s) {
+    constexpr int lds = WideTile<RG>::LDS;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_wide_kernel<DT, RG>, lds));
+    hipLaunchKernelGGL((mx_wide_kernel<DT, RG>), dim3((unsigned)(ceil_div(a.d_out, 64 * RG) * ceil_div(a.n_tok, MT))),
+                       dim3(128 * RG), lds, s, a);
+    return GPTQ_OK;
+}
+
 template <Act DT>
 gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    if (a.n_tok <= 256) {
+    const int xr = getenv("XRT") ? atoi(getenv("XRT")) : 0;
+    if (xr ? xr == 1 : a.n_tok <= 256) {
         const double xb = DT == ACT_F32 ? 4.0 : DT == ACT_FP8 ? 1.03 : DT == ACT_FP4 ? 0.53 : 2.0;
         const int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
         int best = 0;
@@ -670,8 +901,12 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
         }
         return GPTQ_OK;
     }
+    if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
+        if (xr == 3) return launch_wide<DT, 2>(a, s);
+        if (xr == 4) return launch_wide<DT, 4>(a, s);
+    }
     // tiles of 256 rows where they fill the chip twice, else of 128
-    if (getenv("XR") ? atoi(getenv("XR")) == 4 : ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
+    if (xr == 5 || ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
     return launch_many<DT, 2>(a, s);
 }
 
@@ -737,12 +972,12 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
     gptq_status st = GPTQ_OK;
     if (xf == GPTQ_MX_FP8) {
         st = launch_parts<ACT_FP8>(m, s);
-    } else if (n_tok <= 64) {
+    } else if (getenv("XRT") ? atoi(getenv("XRT")) == 1 : n_tok <= 64) {
         st = launch_parts<ACT_FP4>(m, s);
     } else {
         // tiles of 256 rows where they fill the chip, else of 128
         const MxArgs a{xc, xs, m};
-        if (ceil_div(d_out, 256) * ceil_div(n_tok, 128) >= 256) st = launch_mx<4>(a, s);
+        if (getenv("XRT") ? atoi(getenv("XRT")) == 4 : ceil_div(d_out, 256) * ceil_div(n_tok, 128) >= 256) st = launch_mx<4>(a, s);
         else st = launch_mx<2>(a, s);
     }
     if (st != GPTQ_OK) return st;
