@@ -1,7 +1,7 @@
 // Products with e2m1 weights: Y = X W^T (include/gptq.h, gptq_mx_matmul and
 // gptq_mx_matmul_quantized).
+#include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "mx.hpp"
@@ -38,9 +38,10 @@ struct MatArgs {
 //
 // Float16 activations enter as they are, with weights as float16, for blocks
 // whose scale leaves them in float16's range (byte 104 .. 140: 2^-24 ..
-// 6 * 2^13), which those of trained weights do.  Other blocks count as zeros
-// there, and a wave that met one adds theirs in a loop of its own afterwards,
-// with activations in two parts.
+// 6 * 2^13), which those of trained weights do.  A wave that met another block
+// (that counted as zeros till then) drops its sums and takes them again from
+// the start with activations in two parts.  (Adding the missing blocks alone
+// would not do: an infinite activation times the zeros is NaN.)
 // ---------------------------------------------------------------------------
 template <Act DT>
 constexpr int parts_of() { return DT == ACT_F16 ? 2 : DT == ACT_F32 ? 3 : 1; }
@@ -217,20 +218,19 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
         for (int j = 0; j < TT; ++j) d.x[j].template load<decltype(whole)::value>(a, tok[j], 128 * (int64_t)st + 32 * g);
     };
     bool left = false;       // float16: a block was left out
-    // REST: the blocks that were
-    const auto multiply = [&](const Step& d, auto rest) {
-        constexpr bool REST = decltype(rest)::value, HALF = DT == ACT_F16 && !REST;
+    const auto multiply = [&](const Step& d, auto half) {
+        constexpr bool HALF = decltype(half)::value;
         u32x4_t codes[RT];
         uint32_t sc[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             codes[i] = d.w[i];
             sc[i] = d.s[i];
-            if constexpr (DT == ACT_F16) {
+            if constexpr (HALF) {
                 const bool fits = scale_fits_f16(sc[i]);
-                if constexpr (HALF) left |= !fits && (some(codes[i]) || sc[i] == 255u);
-                codes[i] = codes_if(fits == HALF, codes[i]);
-                if (fits != HALF) sc[i] = 127u;
+                left |= !fits && (some(codes[i]) || sc[i] == 255u);
+                codes[i] = codes_if(fits, codes[i]);
+                if (!fits) sc[i] = 127u;
             }
         }
 #pragma unroll
@@ -255,6 +255,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
         }
     };
 
+    using Half = std::bool_constant<DT == ACT_F16>;
     // Steps in flight: enough for about 32 KiB of weights per compute unit.
     constexpr int PF = RT * TT > 4 || (DT == ACT_F32 && TT > 1) ? 1 : RT * TT > 1 || DT == ACT_F32 ? 2 : 4;
     const int mine = (a.full - wave + FEW_WAVES - 1) / FEW_WAVES;    // whole steps of this wave
@@ -267,20 +268,27 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
             for (int i = 0; i < PF; ++i) {
                 Step cur = d[i];
                 load(d[i], wave + FEW_WAVES * min(s0 + i + PF, mine - 1), std::true_type{});
-                if (s0 + i < mine) multiply(cur, std::false_type{});
+                if (s0 + i < mine) multiply(cur, Half{});
             }
         }
     }
-    for (int st = a.full + wave; st < a.steps; st += FEW_WAVES) {
+    for (int st = a.full + ((wave - a.full) & (FEW_WAVES - 1)); st < a.steps; st += FEW_WAVES) {
         Step d;
         load(d, st, std::false_type{});
-        multiply(d, std::false_type{});
+        multiply(d, Half{});
     }
     if constexpr (DT == ACT_F16) {
-        for (int st = __any(left) ? wave : a.steps; st < a.steps; st += FEW_WAVES) {
+        const bool again = __any(left);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = again ? 0.f : acc[i][j][e];
+        for (int st = again ? wave : a.steps; st < a.steps; st += FEW_WAVES) {
             Step d;
             load(d, st, std::false_type{});
-            multiply(d, std::true_type{});
+            multiply(d, std::false_type{});
         }
     }
 
@@ -305,16 +313,17 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 64 RW weight rows x 128 tokens per workgroup of 2 x 2 waves,
-// each 32 RW x 64 in v_mfma_f32_32x32x16.  Activations go through two LDS
+// Many tokens, any activations: 128 weight rows x 128 tokens per workgroup of
+// 2 x 2 waves, each 64 x 64 in v_mfma_f32_32x32x16.  Activations go through two LDS
 // buffers of 64 columns (float32 ones as their three parts), weights straight
 // from memory into the lanes that multiply them: lane l holds row l % 32 and,
 // of every 64 columns, block l / 32.  Both are fetched a step ahead.
 // ---------------------------------------------------------------------------
 constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
-template <Act DT, int RW>
+template <Act DT>
 __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
+    constexpr int RW = 2;
     constexpr int NP = DT == ACT_F32 ? 3 : 1;           // planes in LDS
     constexpr int BUF = NP * MT * X_ROW;
     extern __shared__ __attribute__((aligned(16))) char xs[];   // two buffers
@@ -428,7 +437,14 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
         __syncthreads();
     }
     if constexpr (DT == ACT_F16) {
-        for (int st = __any(left) ? 0 : last + 1; st <= last; ++st) {
+        const bool again = __any(left);
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = again ? 0.f : acc[i][j][e];
+        for (int st = again ? 0 : last + 1; st <= last; ++st) {
             load_w(st);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -440,8 +456,7 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
                     split_f16(y.w[0], p);
 #pragma unroll
                     for (int i = 0; i < RW; ++i) {
-                        const bool fits = scale_fits_f16(sc[i]);
-                        const u32x4_t v = fp4x8<true>(fits ? 0u : w[i][c], mx_scale(fits ? 127u : sc[i]));
+                        const u32x4_t v = fp4x8<true>(w[i][c], mx_scale(sc[i]));
                         acc[i][j] = H16<true>::mfma32(v, p[0], acc[i][j]);
                         acc[i][j] = H16<true>::mfma32(v, p[1], acc[i][j]);
                     }
@@ -618,10 +633,18 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
     }
     wait_vmem<0>();                                         // nothing lands in LDS that is another's by then
 
-    // the columns after the last whole stage, and for float16 the blocks that
-    // were left out before it
+    // the columns after the last whole stage, or all of them
     const int last = 2 * a.steps;
-    for (int st = DT == ACT_F16 && __any(left) ? 0 : 2 * stages; st < last; ++st) {
+    const bool again = DT == ACT_F16 && __any(left);
+    if constexpr (DT == ACT_F16) {
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = again ? 0.f : acc[i][j][e];
+    }
+    for (int st = again ? 0 : 2 * stages; st < last; ++st) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -633,13 +656,8 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
                     const int64_t row = min(r0 + rw + 32 * i + i32, a.d_out - 1);
-                    uint32_t code = *(const uint32_t*)(a.W + row * a.w_row + 32 * (int64_t)st + 16 * h + 4 * c);
-                    uint32_t byte = a.S[row * a.s_row + 2 * (int64_t)st + h];
-                    if (st < 2 * stages && scale_fits_f16(byte)) {
-                        code = 0u;
-                        byte = 127u;
-                    }
-                    const u32x4_t v = fp4x8<true>(code, mx_scale(byte));
+                    const uint32_t code = *(const uint32_t*)(a.W + row * a.w_row + 32 * (int64_t)st + 16 * h + 4 * c);
+                    const u32x4_t v = fp4x8<true>(code, mx_scale(a.S[row * a.s_row + 2 * (int64_t)st + h]));
 #pragma unroll
                     for (int k = 0; k < parts_of<DT>(); ++k) acc[i][j] = H16<true>::mfma32(v, p[k], acc[i][j]);
                 }
@@ -847,22 +865,20 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
     }
 }
 
-// The few-token kernel's tile: the least bytes through a compute unit, where
-// a workgroup reads 16 RT rows of codes and 16 TT tokens for every column and
-// 256 of them run at a time.
 template <Act DT, int RT, int TT>
-void launch_few(const MatArgs& a, hipStream_t s) {
+gptq_status launch_few(const MatArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
                        dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
                        dim3(64 * FEW_WAVES), 0, s, a);
+    return GPTQ_OK;
 }
 
-template <Act DT, int RW>
+template <Act DT>
 gptq_status launch_many(const MatArgs& a, hipStream_t s) {
     constexpr int lds = 2 * (DT == ACT_F32 ? 3 : 1) * MT * X_ROW;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_many_kernel<DT, RW>, lds));
-    hipLaunchKernelGGL((mx_many_kernel<DT, RW>), dim3((unsigned)(ceil_div(a.d_out, 64 * RW) * ceil_div(a.n_tok, MT))),
-                       dim3(256), lds, s, a);
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_many_kernel<DT>, lds));
+    hipLaunchKernelGGL(mx_many_kernel<DT>, dim3((unsigned)(ceil_div(a.d_out, 128) * ceil_div(a.n_tok, MT))), dim3(256), lds,
+                       s, a);
     return GPTQ_OK;
 }
 
@@ -875,39 +891,60 @@ gptq_status launch_wide(const MatArgs& a, hipStream_t s) {
     return GPTQ_OK;
 }
 
+// Workgroups of tiles of r rows x t tokens, in rounds of one per compute unit.
+double rounds(const MatArgs& a, int64_t r, int64_t t) {
+    return std::ceil((double)(ceil_div(a.d_out, r) * ceil_div(a.n_tok, t)) / 256.0);
+}
+
+// Which kernel, and which tile.  A few-token workgroup reads 16 RT rows of
+// codes and 16 TT tokens for every column, and its time goes by those bytes:
+// the unit below is a byte of 16 columns through a compute unit per round,
+// 0.086 us per 128 columns with 16-bit activations.  The others' times per
+// round, measured in it at 4096 columns: 128 x 128 tiles from LDS rings 12.8,
+// 256 x 128 22; through registers 36 (float32) or 21, where three workgroups
+// share a compute unit.  (For example 512 tokens 4096 -> 4096, bf16: few-token
+// 52 us, rings 28 us; 128 tokens: 18 and 27 us.)
 template <Act DT>
 gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    const int xr = getenv("XRT") ? atoi(getenv("XRT")) : 0;
-    if (xr ? xr == 1 : a.n_tok <= 256) {
-        const double xb = DT == ACT_F32 ? 4.0 : DT == ACT_FP8 ? 1.03 : DT == ACT_FP4 ? 0.53 : 2.0;
-        const int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
-        int best = 0;
-        double least = 1e30;
-        for (int i = 0; i < 6; ++i) {
-            const double wg = (double)(ceil_div(a.d_out, 16 * rt[i]) * ceil_div(a.n_tok, 16 * tt[i]));
-            const double cost = std::ceil(wg / 256.0) * (0.53 * rt[i] + xb * tt[i]);
-            if (cost < least) {
-                least = cost;
-                best = i;
-            }
+    const double xb = DT == ACT_F32 ? 4.0 : DT == ACT_FP8 ? 1.03 : DT == ACT_FP4 ? 0.53 : 2.0;
+    const int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
+    int best = 0;
+    double least = 1e30;
+    const auto offer = [&](int id, double cost) {
+        if (cost < least) {
+            least = cost;
+            best = id;
         }
-        switch (best) {
-            case 0: launch_few<DT, 1, 1>(a, s); break;
-            case 1: launch_few<DT, 2, 1>(a, s); break;
-            case 2: launch_few<DT, 4, 1>(a, s); break;
-            case 3: launch_few<DT, 2, 2>(a, s); break;
-            case 4: launch_few<DT, 4, 2>(a, s); break;
-            default: launch_few<DT, 4, 4>(a, s); break;
+    };
+    for (int i = 0; i < 6; ++i) offer(i, rounds(a, 16 * rt[i], 16 * tt[i]) * (0.53 * rt[i] + xb * tt[i]));
+    if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
+        // whole columns of 128, rows on 16 bytes, offsets of a tile in 32 bits
+        if (a.full > 0 && a.ld_x < (int64_t(1) << 23)) {
+            offer(6, rounds(a, 128, MT) * 12.8);
+            offer(7, rounds(a, 256, MT) * 22.0);
+        } else {
+            offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 21.0);
         }
-        return GPTQ_OK;
+    } else if constexpr (DT == ACT_F32) {
+        offer(8, rounds(a, 128, MT) * 36.0);
+    } else if constexpr (DT == ACT_FP8) {
+        offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 21.0);
+    }
+    switch (best) {
+        case 0: return launch_few<DT, 1, 1>(a, s);
+        case 1: return launch_few<DT, 2, 1>(a, s);
+        case 2: return launch_few<DT, 4, 1>(a, s);
+        case 3: return launch_few<DT, 2, 2>(a, s);
+        case 4: return launch_few<DT, 4, 2>(a, s);
+        case 5: return launch_few<DT, 4, 4>(a, s);
+        default: break;
     }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
-        if (xr == 3) return launch_wide<DT, 2>(a, s);
-        if (xr == 4) return launch_wide<DT, 4>(a, s);
+        if (best == 6) return launch_wide<DT, 2>(a, s);
+        if (best == 7) return launch_wide<DT, 4>(a, s);
     }
-    // tiles of 256 rows where they fill the chip twice, else of 128
-    if (xr == 5 || ceil_div(a.d_out, 256) * ceil_div(a.n_tok, MT) >= 512) return launch_many<DT, 4>(a, s);
-    return launch_many<DT, 2>(a, s);
+    if constexpr (DT != ACT_FP4) return launch_many<DT>(a, s);
+    return GPTQ_OK;
 }
 
 template <int RW>
@@ -972,13 +1009,17 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
     gptq_status st = GPTQ_OK;
     if (xf == GPTQ_MX_FP8) {
         st = launch_parts<ACT_FP8>(m, s);
-    } else if (getenv("XRT") ? atoi(getenv("XRT")) == 1 : n_tok <= 64) {
-        st = launch_parts<ACT_FP4>(m, s);
     } else {
-        // tiles of 256 rows where they fill the chip, else of 128
+        // The few-token kernel by bytes as above (a unit is 0.156 us here);
+        // tiles of 128 x 128 take 3 of them a round, of 256 x 128 5.9.
+        double few = 1e30;
+        for (int rt = 1; rt <= 4; rt *= 2)
+            for (int tt = 1; tt <= rt; tt *= 2) few = std::min(few, rounds(m, 16 * rt, 16 * tt) * 0.53 * (rt + tt));
+        const double narrow = rounds(m, 128, 128) * 3.0, broad = rounds(m, 256, 128) * 5.9;
         const MxArgs a{xc, xs, m};
-        if (getenv("XRT") ? atoi(getenv("XRT")) == 4 : ceil_div(d_out, 256) * ceil_div(n_tok, 128) >= 256) st = launch_mx<4>(a, s);
-        else st = launch_mx<2>(a, s);
+        if (few <= narrow && few <= broad) st = launch_parts<ACT_FP4>(m, s);
+        else if (narrow <= broad) st = launch_mx<2>(a, s);
+        else st = launch_mx<4>(a, s);
     }
     if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();

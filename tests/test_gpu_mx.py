@@ -296,3 +296,86 @@ def test_weights_of_every_size(n, d_in, d_out, dtype):
     x, wv = X.double().numpy(), M.mx_values(w, ws, "fp4", d_in)
     bound = (4 * d_in + 64) * 2.0 ** -23 * (np.abs(x) @ np.abs(wv).T)
     assert (np.abs(Y - x @ wv.T) <= bound).all()
+
+
+# Enough rows and tokens for every matrix-core tile; d_in ends inside a step, so the last columns take another path.
+LARGE = [(1100, 200, 1100), (2100, 328, 2100), (1500, 120, 1500), (4200, 392, 1030)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32", "fp4", "fp8"])
+@pytest.mark.parametrize("n,d_in,d_out", LARGE)
+def test_large_products(n, d_in, d_out, kind):
+    """Aligned and unaligned activations, an output inside a larger one, an infinity, a NaN and a NaN weight block."""
+    rng = np.random.default_rng(n + d_in)
+    w, ws = _weights(rng, d_out, d_in)
+    wt = torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV)
+    wv = M.mx_values(w, ws, "fp4", d_in)
+    x = rng.standard_normal((n, d_in)) * np.exp(2 * rng.standard_normal(d_in))
+    room = torch.full((n + 2, d_out + 7), 5.0, device=DEV)
+    out = room[1: n + 1, 3: 3 + d_out]
+    if kind in TYPES:
+        base = torch.zeros(n, d_in + 24, dtype=TYPES[kind], device=DEV)
+        for at in (0, 8, 1):
+            X = base[:, at: at + d_in]
+            X.copy_(torch.from_numpy(x))
+            P.mx_matmul(X, *wt, out=out)
+            _check(out, X.double().cpu().numpy(), wv)
+            out.fill_(5.0)
+            assert (room == 5.0).all()
+            bad = X.clone() if at == 0 else X
+            bad[n - 1, 7], bad[130, d_in - 1] = np.inf, np.nan
+            ws_nan = wt[1].clone()
+            ws_nan[d_out - 2, 1] = 255
+            Y = P.mx_matmul(bad, wt[0], ws_nan).cpu().numpy()
+            keep = np.delete(np.arange(n), [130, n - 1])
+            assert np.isnan(Y[130]).all() and np.isnan(Y[:, d_out - 2]).all()
+            assert np.isfinite(np.delete(Y[keep], d_out - 2, 1)).all()
+            with np.errstate(invalid="ignore"):
+                assert np.array_equal(np.delete(Y[n - 1], d_out - 2), np.delete(np.inf * wv[:, 7], d_out - 2), equal_nan=True)
+    else:
+        xc, xs = M.mx_quantize(x, kind)
+        xt = torch.from_numpy(xc).to(DEV), torch.from_numpy(xs).to(DEV)
+        P.mx_matmul_quantized(*xt, *wt, x_fmt=kind, out=out)
+        _check(out, M.mx_values(xc, xs, kind, d_in), wv)
+        out.fill_(5.0)
+        assert (room == 5.0).all()
+        xt[1][130, 1] = 255
+        ws_nan = wt[1].clone()
+        ws_nan[d_out - 2, 1] = 255
+        Y = P.mx_matmul_quantized(*xt, wt[0], ws_nan, x_fmt=kind).cpu().numpy()
+        assert np.isnan(Y[130]).all() and np.isnan(Y[:, d_out - 2]).all()
+        assert np.isfinite(np.delete(np.delete(Y, 130, 0), d_out - 2, 1)).all()
+
+
+@pytest.mark.parametrize("n,d_in,d_out", LARGE[:2])
+def test_large_products_of_weights_of_every_size(n, d_in, d_out):
+    """Float16 activations by weight blocks inside and outside float16's range, in tiles of many tokens."""
+    test_weights_of_every_size(n, d_in, d_out, "f16")
+
+
+def test_tokens_far_apart():
+    """A row stride whose tile passes 32-bit offsets."""
+    rng = np.random.default_rng(3)
+    n, d_in, d_out, ld = 600, 128, 1300, 1 << 24
+    w, ws = _weights(rng, d_out, d_in)
+    base = torch.zeros((n - 1) * ld + d_in, dtype=torch.bfloat16, device=DEV)
+    X = torch.as_strided(base, (n, d_in), (ld, 1))
+    X.copy_(torch.from_numpy(rng.standard_normal((n, d_in))))
+    Y = P.mx_matmul(X, torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV))
+    _check(Y, X.double().cpu().numpy(), M.mx_values(w, ws, "fp4", d_in))
+
+
+@pytest.mark.parametrize("n,d_out", [(3, 40), (300, 300), (1100, 1100)])
+def test_infinite_float16_by_weights_outside_its_range(n, d_out):
+    """An infinity meets weights inside and outside float16's range in one sum: no zero stands in for either."""
+    rng = np.random.default_rng(n)
+    d_in = 1224
+    e = np.repeat(rng.choice([-40.0, -5.0, 25.0], (d_out, -(-d_in // 32)), p=[0.05, 0.9, 0.05]), 32, 1)[:, :d_in]
+    w, ws = M.mx_quantize(rng.uniform(1.0, 1.9, (d_out, d_in)) * rng.choice([-1.0, 1.0], (d_out, d_in)) * 2.0 ** e, "fp4")
+    wv = M.mx_values(w, ws, "fp4", d_in)
+    assert (wv != 0).all()
+    x = rng.standard_normal((n, d_in))
+    at = rng.integers(0, d_in, n)
+    x[np.arange(n), at] = np.inf
+    Y = P.mx_matmul(torch.from_numpy(x).half().to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV))
+    assert np.array_equal(Y.cpu().numpy(), np.inf * wv[:, at].T)
