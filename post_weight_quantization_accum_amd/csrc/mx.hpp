@@ -262,17 +262,18 @@ __device__ __forceinline__ u32x4_t buffer_of(const void* p, int64_t bytes) {
     r.y = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
     r.z = __builtin_amdgcn_readfirstlane((uint32_t)min(bytes, (int64_t)0xFFFFFFFF));
     r.w = 0x00020000u;
+    asm volatile("s_nop 4" : "+s"(r));      // scalars written by the vector unit: five wait states before a load takes them
     return r;
 }
 // Lane l's 16 (4) bytes at buffer offset `off` land at LDS address `to` + 16 l
 // (4 l).  Written as inline asm so that the compiler does not make every later
 // LDS read wait for it; the kernel waits itself (wait_vmem, then a barrier).
-// No register receives data.
+// No register receives data; the wait state after m0 is this code's to keep.
 __device__ __forceinline__ void dma_16(uint32_t to, uint32_t off, u32x4_t buf) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
 }
 __device__ __forceinline__ void dma_4(uint32_t to, uint32_t off, u32x4_t buf) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(buf) : "memory");
 }
 // At most N of this wave's memory loads still under way.
 template <int N>

@@ -171,32 +171,53 @@ __device__ __forceinline__ void store4(const MatArgs& a, int64_t t, int64_t r, f
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: a workgroup computes 16 RT weight rows x 16 TT tokens; its eight
-// waves share the 128-column steps, and their sums meet in LDS.
+// Few tokens: a workgroup computes 16 RT weight rows x 16 TT tokens; its waves
+// take a share of the 128-column steps each, and their sums meet in LDS.
+//
+// Such a product is bound by how many bytes are on their way at once, and by
+// how they are asked for: a lane's own load of 16 bytes is a request to the
+// cache by itself unless its neighbours' continue it, and with a matrix
+// instruction's rows on neighbouring lanes none does (13 x 11008 -> 4096
+// float16: 43000 requests per compute unit, 19 us).  So each wave brings its
+// steps into a ring of LDS slots of its own, four lanes to 64 bytes in a row,
+// RING steps ahead, without registers and without a barrier.  Rows there are
+// whole (64 bytes of codes, 64 .. 512 of activations), with 16-byte chunk c at
+// slot c ^ swizzle(row), so that reads of one chunk of eight rows hit all
+// banks.  Reads of tokens and steps past the end fall outside their buffer,
+// make no request and give zeros; rows past the end repeat the last one.
+//
 // v_mfma_f32_16x16x32 with a lane's four k-groups of eight chosen as one block
 // of 32 columns: lane l holds row l % 16, block l / 16 of the step (16 bytes
 // of codes, one scale), and activations of token l % 16 in the same columns.
-// Everything goes straight from memory to the lanes that multiply it.  Rows
-// and tokens past the end are read from the last one and not stored.
+// Columns after the last whole 128 (all, where activations do not start on 16
+// bytes) come from memory directly.
 // ---------------------------------------------------------------------------
-constexpr int FEW_WAVES = 8;
+constexpr int LDS_BYTES = 160 * 1024;      // of a compute unit
 
 template <Act DT, int RT, int TT>
-__global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
-    constexpr int NP = parts_of<DT>();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+struct FewTile {
+    static constexpr int X_ROW = DT == ACT_F32 ? 512 : DT == ACT_FP8 ? 128 : DT == ACT_FP4 ? 64 : 256;   // bytes of a token
+    static constexpr int XS = DT == ACT_FP8 || DT == ACT_FP4 ? TT : 0;                       // 16-row groups of X scales
+    static constexpr int W_DMA = RT, X_DMA = TT * X_ROW / 64, DMA = W_DMA + X_DMA + RT + XS;
+    static constexpr int S_AT = 1024 * (W_DMA + X_DMA), STAGE = S_AT + 256 * (RT + XS);
+    static constexpr int WAVES = 2 * 8 * STAGE <= LDS_BYTES ? 8 : 4;
+    static constexpr int RING = LDS_BYTES / (WAVES * STAGE) < 4 ? LDS_BYTES / (WAVES * STAGE) : 4;
+    static constexpr int AT = RT * TT < 4 ? RT * TT : 4;                                      // tiles joined at a time
+    static constexpr int BYTES = WAVES * (RING * STAGE > 1024 * AT ? RING * STAGE : 1024 * AT);
+    static constexpr bool FITS = RING >= 2 && (RING - 1) * DMA < 64;
+};
+constexpr uint32_t NOWHERE = 1u << 30;     // an offset past every tile's buffer, also with another added
+
+template <Act DT, int RT, int TT, int THREADS = 64 * FewTile<DT, RT, TT>::WAVES>
+__global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
+    using T = FewTile<DT, RT, TT>;
+    constexpr int NP = parts_of<DT>(), CH = T::X_ROW / 16, PER = CH < 16 ? 16 / CH : 1, LOW = CH < 16 ? CH - 1 : 15;
+    using Half = std::bool_constant<DT == ACT_F16>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i16 = lane & 15, g = lane >> 4;
     const int64_t r0 = (int64_t)blockIdx.x * (16 * RT), t0 = (int64_t)blockIdx.y * (16 * TT);
-    const uint8_t *wp[RT], *sp[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        const int64_t row = min(r0 + 16 * i + i16, a.d_out - 1);
-        wp[i] = a.W + row * a.w_row + 16 * g;
-        sp[i] = a.S + row * a.s_row + g;
-    }
-    int64_t tok[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) tok[i] = min(t0 + 16 * i + i16, a.n_tok - 1);
+    const int64_t wn = min((int64_t)(16 * RT), a.d_out - r0), xn = min((int64_t)(16 * TT), a.n_tok - t0);
     f32x4_t acc[RT][TT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -207,15 +228,6 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
         u32x4_t w[RT];
         uint32_t s[RT];
         Raw<DT> x[TT];
-    };
-    const auto load = [&](Step& d, int st, auto whole) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            d.w[i] = *(const u32x4_t*)(wp[i] + 64 * (int64_t)st);
-            d.s[i] = sp[i][4 * (int64_t)st];
-        }
-#pragma unroll
-        for (int j = 0; j < TT; ++j) d.x[j].template load<decltype(whole)::value>(a, tok[j], 128 * (int64_t)st + 32 * g);
     };
     bool left = false;       // float16: a block was left out
     const auto multiply = [&](const Step& d, auto half) {
@@ -255,28 +267,87 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
         }
     };
 
-    using Half = std::bool_constant<DT == ACT_F16>;
-    // Steps in flight: enough for about 32 KiB of weights per compute unit.
-    constexpr int PF = RT * TT > 4 || (DT == ACT_F32 && TT > 1) ? 1 : RT * TT > 1 || DT == ACT_F32 ? 2 : 4;
-    const int mine = (a.full - wave + FEW_WAVES - 1) / FEW_WAVES;    // whole steps of this wave
-    if (mine > 0) {
-        Step d[PF];
+    // this wave's whole steps, in a row
+    const int first = a.full * wave / T::WAVES, end = a.full * (wave + 1) / T::WAVES;
+    if (first < end) {
+        constexpr int XB = T::XS ? 1 : DT == ACT_F32 ? 4 : 2;                    // bytes per element of ld_x
+        const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), wsb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row);
+        const u32x4_t xb = buffer_of((const char*)a.X + t0 * a.ld_x * XB, ((xn - 1) * a.ld_x + (T::XS ? a.ld_x : a.d_in)) * XB);
+        const u32x4_t xsb = T::XS ? buffer_of(a.XS + t0 * a.s_row, xn * a.s_row) : wsb;
+        uint32_t woff[T::W_DMA], xoff[T::X_DMA], wsoff[RT], xsoff[T::XS ? T::XS : 1];
 #pragma unroll
-        for (int i = 0; i < PF; ++i) load(d[i], wave + FEW_WAVES * min(i, mine - 1), std::true_type{});
-        for (int s0 = 0; s0 < mine; s0 += PF) {
+        for (int k = 0; k < RT; ++k) {
+            const int r = 16 * k + (lane >> 2);
+            woff[k] = (uint32_t)(min((int64_t)r, wn - 1) * a.w_row + 16 * ((lane & 3) ^ (r >> 2 & 3)));
+            wsoff[k] = lane < 16 ? (uint32_t)(min((int64_t)(16 * k + lane), wn - 1) * a.s_row) : NOWHERE;
+        }
 #pragma unroll
-            for (int i = 0; i < PF; ++i) {
-                Step cur = d[i];
-                load(d[i], wave + FEW_WAVES * min(s0 + i + PF, mine - 1), std::true_type{});
-                if (s0 + i < mine) multiply(cur, Half{});
+        for (int k = 0; k < T::X_DMA; ++k) {
+            const int at = 64 * k + lane, t = at / CH, c = at % CH ^ (t / PER & LOW);
+            xoff[k] = t < xn ? (uint32_t)(t * a.ld_x * XB + 16 * c) : NOWHERE;
+        }
+#pragma unroll
+        for (int k = 0; k < T::XS; ++k) xsoff[k] = lane < 16 && 16 * k + lane < xn ? (uint32_t)((16 * k + lane) * a.s_row) : NOWHERE;
+        const uint32_t base = (uint32_t)(uintptr_t)lds + wave * (T::RING * T::STAGE);
+        const auto fetch = [&](int st, int slot) {
+            const uint32_t at = base + slot * T::STAGE;
+            const bool is = st < end;
+            const uint32_t wo = is ? 64u * st : NOWHERE, xo = is ? (uint32_t)T::X_ROW * st : NOWHERE, so = is ? 4u * st : NOWHERE;
+#pragma unroll
+            for (int k = 0; k < RT; ++k) dma_16(at + 1024 * k, woff[k] + wo, wb);
+#pragma unroll
+            for (int k = 0; k < T::X_DMA; ++k) dma_16(at + 1024 * (RT + k), xoff[k] + xo, xb);
+#pragma unroll
+            for (int k = 0; k < RT; ++k) dma_4(at + T::S_AT + 256 * k, wsoff[k] + so, wsb);
+#pragma unroll
+            for (int k = 0; k < T::XS; ++k) dma_4(at + T::S_AT + 256 * (RT + k), xsoff[k] + so, xsb);
+        };
+#pragma unroll
+        for (int i = 0; i < T::RING; ++i) fetch(first + i, i);
+        for (int s0 = first; s0 < end; s0 += T::RING) {
+#pragma unroll
+            for (int i = 0; i < T::RING; ++i) {
+                if (s0 + i < end) {
+                    wait_vmem<(T::RING - 1) * T::DMA>();
+                    const char* p = lds + wave * (T::RING * T::STAGE) + i * T::STAGE;
+                    Step d;
+#pragma unroll
+                    for (int k = 0; k < RT; ++k) {
+                        d.w[k] = *(const u32x4_t*)(p + 1024 * k + 64 * i16 + 16 * (g ^ (i16 >> 2)));
+                        d.s[k] = *(const uint8_t*)(p + T::S_AT + 256 * k + 4 * i16 + g);
+                    }
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) {
+#pragma unroll
+                        for (int e = 0; e < CH / 4; ++e)
+                            d.x[j].w[e] = *(const u32x4_t*)(p + 1024 * RT + (16 * j + i16) * T::X_ROW +
+                                                            16 * ((CH / 4 * g + e) ^ (i16 / PER & LOW)));
+                        if constexpr (T::XS > 0) d.x[j].s = *(const uint8_t*)(p + T::S_AT + 256 * (RT + j) + 4 * i16 + g);
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // read before the slot is filled again
+                    fetch(s0 + i + T::RING, i);
+                    multiply(d, Half{});
+                }
             }
         }
+        wait_vmem<0>();
     }
-    for (int st = a.full + ((wave - a.full) & (FEW_WAVES - 1)); st < a.steps; st += FEW_WAVES) {
+
+    // steps whose columns come from memory directly
+    const auto direct = [&](int st, auto half) {
         Step d;
-        load(d, st, std::false_type{});
-        multiply(d, Half{});
-    }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int64_t row = min(r0 + 16 * i + i16, a.d_out - 1);
+            d.w[i] = *(const u32x4_t*)(a.W + row * a.w_row + 64 * (int64_t)st + 16 * g);
+            d.s[i] = a.S[row * a.s_row + 4 * (int64_t)st + g];
+        }
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+            d.x[j].template load<false>(a, min(t0 + 16 * j + i16, a.n_tok - 1), 128 * (int64_t)st + 32 * g);
+        multiply(d, half);
+    };
+    for (int st = a.full + wave; st < a.steps; st += T::WAVES) direct(st, Half{});
     if constexpr (DT == ACT_F16) {
         const bool again = __any(left);
 #pragma unroll
@@ -285,27 +356,26 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void mx_few_kernel(MatArgs a) {
             for (int j = 0; j < TT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = again ? 0.f : acc[i][j][e];
-        for (int st = again ? wave : a.steps; st < a.steps; st += FEW_WAVES) {
-            Step d;
-            load(d, st, std::false_type{});
-            multiply(d, std::false_type{});
+        if (again) {
+            for (int st = first; st < end; ++st) direct(st, std::false_type{});
+            for (int st = a.full + wave; st < a.steps; st += T::WAVES) direct(st, std::false_type{});
         }
     }
 
-    // the waves' sums, in the order of the waves, four tiles at a time
-    constexpr int TILES = RT * TT, AT = TILES < 4 ? TILES : 4;
-    __shared__ f32x4_t part[FEW_WAVES][AT][64];
+    // the waves' sums, in the order of the waves, AT tiles at a time
+    constexpr int AT = T::AT;
+    f32x4_t* part = (f32x4_t*)lds;
 #pragma unroll
-    for (int b = 0; b < TILES; b += AT) {
-        if (b) __syncthreads();
-#pragma unroll
-        for (int e = 0; e < AT; ++e) part[wave][e][lane] = acc[(b + e) / TT][(b + e) % TT];
+    for (int b = 0; b < RT * TT; b += AT) {
         __syncthreads();
-        for (int e = threadIdx.x; e < AT * 64; e += 64 * FEW_WAVES) {
-            const int tile = b + (e >> 6), l = e & 63;
-            f32x4_t v = part[0][e >> 6][l];
 #pragma unroll
-            for (int q = 1; q < FEW_WAVES; ++q) v += part[q][e >> 6][l];
+        for (int e = 0; e < AT; ++e) part[(wave * AT + e) * 64 + lane] = acc[(b + e) / TT][(b + e) % TT];
+        __syncthreads();
+        for (int e = threadIdx.x; e < AT * 64; e += 64 * T::WAVES) {
+            const int tile = b + (e >> 6), l = e & 63;
+            f32x4_t v = part[e];
+#pragma unroll
+            for (int q = 1; q < T::WAVES; ++q) v += part[q * AT * 64 + e];
             const int64_t t = t0 + 16 * (tile % TT) + (l & 15), r = r0 + 16 * (tile / TT) + 4 * (l >> 4);
             if (t < a.n_tok) store4(a, t, r, v[0], v[1], v[2], v[3]);
         }
@@ -690,12 +760,6 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
 // per row, where a word per lane was 64 of them and took as long as the
 // codes), half of the rows with each stage, and held in registers from there.
 // ---------------------------------------------------------------------------
-struct MxArgs {
-    const uint8_t* X;
-    const uint8_t* XS;
-    MatArgs m;             // X, XS, ld_x, aligned, full unused
-};
-
 template <int RW>
 struct MxTile {
     static constexpr int WR = 64 * RW, ROWS = WR + 128;
@@ -712,22 +776,22 @@ __device__ __forceinline__ f16_t mfma_fp4(u32x4_t w, u32x4_t x, f16_t c, uint32_
 }
 
 template <int RW>
-__global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
+__global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
     using T = MxTile<RW>;
     constexpr int DMA = T::C_DMA + T::S_DMA;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i32 = lane & 31, h = lane >> 5;
-    const uint32_t nt = (uint32_t)((a.m.n_tok + 127) / 128), n = gridDim.x, per = n / 8;
+    const uint32_t nt = (uint32_t)((a.n_tok + 127) / 128), n = gridDim.x, per = n / 8;
     const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
     const int64_t r0 = (int64_t)(id / nt) * T::WR, t0 = (int64_t)(id % nt) * 128;
     const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
 
     // Buffers over the tile's rows (they end with the matrix; the last stage
     // may read past a row's end, into columns that are not multiplied).
-    const int64_t wn = min((int64_t)T::WR, a.m.d_out - r0), xn = min((int64_t)128, a.m.n_tok - t0);
-    const u32x4_t wb = buffer_of(a.m.W + r0 * a.m.w_row, wn * a.m.w_row), xb = buffer_of(a.X + t0 * a.m.w_row, xn * a.m.w_row);
-    const u32x4_t wsb = buffer_of(a.m.S + r0 * a.m.s_row, wn * a.m.s_row), xsb = buffer_of(a.XS + t0 * a.m.s_row, xn * a.m.s_row);
+    const int64_t wn = min((int64_t)T::WR, a.d_out - r0), xn = min((int64_t)128, a.n_tok - t0);
+    const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), xb = buffer_of((const uint8_t*)a.X + t0 * a.w_row, xn * a.w_row);
+    const u32x4_t wsb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row), xsb = buffer_of(a.XS + t0 * a.s_row, xn * a.s_row);
     // Codes: instruction j of wave w takes rows 8 (w + 4 j) .. + 7, lane l row
     // l / 8 and slot l % 8 of them.
     uint32_t coff[T::C_DMA];
@@ -735,7 +799,7 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
     for (int j = 0; j < T::C_DMA; ++j) {
         const int r = 8 * (wave + 4 * j) + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
         const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
-        coff[j] = (uint32_t)(row * a.m.w_row + 16 * c);
+        coff[j] = (uint32_t)(row * a.w_row + 16 * c);
     }
     // Scales of two stages: instruction j of wave w takes rows 16 (w + 4 j) ..
     // + 15, lane l word l % 4 of row l / 4; the first S_DMA of them make one
@@ -745,10 +809,10 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
     for (int j = 0; j < 2 * T::S_DMA; ++j) {
         const int r = 16 * (wave + 4 * j) + (lane >> 2);
         const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
-        soff[j] = (uint32_t)(row * a.m.s_row + 4 * (lane & 3));
+        soff[j] = (uint32_t)(row * a.s_row + 4 * (lane & 3));
     }
     const uint32_t base = (uint32_t)(uintptr_t)lds;
-    const int stages = (a.m.steps + 1) / 2, pairs = (stages + 1) / 2;
+    const int stages = (a.steps + 1) / 2, pairs = (stages + 1) / 2;
     // quarter q of a stage's codes
     const auto fetch = [&](int st, int slot, int q) {
         const uint32_t at = base + slot * T::STAGE, co = __builtin_amdgcn_readfirstlane(128 * st);
@@ -829,7 +893,7 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
         using Q1 = std::integral_constant<int, 1>;
         using Q2 = std::integral_constant<int, 2>;
         using Q3 = std::integral_constant<int, 3>;
-        const bool both = 2 * st + 1 < a.m.steps;       // uniform: the last stage can be half a one
+        const bool both = 2 * st + 1 < a.steps;       // uniform: the last stage can be half a one
         read(Q0{});
         read(Q1{});
         step(Q0{});
@@ -856,20 +920,24 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MxArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
-        if (t >= a.m.n_tok) continue;
+        if (t >= a.n_tok) continue;
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-                store4(a.m, t, r0 + rw + 32 * i + 2 * e + 4 * h, acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
+                store4(a, t, r0 + rw + 32 * i + 2 * e + 4 * h, acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
     }
 }
 
 template <Act DT, int RT, int TT>
 gptq_status launch_few(const MatArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
-                       dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
-                       dim3(64 * FEW_WAVES), 0, s, a);
+    using T = FewTile<DT, RT, TT>;
+    if constexpr (T::FITS) {
+        GPTQ_HIP(ensure_lds_limit((const void*)mx_few_kernel<DT, RT, TT>, T::BYTES));
+        hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
+                           dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
+                           dim3(64 * T::WAVES), T::BYTES, s, a);
+    }
     return GPTQ_OK;
 }
 
@@ -891,23 +959,37 @@ gptq_status launch_wide(const MatArgs& a, hipStream_t s) {
     return GPTQ_OK;
 }
 
+template <int RW>
+gptq_status launch_mx(const MatArgs& a, hipStream_t s) {
+    constexpr int lds = MxTile<RW>::LDS;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW>, lds));
+    hipLaunchKernelGGL(mx_mx_kernel<RW>, dim3((unsigned)(ceil_div(a.d_out, 64 * RW) * ceil_div(a.n_tok, 128))),
+                       dim3(256), lds, s, a);
+    return GPTQ_OK;
+}
+
 // Workgroups of tiles of r rows x t tokens, in rounds of one per compute unit.
 double rounds(const MatArgs& a, int64_t r, int64_t t) {
     return std::ceil((double)(ceil_div(a.d_out, r) * ceil_div(a.n_tok, t)) / 256.0);
 }
 
-// Which kernel, and which tile.  A few-token workgroup reads 16 RT rows of
-// codes and 16 TT tokens for every column, and its time goes by those bytes:
-// the unit below is a byte of 16 columns through a compute unit per round,
-// 0.086 us per 128 columns with 16-bit activations.  The others' times per
-// round, measured in it at 4096 columns: 128 x 128 tiles from LDS rings 12.8,
-// 256 x 128 22; through registers 36 (float32) or 21, where three workgroups
-// share a compute unit.  (For example 512 tokens 4096 -> 4096, bf16: few-token
-// 52 us, rings 28 us; 128 tokens: 18 and 27 us.)
+// Which kernel, and which tile: the least of rounds x time per round, measured
+// in us at 4096 columns (they grow alike with the columns).  Few-token tiles of
+// 16 RT x 16 TT for (RT, TT) = (1,1) (2,1) (4,1) (2,2) (4,2) (4,4), 0 where LDS
+// does not hold two steps per wave; then the others: 16-bit 128 x 128 and 256 x
+// 128 from LDS rings, else 128 x 128 through registers, at 69 (e4m3) of which
+// two or three share a compute unit; e2m1 by e2m1 as the 16-bit ones.  For example bf16 4096 -> 4096: 32 tokens
+// (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256 tokens (4,2) 20, 128 x 128 26; 2048
+// tokens 256 x 128 63, 128 x 128 72.
 template <Act DT>
 gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    const double xb = DT == ACT_F32 ? 4.0 : DT == ACT_FP8 ? 1.03 : DT == ACT_FP4 ? 0.53 : 2.0;
-    const int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
+    constexpr double us[5][6] = {{13, 16.4, 19.2, 30.3, 0, 0},      // float32
+                                 {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // float16
+                                 {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // bfloat16
+                                 {3.5, 4.8, 6.6, 5.9, 9.1, 13.4},   // e4m3
+                                 {2.1, 4.1, 6.6, 5.9, 8.7, 13.3}};  // e2m1
+    static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
+    constexpr int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
     int best = 0;
     double least = 1e30;
     const auto offer = [&](int id, double cost) {
@@ -916,19 +998,22 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
             best = id;
         }
     };
-    for (int i = 0; i < 6; ++i) offer(i, rounds(a, 16 * rt[i], 16 * tt[i]) * (0.53 * rt[i] + xb * tt[i]));
+    for (int i = 0; i < 6; ++i)
+        if (us[DT][i] > 0) offer(i, rounds(a, 16 * rt[i], 16 * tt[i]) * us[DT][i]);
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
-        // whole columns of 128, rows on 16 bytes, offsets of a tile in 32 bits
-        if (a.full > 0 && a.ld_x < (int64_t(1) << 23)) {
-            offer(6, rounds(a, 128, MT) * 12.8);
-            offer(7, rounds(a, 256, MT) * 22.0);
+        if (a.full > 0) {
+            offer(6, rounds(a, 128, MT) * 25.0);
+            offer(7, rounds(a, 256, MT) * 43.0);
         } else {
-            offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 21.0);
+            offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 75.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(8, rounds(a, 128, MT) * 36.0);
+        offer(8, rounds(a, 128, MT) * 160.0);
     } else if constexpr (DT == ACT_FP8) {
-        offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 21.0);
+        offer(8, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
+    } else {
+        offer(6, rounds(a, 128, MT) * 13.0);
+        offer(7, rounds(a, 256, MT) * 25.0);
     }
     switch (best) {
         case 0: return launch_few<DT, 1, 1>(a, s);
@@ -943,18 +1028,10 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
         if (best == 6) return launch_wide<DT, 2>(a, s);
         if (best == 7) return launch_wide<DT, 4>(a, s);
     }
-    if constexpr (DT != ACT_FP4) return launch_many<DT>(a, s);
-    return GPTQ_OK;
+    if constexpr (DT == ACT_FP4) return best == 6 ? launch_mx<2>(a, s) : launch_mx<4>(a, s);
+    else return launch_many<DT>(a, s);
 }
 
-template <int RW>
-gptq_status launch_mx(const MxArgs& a, hipStream_t s) {
-    constexpr int lds = MxTile<RW>::LDS;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW>, lds));
-    hipLaunchKernelGGL(mx_mx_kernel<RW>, dim3((unsigned)(ceil_div(a.m.d_out, 64 * RW) * ceil_div(a.m.n_tok, 128))),
-                       dim3(256), lds, s, a);
-    return GPTQ_OK;
-}
 
 MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int64_t d_in, int64_t d_out, float* Y,
                  int64_t ld_y) {
@@ -987,7 +1064,8 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
     a.X = X;
     a.ld_x = ld_x;
     a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
-    a.full = a.aligned ? (int)(d_in / MX_PAD) : 0;
+    // offsets within a tile's tokens stay below 2^30
+    a.full = a.aligned && ld_x <= (int64_t(1) << 20) ? (int)(d_in / MX_PAD) : 0;
     gptq_status st;
     switch (dt) {
         case GPTQ_BF16: st = launch_parts<ACT_BF16>(a, s); break;
@@ -1006,21 +1084,7 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
     m.X = xc;
     m.XS = xs;
     m.ld_x = mx_code_bytes(d_in, xf);
-    gptq_status st = GPTQ_OK;
-    if (xf == GPTQ_MX_FP8) {
-        st = launch_parts<ACT_FP8>(m, s);
-    } else {
-        // The few-token kernel by bytes as above (a unit is 0.156 us here);
-        // tiles of 128 x 128 take 3 of them a round, of 256 x 128 5.9.
-        double few = 1e30;
-        for (int rt = 1; rt <= 4; rt *= 2)
-            for (int tt = 1; tt <= rt; tt *= 2) few = std::min(few, rounds(m, 16 * rt, 16 * tt) * 0.53 * (rt + tt));
-        const double narrow = rounds(m, 128, 128) * 3.0, broad = rounds(m, 256, 128) * 5.9;
-        const MxArgs a{xc, xs, m};
-        if (few <= narrow && few <= broad) st = launch_parts<ACT_FP4>(m, s);
-        else if (narrow <= broad) st = launch_mx<2>(a, s);
-        else st = launch_mx<4>(a, s);
-    }
+    const gptq_status st = xf == GPTQ_MX_FP8 ? launch_parts<ACT_FP8>(m, s) : launch_parts<ACT_FP4>(m, s);
     if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
