@@ -1,11 +1,12 @@
 // Writing keys and values into the pages of a cache, and reading sequences
 // back (include/gptq.h, "A paged cache of keys and values").
 //
-// Both move rows of head_dim values in units of eight, a lane each, keys in
-// the first half of the grid and values in the second; a block of 32 channels
-// is a quad of lanes (head_dim is a multiple of 32), quantised as by
-// mx_quantize_kernel.  Both are bound by memory, or by their launch for a
-// handful of tokens.
+// Both move rows of head_dim values in units of eight, a lane each, which
+// takes its unit of the keys and of the values: they share the place, and the
+// way to it (slot or table entry, loads that wait on each other) costs as much
+// as the data.  A block of 32 channels is a quad of lanes (head_dim is a
+// multiple of 32), quantised as by mx_quantize_kernel.  Both are bound by
+// memory, or by their launch for a handful of tokens.
 #include "mx.hpp"
 
 namespace gptq {
@@ -33,42 +34,51 @@ struct WriteArgs {
     const int64_t* slots;
     int64_t n_units;       // tokens * units per token
     FastDiv upt, uph;      // units per token, per head
-    uint32_t half;         // workgroups per matrix
 };
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
-    const int m = blockIdx.x >= a.half;
-    const int64_t u = (int64_t)(blockIdx.x - (m ? a.half : 0)) * 256 + threadIdx.x;
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (u >= a.n_units) return;
     const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
     const uint32_t k = (uint32_t)(u - t * a.upt.d);
     const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
     const int64_t slot = a.slots[t];
+    // the values do not wait for the slot
+    uint32_t w[2][4];      // of 16-bit rows
+    float v[2][8];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if constexpr (F == GPTQ_MX_NONE) {
+            const uint16_t* p = (const uint16_t*)a.X[m] + t * a.ld[m] + 8 * k;
+            if (a.aligned[m]) {
+                const uint4 x = *(const uint4*)p;
+                w[m][0] = x.x; w[m][1] = x.y; w[m][2] = x.z; w[m][3] = x.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[m][i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+            }
+        } else {
+            load8_f32(a.X[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v[m]);
+        }
+    }
     // a quad shares its token: it leaves or stays as one
     if (slot < 0 || slot >= a.c.n_pages * a.c.page.d) return;
     const int64_t page = slot <= (int64_t)UINT32_MAX ? div_by((uint32_t)slot, a.c.page) : slot / a.c.page.d;
     const int64_t row = row_of(a.c, page, (int)head, (int)(slot - page * a.c.page.d));
     const int64_t at = row * (a.c.d / 8) + c;
-    if constexpr (F == GPTQ_MX_NONE) {
-        const uint16_t* p = (const uint16_t*)a.X[m] + t * a.ld[m] + 8 * k;
-        uint4 w;
-        if (a.aligned[m]) {
-            w = *(const uint4*)p;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if constexpr (F == GPTQ_MX_NONE) {
+            ((uint4*)a.c.rows[m])[at] = make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]);
         } else {
-            w = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16,
-                           p[6] | (uint32_t)p[7] << 16);
+            uint32_t byte;
+            u32x2_t code;
+            quantize_block8<F>(v[m], byte, code);
+            if constexpr (F == GPTQ_MX_FP4) ((uint32_t*)a.c.rows[m])[at] = code.x;
+            else ((u32x2_t*)a.c.rows[m])[at] = code;
+            if ((c & 3) == 0) a.c.scales[m][at >> 2] = (uint8_t)byte;
         }
-        ((uint4*)a.c.rows[m])[at] = w;
-    } else {
-        float v[8];
-        load8_f32(a.X[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v);
-        uint32_t byte;
-        u32x2_t w;
-        quantize_block8<F>(v, byte, w);
-        if constexpr (F == GPTQ_MX_FP4) ((uint32_t*)a.c.rows[m])[at] = w.x;
-        else ((u32x2_t*)a.c.rows[m])[at] = w;
-        if ((c & 3) == 0) a.c.scales[m][at >> 2] = (uint8_t)byte;
     }
 }
 
@@ -85,45 +95,80 @@ struct ReadArgs {
     gptq_dtype dt;
     int64_t n_units;
     FastDiv upt, uph;
-    uint32_t half;
 };
+
+// The last of n sequences that starts at or before row t (the first if none
+// does), with its start and the next one's; the same for the whole wave, whose
+// lanes look at 64 starts at a time.
+struct Place {
+    int seq;
+    int32_t start, next;
+};
+__device__ __forceinline__ Place sequence_of(const int32_t* start, int n, int32_t t) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, span = n;
+    while (span > 63) {
+        const int step = (span + 62) / 63, i = lane * step;
+        const int found = __popcll(__ballot(i < span && start[lo + min(i, span - 1)] <= t));
+        const int at = max(found - 1, 0) * step;
+        lo += at;
+        span = min(step, span - at);
+    }
+    const int32_t mine = start[lo + min(lane, span)];            // span <= 63: the one behind them is there too
+    const int at = max((int)__popcll(__ballot(lane < span && mine <= t)) - 1, 0);
+    return Place{__builtin_amdgcn_readfirstlane(lo + at), __builtin_amdgcn_readlane(mine, at),
+                 __builtin_amdgcn_readlane(mine, at + 1)};
+}
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
-    const int m = blockIdx.x >= a.half;
-    const int64_t u = (int64_t)(blockIdx.x - (m ? a.half : 0)) * 256 + threadIdx.x;
-    if (u >= a.n_units) return;
+    int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool is = u < a.n_units;
+    u = is ? u : a.n_units - 1;
     const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
     const uint32_t k = (uint32_t)(u - t * a.upt.d);
     const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
-    // the last sequence that starts at or before row t
-    if (t < a.row_start[0] || t >= a.row_start[a.n_seq]) return;
-    int lo = 0, hi = a.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_start[mid] <= t) lo = mid;
-        else hi = mid;
+    // the sequence of the wave's first row, or one behind it
+    Place p = sequence_of(a.row_start, a.n_seq, __builtin_amdgcn_readfirstlane((int)t));
+    if (p.next <= t) {
+        int hi = a.n_seq;
+        while (hi - p.seq > 1) {
+            const int mid = (p.seq + hi) >> 1;
+            if (a.row_start[mid] <= t) p.seq = mid;
+            else hi = mid;
+        }
+        p.start = a.row_start[p.seq];
+        p.next = a.row_start[p.seq + 1];
     }
-    const uint32_t pos = (uint32_t)(t - a.row_start[lo]);
+    if (!is || t < p.start || t >= p.next) return;
+    const uint32_t pos = (uint32_t)(t - p.start);
     const uint32_t slot = div_by(pos, a.c.page);
-    const int64_t page = slot < a.max_pages ? a.table[(int64_t)lo * a.max_pages + slot] : -1;
-    float v[8];
+    const int64_t page = slot < a.max_pages ? a.table[(int64_t)p.seq * a.max_pages + slot] : -1;
+    float v[2][8];
     if (page < 0 || page >= a.c.n_pages) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7FC00000u);
+        for (int i = 0; i < 8; ++i) v[0][i] = v[1][i] = __uint_as_float(0x7FC00000u);
     } else {
         const int64_t row = row_of(a.c, page, (int)head, (int)(pos - slot * a.c.page.d));
         const int64_t at = row * (a.c.d / 8) + c;
         if constexpr (F == GPTQ_MX_NONE) {
-            load8_f32(a.c.rows[m], a.held, 8 * at, 8, true, v);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) load8_f32(a.c.rows[m], a.held, 8 * at, 8, true, v[m]);
         } else {
-            u32x2_t w = {0u, 0u};
-            if constexpr (F == GPTQ_MX_FP4) w.x = ((const uint32_t*)a.c.rows[m])[at];
-            else w = ((const u32x2_t*)a.c.rows[m])[at];
-            values8<F>(w.x, w.y, a.c.scales[m][at >> 2], v);
+            u32x2_t w[2] = {{0u, 0u}, {0u, 0u}};
+            uint8_t byte[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if constexpr (F == GPTQ_MX_FP4) w[m].x = ((const uint32_t*)a.c.rows[m])[at];
+                else w[m] = ((const u32x2_t*)a.c.rows[m])[at];
+                byte[m] = a.c.scales[m][at >> 2];
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) values8<F>(w[m].x, w[m].y, byte[m], v[m]);
         }
     }
-    store8(a.Y[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) store8(a.Y[m], a.dt, t * a.ld[m] + 8 * k, 8, a.aligned[m], v[m]);
 }
 
 Store store_of(const gptq_kv_cache& c) {
@@ -149,10 +194,9 @@ gptq_status units(A& a, const gptq_kv_cache& c, int64_t n_rows, dim3& grid) {
     a.upt = fast_div((uint32_t)(uph * c.n_kv_heads));
     a.uph = fast_div((uint32_t)uph);
     a.n_units = n_rows * a.upt.d;
-    const int64_t half = ceil_div(a.n_units, 256);
-    if (2 * half > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-    a.half = (uint32_t)half;
-    grid = dim3((unsigned)(2 * half));
+    const int64_t n = ceil_div(a.n_units, 256);
+    if (n > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+    grid = dim3((unsigned)n);
     return GPTQ_OK;
 }
 

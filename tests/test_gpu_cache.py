@@ -373,3 +373,25 @@ def test_python_refusals():
     with pytest.raises(P.Unsupported):
         P.cache_write(P.new_cache(2, 16, 1, 160, device=DEV), torch.zeros(1, 1, 160, device=DEV),
                       torch.zeros(1, 1, 160, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV))
+
+
+@pytest.mark.parametrize("n_seq", [1, 2, 62, 63, 64, 65, 300, 5000])
+def test_read_of_many_sequences(n_seq):
+    """Empty, short and long sequences in any number, rows before the first and behind the last left alone."""
+    rng = np.random.default_rng(n_seq)
+    n_kv, d, page = 1, 32, 4
+    n = rng.choice([0, 1, 2, 9], n_seq, p=[0.5, 0.2, 0.2, 0.1])
+    n[rng.integers(0, n_seq)] = 37
+    start = 5 + np.concatenate([[0], np.cumsum(n)])
+    pages = rng.permutation(n_seq * 10)
+    cache = P.new_cache(n_seq * 10, page, n_kv, d, fmt="fp8", device=DEV)
+    table = pages.reshape(n_seq, 10).astype(np.int32)
+    X = torch.from_numpy(rng.standard_normal((start[-1] - 5, n_kv, d))).to(torch.bfloat16).to(DEV)
+    slots = np.concatenate([table[i, np.arange(k) // page].astype(np.int64) * page + np.arange(k) % page for i, k in enumerate(n)])
+    P.cache_write(cache, X, -X, torch.from_numpy(slots).to(DEV))
+    out = tuple(torch.full((start[-1] + 6, n_kv, d), 7.0, device=DEV) for _ in range(2))
+    K, V = P.cache_read(cache, torch.from_numpy(table).to(DEV), torch.from_numpy(start.astype(np.int32)).to(DEV), len(out[0]), out=out)
+    want = M.mx_values(*M.mx_quantize(X[:, 0].double().cpu().numpy(), "fp8"), "fp8", d)[:, None]
+    for t, w in ((K, want), (V, -want)):
+        assert np.array_equal(t[5:-6].double().cpu().numpy(), w)
+        assert (t[:5] == 7.0).all() and (t[-6:] == 7.0).all()
