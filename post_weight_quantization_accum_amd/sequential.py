@@ -15,6 +15,14 @@ layer norm, ReLU as in OPT):
     r  = relu(h1 W_fc1^T)                 fc2 <- H(r)
     X' = h1 + r W_fc2^T                   (the next block's input)
 
+With attention=Attention(...) the tokens are sequences and A is their causal
+attention instead, as a serving program computes it: keys and values, products
+of the quantized k and v, are written into the pages of a cache (16 bits or
+microscaled, so that the layers behind see that rounding too) and read by
+cache_attention from there.
+
+    A  = attention(X W_q^T, cache of X W_k^T and X W_v^T)
+
 Every product uses the already-quantized weights, computed by
 gptq_dequant_matmul from the packed words (with act-order: packed in
 quantization order, activations gathered into that order first).  Products come out
@@ -27,8 +35,9 @@ from __future__ import annotations
 
 import dataclasses
 
-from . import (dequant_matmul, factored_supported, gather_columns, hessian_accumulate, load, pack, pack_permuted,
-               prepare_hinv, prepare_hinv_factored, quantize_layer, quantize_layer_factored)
+from . import (cache_attention, cache_write, dequant_matmul, factored_supported, gather_columns, hessian_accumulate,
+               load, new_cache, pack, pack_permuted, prepare_hinv, prepare_hinv_factored, quantize_layer,
+               quantize_layer_factored)
 
 LAYERS = ("q", "k", "v", "out", "fc1", "fc2")
 
@@ -36,13 +45,28 @@ LAYERS = ("q", "k", "v", "out", "fc1", "fc2")
 @dataclasses.dataclass
 class Block:
     """Weights of one block (device tensors, d_out x d_in, fp16/bf16/fp32):
-    q, k, v, out: hidden x hidden; fc1: ffn x hidden; fc2: hidden x ffn."""
+    q, k, v, out: hidden x hidden; fc1: ffn x hidden; fc2: hidden x ffn.
+    With attention of fewer kv heads, k and v have kv_heads * head_dim rows."""
     q: object
     k: object
     v: object
     out: object
     fc1: object
     fc2: object
+
+
+@dataclasses.dataclass
+class Attention:
+    """Attention inside a block: heads of q; kv_heads of k and v (heads unless
+    given); lengths: tokens of each sequence, in the order of X's rows (one
+    sequence of all of them unless given); fmt, page_size: the cache's, as in
+    new_cache; window: as in cache_attention."""
+    heads: int
+    kv_heads: int | None = None
+    lengths: object = None
+    fmt: str = "16bit"
+    page_size: int = 64
+    window: int = 0
 
 
 def _torch():
@@ -109,18 +133,70 @@ def _product(X, q, cfg, stats: dict | None):
     return Y
 
 
-def quantize_block(block: Block, X, cfg, stats: dict | None = None, want_w_hat: bool = True):
+def _attention_shape(block: Block, X, attention: Attention):
+    """(lengths, kv heads, head_dim), checked against the block and its tokens."""
+    n, heads, kv_heads = X.shape[0], attention.heads, attention.kv_heads or attention.heads
+    lengths = [n] if attention.lengths is None else [int(k) for k in attention.lengths]
+    if sum(lengths) != n or min(lengths, default=0) < 0:
+        raise ValueError("attention.lengths must add up to the tokens")
+    if heads < 1 or kv_heads < 1 or heads % kv_heads or block.q.shape[0] % heads:
+        raise ValueError("attention.heads must divide q's rows, and attention.kv_heads the heads")
+    d = block.q.shape[0] // heads
+    if d not in (32, 64, 96, 128):
+        raise ValueError("head_dim must be 32, 64, 96 or 128")
+    if block.k.shape[0] != kv_heads * d or block.v.shape[0] != kv_heads * d:
+        raise ValueError("k and v must have kv_heads * head_dim rows")
+    if attention.page_size < 1 or attention.window < 0:
+        raise ValueError("attention.page_size must be positive and attention.window not negative")
+    return lengths, kv_heads, d
+
+
+def _attend(X, res, cfg, attention: Attention, shape, stats: dict | None):
+    """Causal attention of the sequences in X by the quantized q, k, v."""
+    torch = _torch()
+    (lengths, kv_heads, d), n, dt, dev = shape, X.shape[0], X.dtype, X.device
+    Q, K, V = (_product(X, res[name], cfg, stats).to(dt) for name in ("q", "k", "v"))
+    page = attention.page_size
+    pages = [-(-k // page) for k in lengths]
+    cache = new_cache(sum(pages), page, kv_heads, d, fmt=attention.fmt, dtype=dt, device=dev)
+    # sequence after sequence: its pages in a row, its tokens from the first one's start
+    table = torch.zeros((len(lengths), max(pages, default=0)), dtype=torch.int32)
+    slots = torch.empty(n, dtype=torch.int64)
+    at = first = 0
+    for s, (k, m) in enumerate(zip(lengths, pages)):
+        table[s, :m] = torch.arange(first, first + m, dtype=torch.int32)
+        slots[at: at + k] = torch.arange(first * page, first * page + k)
+        at, first = at + k, first + m
+    length = torch.tensor(lengths, dtype=torch.int32)
+    start = torch.cat([torch.zeros(1, dtype=torch.int32), length.cumsum(0, dtype=torch.int32)])
+    if stats is not None:
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+    cache_write(cache, K.unflatten(1, (kv_heads, d)), V.unflatten(1, (kv_heads, d)), slots.to(dev))
+    A = cache_attention(Q.unflatten(1, (attention.heads, d)), cache, start.to(dev), length.to(dev), table.to(dev),
+                        max_q=max(lengths, default=0), window=attention.window).flatten(1)
+    if stats is not None:
+        e1.record()
+        torch.cuda.synchronize()
+        stats["attention_ms"] = stats.get("attention_ms", 0.0) + e0.elapsed_time(e1)
+    return A
+
+
+def quantize_block(block: Block, X, cfg, stats: dict | None = None, want_w_hat: bool = True,
+                   attention: Attention | None = None):
     """Quantize one block from its input activations X (tokens x hidden,
     device, fp16/bf16).  Returns (per-layer outputs of quantize_layer plus
     perm and packed, the activations each layer was quantized on, the next
     block's input X').  want_w_hat=False skips the float32 reconstructions
-    (4 bytes per weight)."""
+    (4 bytes per weight).  attention: identity unless given (stats then gets
+    attention_ms)."""
     dt = X.dtype
+    shape = None if attention is None else _attention_shape(block, X, attention)
     res, inputs = {}, {}
     res.update(_quantize_shared({"q": block.q, "k": block.k, "v": block.v}, X, cfg, stats, want_w_hat))
     for n in ("q", "k", "v"):
         inputs[n] = X
-    A = _product(X, res["v"], cfg, stats).to(dt)
+    A = _product(X, res["v"], cfg, stats).to(dt) if attention is None else _attend(X, res, cfg, attention, shape, stats)
     inputs["out"] = A
     res.update(_quantize_shared({"out": block.out}, A, cfg, stats, want_w_hat))
     h1f = X.float() + _product(A, res["out"], cfg, stats)
@@ -134,7 +210,8 @@ def quantize_block(block: Block, X, cfg, stats: dict | None = None, want_w_hat: 
     return res, inputs, X_next
 
 
-def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool = True):
+def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool = True,
+                   attention: Attention | None = None):
     """Quantize the blocks in order; block b+1 is calibrated on the output of
     the already-quantized block b.  Returns a list of (outputs, inputs) per
     block and the stack's output activations."""
@@ -142,7 +219,7 @@ def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool 
     out = []
     X = X0
     for b in blocks:
-        res, inputs, X = quantize_block(b, X, cfg, stats, want_w_hat)
+        res, inputs, X = quantize_block(b, X, cfg, stats, want_w_hat, attention)
         out.append((res, inputs))
     return out, X
 
@@ -151,4 +228,4 @@ def new_stats() -> dict:
     return {"hessian_ms": 0.0, "solver_ms": 0.0, "product_ms": 0.0}
 
 
-__all__ = ["Block", "LAYERS", "quantize_block", "quantize_stack", "new_stats"]
+__all__ = ["Attention", "Block", "LAYERS", "quantize_block", "quantize_stack", "new_stats"]

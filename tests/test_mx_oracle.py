@@ -193,3 +193,16 @@ def test_python_refuses_cpu_tensors_and_bad_formats():
     c.k = c.k[..., :16]
     with pytest.raises(TypeError):
         P.cache_write(c, x, x, x)
+
+
+def test_sequential_attention_refusals():
+    """Shapes that do not fit are refused before any work on the GPU."""
+    from post_weight_quantization_accum_amd import sequential as S
+    w = lambda r: torch.zeros(r, 256)
+    X = torch.zeros(10, 256, dtype=torch.bfloat16)
+    block = S.Block(w(256), w(128), w(128), w(256), w(512), torch.zeros(256, 512))
+    for bad in (S.Attention(4, 2, [5, 4]), S.Attention(4, 2, [11, -1]), S.Attention(3, 3), S.Attention(4, 3),
+                S.Attention(4), S.Attention(16, 8), S.Attention(0), S.Attention(4, 2, page_size=0),
+                S.Attention(4, 2, window=-1)):
+        with pytest.raises(ValueError):
+            S.quantize_block(block, X, None, attention=bad)
