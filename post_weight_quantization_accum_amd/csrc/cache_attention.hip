@@ -28,8 +28,13 @@ namespace {
 
 constexpr int FEW_ROWS = 16, MANY_ROWS = 128;
 constexpr int FEW_WAVES = 8;                      // of a few-row workgroup, each with steps of its own
-// Sequences of at most this many rows go to the few-row kernel.
-constexpr int FEW_MOST = 64;
+// Sequences of at most this many rows go to the few-row kernel, which reads the
+// cache once per 16 rows: the fewer bytes a key has, the longer that pays (8
+// kv heads of 128 channels, pages of 16; few-row / many-row kernel, us: 32 x
+// 4096 e2m1 16 rows 30 / 113, 64 rows 86 / 123, 128 rows 130 / 130; 8 x 4096
+// 16 bits 16 rows 30 / 33, 32 rows 42 / 32, 64 rows 66 / 36; 1 x 32768 16 bits
+// 32 rows 45 / 46, 64 rows 71 / 48).
+constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == GPTQ_MX_FP8 ? 48 : 32; }
 constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
 constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
 constexpr float RAISE = 8.0f;
@@ -692,6 +697,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
             const char* kt = lds + b * BUF;
             const char* vt = kt + MANY_KEYS * K_ROW;
             // S^T: this lane gets row n, keys key0 + 32 i + 8 (e / 4) + 4 h + e % 4
+            __builtin_amdgcn_s_setprio(1);                  // of the two waves of a SIMD, the one with products first (573 -> 555 us)
             f16_t s[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -701,6 +707,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                 for (int k = 0; k < QC; ++k)
                     s[i] = H16<BF>::mfma32(*(const u32x4_t*)(kt + (32 * i + n) * K_ROW + 32 * k + 16 * h), q[k], s[i]);
             }
+            __builtin_amdgcn_s_setprio(0);
             const bool whole = key0 + MANY_KEYS <= pos0 + 1 && (a.window == 0 || key0 > pos1 - a.window);
             float x[32], mx = NEG_INF;
 #pragma unroll
@@ -739,6 +746,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                 p[e >> 2][e & 3] = H16<BF>::pack(x[2 * e], x[2 * e + 1]);
                 l = H16<BF>::add2(p[e >> 2][e & 3], l);
             }
+            __builtin_amdgcn_s_setprio(1);
             const char* vr = vt + (4 * h + ((lane & 15) >> 2)) * V_ROW + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -747,6 +755,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                     const char* v = vr + 16 * k * V_ROW + 64 * i;
                     acc[i] = H16<BF>::mfma32(tr_pair(v, v + 8 * V_ROW), p[k], acc[i]);
                 }
+            __builtin_amdgcn_s_setprio(0);
         }
         store(b ^ 1, step + 1);
         __syncthreads();
@@ -878,7 +887,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
 // What is launched: which sequences go to which kernel, and in how many parts.
 struct Plan {
     bool few, many;
-    int64_t few_max;
+    int64_t few_most, few_max;     // rows that the few-row kernel is best at; that it takes
     int64_t few_slots, many_slots;
     int per_seq, few_split, many_split;
     int D;
@@ -890,10 +899,11 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
     p.D = c.head_dim <= 64 ? 64 : 128;
     // The hint decides only between kernels: each launch takes every sequence
     // that no other one does, however many rows it has.
-    p.many = most > FEW_MOST;
+    p.few_most = few_most(c.format);
+    p.many = most > p.few_most;
     p.few = !(p.many && s.n_seq == 1);
-    p.few_max = !p.many ? INT64_MAX : p.few ? FEW_MOST : -1;
-    p.per_seq = (int)ceil_div(std::min<int64_t>(most, FEW_MOST), FEW_ROWS);
+    p.few_max = !p.many ? INT64_MAX : p.few ? p.few_most : -1;
+    p.per_seq = (int)ceil_div(std::min(most, p.few_most), FEW_ROWS);
     p.few_slots = p.few ? s.n_seq * p.per_seq : 0;
     p.many_slots = p.many ? rows / MANY_ROWS + s.n_seq : 0;
     // Parts: where there are fewer workgroups than fill the chip once (one of
@@ -914,7 +924,7 @@ void launch(AttnArgs& a, const Plan& p, hipStream_t s) {
     if (p.many) {
         a.n_slots = (int)p.many_slots;
         a.n_split = p.many_split;
-        a.rows_min = p.few ? FEW_MOST : 0;
+        a.rows_min = p.few ? p.few_most : 0;
         a.rows_max = INT64_MAX;
         hipLaunchKernelGGL((cache_many_kernel<F, BF, D>), dim3((unsigned)(p.many_slots * a.n_kv * p.many_split)),
                            dim3(256), 0, s, a);
@@ -938,8 +948,8 @@ void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) 
     }
     if (p.few_split > 1 || p.many_split > 1) {
         JoinArgs j{a, p.few_max, p.few_split, p.many_split, 0};
-        if (p.many && p.many_split == 1) j.rows_per_seq = FEW_MOST;   // only the few-row kernel made parts
-        const int64_t rows = j.rows_per_seq ? (int64_t)a.n_seq * a.n_kv * FEW_MOST : a.n_rows;
+        if (p.many && p.many_split == 1) j.rows_per_seq = (int)p.few_most;   // only the few-row kernel made parts
+        const int64_t rows = j.rows_per_seq ? (int64_t)a.n_seq * a.n_kv * p.few_most : a.n_rows;
         // one wave walks a few parts as fast as four do, and four rows share its workgroup
         if (std::max(p.few_split, p.many_split) > 8)
             hipLaunchKernelGGL((cache_join_kernel<BF, D, 4>), dim3((unsigned)rows), dim3(256), 0, s, j);
@@ -995,7 +1005,7 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     a.rows_min = a.rows_max = 0;
     // tiles, rows of a sequence and workgroups are counted in 32 bits
     if (a.n_rows > INT32_MAX || p.few_slots * a.n_kv * p.few_split > INT32_MAX ||
-        p.many_slots * a.n_kv * p.many_split > INT32_MAX || s.n_seq * a.n_kv * FEW_MOST > INT32_MAX)
+        p.many_slots * a.n_kv * p.many_split > INT32_MAX || s.n_seq * a.n_kv * p.few_most > INT32_MAX)
         return GPTQ_ERR_UNSUPPORTED;
     const bool bf = dt == GPTQ_BF16;
     if (p.D == 64) {
