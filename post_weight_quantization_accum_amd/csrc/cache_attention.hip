@@ -20,6 +20,7 @@
 // a score exceeds it by 2^8 (powers of two): until then the weights are at
 // most 2^8, far from any overflow, and nothing has to be rescaled.
 #include <algorithm>
+#include <cmath>
 
 #include "mx.hpp"
 
@@ -906,16 +907,43 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
     p.per_seq = (int)ceil_div(std::min(most, p.few_most), FEW_ROWS);
     p.few_slots = p.few ? s.n_seq * p.per_seq : 0;
     p.many_slots = p.many ? rows / MANY_ROWS + s.n_seq : 0;
-    // Parts: where there are fewer workgroups than fill the chip once (one of
-    // the few-row kernel's to a compute unit, two of the other's), and none
-    // shorter than the least.
+    // Parts of the keys: as many as make the least of the time, in us, of the
+    // workgroups (all taken as long as the table allows) in rounds over the
+    // chip, and of joining (10, and the parts written and read).  A few-row
+    // workgroup has a compute unit to itself and takes 20 bytes of the cache
+    // per ns; of the other kernel two share one, 2 us a step, and one alone
+    // takes 0.84 of that.  (One sequence of 16384 16-bit positions, 8 x 4
+    // heads of 128: 1024 tokens in 1 part 477 us, 2 313, 3 391; 512 tokens in
+    // 3 198, 4 170, 7 192; 2048 tokens in 1 567, 2 615.)  More than fill the chip
+    // once are left whole, and the few-row kernel's parts fill it at most once:
+    // ragged sequences level out by themselves there (33 sequences of up to
+    // 4096 e2m1 positions, 8 kv heads: 1 part 37 us, 4 70).
     int64_t keys = (int64_t)c.page_size * s.max_pages;
     if (s.window) keys = std::min(keys, s.window + s.max_q);
-    const auto split = [&](int64_t slots, int64_t room, int64_t limit, int64_t least) {
-        return slots == 0 ? 1 : std::max<int64_t>(1, std::min({limit, room / (slots * c.n_kv_heads), keys / least}));
+    const int64_t key_bytes = 2 * c.head_dim * (c.format == GPTQ_MX_NONE ? 32 : c.format == GPTQ_MX_FP8 ? 17 : 9) / 16;
+    const auto split = [&](double wgs, int64_t limit, int64_t least, double us, bool pairs) {
+        int best = 1;
+        double cost = 1e300;
+        if (wgs >= (pairs ? 512.0 : 256.0)) limit = 1;
+        if (!pairs) limit = std::min(limit, (int64_t)(256.0 / wgs));
+        for (int64_t n = 1; n <= std::max<int64_t>(1, std::min(limit, keys / least)); ++n) {
+            double rounds = std::ceil(wgs * (double)n / 256.0);
+            if (pairs) rounds = std::floor(rounds / 2) + (std::fmod(rounds, 2.0) != 0.0 ? 0.84 : 0.0);
+            const double join = n > 1 ? 10.0 + (double)n * (double)(s.n_tok * s.n_heads) * p.D * 8.0 / 4e6 : 0.0;
+            const double total = us * rounds / (double)n + join;
+            if (total < cost) {
+                cost = total;
+                best = (int)n;
+            }
+        }
+        return best;
     };
-    p.few_split = (int)split(p.few_slots, 256, 64, FEW_KEYS * FEW_MIN);
-    p.many_split = (int)split(p.many_slots, 512, 32, MANY_KEYS * MANY_MIN);
+    p.few_split = p.many_split = 1;
+    if (p.few)
+        p.few_split = split((double)(p.few_slots * c.n_kv_heads), 64, FEW_KEYS * FEW_MIN, (double)(keys * key_bytes) / 20e3, false);
+    if (p.many)
+        p.many_split = split((double)((ceil_div(rows, MANY_ROWS) + (s.n_seq - 1) / 2) * c.n_kv_heads), 32,
+                             MANY_KEYS * MANY_MIN, (double)keys * 2.0 / MANY_KEYS, true);
     return p;
 }
 

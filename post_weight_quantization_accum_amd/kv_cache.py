@@ -144,8 +144,8 @@ def cache_read(cache: KVCache, table, row_start, n_rows: int, dtype=None, out=No
         dtype = out[0].dtype if out is not None else cache.k.dtype if cache.fmt == "16bit" else torch.bfloat16
     with _on(dev, stream):
         if out is None:
-            K = torch.empty((n_rows, heads, d), dtype=dtype, device=table.device)
-            V = torch.empty((n_rows, heads, d), dtype=dtype, device=table.device)
+            K = table.new_empty((n_rows, heads, d), dtype=dtype)
+            V = K.new_empty((n_rows, heads, d))
         else:
             K, V = out
             _gpu(table, K, V)
@@ -183,7 +183,7 @@ def cache_attention(Q, cache: KVCache, q_start, kv_len, table, *, max_q: int | N
     with _on(dev, stream):
         nws = lib.gptq_cache_attention_workspace(c, n, n_heads, n_seq, max_pages, max_q, window)
         if out is None:
-            out, ld_o = torch.empty((n, n_heads, d), dtype=Q.dtype, device=Q.device), n_heads * d
+            out, ld_o = Q.new_empty((n, n_heads, d)), n_heads * d
         else:
             _gpu(Q, out)
             n_o, ld_o, _ = _heads(out, "out", n_heads, d)
@@ -193,7 +193,7 @@ def cache_attention(Q, cache: KVCache, q_start, kv_len, table, *, max_q: int | N
             _gpu(Q, workspace)
             nws = workspace.numel() * workspace.element_size()
         elif nws:
-            workspace = torch.empty(nws, dtype=torch.uint8, device=Q.device)
+            workspace = Q.new_empty(nws, dtype=torch.uint8)
         st = lib.gptq_cache_attention(c, Q.data_ptr(), _dtype_code(Q), n, n_heads, ld_q, q_start.data_ptr(),
                                       kv_len.data_ptr(), table.data_ptr(), max_pages, n_seq, max_q,
                                       d ** -0.5 if scale is None else scale, window, out.data_ptr(), ld_o,

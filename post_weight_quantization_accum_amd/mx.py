@@ -119,8 +119,8 @@ def mx_quantize(X, fmt: str = "fp4", out=None, stream=None):
     wide = units * (64 if f == _lib.MX_FP4 else 128), units * 4
     with _on(dev, stream):
         if out is None:
-            codes = torch.empty((n, wide[0]), dtype=torch.uint8, device=X.device)
-            scales = torch.empty((n, wide[1]), dtype=torch.uint8, device=X.device)
+            codes = X.new_empty((n, wide[0]), dtype=torch.uint8)
+            scales = codes.new_empty((n, wide[1]))
         else:
             codes, scales = out
             _gpu(X, codes, scales)
@@ -142,7 +142,7 @@ def mx_dequantize(codes, scales, n_cols: int, fmt: str = "fp4", dtype=None, out=
         raise ValueError("n_cols does not match the width of codes")
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((n, n_cols), dtype=dtype or torch.float32, device=codes.device)
+            out = codes.new_empty((n, n_cols), dtype=dtype or torch.float32)
             ld = n_cols
         else:
             _gpu(codes, out)
@@ -159,7 +159,7 @@ def mx_dequantize(codes, scales, n_cols: int, fmt: str = "fp4", dtype=None, out=
 def _product_out(out, n_tok, d_out, like):
     torch = _torch()
     if out is None:
-        return torch.empty((n_tok, d_out), dtype=torch.float32, device=like.device), max(d_out, 1)
+        return like.new_empty((n_tok, d_out), dtype=torch.float32), max(d_out, 1)
     if out.get_device() != like.get_device() or out.dtype != torch.float32 or tuple(out.shape) != (n_tok, d_out) or \
             (d_out > 1 and out.stride(1) != 1):
         raise TypeError("out must be float32 tokens x d_out with unit column stride, on the inputs' GPU")
