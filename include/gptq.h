@@ -398,10 +398,14 @@ gptq_status gptq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, gptq
 /* Y[t][r] = sum_{k < d_in} X[t][k] w[r][k], w the d_out x d_in e2m1 values of
  * (codes, scales).  X: n_tok x d_in of x_dtype, row stride ld_x; Y: float32,
  * n_tok x d_out, row stride ld_y, overwritten.  The weights enter the
- * matrix cores as bfloat16, which holds every one of them exactly; float16
- * and float32 activations enter as two and three bfloat16 parts that sum to
- * them, so no product is rounded; sums are float32.  An infinity or NaN in X
- * reaches its token's outputs as in float32 arithmetic.
+ * matrix cores as bfloat16, which holds every one of them exactly; float32
+ * activations enter as three bfloat16 parts that sum to them, float16 ones as
+ * they are by float16 weights where the scales (2^-23 .. 2^13) allow it and as
+ * two bfloat16 parts elsewhere.  So no product is rounded; sums are float32.
+ * An infinity or NaN in X reaches its token's outputs as in float32
+ * arithmetic, and no other's.  Which kernel runs, and so the order of a sum,
+ * depends on the sizes, the type and X's alignment; the same call gives the
+ * same bits.
  * Errors: GPTQ_ERR_INVALID_ARG for a bad dtype, sizes outside [0, 2^20]
  * (d_in >= 1), ld_x < d_in, ld_y < d_out, misaligned codes or a null pointer.
  * n_tok == 0 or d_out == 0: nothing is launched.  Asynchronous, no workspace. */
@@ -488,7 +492,8 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * q_start: device int32[n_seq + 1], ascending; kv_len: device int32[n_seq];
  * table: device int32[n_seq][max_pages].
  * max_q: the largest number of new tokens of one sequence (a hint for the
- * choice of kernels; results do not depend on it).
+ * choice of kernels: results depend on it, as on max_pages, only in the order
+ * of float32 sums).
  * workspace: gptq_cache_attention_workspace(...) bytes (may be 0), for parts
  * of long sequences.  Asynchronous.
  * Errors: GPTQ_ERR_INVALID_ARG for a bad cache, dtype, size, stride or

@@ -349,7 +349,15 @@ __device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head
 }
 
 // ---------------------------------------------------------------------------
-// Few rows.
+// Few rows: a workgroup of eight waves, each with every eighth step of 64 keys.
+// A lane reads its part of a key's channels straight into the matrix operand;
+// V passes through the wave's own LDS to be transposed, half a step at a time,
+// so that the waves never wait for each other before the join at the end.
+// Bound by the cache's bytes: 32 sequences of up to 4096 e2m1 positions, 8 kv
+// heads of 128 with 4 heads each, 26.6 us (90 MB, 3.4 TB/s: the longest of the
+// 256 workgroups has 1.5 times the mean); with 16 bits 85 us (4.0 TB/s); one
+// sequence of 65536 e4m3 positions 31 us in 32 parts (4.5 TB/s) and 4.5 us for
+// their join.  Steps of 32 keys on four waves took 43 and 77 us.
 // ---------------------------------------------------------------------------
 // Waves per SIMD that the registers are kept for: 16-bit rows take four times
 // those of e2m1.
@@ -592,7 +600,15 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.
+// Many rows: a workgroup of four waves, each with 32 rows, over tiles of 64 keys
+// that all of them share, in two LDS buffers (the next tile's keys and values
+// arrive in registers while this one is worked on, and are converted once for
+// 128 rows).  Bound by the matrix instructions and the weights' arithmetic,
+// which take about as long each and overlap only between the two waves of a
+// SIMD: 2048 tokens over 16384 16-bit positions, 8 kv heads of 128 with 4 heads
+// each, 562 us (917 TFLOP/s); e2m1 538 us.  Keys fetched two tiles ahead (no
+// faster), and softmax of one half of a tile beside the products of the other
+// (765 us: its registers spill), were tried and not kept.
 // ---------------------------------------------------------------------------
 template <gptq_mx_format F, bool BF, int D>
 __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
@@ -792,6 +808,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
 // ---------------------------------------------------------------------------
 // The parts of a row joined: a workgroup per token and head, O = sum_p
 // 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p, each wave with every fourth part.
+// 32 rows of 32 parts take 4.5 us, most of it the launch.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
     AttnArgs a;
