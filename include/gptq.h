@@ -385,7 +385,9 @@ int64_t gptq_mx_scales_per_row(int64_t n_cols);
 
 /* X: n_rows x n_cols of x_dtype, row stride ld_x, any alignment.  Every byte
  * of codes and scales, the padding's included, is written.  Sizes in
- * [0, 2^20] (n_cols >= 1).  n_rows == 0: nothing is launched.  Asynchronous. */
+ * [0, 2^20] (n_cols >= 1), and at most 2^35 - 2^13 values, the padding
+ * included (GPTQ_ERR_UNSUPPORTED above, here and in the three calls that move
+ * values below).  n_rows == 0: nothing is launched.  Asynchronous. */
 gptq_status gptq_mx_quantize(const void* X, gptq_dtype x_dtype, int64_t n_rows, int64_t n_cols, int64_t ld_x,
                              gptq_mx_format format, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 
@@ -499,7 +501,9 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * Errors: GPTQ_ERR_INVALID_ARG for a bad cache, dtype, size, stride or
  * pointer, n_heads not a multiple of n_kv_heads, a scale that is not a
  * positive number, or a window outside [0, 2^30];
- * GPTQ_ERR_UNSUPPORTED for another head_dim; GPTQ_ERR_WORKSPACE. */
+ * GPTQ_ERR_UNSUPPORTED for another head_dim, and for more than 2^31 - 1 rows
+ * (n_tok * n_heads) or 2^32 threads of a launch (some 2^23 sequences times
+ * kv heads); GPTQ_ERR_WORKSPACE. */
 size_t gptq_cache_attention_workspace(const gptq_kv_cache* cache, int64_t n_tok, int64_t n_heads, int64_t n_seq,
                                       int64_t max_pages, int64_t max_q, int64_t window);
 gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq_dtype q_dtype, int64_t n_tok,

@@ -993,7 +993,8 @@ void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) 
     }
     if (p.few_split > 1 || p.many_split > 1) {
         JoinArgs j{a, p.few_max, p.few_split, p.many_split, 0};
-        if (p.many && p.many_split == 1) j.rows_per_seq = (int)p.few_most;   // only the few-row kernel made parts
+        // only the few-row kernel made parts, and its sequences have fewer rows than there are in all
+        if (p.many && p.many_split == 1 && (int64_t)a.n_seq * a.n_kv * p.few_most < a.n_rows) j.rows_per_seq = (int)p.few_most;
         const int64_t rows = j.rows_per_seq ? (int64_t)a.n_seq * a.n_kv * p.few_most : a.n_rows;
         // one wave walks a few parts as fast as four do, and four rows share its workgroup
         if (std::max(p.few_split, p.many_split) > 8)
@@ -1048,9 +1049,9 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     a.part_ml = parts > 1 ? a.part_o + (int64_t)parts * a.n_rows * p.D : nullptr;
     a.n_slots = a.per_seq = a.n_split = 1;
     a.rows_min = a.rows_max = 0;
-    // tiles, rows of a sequence and workgroups are counted in 32 bits
-    if (a.n_rows > INT32_MAX || p.few_slots * a.n_kv * p.few_split > INT32_MAX ||
-        p.many_slots * a.n_kv * p.many_split > INT32_MAX || s.n_seq * a.n_kv * p.few_most > INT32_MAX)
+    // rows of a sequence and the threads of a launch are counted in 32 bits
+    if (a.n_rows > INT32_MAX || (parts > 1 && a.n_rows * 256 > MAX_THREADS) || p.few_slots * a.n_kv * p.few_split * 64 * FEW_WAVES > MAX_THREADS ||
+        p.many_slots * a.n_kv * p.many_split * 256 > MAX_THREADS)
         return GPTQ_ERR_UNSUPPORTED;
     const bool bf = dt == GPTQ_BF16;
     if (p.D == 64) {

@@ -41,10 +41,10 @@ struct WriteArgs {
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t u = blockIdx.x * 256 + threadIdx.x;
     if (u >= a.n_units) return;
-    const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
-    const uint32_t k = (uint32_t)(u - t * a.upt.d);
+    const int64_t t = div_by(u, a.upt);
+    const uint32_t k = u - (uint32_t)t * a.upt.d;
     const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
     const int64_t slot = a.slots[t];
     // the values do not wait for the slot
@@ -125,11 +125,11 @@ __device__ __forceinline__ Place sequence_of(const int32_t* start, int n, int32_
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
-    int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const bool is = u < a.n_units;
-    u = is ? u : a.n_units - 1;
-    const int64_t t = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upt) : u / a.upt.d;
-    const uint32_t k = (uint32_t)(u - t * a.upt.d);
+    const uint32_t id = blockIdx.x * 256 + threadIdx.x;
+    const bool is = id < a.n_units;
+    const uint32_t u = is ? id : (uint32_t)a.n_units - 1u;
+    const int64_t t = div_by(u, a.upt);
+    const uint32_t k = u - (uint32_t)t * a.upt.d;
     const uint32_t head = div_by(k, a.uph), c = k - head * a.uph.d;
     // the sequence of the wave's first row, or one behind it
     Place p = sequence_of(a.row_start, a.n_seq, __builtin_amdgcn_readfirstlane((int)t));
@@ -197,9 +197,8 @@ gptq_status units(A& a, const gptq_kv_cache& c, int64_t n_rows, dim3& grid) {
     a.upt = fast_div((uint32_t)(uph * c.n_kv_heads));
     a.uph = fast_div((uint32_t)uph);
     a.n_units = n_rows * a.upt.d;
-    const int64_t n = ceil_div(a.n_units, 256);
-    if (n > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-    grid = dim3((unsigned)n);
+    if (a.n_units > MAX_THREADS) return GPTQ_ERR_UNSUPPORTED;
+    grid = dim3((unsigned)ceil_div(a.n_units, 256));
     return GPTQ_OK;
 }
 

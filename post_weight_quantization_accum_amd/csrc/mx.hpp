@@ -292,6 +292,7 @@ __device__ __forceinline__ void meet() {
 // ---------------------------------------------------------------------------
 // Launchers (arguments validated in mx_api.hip).
 // ---------------------------------------------------------------------------
+constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1024;   // of a launch, its last workgroup included
 gptq_status mx_quantize_launch(const void* X, gptq_dtype dt, int64_t n_rows, int64_t n_cols, int64_t ld_x,
                                gptq_mx_format f, uint8_t* codes, uint8_t* scales, hipStream_t s);
 gptq_status mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, gptq_mx_format f, int64_t n_rows,

@@ -1077,6 +1077,7 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
     MatArgs a = mat_args(codes, scales, n_tok, d_in, d_out, Y, ld_y);
     a.X = X;
     a.ld_x = ld_x;
+    if (n_tok == 1) ld_x = a.ld_x = ceil_div(d_in, 8) * 8;   // of no use
     a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
     // offsets within a tile's tokens stay below 2^30
     a.full = a.aligned && ld_x <= (int64_t(1) << 20) ? (int)(d_in / MX_PAD) : 0;

@@ -26,10 +26,10 @@ struct QuantArgs {
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t u = blockIdx.x * 256 + threadIdx.x;
     // units per row is a multiple of 16, so a quad is wholly in or out
     if (u >= a.n_units) return;
-    const int64_t r = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upr) : u / a.upr.d;
+    const uint32_t r = div_by(u, a.upr);
     const int c = (int)(u - r * a.upr.d) * 8;
     const int n = (int)min((int64_t)8, max((int64_t)0, a.n_cols - c));
     float v[8];
@@ -56,9 +56,9 @@ struct DequantArgs {
 
 template <gptq_mx_format F>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantArgs a) {
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t u = blockIdx.x * 256 + threadIdx.x;
     if (u >= a.n_units) return;
-    const int64_t r = a.n_units <= (int64_t)UINT32_MAX ? div_by((uint32_t)u, a.upr) : u / a.upr.d;
+    const uint32_t r = div_by(u, a.upr);
     const int64_t k = u - r * a.upr.d, at = r * a.upr_pad + k;
     const int n = (int)min((int64_t)8, a.n_cols - 8 * k);
     u32x2_t w = {0u, 0u};
@@ -86,9 +86,8 @@ gptq_status mx_quantize_launch(const void* X, gptq_dtype dt, int64_t n_rows, int
     a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * elem_bytes(dt))) % 16 == 0;
     a.codes = codes;
     a.scales = scales;
-    const int64_t blocks = ceil_div(a.n_units, 256);
-    if (blocks > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks), block(256);
+    if (a.n_units > MAX_THREADS) return GPTQ_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ceil_div(a.n_units, 256)), block(256);
     if (f == GPTQ_MX_FP4) hipLaunchKernelGGL(mx_quantize_kernel<GPTQ_MX_FP4>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(mx_quantize_kernel<GPTQ_MX_FP8>, grid, block, 0, s, a);
     GPTQ_LAUNCH_CHECK();
@@ -109,9 +108,8 @@ gptq_status mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, gp
     a.aligned = ((uintptr_t)Y | (uintptr_t)(ld_y * elem_bytes(dt))) % 16 == 0;
     a.Y = Y;
     a.dt = dt;
-    const int64_t blocks = ceil_div(a.n_units, 256);
-    if (blocks > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks), block(256);
+    if (a.n_units > MAX_THREADS) return GPTQ_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ceil_div(a.n_units, 256)), block(256);
     if (f == GPTQ_MX_FP4) hipLaunchKernelGGL(mx_dequantize_kernel<GPTQ_MX_FP4>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(mx_dequantize_kernel<GPTQ_MX_FP8>, grid, block, 0, s, a);
     GPTQ_LAUNCH_CHECK();

@@ -395,3 +395,39 @@ def test_read_of_many_sequences(n_seq):
     for t, w in ((K, want), (V, -want)):
         assert np.array_equal(t[5:-6].double().cpu().numpy(), w)
         assert (t[:5] == 7.0).all() and (t[-6:] == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp8", "fp4"])
+@pytest.mark.parametrize("q", [8, 9, 12, 13, 16, 17, 40])
+def test_rows_around_the_kernels_limits(q, fmt):
+    """32, 48 and 64 rows of a sequence and one more token, whole and in parts, with shorter sequences beside them."""
+    for kv in ([q + 3, 70, q], [2500, 40, q]):
+        p = Paged(q, kv, 1, 128, 16, fmt, "bf16", garbage=True).write()
+        qs = [q, 3, q]
+        out, Q, scale = attend(p, qs, 4, max_q=q)
+        check(out, Q, p, qs, scale)
+
+
+def test_long_sequences_captured_and_replayed():
+    """Parts and their join in a graph: lengths change between replays, other work runs in between."""
+    p = Paged(4, [6000, 100, 3000], 2, 128, 64, "fp8", "bf16").write()
+    start, kv, table = p.tensors([1, 1, 1])
+    Q = torch.from_numpy(p.rng.standard_normal((3, 8, 128))).to(torch.bfloat16).to(DEV)
+    P.cache_attention(Q, p.cache, start, kv, table, max_q=1)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = P.cache_attention(Q, p.cache, start, kv, table, max_q=1)
+        graphs.append((g, out))
+    for lengths in ([6000, 100, 3000], [1, 0, 2999], [4097, 64, 65], [0, 0, 0]):
+        kv.copy_(torch.tensor(lengths, dtype=torch.int32))
+        want = P.cache_attention(Q, p.cache, start, kv, table, max_q=1)
+        for _, out in graphs:
+            out.fill_(9.0)
+        torch.cuda.synchronize()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for _, out in graphs), lengths

@@ -138,3 +138,32 @@ def test_block_quantized_with_attention(fmt, kv_heads, lengths, window):
     assert torch.equal(h1, inputs["fc1"]) and torch.isfinite(out).all()
     stack, last = S.quantize_stack([block], X, cfg, attention=att)
     assert torch.equal(last, out)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, with workspaces and outputs of their own, give what they give alone."""
+    rng = np.random.default_rng(12)
+    work = []
+    for i, (fmt, dtype) in enumerate((("fp8", "bf16"), ("fp4", "f16"))):
+        p = Paged(20 + i, [9000, 500, 4000], 2, 128, 64, fmt, dtype).write()
+        Q = torch.from_numpy(rng.standard_normal((3, 8, 128))).to(p.dtype).to(DEV)
+        w = P.mx_quantize(torch.from_numpy(rng.standard_normal((700, 640))).float().to(DEV))
+        X = torch.from_numpy(rng.standard_normal((40 + 600 * i, 640))).to(p.dtype).to(DEV)
+        work.append((p, Q, p.tensors([1, 1, 1]), w, X))
+
+    def run(item, stream=None):
+        p, Q, (start, kv, table), w, X = item
+        return (P.cache_attention(Q, p.cache, start, kv, table, max_q=1, stream=stream), P.mx_matmul(X, *w, stream=stream),
+                P.mx_matmul_quantized(*P.mx_quantize(X, stream=stream), *w, stream=stream))
+
+    alone = [run(item) for item in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = [[] for _ in work]
+    for _ in range(5):
+        for i, item in enumerate(work):
+            got[i].append(run(item, streams[i]))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, alone[i]))
