@@ -115,23 +115,27 @@ struct Raw {
     }
 };
 
-// bfloat16 parts of eight float32 values.
-template <int NP>
+// bfloat16 parts of eight float32 values: the top half of each, then that of
+// what is left; below an infinity or NaN 0 (ODD: where there may be some, which
+// the first part sees: all others are of finite values).
+template <int NP, bool ODD>
 __device__ __forceinline__ void split(float (&v)[8], u32x4_t (&p)[NP]) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        uint32_t w[8];
+    for (int j = 0; j < NP; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = __float_as_uint(v[i]);
-            const bool fin = (b & 0x7F800000u) != 0x7F800000u;
-            // a NaN whose top bits are an infinity's keeps a quiet bit
-            w[i] = b | ((b & 0x7FFFFFFFu) > 0x7F800000u ? 0x00400000u : 0u);
-            v[i] = fin ? v[i] - __uint_as_float(b & 0xFFFF0000u) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float& x = v[2 * i + k];
+                w[k] = __float_as_uint(x);
+                const bool fin = !ODD || j > 0 || (w[k] & 0x7F800000u) != 0x7F800000u;
+                x = fin ? x - __uint_as_float(w[k] & 0xFFFF0000u) : 0.0f;
+                // a NaN whose top bits are an infinity's keeps a quiet bit
+                if (ODD && j == 0 && (w[k] & 0x7FFFFFFFu) > 0x7F800000u) w[k] |= 0x00400000u;
+            }
+            p[j][i] = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[j][i] = w[2 * i] >> 16 | (w[2 * i + 1] & 0xFFFF0000u);
-    }
 }
 // The same of eight float16.
 __device__ __forceinline__ void split_f16(u32x4_t h, u32x4_t (&p)[2]) {
@@ -141,15 +145,24 @@ __device__ __forceinline__ void split_f16(u32x4_t h, u32x4_t (&p)[2]) {
         v[2 * i] = H16<false>::to_f32((uint16_t)h[i]);
         v[2 * i + 1] = H16<false>::to_f32((uint16_t)(h[i] >> 16));
     }
-    split<2>(v, p);
+    split<2, true>(v, p);
 }
-template <Act DT, int N>
+// An infinity or NaN among float32 values.
+template <int N>
+__device__ __forceinline__ bool odd(const Raw<ACT_F32, N>& x) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 8 * N; ++i) any |= !__builtin_isfinite(__uint_as_float(x.w[i >> 2][i & 3]));
+    return any;
+}
+// ODD: whether float32 values may be infinite or NaN
+template <bool ODD, Act DT, int N>
 __device__ __forceinline__ void parts(const Raw<DT, N>& x, int c, u32x4_t (&p)[parts_of<DT>()]) {
     if constexpr (DT == ACT_F32) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x.w[2 * c + (i >> 2)][i & 3]);
-        split<3>(v, p);
+        split<3, ODD>(v, p);
     } else if constexpr (DT == ACT_F16) {
         split_f16(x.w[c], p);
     } else {
@@ -235,8 +248,8 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
         Raw<DT> x[TT];
     };
     bool left = false;       // float16: a block was left out
-    const auto multiply = [&](const Step& d, auto half) {
-        constexpr bool HALF = decltype(half)::value;
+    const auto multiply_as = [&](const Step& d, auto half, auto may) {
+        constexpr bool HALF = decltype(half)::value, ODD = decltype(may)::value;
         u32x4_t codes[RT];
         uint32_t sc[RT];
 #pragma unroll
@@ -262,13 +275,27 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
                     for (int i = 0; i < RT; ++i) acc[i][j] = H16<false>::mfma16(w[i], d.x[j].eight(c), acc[i][j]);
                 } else {
                     u32x4_t p[NP];
-                    parts(d.x[j], c, p);
+                    parts<ODD>(d.x[j], c, p);
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
 #pragma unroll
                         for (int i = 0; i < RT; ++i) acc[i][j] = H16<true>::mfma16(w[i], p[q], acc[i][j]);
                 }
             }
+        }
+    };
+
+    // Float32: one look at a step's values leaves half of the work on their parts
+    // (13 tokens 4096 -> 4096 9.3 us, 14.6 with every part looking for itself).
+    const auto multiply = [&](const Step& d, auto half) {
+        if constexpr (DT == ACT_F32) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < TT; ++j) any |= odd(d.x[j]);
+            if (__any(any)) multiply_as(d, half, std::true_type{});
+            else multiply_as(d, half, std::false_type{});
+        } else {
+            multiply_as(d, half, std::true_type{});
         }
     };
 
@@ -394,8 +421,8 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
 // from memory into the lanes that multiply them: lane l holds row l % 32 and,
 // of every 64 columns, block l / 32.  Both are fetched a step ahead.  Bound by
 // the conversions (float32: three products for one as well).  Measured: 2048 x
-// 4096 -> 4096 with e4m3 activations 99 us (700 TFLOP/s); 300 float32 tokens
-// 4096 -> 4096 take 160 us here, 94 us by the few-token kernel.
+// 4096 -> 4096 with e4m3 activations 99 us (690 TFLOP/s), with float32 ones
+// 260 us (265 TFLOP/s; 328 with every part looking for infinities).
 // ---------------------------------------------------------------------------
 constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
@@ -452,7 +479,7 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
             char* p = xs + b * BUF + (e >> 3) * X_ROW + 16 * (e & 7);
             if constexpr (DT == ACT_F32) {
                 u32x4_t v[3];
-                parts(x[q], 0, v);
+                parts<true>(x[q], 0, v);
 #pragma unroll
                 for (int j = 0; j < 3; ++j) *(u32x4_t*)(p + j * MT * X_ROW) = v[j];
             } else {
@@ -734,7 +761,7 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
                 Raw<DT, 1> y;
                 y.template load<false>(a, min(t0 + tw + 32 * j + i32, a.n_tok - 1), (int64_t)MK * st + 32 * h + 8 * c);
                 u32x4_t p[parts_of<DT>()];
-                parts(y, 0, p);
+                parts<true>(y, 0, p);
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
                     const int64_t row = min(r0 + rw + 32 * i + i32, a.d_out - 1);
@@ -997,7 +1024,7 @@ double rounds(const MatArgs& a, int64_t r, int64_t t) {
 // tokens 256 x 128 63, 128 x 128 72.
 template <Act DT>
 gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    constexpr double us[5][6] = {{13, 16.4, 19.2, 30.3, 0, 0},      // float32
+    constexpr double us[5][6] = {{7.8, 10.5, 13.5, 20, 0, 0},       // float32
                                  {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // float16
                                  {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // bfloat16
                                  {3.5, 4.8, 6.6, 5.9, 9.1, 13.4},   // e4m3
@@ -1022,7 +1049,7 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
             offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 75.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(8, rounds(a, 128, MT) * 160.0);
+        offer(8, rounds(a, 128, MT) * 130.0);
     } else if constexpr (DT == ACT_FP8) {
         offer(8, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
     } else {

@@ -379,3 +379,25 @@ def test_infinite_float16_by_weights_outside_its_range(n, d_out):
     x[np.arange(n), at] = np.inf
     Y = P.mx_matmul(torch.from_numpy(x).half().to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV))
     assert np.array_equal(Y.cpu().numpy(), np.inf * wv[:, at].T)
+
+
+@pytest.mark.parametrize("n", [3, 40, 1500])
+def test_float32_of_every_size(n):
+    """Float32 activations from 2^-100 to 2^100, and infinities and NaN of small payloads among them."""
+    rng = np.random.default_rng(n)
+    d_in, d_out = 400, 1500
+    w, ws = _weights(rng, d_out, d_in)
+    wv = M.mx_values(w, ws, "fp4", d_in)
+    wt = torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV)
+    x = rng.standard_normal((n, d_in)) * 2.0 ** rng.integers(-100, 100, (n, 1))
+    X = torch.from_numpy(x).float()
+    Y = P.mx_matmul(X.to(DEV), *wt).double().cpu().numpy()
+    x = X.double().numpy()
+    bound = (4 * d_in + 64) * 2.0 ** -23 * (np.abs(x) @ np.abs(wv).T)
+    assert (np.abs(Y - x @ wv.T) <= bound).all()
+    bits = X.numpy().view(np.uint32).copy()
+    bits[0, 5], bits[1, 150], bits[2, 399] = 0x7F800000, 0x7F800001, 0xFF80FFFF      # an infinity, NaN with low payloads
+    Y2 = P.mx_matmul(torch.from_numpy(bits.view(np.float32)).to(DEV), *wt).double().cpu().numpy()
+    assert np.isnan(Y2[1:3]).all() and np.array_equal(Y2[3:], Y[3:])
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(Y2[0], np.inf * wv[:, 5], equal_nan=True)
