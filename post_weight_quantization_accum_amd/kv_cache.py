@@ -9,7 +9,7 @@ import dataclasses
 
 from . import _lib
 from ._lib import load
-from .mx import _current, _dtype_code, _gpu, _on, _torch
+from .mx import _codes, _current, _dtype_code, _gpu, _on, _torch
 
 FORMATS = {"16bit": _lib.MX_NONE, "fp8": _lib.MX_FP8, "fp4": _lib.MX_FP4}
 
@@ -58,7 +58,7 @@ def new_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt:
 
 
 def _cache(c: KVCache):
-    """(reference to gptq_kv_cache, GPU, kv heads, head_dim) of c, with its tensors checked."""
+    """(gptq_kv_cache, GPU, kv heads, head_dim) of c, with its tensors checked."""
     torch = _torch()
     f = FORMATS.get(c.fmt)
     if f is None:
@@ -76,15 +76,15 @@ def _cache(c: KVCache):
     if d % 32:
         raise ValueError("the cache's head_dim must be a multiple of 32")
     if not f:
-        return ctypes.byref(_lib.Cache(k.data_ptr(), v.data_ptr(), None, None, n_pages, page, heads, d, f,
-                                       _dtype_code(k))), _gpu(k, v), heads, d
+        return _lib.Cache(k.data_ptr(), v.data_ptr(), None, None, n_pages, page, heads, d, f, _codes[dt]), \
+            _gpu(k, v), heads, d
     ks, vs = c.k_scales, c.v_scales
     want = (n_pages, heads, page, d // 32)
     for t in (ks, vs):
         if t is None or t.dtype != torch.uint8 or t.shape != want or not t.is_contiguous():
             raise TypeError(f"cache.k_scales and cache.v_scales must be contiguous uint8 tensors of shape {want}")
-    return ctypes.byref(_lib.Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page, heads, d, f,
-                                   0)), _gpu(k, v, ks, vs), heads, d
+    return _lib.Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page, heads, d, f, 0), \
+        _gpu(k, v, ks, vs), heads, d
 
 
 def _heads(X, name, n_heads, head_dim):
@@ -145,14 +145,15 @@ def cache_read(cache: KVCache, table, row_start, n_rows: int, dtype=None, out=No
     with _on(dev, stream):
         if out is None:
             K = table.new_empty((n_rows, heads, d), dtype=dtype)
-            V = K.new_empty((n_rows, heads, d))
+            V = torch.empty_like(K)
+            ld_k = ld_v = heads * d
         else:
             K, V = out
             _gpu(table, K, V)
-        n_k, ld_k, _ = _heads(K, "out", heads, d)
-        n_v, ld_v, _ = _heads(V, "out", heads, d)
-        if n_k != n_rows or n_v != n_rows or K.dtype != dtype or V.dtype != dtype:
-            raise TypeError("out must be two tensors of n_rows rows and dtype")
+            n_k, ld_k, _ = _heads(K, "out", heads, d)
+            n_v, ld_v, _ = _heads(V, "out", heads, d)
+            if n_k != n_rows or n_v != n_rows or K.dtype != dtype or V.dtype != dtype:
+                raise TypeError("out must be two tensors of n_rows rows and dtype")
         st = lib.gptq_cache_read(c, table.data_ptr(), max_pages, n_seq, row_start.data_ptr(), n_rows, K.data_ptr(),
                                  V.data_ptr(), _dtype_code(K), ld_k, ld_v, _current(dev))
     if st:
