@@ -1016,21 +1016,22 @@ double rounds(const MatArgs& a, int64_t r, int64_t t) {
 
 // Which kernel, and which tile: the least of rounds x time per round, measured
 // in us at 4096 columns (they grow alike with the columns).  Few-token tiles of
-// 16 RT x 16 TT for (RT, TT) = (1,1) (2,1) (4,1) (2,2) (4,2) (4,4), 0 where LDS
-// does not hold two steps per wave; then the others: 16-bit 128 x 128 and 256 x
-// 128 from LDS rings, else 128 x 128 through registers, at 69 (e4m3) of which
-// two or three share a compute unit; e2m1 by e2m1 as the 16-bit ones.  For example bf16 4096 -> 4096: 32 tokens
-// (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256 tokens (4,2) 20, 128 x 128 26; 2048
-// tokens 256 x 128 63, 128 x 128 72.
+// 16 RT x 16 TT for (RT, TT) = (1,1) (2,1) (3,1) (4,1) (2,2) (4,2) (4,4), 0
+// where LDS does not hold two steps per wave; then the others: 16-bit 128 x 128
+// and 256 x 128 from LDS rings, and so e2m1 by e2m1; else 128 x 128 through
+// registers, where two (float32) or three workgroups share a compute unit.  For
+// example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256
+// tokens (4,2) 20, 128 x 128 26; 2048 tokens 256 x 128 63, 128 x 128 72.  One
+// token 4096 -> 11008: (3,1) 8.5, (4,1) 9.9, (2,1) 11.3, (1,1) 13.0.
 template <Act DT>
 gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    constexpr double us[5][6] = {{7.8, 10.5, 13.5, 20, 0, 0},       // float32
-                                 {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // float16
-                                 {3.9, 5.0, 6.9, 6.4, 9.4, 0},      // bfloat16
-                                 {3.5, 4.8, 6.6, 5.9, 9.1, 13.4},   // e4m3
-                                 {2.1, 4.1, 6.6, 5.9, 8.7, 13.3}};  // e2m1
+    constexpr double us[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // float32
+                                 {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // float16
+                                 {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // bfloat16
+                                 {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
+                                 {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 13.3}};    // e2m1
     static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
-    constexpr int rt[6] = {1, 2, 4, 2, 4, 4}, tt[6] = {1, 1, 1, 2, 2, 4};
+    constexpr int rt[7] = {1, 2, 3, 4, 2, 4, 4}, tt[7] = {1, 1, 1, 1, 2, 2, 4};
     int best = 0;
     double least = 1e30;
     const auto offer = [&](int id, double cost) {
@@ -1039,37 +1040,38 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
             best = id;
         }
     };
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 7; ++i)
         if (us[DT][i] > 0) offer(i, rounds(a, 16 * rt[i], 16 * tt[i]) * us[DT][i]);
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
         if (a.full > 0) {
-            offer(6, rounds(a, 128, MT) * 25.0);
-            offer(7, rounds(a, 256, MT) * 43.0);
+            offer(7, rounds(a, 128, MT) * 25.0);
+            offer(8, rounds(a, 256, MT) * 43.0);
         } else {
-            offer(8, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 75.0);
+            offer(9, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 75.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(8, rounds(a, 128, MT) * 130.0);
+        offer(9, rounds(a, 128, MT) * 130.0);
     } else if constexpr (DT == ACT_FP8) {
-        offer(8, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
+        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
     } else {
-        offer(6, rounds(a, 128, MT) * 13.0);
-        offer(7, rounds(a, 256, MT) * 25.0);
+        offer(7, rounds(a, 128, MT) * 13.0);
+        offer(8, rounds(a, 256, MT) * 25.0);
     }
     switch (best) {
         case 0: return launch_few<DT, 1, 1>(a, s);
         case 1: return launch_few<DT, 2, 1>(a, s);
-        case 2: return launch_few<DT, 4, 1>(a, s);
-        case 3: return launch_few<DT, 2, 2>(a, s);
-        case 4: return launch_few<DT, 4, 2>(a, s);
-        case 5: return launch_few<DT, 4, 4>(a, s);
+        case 2: return launch_few<DT, 3, 1>(a, s);
+        case 3: return launch_few<DT, 4, 1>(a, s);
+        case 4: return launch_few<DT, 2, 2>(a, s);
+        case 5: return launch_few<DT, 4, 2>(a, s);
+        case 6: return launch_few<DT, 4, 4>(a, s);
         default: break;
     }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
-        if (best == 6) return launch_wide<DT, 2>(a, s);
-        if (best == 7) return launch_wide<DT, 4>(a, s);
+        if (best == 7) return launch_wide<DT, 2>(a, s);
+        if (best == 8) return launch_wide<DT, 4>(a, s);
     }
-    if constexpr (DT == ACT_FP4) return best == 6 ? launch_mx<2>(a, s) : launch_mx<4>(a, s);
+    if constexpr (DT == ACT_FP4) return best == 7 ? launch_mx<2>(a, s) : launch_mx<4>(a, s);
     else return launch_many<DT>(a, s);
 }
 

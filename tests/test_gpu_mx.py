@@ -401,3 +401,10 @@ def test_float32_of_every_size(n):
     assert np.isnan(Y2[1:3]).all() and np.array_equal(Y2[3:], Y[3:])
     with np.errstate(invalid="ignore"):
         assert np.array_equal(Y2[0], np.inf * wv[:, 5], equal_nan=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32", "fp4", "fp8"])
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 520, 11000), (16, 1024, 12288 - 5), (30, 640, 9000), (5, 384, 6000), (33, 256, 17000)])
+def test_few_tokens_by_many_rows(n, d_in, d_out, kind):
+    """One round of every few-token tile, with rows past the end of the last."""
+    test_integers_come_out_exactly(n, d_in, d_out, kind)
