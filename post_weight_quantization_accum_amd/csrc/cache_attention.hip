@@ -606,7 +606,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
 // 128 rows).  Bound by the matrix instructions and the weights' arithmetic,
 // which take about as long each and overlap only between the two waves of a
 // SIMD: 2048 tokens over 16384 16-bit positions, 8 kv heads of 128 with 4 heads
-// each, 562 us (917 TFLOP/s); e2m1 538 us.  Keys fetched two tiles ahead (no
+// each, 562 to 580 us by card (890 to 917 TFLOP/s); e2m1 538 us.  Keys fetched two tiles ahead (no
 // faster), and softmax of one half of a tile beside the products of the other
 // (765 us: its registers spill), were tried and not kept.
 // ---------------------------------------------------------------------------

@@ -1031,6 +1031,11 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
                                  {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
                                  {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 13.3}};    // e2m1
     static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
+    static_assert((us[DT][0] > 0) == FewTile<DT, 1, 1>::FITS && (us[DT][1] > 0) == FewTile<DT, 2, 1>::FITS &&
+                      (us[DT][2] > 0) == FewTile<DT, 3, 1>::FITS && (us[DT][3] > 0) == FewTile<DT, 4, 1>::FITS &&
+                      (us[DT][4] > 0) == FewTile<DT, 2, 2>::FITS && (us[DT][5] > 0) == FewTile<DT, 4, 2>::FITS &&
+                      (us[DT][6] > 0) == FewTile<DT, 4, 4>::FITS,
+                  "zeros where a tile does not fit");
     constexpr int rt[7] = {1, 2, 3, 4, 2, 4, 4}, tt[7] = {1, 1, 1, 1, 2, 2, 4};
     int best = 0;
     double least = 1e30;
