@@ -39,6 +39,7 @@ constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == G
 constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
 constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
 constexpr float RAISE = 8.0f;
+constexpr float FAR = 256.0f;                     // an exponent of a maximum that is taken off the scores themselves
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 struct AttnArgs {
@@ -246,6 +247,20 @@ __device__ __forceinline__ u32x4_t tr_pair(const char* p, const char* q) {
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// What the weights of a row with maximum m lose in their exponents,
+// exp2(x * scale - base).  Where m * scale is so large that its rounding would
+// show in them (2^-16 of a weight at FAR; from 2^27 on the weights would all
+// be 0 or infinite), the scores lose m before they are scaled, which is exact
+// near the maximum, and base is 0.
+template <int N>
+__device__ __forceinline__ float base_of(const AttnArgs& a, float m, float (&x)[N]) {
+    const float top = m == NEG_INF ? 0.0f : m, base = top * a.scale;
+    if (!__any(fabsf(base) > FAR)) return base;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] -= top;
+    return 0.0f;
 }
 
 // Infinities and NaN in V.  A weight of 0 does not keep them from a token
@@ -493,7 +508,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, x[i]);
-        if (__any(mx > m + a.raise)) {
+        if (__any(mx - m > a.raise)) {
             mx = fmaxf(mx, m);
             mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
@@ -503,7 +518,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
             l *= f;
             m = mx;
         }
-        const float base = m == NEG_INF ? 0.0f : m * a.scale;
+        const float base = base_of(a, m, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
         const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
@@ -551,7 +566,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
 #pragma unroll
     for (int i = 0; i < CT; ++i) *(f32x4_t*)(ow + n * O_ROW + 16 * i + 4 * g) = acc[i];
     if (g == 0) {
-        ml[wave][n][0] = m * a.scale;
+        ml[wave][n][0] = m;
         ml[wave][n][1] = l;
     }
     taken = __syncthreads_or(taken);
@@ -566,7 +581,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
     for (int i = 0; i < CH; ++i) o[i] = 0.0f;
 #pragma unroll
     for (int w = 0; w < FEW_WAVES; ++w) {
-        const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - bj);
+        const float f = __builtin_amdgcn_exp2f((ml[w][r][0] - bj) * a.scale);
         lj += f * ml[w][r][1];
         const float* p = (const float*)(lds + w * WAVE_B) + r * O_ROW + c0;
 #pragma unroll
@@ -741,7 +756,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e) mx = fmaxf(mx, x[e]);
-            if (__any(mx > m + a.raise)) {
+            if (__any(mx - m > a.raise)) {
                 mx = fmaxf(mx, m);
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
                 const float f = mx == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f((m - mx) * a.scale);
@@ -752,7 +767,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                 l *= f;
                 m = mx;
             }
-            const float base = m == NEG_INF ? 0.0f : m * a.scale;
+            const float base = base_of(a, m, x);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
             // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it, and
@@ -798,7 +813,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
             }
         if (n_parts != 1 && h == 0) {
             const int64_t at = (out.f - a.part_o) / D;
-            a.part_ml[2 * at] = m * a.scale;
+            a.part_ml[2 * at] = m;
             a.part_ml[2 * at + 1] = l;
         }
     }
@@ -807,7 +822,8 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // The parts of a row joined: a workgroup per token and head, O = sum_p
-// 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p, each wave with every fourth part.
+// 2^((m_p - m) scale) O_p / sum_p 2^((m_p - m) scale) l_p, each wave with every
+// fourth part.
 // 32 rows of 32 parts take 4.5 us, most of it the launch.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
@@ -877,7 +893,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
     for (int p = wave % WAVES; p < n; p += WAVES) {
         const int64_t at = p * a.n_rows;
         const float2 v = ml[at];
-        const float f = __builtin_amdgcn_exp2f(v.x - base);
+        const float f = __builtin_amdgcn_exp2f((v.x - base) * a.scale);
         l += f * v.y;
 #pragma unroll
         for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[(at + at0) * D + CH * lane + i];

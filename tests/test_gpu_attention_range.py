@@ -1,0 +1,70 @@
+"""Attention at scores far from zero (needs an MI355X).
+
+The scores here are sums of products that float32 holds exactly, so that a
+weight's exponent, (score - largest) * scale, is all that is computed: off by
+at most 3 * 2^-24 of its size (two factors, one product), which is at most
+10 where a weight counts, and 2^-22 for the power of two: together less than
+2^-19 of the weight.  With eps / 2 half a step of the 16-bit type, and
+M = sum_j p_j |v_j|, an output is off by at most
+  (2 * 2^-19 + eps / 2 + (n_keys + 64) 2^-23) M + (eps / 2) |o| + 2^-25
+(weights rounded to the type, sums in float32, the output's rounding).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx_oracle as M
+from test_gpu_cache import TYPES, Paged, attend
+
+pytestmark = pytest.mark.gpu
+
+# kv lengths, new tokens, heads per kv head: few rows, whole and in parts; many rows, whole and in parts
+FORMS = [([300, 70], [1, 3], 4), ([9000, 200], [1, 1], 4), ([300, 64], [150, 64], 2), ([9000], [200], 2)]
+
+
+def _compare(out, Q, p, q, scale):
+    eps = torch.finfo(p.dtype).eps
+    at = 0
+    for s, n in enumerate(q):
+        k, v = (p.held(w)[p.start[s]: p.start[s + 1]] for w in (0, 1))
+        o, mag, _ = M.attention(Q[at: at + n].double().cpu().numpy(), k, v, p.kv[s], scale)
+        bound = (2.0 ** -18 + eps / 2 + (p.kv[s] + 64) * 2.0 ** -23) * mag + eps / 2 * np.abs(o) + 2.0 ** -25
+        got = out[at: at + n].double().cpu().numpy()
+        assert np.isfinite(got).all()
+        assert (np.abs(got - o) <= bound).all(), (s, np.max(np.abs(got - o) / bound))
+        at += n
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kv,q,group", FORMS)
+def test_scores_of_billions(kv, q, group, dtype):
+    """All scores equal, and one key above the others: means, and that key's value."""
+    d, unit = 128, 64.0 if dtype == "f16" else 4096.0
+    for a in (129, 131, 135, 141):
+        p = Paged(a, kv, 1, d, 64, "16bit", dtype)
+        K = torch.full((sum(kv), 1, d), a * unit)
+        for s in range(len(kv)):
+            K[p.start[s] + kv[s] - 20] = (a + 1) * unit      # some of the tokens of a chunk see it
+        Q = torch.full((sum(q), group, d), a * unit, dtype=p.dtype, device="cuda")
+        for keys in (torch.full_like(K, a * unit), K):
+            p.new[0] = keys.to(p.dtype)
+            p.write()
+            out, Q, scale = attend(p, q, group, Q=Q)
+            _compare(out, Q, p, q, scale)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kv,q,group", FORMS)
+def test_close_scores_far_from_zero(kv, q, group, dtype):
+    """Scores of 127 * 2^16 + r, r from -8 to 8 along the keys, negative ones too: the weights are those of r alone."""
+    d = 128
+    for sign in (1.0, -1.0):
+        p = Paged(len(kv), kv, 1, d, 64, "16bit", dtype)
+        K = torch.full((sum(kv), 1, d), 2.0 ** 7)
+        K[..., -1] = torch.cat([torch.linspace(-8, 8, m).round() for m in kv])[:, None]
+        p.new[0] = K.to(p.dtype)
+        p.write()
+        Q = torch.full((sum(q), group, d), sign * 2.0 ** 9, dtype=p.dtype, device="cuda")
+        Q[..., -1] = 1.0
+        out, Q, _ = attend(p, q, group, Q=Q, scale=0.125)
+        _compare(out, Q, p, q, 0.125)
