@@ -484,7 +484,8 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * alignment.  Microscaled keys and values are rounded to q_dtype as they are
  * read (exact for bfloat16, and for float16 where they came from a float16).
  * Scores, maxima, sums and outputs are held in float32; the weights of the
- * value sum are rounded to q_dtype.
+ * value sum are rounded to q_dtype (in float16 small ones to a multiple of at
+ * most 2^-31 of the largest).
  * A token that attends to nothing (p < 0, or weights that are all zero) gets
  * zeros.  Keys and values at positions that a token does not attend to have
  * no influence on it, whatever they hold.  A page outside [0, n_pages), or a

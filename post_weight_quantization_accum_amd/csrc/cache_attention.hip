@@ -17,8 +17,9 @@
 // output, a maximum and a sum per row and part) that cache_join_kernel joins.
 //
 // Softmax runs over the keys with a running maximum that is raised only when
-// a score exceeds it by 2^8 (powers of two): until then the weights are at
-// most 2^8, far from any overflow, and nothing has to be rescaled.
+// a score exceeds it by 2^8 (powers of two; raising late is a published idea):
+// until then the weights are at most 2^8 (2^15 in float16, see lift()), below
+// any overflow, and nothing has to be rescaled.
 #include <algorithm>
 #include <cmath>
 
@@ -39,6 +40,11 @@ constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == G
 constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
 constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
 constexpr float RAISE = 8.0f;
+// Float16 weights are 2^7 times as large (at most 2^15), so that those are not
+// lost that are below 2^-25 of the largest, which thousands of keys of a long
+// cache can be: from 2^-32 on they count.  bfloat16 has no such border.
+template <bool BF>
+constexpr float lift() { return BF ? 0.0f : 7.0f; }
 constexpr float FAR = 256.0f;                     // an exponent of a maximum that is taken off the scores themselves
 constexpr float NEG_INF = -__builtin_huge_valf();
 
@@ -253,14 +259,14 @@ __device__ __forceinline__ void wave_sync() {
 // exp2(x * scale - base).  Where m * scale is so large that its rounding would
 // show in them (2^-16 of a weight at FAR; from 2^27 on the weights would all
 // be 0 or infinite), the scores lose m before they are scaled, which is exact
-// near the maximum, and base is 0.
-template <int N>
+// near the maximum, and base is 0 (but for the lift).
+template <bool BF, int N>
 __device__ __forceinline__ float base_of(const AttnArgs& a, float m, float (&x)[N]) {
     const float top = m == NEG_INF ? 0.0f : m, base = top * a.scale;
-    if (!__any(fabsf(base) > FAR)) return base;
+    if (!__any(fabsf(base) > FAR)) return base - lift<BF>();
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] -= top;
-    return 0.0f;
+    return -lift<BF>();
 }
 
 // Infinities and NaN in V.  A weight of 0 does not keep them from a token
@@ -518,7 +524,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
             l *= f;
             m = mx;
         }
-        const float base = base_of(a, m, x);
+        const float base = base_of<BF>(a, m, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
         const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
@@ -767,7 +773,7 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                 l *= f;
                 m = mx;
             }
-            const float base = base_of(a, m, x);
+            const float base = base_of<BF>(a, m, x);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
             // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it, and

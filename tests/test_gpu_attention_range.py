@@ -13,6 +13,7 @@ import numpy as np
 import pytest
 import torch
 
+import post_weight_quantization_accum_amd as P
 from oracle import mx_oracle as M
 from test_gpu_cache import TYPES, Paged, attend
 
@@ -68,3 +69,37 @@ def test_close_scores_far_from_zero(kv, q, group, dtype):
         Q[..., -1] = 1.0
         out, Q, _ = attend(p, q, group, Q=Q, scale=0.125)
         _compare(out, Q, p, q, 0.125)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("seqs,new", [(64, 64), (1, 1), (1, 64), (40, 1)])
+def test_one_key_and_a_long_tail(seqs, new, dtype):
+    """131072 keys: the first outweighs each other one by 2^25 (2^21), all others together weigh 2^-8 (2^-4) of it.
+
+    With w a tail key's weight, N their number and o = (N w - 1) / (1 + N w)
+    (values 1 and -1), do <= 2 d(N w): a tail weight is off by half a step, or
+    in float16 by half its smallest step, 2^-25 beside a largest weight of 2^7.
+    A matrix instruction adds 16 keys to a sum of at most 1 (2^-23 each, it may
+    cut), the weights' sum grows by a step of 64 keys at a time (2^-24).
+    """
+    page, d, kv, heads = 64, 32, 1 << 17, 16
+    t = TYPES[dtype]
+    eps = torch.finfo(t).eps
+    cache = P.new_cache(kv // page, page, 1, d, fmt="16bit", dtype=t, device="cuda")
+    cache.v.fill_(1.0)
+    cache.v[0, 0, 0] = -1.0
+    table = torch.arange(kv // page, dtype=torch.int32, device="cuda").repeat(seqs, 1).contiguous()
+    start = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * new
+    lens = torch.full((seqs,), kv, dtype=torch.int32, device="cuda")
+    Q = torch.zeros(seqs * new, heads, d, dtype=t, device="cuda")
+    Q[..., 0] = 1.0
+    for top in (17.4375, 15.0):
+        cache.k[0, 0, 0, 0] = top
+        out = P.cache_attention(Q, cache, start, lens, table, max_q=new, scale=1.0).double().cpu().numpy()
+        n = kv - new + np.arange(new, dtype=np.float64)
+        w = np.exp(-float(torch.tensor(top).to(t)))
+        o = (n * w - 1) / (1 + n * w)
+        bound = 2 * n * w * max(eps / 2, 2.0 ** -32 / w if dtype == "f16" else 0.0) + (n / 16 + 64) * 2.0 ** -23 + \
+            (n / 64 + 64) * 2.0 ** -24 + eps / 2 * np.abs(o)
+        err = np.abs(out.reshape(seqs, new, -1) - o[:, None])
+        assert (err <= bound[:, None]).all(), np.max(err / bound[:, None])
