@@ -255,18 +255,22 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// What the weights of a row with maximum m lose in their exponents,
-// exp2(x * scale - base).  Where m * scale is so large that its rounding would
-// show in them (2^-16 of a weight at FAR; from 2^27 on the weights would all
-// be 0 or infinite), the scores lose m before they are scaled, which is exact
-// near the maximum, and base is 0 (but for the lift).
-template <bool BF, int N>
-__device__ __forceinline__ float base_of(const AttnArgs& a, float m, float (&x)[N]) {
-    const float top = m == NEG_INF ? 0.0f : m, base = top * a.scale;
-    if (!__any(fabsf(base) > FAR)) return base - lift<BF>();
+// What the weights of a row lose in their exponents, exp2(x * scale - base),
+// from the row's maximum m on.  Where m * scale is so large in some row that
+// its rounding would show in the weights (2^-16 of them at FAR; from 2^27 on
+// they would all be 0 or infinite), the wave is "far": its scores lose m before
+// they are scaled, which is exact near the maximum, and base is only the lift.
+template <bool BF>
+__device__ __forceinline__ bool set_base(const AttnArgs& a, float m, float& base) {
+    base = (m == NEG_INF ? 0.0f : m) * a.scale;
+    const bool far = __any(fabsf(base) > FAR);
+    base = (far ? 0.0f : base) - lift<BF>();
+    return far;
+}
+template <int N>
+__device__ __forceinline__ void near_zero(float (&x)[N], float m) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] -= top;
-    return -lift<BF>();
+    for (int i = 0; i < N; ++i) x[i] -= m == NEG_INF ? 0.0f : m;
 }
 
 // Infinities and NaN in V.  A weight of 0 does not keep them from a token
@@ -445,8 +449,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
     f32x4_t acc[CT];
 #pragma unroll
     for (int i = 0; i < CT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = NEG_INF, l = 0.0f;
-    bool taken = false;
+    float m = NEG_INF, l = 0.0f, base = -lift<BF>();
+    bool far = false, taken = false;
     char* const vt = lds + wave * WAVE_B;
 
     // Keys and values of a step, fetched while the one before is worked on: K
@@ -523,10 +527,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
             for (int i = 0; i < CT; ++i) acc[i] *= f;
             l *= f;
             m = mx;
+            far = set_base<BF>(a, m, base);
         }
-        const float base = base_of<BF>(a, m, x);
+        if (far) near_zero(x, m);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale, -base));
+        float sum = 0.0f;
         const bool mixed = mixed_step(a, key0, FEW_KEYS, pos0, pos1);
         const char* vr = vt + (4 * g + (n >> 2)) * V_ROW + 8 * (n & 3);
 #pragma unroll
@@ -549,17 +555,19 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
             }
             wave_sync();
             // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it,
-            // and so rounded in their sum
+            // and so rounded in their sum, which gets those of a step at once (a long cache's
+            // small weights one by one would not change a large sum)
             const float* w = x + 8 * f;
             const u32x4_t p = {H16<BF>::pack(w[0], w[1]), H16<BF>::pack(w[2], w[3]), H16<BF>::pack(w[4], w[5]),
                                H16<BF>::pack(w[6], w[7])};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l = H16<BF>::add2(p[i], l);
+            for (int i = 0; i < 4; ++i) sum = H16<BF>::add2(p[i], sum);
 #pragma unroll
             for (int i = 0; i < CT; ++i)
                 acc[i] = H16<BF>::mfma16(tr_pair(vr + 32 * i, vr + 16 * V_ROW + 32 * i), p, acc[i]);
             wave_sync();
         }
+        l += sum;
         edge = edgen;
 #pragma unroll
         for (int h = 0; h < 4; ++h) row4[h] = rown[h];
@@ -677,7 +685,8 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
     for (int i = 0; i < CT; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-    float m = NEG_INF, l = 0.0f;
+    float m = NEG_INF, l = 0.0f, base = -lift<BF>();
+    bool far = false;
 
     // lane l looks after key l of a step
     const auto entry_of = [&](int step) { return table_entry(a, t, step * MANY_KEYS + lane); };
@@ -772,18 +781,22 @@ __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
                     for (int e = 0; e < 16; ++e) acc[i][e] *= f;
                 l *= f;
                 m = mx;
+                far = set_base<BF>(a, m, base);
             }
-            const float base = base_of<BF>(a, m, x);
+            if (far) near_zero(x, m);
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale, -base));
             // the weights as the matrix operand: rounded to the 16-bit type, as V is held in it, and
-            // so rounded in their sum (two at a time)
+            // so rounded in their sum (two at a time; a step's at once: a long cache's small weights
+            // one by one would not change a large sum)
             u32x4_t p[4];
+            float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 p[e >> 2][e & 3] = H16<BF>::pack(x[2 * e], x[2 * e + 1]);
-                l = H16<BF>::add2(p[e >> 2][e & 3], l);
+                sum = H16<BF>::add2(p[e >> 2][e & 3], sum);
             }
+            l += sum;
             __builtin_amdgcn_s_setprio(1);
             const char* vr = vt + (4 * h + ((lane & 15) >> 2)) * V_ROW + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
 #pragma unroll

@@ -103,3 +103,25 @@ def test_one_key_and_a_long_tail(seqs, new, dtype):
             (n / 64 + 64) * 2.0 ** -24 + eps / 2 * np.abs(o)
         err = np.abs(out.reshape(seqs, new, -1) - o[:, None])
         assert (err <= bound[:, None]).all(), np.max(err / bound[:, None])
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_sum_of_weights_beside_a_large_one(new):
+    """The keys of the test above with values 1 and 0: o = 1 / (1 + N w), and only the weights' sum can lose any.
+
+    do <= d(N w): n 2^-32 from the weights, (n / 64 + 64) 2^-24 from a sum that grows by a step of 64 keys at a time.
+    """
+    page, d, kv, heads, seqs = 64, 32, 1 << 17, 16, 64
+    cache = P.new_cache(kv // page, page, 1, d, fmt="16bit", dtype=torch.float16, device="cuda")
+    cache.v[0, 0, 0] = 1.0
+    cache.k[0, 0, 0, 0] = 17.4375
+    table = torch.arange(kv // page, dtype=torch.int32, device="cuda").repeat(seqs, 1).contiguous()
+    start = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * new
+    Q = torch.zeros(seqs * new, heads, d, dtype=torch.float16, device="cuda")
+    Q[..., 0] = 1.0
+    out = P.cache_attention(Q, cache, start, torch.full((seqs,), kv, dtype=torch.int32, device="cuda"), table, max_q=new, scale=1.0)
+    n = kv - new + np.arange(new, dtype=np.float64)
+    o = 1 / (1 + n * np.exp(-17.4375))
+    bound = n * 2.0 ** -32 + (n / 64 + 64) * 2.0 ** -24 + 2.0 ** -11 * o
+    err = np.abs(out.double().cpu().numpy().reshape(seqs, new, -1) - o[:, None])
+    assert (err <= bound[:, None]).all(), np.max(err / bound[:, None])
