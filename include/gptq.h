@@ -500,8 +500,8 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * workspace: gptq_cache_attention_workspace(...) bytes (may be 0), for parts
  * of long sequences.  Asynchronous.
  * Errors: GPTQ_ERR_INVALID_ARG for a bad cache, dtype, size, stride or
- * pointer, n_heads not a multiple of n_kv_heads, a scale that is not a
- * positive number, or a window outside [0, 2^30];
+ * pointer, n_heads not a multiple of n_kv_heads, a scale outside
+ * [2^-100, 2^100], or a window outside [0, 2^30];
  * GPTQ_ERR_UNSUPPORTED for another head_dim, and for more than 2^31 - 1 rows
  * (n_tok * n_heads) or 2^32 threads of a launch (some 2^23 sequences times
  * kv heads); GPTQ_ERR_WORKSPACE. */

@@ -133,7 +133,7 @@ gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq
     if (!is_half(q_dtype) || (cache->format == GPTQ_MX_NONE && q_dtype != cache->dtype)) return GPTQ_ERR_INVALID_ARG;
     if (!check_shape(cache, n_tok, n_heads, n_seq, max_pages, max_q, window)) return GPTQ_ERR_INVALID_ARG;
     if (ld_q < n_heads * cache->head_dim || ld_o < n_heads * cache->head_dim) return GPTQ_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || scale > 3e38f) return GPTQ_ERR_INVALID_ARG;
+    if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return GPTQ_ERR_INVALID_ARG;   // its reciprocal is used, too
     if (n_tok == 0 || n_seq == 0) return GPTQ_OK;
     if (!elems(Q, q_dtype) || !elems(O, q_dtype) || !on(q_start, 4) || !on(kv_len, 4) || (max_pages && !on(table, 4)))
         return GPTQ_ERR_INVALID_ARG;

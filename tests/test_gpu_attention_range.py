@@ -125,3 +125,17 @@ def test_sum_of_weights_beside_a_large_one(new):
     bound = n * 2.0 ** -32 + (n / 64 + 64) * 2.0 ** -24 + 2.0 ** -11 * o
     err = np.abs(out.double().cpu().numpy().reshape(seqs, new, -1) - o[:, None])
     assert (err <= bound[:, None]).all(), np.max(err / bound[:, None])
+
+
+@pytest.mark.parametrize("kv,q,group", FORMS)
+@pytest.mark.parametrize("power", [-100, 100])
+def test_scales_at_the_ends(kv, q, group, power):
+    """Scores that the scale brings down to nothing (means) or up to 2^100 times their size."""
+    p = Paged(3, kv, 1, 64, 64, "16bit", "bf16")
+    p.new[0] = torch.zeros_like(p.new[0])
+    p.new[0][..., 0] = torch.cat([torch.arange(m) % 7 for m in kv])[:, None].to(torch.bfloat16)
+    p.write()
+    Q = torch.zeros(sum(q), group, 64, dtype=torch.bfloat16, device="cuda")
+    Q[..., 0] = 1.0 if power < 0 else 2.0 ** -100
+    out, Q, scale = attend(p, q, group, Q=Q, scale=2.0 ** power)
+    _compare(out, Q, p, q, scale)
