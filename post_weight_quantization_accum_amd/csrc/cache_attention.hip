@@ -39,6 +39,11 @@ constexpr int FEW_WAVES = 8;                      // of a few-row workgroup, eac
 constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == GPTQ_MX_FP8 ? 48 : 32; }
 constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
 constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
+// Positions from here on count as past the table: keys are fetched up to two
+// steps ahead of eight waves' (1100 positions), and those numbers must not pass
+// 31 bits either.
+constexpr int64_t POSITIONS = (int64_t(1) << 31) - 4096;
+static_assert(4096 > 3 * FEW_WAVES * FEW_KEYS && 4096 > 4 * MANY_KEYS, "room for the steps ahead");
 constexpr float RAISE = 8.0f;
 // Float16 weights are 2^7 times as large (at most 2^15), so that those are not
 // lost that are below 2^-25 of the largest, which thousands of keys of a long
@@ -59,7 +64,7 @@ struct AttnArgs {
     bool q_aligned, o_aligned;     // rows of 16 bytes, of 8 bytes
     const int32_t *q_start, *kv_len, *table;
     int64_t max_pages;
-    int cap;                       // positions that the table reaches
+    int cap;                       // positions that the table reaches (at most POSITIONS)
     int n_seq, n_tok;
     FastDiv group;                 // heads per key-value head
     float scale;                   // times log2(e)
@@ -1070,7 +1075,7 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     a.kv_len = kv_len;
     a.table = table;
     a.max_pages = s.max_pages;
-    a.cap = (int)std::min<int64_t>((int64_t)c.page_size * s.max_pages, INT32_MAX - MANY_KEYS);
+    a.cap = (int)std::min<int64_t>((int64_t)c.page_size * s.max_pages, POSITIONS);
     a.n_seq = (int)s.n_seq;
     a.n_tok = (int)s.n_tok;
     a.group = fast_div((uint32_t)(s.n_heads / c.n_kv_heads));

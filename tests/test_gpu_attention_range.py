@@ -139,3 +139,28 @@ def test_scales_at_the_ends(kv, q, group, power):
     Q[..., 0] = 1.0 if power < 0 else 2.0 ** -100
     out, Q, scale = attend(p, q, group, Q=Q, scale=2.0 ** power)
     _compare(out, Q, p, q, scale)
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+@pytest.mark.parametrize("new", [2, 200])
+def test_positions_near_two_to_the_31(new, fmt):
+    """Two pages that a table repeats 16384 times, and a window: what stands at the last positions that count equals
+    what stands a multiple of both pages before; tokens behind are NaN."""
+    page, d, heads, last = 1 << 16, 64, 2, (1 << 31) - 4096
+    cache = P.new_cache(2, page, 1, d, fmt=fmt, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(new)
+    K, V = (torch.randn(2 * page, 1, d, device="cuda", generator=gen).to(torch.bfloat16) for _ in range(2))
+    P.cache_write(cache, K, V, torch.arange(2 * page, dtype=torch.int64, device="cuda"))
+    table = torch.tensor([0, 1], dtype=torch.int32, device="cuda").repeat(16384)[None].contiguous()
+    start = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    Q = torch.randn(new, heads, d, device="cuda", generator=gen).to(torch.bfloat16)
+
+    def at(kv):
+        return P.cache_attention(Q, cache, start, torch.tensor([kv], dtype=torch.int32, device="cuda"), table, max_q=new, window=700)
+
+    assert last % (2 * page) > 1000
+    near = at(last % (2 * page) + 2 * page)
+    assert torch.isfinite(near).all() and torch.equal(at(last), near)
+    past = at(last + 1)
+    assert past[-1].isnan().all() and torch.isfinite(past[:-1]).all()
+    assert at((1 << 31) - 1).isnan().all()
