@@ -504,9 +504,16 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * [2^-100, 2^100], or a window outside [0, 2^30];
  * GPTQ_ERR_UNSUPPORTED for another head_dim, and for more than 2^31 - 1 rows
  * (n_tok * n_heads) or 2^32 threads of a launch (some 2^23 sequences times
- * kv heads); GPTQ_ERR_WORKSPACE. */
+ * kv heads); GPTQ_ERR_WORKSPACE.
+ * gptq_cache_attention_plan: how a call of these sizes would be computed, for
+ * profiles and tests: plan[0], plan[1] (host memory) get the parts that the
+ * kernel for sequences of few rows and the one for many cut the keys into (1:
+ * whole, 0: not launched), plan[2] the rows for which the workspace holds
+ * parts.  GPTQ_ERR_UNSUPPORTED where the call would refuse the sizes. */
 size_t gptq_cache_attention_workspace(const gptq_kv_cache* cache, int64_t n_tok, int64_t n_heads, int64_t n_seq,
                                       int64_t max_pages, int64_t max_q, int64_t window);
+gptq_status gptq_cache_attention_plan(const gptq_kv_cache* cache, int64_t n_tok, int64_t n_heads, int64_t n_seq,
+                                      int64_t max_pages, int64_t max_q, int64_t window, int64_t* plan);
 gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq_dtype q_dtype, int64_t n_tok,
                                  int64_t n_heads, int64_t ld_q, const int32_t* q_start, const int32_t* kv_len,
                                  const int32_t* table, int64_t max_pages, int64_t n_seq, int64_t max_q,

@@ -31,7 +31,7 @@ EXPORTS = (
     "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
     "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
     "gptq_mx_matmul_quantized", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
-    "gptq_cache_attention", "gptq_status_string", "gptq_version",
+    "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_status_string", "gptq_version",
 )
 
 
@@ -165,6 +165,8 @@ def load(path: str | None = None):
     lib.gptq_cache_read.restype = ci
     lib.gptq_cache_attention_workspace.argtypes = [cachep, i64, i64, i64, i64, i64, i64]
     lib.gptq_cache_attention_workspace.restype = sz
+    lib.gptq_cache_attention_plan.argtypes = [cachep, i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    lib.gptq_cache_attention_plan.restype = ci
     lib.gptq_cache_attention.argtypes = [cachep, vp, ci, i64, i64, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, i64,
                                          vp, i64, vp, sz, vp]
     lib.gptq_cache_attention.restype = ci

@@ -75,9 +75,10 @@ struct AttnArgs {
     int per_seq;                   // of the few-row kernel's workgroups per sequence
     int n_split;
     int64_t rows_min, rows_max;    // of the sequences this launch takes
-    float* part_o;                 // [part][token][head][D]
-    float* part_ml;                // [part][token][head][2]
-    int64_t n_rows;                // tokens * heads
+    float* part_o;                 // [part][part_rows][D]
+    float* part_ml;                // [part][part_rows][2]
+    int64_t part_rows;             // per_seq_head > 0: sequences * kv heads * per_seq_head, else tokens * heads
+    int per_seq_head;              // rows that a sequence and kv head has room for
 };
 
 // A tile of rows of one sequence, and the keys that any of them attends to.
@@ -337,6 +338,12 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, uint16_t* p, float 
     }
 }
 
+// Number of a row among those that can have parts.
+__device__ __forceinline__ int64_t part_row(const AttnArgs& a, const Tile& t, int head, int row, int tok, int hd) {
+    return a.per_seq_head ? ((int64_t)t.seq * a.n_kv + head) * a.per_seq_head + row
+                          : (int64_t)(t.q0 + tok) * (a.n_kv * (int)a.group.d) + hd;
+}
+
 // Where a row's outputs are: in O, or in the part's float32 rows.
 struct Out {
     uint16_t* o;
@@ -346,7 +353,7 @@ __device__ __forceinline__ Out out_of(const AttnArgs& a, const Tile& t, int head
     const int tok = (int)div_by((uint32_t)row, a.group), g = (int)a.group.d, hd = head * g + row - tok * g;
     Out r = {nullptr, nullptr};
     if (direct) r.o = a.O + (int64_t)(t.q0 + tok) * a.ld_o + (int64_t)hd * a.d;
-    else r.f = a.part_o + ((int64_t)part * a.n_rows + (int64_t)(t.q0 + tok) * (a.n_kv * g) + hd) * D;
+    else r.f = a.part_o + (part * a.part_rows + part_row(a, t, head, row, tok, hd)) * D;
     return r;
 }
 
@@ -854,7 +861,6 @@ struct JoinArgs {
     AttnArgs a;
     int64_t few_max;               // sequences of at most this many rows were the few-row kernel's
     int few_split, many_split;
-    int rows_per_seq;              // > 0: only the first so many rows of each sequence and head, none of longer ones
 };
 
 // WAVES waves to a row, 4 / WAVES rows to a workgroup.
@@ -868,21 +874,21 @@ __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
     const int heads = a.n_kv * (int)a.group.d;
     Tile t;
     int row = -1, tok = 0, hd = 0;
-    if (j.rows_per_seq) {
-        const int64_t sh = id / j.rows_per_seq;
-        row = (int)(id - sh * j.rows_per_seq);
+    if (a.per_seq_head) {          // none of the sequences of more rows has parts
+        const int64_t sh = id / a.per_seq_head;
+        row = (int)(id - sh * a.per_seq_head);
         const int s = (int)(sh / a.n_kv), kv = (int)(sh - (int64_t)s * a.n_kv);
         if (s >= a.n_seq) row = -1;
         else {
             sequence(a, s, t);
-            if (t.rows > j.rows_per_seq || row >= t.rows) row = -1;
+            if (t.rows > a.per_seq_head || row >= t.rows) row = -1;
             else {
                 const int i = (int)div_by((uint32_t)row, a.group);
                 tok = t.q0 + i;
                 hd = kv * (int)a.group.d + row - i * (int)a.group.d;
             }
         }
-    } else if (id < a.n_rows) {
+    } else if (id < a.part_rows) {
         tok = (int)(id / heads);
         hd = (int)(id - (int64_t)tok * heads);
         const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, tok, [&](int i) { return a.q_start[i]; }));
@@ -903,10 +909,9 @@ __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
     }
     // the same for all waves of a row, and of the workgroup where they meet
     if (n == 1) return;
-    const int64_t at0 = (int64_t)tok * heads + hd;
-    const float2* ml = (const float2*)a.part_ml + at0;
+    const float2* ml = (const float2*)a.part_ml + id;      // parts are kept in the order of the ids
     float m = NEG_INF;
-    for (int p = lane; p < n; p += 64) m = fmaxf(m, ml[p * a.n_rows].x);
+    for (int p = lane; p < n; p += 64) m = fmaxf(m, ml[p * a.part_rows].x);
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
     const float base = m == NEG_INF ? 0.0f : m;
@@ -915,12 +920,12 @@ __global__ __launch_bounds__(256) void cache_join_kernel(JoinArgs j) {
     for (int i = 0; i < CH; ++i) o[i] = 0.0f;
 #pragma unroll 8
     for (int p = wave % WAVES; p < n; p += WAVES) {
-        const int64_t at = p * a.n_rows;
+        const int64_t at = p * a.part_rows;
         const float2 v = ml[at];
         const float f = __builtin_amdgcn_exp2f((v.x - base) * a.scale);
         l += f * v.y;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[(at + at0) * D + CH * lane + i];
+        for (int i = 0; i < CH; ++i) o[i] += f * a.part_o[(at + id) * D + CH * lane + i];
     }
     if constexpr (WAVES > 1) {
 #pragma unroll
@@ -949,6 +954,10 @@ struct Plan {
     int64_t few_slots, many_slots;
     int per_seq, few_split, many_split;
     int D;
+    int64_t part_rows;             // as in AttnArgs; 0: no parts
+    int per_seq_head;
+    int join_waves;                // per row
+    bool fits;                     // what is counted in 32 bits stays there
 };
 
 Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
@@ -978,7 +987,7 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
     int64_t keys = (int64_t)c.page_size * s.max_pages;
     if (s.window) keys = std::min(keys, s.window + s.max_q);
     const int64_t key_bytes = 2 * c.head_dim * (c.format == GPTQ_MX_NONE ? 32 : c.format == GPTQ_MX_FP8 ? 17 : 9) / 16;
-    const auto split = [&](double wgs, int64_t limit, int64_t least, double us, bool pairs) {
+    const auto split = [&](double wgs, int64_t limit, int64_t least, double us, bool pairs, int64_t joined) {
         int best = 1;
         double cost = 1e300;
         if (wgs >= (pairs ? 512.0 : 256.0)) limit = 1;
@@ -986,7 +995,7 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
         for (int64_t n = 1; n <= std::max<int64_t>(1, std::min(limit, keys / least)); ++n) {
             double rounds = std::ceil(wgs * (double)n / 256.0);
             if (pairs) rounds = std::floor(rounds / 2) + (std::fmod(rounds, 2.0) != 0.0 ? 0.84 : 0.0);
-            const double join = n > 1 ? 10.0 + (double)n * (double)(s.n_tok * s.n_heads) * p.D * 8.0 / 4e6 : 0.0;
+            const double join = n > 1 ? 10.0 + (double)n * (double)joined * p.D * 8.0 / 4e6 : 0.0;
             const double total = us * rounds / (double)n + join;
             if (total < cost) {
                 cost = total;
@@ -996,11 +1005,27 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
         return best;
     };
     p.few_split = p.many_split = 1;
-    if (p.few)
-        p.few_split = split((double)(p.few_slots * c.n_kv_heads), 64, FEW_KEYS * FEW_MIN, (double)(keys * key_bytes) / 20e3, false);
+    const int64_t all = rows * c.n_kv_heads, few_rows = s.n_seq * c.n_kv_heads * p.few_most;
     if (p.many)
         p.many_split = split((double)((ceil_div(rows, MANY_ROWS) + (s.n_seq - 1) / 2) * c.n_kv_heads), 32,
-                             MANY_KEYS * MANY_MIN, (double)keys * 2.0 / MANY_KEYS, true);
+                             MANY_KEYS * MANY_MIN, (double)keys * 2.0 / MANY_KEYS, true, all);
+    // Where only the few-row kernel makes parts, and its sequences can have
+    // fewer rows than there are in all, only those rows have room for them and
+    // are joined (a chunk of 2048 tokens beside one decoded token, 8 x 4 heads of
+    // 128, e2m1: 2 MB instead of 136 MB).
+    const bool only_few = p.many && p.many_split == 1 && few_rows < all;
+    if (p.few)
+        p.few_split = split((double)(p.few_slots * c.n_kv_heads), 64, FEW_KEYS * FEW_MIN, (double)(keys * key_bytes) / 20e3, false,
+                            only_few ? few_rows : all);
+    const int parts = std::max(p.few_split, p.many_split);
+    p.per_seq_head = parts > 1 && only_few ? (int)p.few_most : 0;
+    p.part_rows = parts == 1 ? 0 : only_few ? few_rows : all;
+    // one wave walks a few parts as fast as four do, and four rows share its workgroup
+    p.join_waves = parts > 8 ? 4 : 1;
+    // rows, and the threads of a launch, are counted in 32 bits
+    p.fits = all <= INT32_MAX && ceil_div(p.part_rows * p.join_waves, 4) * 256 <= MAX_THREADS &&
+             p.few_slots * c.n_kv_heads * p.few_split * 64 * FEW_WAVES <= MAX_THREADS &&
+             p.many_slots * c.n_kv_heads * p.many_split * 256 <= MAX_THREADS;
     return p;
 }
 
@@ -1031,16 +1056,11 @@ void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) 
         case GPTQ_MX_FP8: launch<GPTQ_MX_FP8, BF, D>(a, p, s); break;
         default: launch<GPTQ_MX_NONE, BF, D>(a, p, s); break;
     }
-    if (p.few_split > 1 || p.many_split > 1) {
-        JoinArgs j{a, p.few_max, p.few_split, p.many_split, 0};
-        // only the few-row kernel made parts, and its sequences have fewer rows than there are in all
-        if (p.many && p.many_split == 1 && (int64_t)a.n_seq * a.n_kv * p.few_most < a.n_rows) j.rows_per_seq = (int)p.few_most;
-        const int64_t rows = j.rows_per_seq ? (int64_t)a.n_seq * a.n_kv * p.few_most : a.n_rows;
-        // one wave walks a few parts as fast as four do, and four rows share its workgroup
-        if (std::max(p.few_split, p.many_split) > 8)
-            hipLaunchKernelGGL((cache_join_kernel<BF, D, 4>), dim3((unsigned)rows), dim3(256), 0, s, j);
-        else
-            hipLaunchKernelGGL((cache_join_kernel<BF, D, 1>), dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, s, j);
+    if (p.part_rows) {
+        const JoinArgs j{a, p.few_max, p.few_split, p.many_split};
+        const dim3 grid((unsigned)ceil_div(p.part_rows * p.join_waves, 4));
+        if (p.join_waves == 4) hipLaunchKernelGGL((cache_join_kernel<BF, D, 4>), grid, dim3(256), 0, s, j);
+        else hipLaunchKernelGGL((cache_join_kernel<BF, D, 1>), grid, dim3(256), 0, s, j);
     }
 }
 
@@ -1048,14 +1068,22 @@ void launch_format(AttnArgs& a, const Plan& p, gptq_mx_format f, hipStream_t s) 
 
 size_t cache_attention_ws(const gptq_kv_cache& c, const AttentionShape& s) {
     const Plan p = plan_of(c, s);
-    const int parts = std::max(p.few_split, p.many_split);
-    return parts > 1 ? (size_t)parts * (size_t)(s.n_tok * s.n_heads) * (size_t)(p.D + 2) * sizeof(float) : 0;
+    return (size_t)std::max(p.few_split, p.many_split) * (size_t)p.part_rows * (size_t)(p.D + 2) * sizeof(float);
+}
+
+gptq_status cache_attention_plan(const gptq_kv_cache& c, const AttentionShape& s, int64_t* plan) {
+    const Plan p = plan_of(c, s);
+    plan[0] = p.few ? p.few_split : 0;
+    plan[1] = p.many ? p.many_split : 0;
+    plan[2] = p.part_rows;
+    return p.fits ? GPTQ_OK : GPTQ_ERR_UNSUPPORTED;
 }
 
 gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape& s, const void* Q, gptq_dtype dt,
                                    int64_t ld_q, const int32_t* q_start, const int32_t* kv_len, const int32_t* table,
                                    float scale, void* O, int64_t ld_o, void* ws, hipStream_t stream) {
     const Plan p = plan_of(c, s);
+    if (!p.fits) return GPTQ_ERR_UNSUPPORTED;
     AttnArgs a;
     a.K = (const uint8_t*)c.k;
     a.V = (const uint8_t*)c.v;
@@ -1083,16 +1111,12 @@ gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape&
     a.raise = RAISE / a.scale;
     a.window = (int)s.window;
     a.span = s.window ? (uint32_t)s.window : 0x80000000u;
-    a.n_rows = s.n_tok * s.n_heads;
-    const int parts = std::max(p.few_split, p.many_split);
+    a.part_rows = p.part_rows;
+    a.per_seq_head = p.per_seq_head;
     a.part_o = (float*)ws;
-    a.part_ml = parts > 1 ? a.part_o + (int64_t)parts * a.n_rows * p.D : nullptr;
+    a.part_ml = p.part_rows ? a.part_o + std::max(p.few_split, p.many_split) * p.part_rows * p.D : nullptr;
     a.n_slots = a.per_seq = a.n_split = 1;
     a.rows_min = a.rows_max = 0;
-    // rows of a sequence and the threads of a launch are counted in 32 bits
-    if (a.n_rows > INT32_MAX || (parts > 1 && a.n_rows * 256 > MAX_THREADS) || p.few_slots * a.n_kv * p.few_split * 64 * FEW_WAVES > MAX_THREADS ||
-        p.many_slots * a.n_kv * p.many_split * 256 > MAX_THREADS)
-        return GPTQ_ERR_UNSUPPORTED;
     const bool bf = dt == GPTQ_BF16;
     if (p.D == 64) {
         if (bf) launch_format<true, 64>(a, p, c.format, stream);

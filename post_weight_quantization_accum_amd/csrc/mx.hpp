@@ -333,6 +333,7 @@ struct AttentionShape {
     int64_t n_tok, n_heads, n_seq, max_pages, max_q, window;
 };
 size_t cache_attention_ws(const gptq_kv_cache& c, const AttentionShape& a);
+gptq_status cache_attention_plan(const gptq_kv_cache& c, const AttentionShape& a, int64_t* plan);
 gptq_status cache_attention_launch(const gptq_kv_cache& c, const AttentionShape& a, const void* Q, gptq_dtype dt,
                                    int64_t ld_q, const int32_t* q_start, const int32_t* kv_len, const int32_t* table,
                                    float scale, void* O, int64_t ld_o, void* ws, hipStream_t s);

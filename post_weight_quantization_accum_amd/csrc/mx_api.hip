@@ -123,6 +123,16 @@ size_t gptq_cache_attention_workspace(const gptq_kv_cache* cache, int64_t n_tok,
     return cache_attention_ws(*cache, AttentionShape{n_tok, n_heads, n_seq, max_pages, max_q, window});
 }
 
+gptq_status gptq_cache_attention_plan(const gptq_kv_cache* cache, int64_t n_tok, int64_t n_heads, int64_t n_seq,
+                                      int64_t max_pages, int64_t max_q, int64_t window, int64_t* plan) {
+    const gptq_status st = check_cache(cache);
+    if (st != GPTQ_OK) return st;
+    if (!plan || !check_shape(cache, n_tok, n_heads, n_seq, max_pages, max_q, window)) return GPTQ_ERR_INVALID_ARG;
+    plan[0] = plan[1] = plan[2] = 0;
+    if (n_tok == 0 || n_seq == 0) return GPTQ_OK;
+    return cache_attention_plan(*cache, AttentionShape{n_tok, n_heads, n_seq, max_pages, max_q, window}, plan);
+}
+
 gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq_dtype q_dtype, int64_t n_tok,
                                  int64_t n_heads, int64_t ld_q, const int32_t* q_start, const int32_t* kv_len,
                                  const int32_t* table, int64_t max_pages, int64_t n_seq, int64_t max_q,
