@@ -38,6 +38,7 @@ import dataclasses
 from . import (cache_attention, cache_write, dequant_matmul, factored_supported, gather_columns, hessian_accumulate,
                load, new_cache, pack, pack_permuted, prepare_hinv, prepare_hinv_factored, quantize_layer,
                quantize_layer_factored)
+from .kv_cache import FORMATS
 
 LAYERS = ("q", "k", "v", "out", "fc1", "fc2")
 
@@ -146,8 +147,12 @@ def _attention_shape(block: Block, X, attention: Attention):
         raise ValueError("head_dim must be 32, 64, 96 or 128")
     if block.k.shape[0] != kv_heads * d or block.v.shape[0] != kv_heads * d:
         raise ValueError("k and v must have kv_heads * head_dim rows")
-    if attention.page_size < 1 or attention.window < 0:
-        raise ValueError("attention.page_size must be positive and attention.window not negative")
+    if attention.page_size < 1 or not 0 <= attention.window <= 1 << 30:
+        raise ValueError("attention.page_size must be positive and attention.window within 0 .. 2^30")
+    if attention.fmt not in FORMATS:
+        raise ValueError(f"attention.fmt must be one of {', '.join(FORMATS)}")
+    if X.dtype not in (_torch().float16, _torch().bfloat16):
+        raise ValueError("attention takes tokens of float16 or bfloat16")
     return lengths, kv_heads, d
 
 

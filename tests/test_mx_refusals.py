@@ -44,3 +44,14 @@ def test_parts_beside_a_chunk_need_room_for_few_rows_only(f, most):
     c = _c(f=f, dt=_lib.BF16, n_pages=1 << 16, page_size=64, n_kv=8, d=32)
     st, (few, many, rows), ws = _plan(c, n=1 << 20, h=32, ns=2, mp=1 << 14, mq=(1 << 20) - 1)
     assert st == _lib.OK and few > 1 and many == 1 and rows == 2 * 8 * most
+
+
+def test_sequential_attention_refused_before_any_work():
+    """A format, type or window that the cache or its attention would refuse after q, k and v are quantized."""
+    from post_weight_quantization_accum_amd import sequential as S
+    w = lambda r: torch.zeros(r, 256)
+    block = S.Block(w(256), w(128), w(128), w(256), w(512), torch.zeros(256, 512))
+    for X, kw in ((torch.bfloat16, dict(fmt="int8")), (torch.bfloat16, dict(fmt=None)), (torch.float32, {}),
+                  (torch.float32, dict(fmt="fp8")), (torch.float16, dict(window=(1 << 30) + 1))):
+        with pytest.raises(ValueError, match="fmt|float16|window"):
+            S.quantize_block(block, torch.zeros(10, 256, dtype=X), None, attention=S.Attention(4, 2, **kw))
