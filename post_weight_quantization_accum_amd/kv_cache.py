@@ -192,6 +192,8 @@ def cache_attention(Q, cache: KVCache, q_start, kv_len, table, *, max_q: int | N
                 raise TypeError("out must match Q in tokens and dtype")
         if workspace is not None:
             _gpu(Q, workspace)
+            if not workspace.is_contiguous():
+                raise TypeError("workspace must be contiguous")
             nws = workspace.numel() * workspace.element_size()
         elif nws:
             workspace = Q.new_empty(nws, dtype=torch.uint8)

@@ -56,3 +56,18 @@ def test_a_chunk_beside_decoded_tokens_in_parts(fmt, dtype, long):
         check_tokens(out, Q, p, q, scale, [[0, n // 2, n - 2, n - 1] if n > 1 else [0] for n in q])
         again, _, _ = attend(p, q, 32, max_q=2048, Q=Q)
         assert torch.equal(out, again)
+
+
+def test_workspace_that_is_not_as_large_as_it_says():
+    """A tensor that repeats its elements has fewer bytes than its shape tells."""
+    p = Paged(1, [20], 2, 64, 16, "fp8", "bf16").write()
+    start, kv, table = p.tensors([1])
+    table = table.repeat(1, 3000).contiguous()
+    Q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    need = P.load().gptq_cache_attention_workspace(_cache(p.cache)[0], 1, 4, 1, table.shape[1], 1, 0)
+    assert need > 0
+    for bad in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need), torch.zeros(2, need, dtype=torch.uint8, device="cuda")[:, ::2]):
+        with pytest.raises(TypeError):
+            P.cache_attention(Q, p.cache, start, kv, table, max_q=1, workspace=bad)
+    good = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(P.cache_attention(Q, p.cache, start, kv, table, max_q=1, workspace=good), P.cache_attention(Q, p.cache, start, kv, table, max_q=1))
