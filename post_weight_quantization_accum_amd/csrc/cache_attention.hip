@@ -135,7 +135,8 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int slot, int rt, T
     const int s = __builtin_amdgcn_readfirstlane(last_at_most(a.n_seq, slot, [&](int i) { return first_slot(a, i, rt); }));
     if (s < 0) return false;
     const int k = __builtin_amdgcn_readfirstlane(slot - first_slot(a, s, rt));
-    if (!sequence(a, s, t) || (int64_t)k * rt >= t.rows) return false;
+    // (k < 0 only where q_start does not ascend: such a tile has no rows)
+    if (k < 0 || !sequence(a, s, t) || (int64_t)k * rt >= t.rows) return false;
     t.row0 = k * rt;
     tile_keys(a, t, rt);
     return true;

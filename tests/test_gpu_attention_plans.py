@@ -71,3 +71,19 @@ def test_workspace_that_is_not_as_large_as_it_says():
             P.cache_attention(Q, p.cache, start, kv, table, max_q=1, workspace=bad)
     good = torch.zeros(need, dtype=torch.uint8, device="cuda")
     assert torch.equal(P.cache_attention(Q, p.cache, start, kv, table, max_q=1, workspace=good), P.cache_attention(Q, p.cache, start, kv, table, max_q=1))
+
+
+@pytest.mark.parametrize("starts", [[0, 200, 50, 250], [250, 0, 240, 10], [0, 150, 0, 0], [-5, 300, 100, 1 << 30]])
+def test_starts_that_do_not_ascend_touch_nothing_else(starts):
+    """Tiles are found by searching the starts: whatever is found, rows stay within the call's tokens."""
+    p = Paged(4, [300, 280, 260], 2, 64, 16, "fp8", "bf16").write()
+    n, heads = 250, 8
+    room = torch.full((n + 40, heads, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    Q = torch.randn(n, heads, 64, device="cuda").to(torch.bfloat16)
+    start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    _, kv, table = p.tensors([1, 1, 1])
+    for wide in (table, torch.cat((table, torch.full((3, 900), -1, dtype=torch.int32, device="cuda")), 1).contiguous()):
+        for max_q in (1, 200):
+            P.cache_attention(Q, p.cache, start, kv, wide, max_q=max_q, out=room[20: 20 + n])
+            torch.cuda.synchronize()
+            assert (room[:20] == 9.0).all() and (room[20 + n:] == 9.0).all()
