@@ -424,6 +424,15 @@ gptq_status gptq_mx_matmul_quantized(const uint8_t* x_codes, const uint8_t* x_sc
                                      int64_t n_tok, int64_t d_in, const uint8_t* codes, const uint8_t* scales,
                                      int64_t d_out, float* Y, int64_t ld_y, hipStream_t stream);
 
+/* Which kernel a product of these sizes takes, for profiles and tests:
+ * activations of x_dtype (x_format GPTQ_MX_NONE) or microscaled ones, aligned:
+ * whether rows of X start on 16 bytes (at most 2^20 values apart).  0 .. 6: a
+ * tile of 16, 32, 48, 64 rows x 16 tokens, 32 x 32, 64 x 32, 64 x 64; 7, 8:
+ * 128, 256 rows x 128 tokens; 9: the general one of 128 x 128.  -1 for sizes
+ * outside [1, 2^20] or a bad type. */
+int32_t gptq_mx_matmul_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64_t n_tok, int64_t d_in, int64_t d_out,
+                              int32_t aligned);
+
 /* ------------------------------------------------------------------------
  * A paged cache of keys and values.
  *

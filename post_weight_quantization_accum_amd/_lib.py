@@ -30,7 +30,7 @@ EXPORTS = (
     "gptq_packed_words_per_row", "gptq_pack", "gptq_pack_permuted",
     "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
     "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
-    "gptq_mx_matmul_quantized", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
+    "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
     "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_status_string", "gptq_version",
 )
 
@@ -159,6 +159,8 @@ def load(path: str | None = None):
     lib.gptq_mx_matmul.restype = ci
     lib.gptq_mx_matmul_quantized.argtypes = [vp, vp, ci, i64, i64, vp, vp, i64, vp, i64, vp]
     lib.gptq_mx_matmul_quantized.restype = ci
+    lib.gptq_mx_matmul_kernel.argtypes = [ci, ci, i64, i64, i64, ctypes.c_int32]
+    lib.gptq_mx_matmul_kernel.restype = ctypes.c_int32
     lib.gptq_cache_write.argtypes = [cachep, vp, vp, ci, i64, i64, i64, vp, vp]
     lib.gptq_cache_write.restype = ci
     lib.gptq_cache_read.argtypes = [cachep, vp, i64, i64, vp, i64, vp, vp, ci, i64, i64, vp]

@@ -303,6 +303,7 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
 gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gptq_mx_format xf, int64_t n_tok,
                                        int64_t d_in, const uint8_t* codes, const uint8_t* scales, int64_t d_out,
                                        float* Y, int64_t ld_y, hipStream_t s);
+int mx_matmul_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_in, int64_t d_out, bool aligned);
 
 // n / d for 32-bit n by a multiplication (d >= 1).
 struct FastDiv {

@@ -88,6 +88,13 @@ gptq_status gptq_mx_matmul_quantized(const uint8_t* x_codes, const uint8_t* x_sc
     return mx_matmul_quantized_launch(x_codes, x_scales, x_format, n_tok, d_in, codes, scales, d_out, Y, ld_y, stream);
 }
 
+int32_t gptq_mx_matmul_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64_t n_tok, int64_t d_in, int64_t d_out,
+                              int32_t aligned) {
+    if (x_format == GPTQ_MX_NONE ? !is_float(x_dtype) : !is_mx(x_format)) return -1;
+    if (!in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 1, MAX_DIM)) return -1;
+    return mx_matmul_kernel(x_dtype, x_format, n_tok, d_in, d_out, aligned != 0);
+}
+
 gptq_status gptq_cache_write(const gptq_kv_cache* cache, const void* K, const void* V, gptq_dtype x_dtype,
                              int64_t n_tok, int64_t ld_k, int64_t ld_v, const int64_t* slots, hipStream_t stream) {
     const gptq_status st = check_cache(cache);

@@ -973,12 +973,10 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
 template <Act DT, int RT, int TT>
 gptq_status launch_few(const MatArgs& a, hipStream_t s) {
     using T = FewTile<DT, RT, TT>;
-    if constexpr (T::FITS) {
-        GPTQ_HIP(ensure_lds_limit((const void*)mx_few_kernel<DT, RT, TT>, T::BYTES));
-        hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
-                           dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
-                           dim3(64 * T::WAVES), T::BYTES, s, a);
-    }
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_few_kernel<DT, RT, TT>, T::BYTES));
+    hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
+                       dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
+                       dim3(64 * T::WAVES), T::BYTES, s, a);
     return GPTQ_OK;
 }
 
@@ -1023,20 +1021,17 @@ double rounds(const MatArgs& a, int64_t r, int64_t t) {
 // example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256
 // tokens (4,2) 20, 128 x 128 26; 2048 tokens 256 x 128 63, 128 x 128 72.  One
 // token 4096 -> 11008: (3,1) 8.5, (4,1) 9.9, (2,1) 11.3, (1,1) 13.0.
-template <Act DT>
-gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
-    constexpr double us[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // float32
+constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // float32
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // float16
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // bfloat16
                                  {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
                                  {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 13.3}};    // e2m1
-    static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
-    static_assert((us[DT][0] > 0) == FewTile<DT, 1, 1>::FITS && (us[DT][1] > 0) == FewTile<DT, 2, 1>::FITS &&
-                      (us[DT][2] > 0) == FewTile<DT, 3, 1>::FITS && (us[DT][3] > 0) == FewTile<DT, 4, 1>::FITS &&
-                      (us[DT][4] > 0) == FewTile<DT, 2, 2>::FITS && (us[DT][5] > 0) == FewTile<DT, 4, 2>::FITS &&
-                      (us[DT][6] > 0) == FewTile<DT, 4, 4>::FITS,
-                  "zeros where a tile does not fit");
-    constexpr int rt[7] = {1, 2, 3, 4, 2, 4, 4}, tt[7] = {1, 1, 1, 1, 2, 2, 4};
+static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
+constexpr int FEW_RT[7] = {1, 2, 3, 4, 2, 4, 4}, FEW_TT[7] = {1, 1, 1, 1, 2, 2, 4};
+
+// 0 .. 6: a few-token tile; 7, 8: 128 (256) x 128 from LDS rings; 9: 128 x 128 through registers.
+template <Act DT>
+int choose(const MatArgs& a) {
     int best = 0;
     double least = 1e30;
     const auto offer = [&](int id, double cost) {
@@ -1046,7 +1041,7 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
         }
     };
     for (int i = 0; i < 7; ++i)
-        if (us[DT][i] > 0) offer(i, rounds(a, 16 * rt[i], 16 * tt[i]) * us[DT][i]);
+        if (FEW_US[DT][i] > 0) offer(i, rounds(a, 16 * FEW_RT[i], 16 * FEW_TT[i]) * FEW_US[DT][i]);
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
         if (a.full > 0) {
             offer(7, rounds(a, 128, MT) * 25.0);
@@ -1062,14 +1057,27 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
         offer(7, rounds(a, 128, MT) * 13.0);
         offer(8, rounds(a, 256, MT) * 25.0);
     }
+    return best;
+}
+
+template <Act DT, int I>
+gptq_status launch_tile(const MatArgs& a, hipStream_t s) {
+    static_assert((FEW_US[DT][I] > 0) == FewTile<DT, FEW_RT[I], FEW_TT[I]>::FITS, "zeros where a tile does not fit");
+    if constexpr (FEW_US[DT][I] > 0) return launch_few<DT, FEW_RT[I], FEW_TT[I]>(a, s);
+    else return GPTQ_ERR_UNSUPPORTED;      // never chosen
+}
+
+template <Act DT>
+gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
+    const int best = choose<DT>(a);
     switch (best) {
-        case 0: return launch_few<DT, 1, 1>(a, s);
-        case 1: return launch_few<DT, 2, 1>(a, s);
-        case 2: return launch_few<DT, 3, 1>(a, s);
-        case 3: return launch_few<DT, 4, 1>(a, s);
-        case 4: return launch_few<DT, 2, 2>(a, s);
-        case 5: return launch_few<DT, 4, 2>(a, s);
-        case 6: return launch_few<DT, 4, 4>(a, s);
+        case 0: return launch_tile<DT, 0>(a, s);
+        case 1: return launch_tile<DT, 1>(a, s);
+        case 2: return launch_tile<DT, 2>(a, s);
+        case 3: return launch_tile<DT, 3>(a, s);
+        case 4: return launch_tile<DT, 4>(a, s);
+        case 5: return launch_tile<DT, 5>(a, s);
+        case 6: return launch_tile<DT, 6>(a, s);
         default: break;
     }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
@@ -1103,7 +1111,21 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
     return a;
 }
 
+// Steps of 16-bit or float32 activations that are read in whole pieces: offsets
+// within a tile's tokens stay below 2^30.
+int whole_steps(bool aligned, int64_t d_in, int64_t ld_x) {
+    return aligned && ld_x <= (int64_t(1) << 20) ? (int)(d_in / MX_PAD) : 0;
+}
+
 }  // namespace
+
+int mx_matmul_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_in, int64_t d_out, bool aligned) {
+    MatArgs a = mat_args(nullptr, nullptr, n_tok, d_in, d_out, nullptr, d_out);
+    if (xf == GPTQ_MX_FP8) return choose<ACT_FP8>(a);
+    if (xf == GPTQ_MX_FP4) return choose<ACT_FP4>(a);
+    a.full = whole_steps(aligned, d_in, d_in);
+    return dt == GPTQ_BF16 ? choose<ACT_BF16>(a) : dt == GPTQ_F16 ? choose<ACT_F16>(a) : choose<ACT_F32>(a);
+}
 
 gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t ld_x,
                              const uint8_t* codes, const uint8_t* scales, int64_t d_out, float* Y, int64_t ld_y,
@@ -1113,8 +1135,7 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
     a.ld_x = ld_x;
     if (n_tok == 1) ld_x = a.ld_x = ceil_div(d_in, 8) * 8;   // of no use
     a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
-    // offsets within a tile's tokens stay below 2^30
-    a.full = a.aligned && ld_x <= (int64_t(1) << 20) ? (int)(d_in / MX_PAD) : 0;
+    a.full = whole_steps(a.aligned, d_in, ld_x);
     gptq_status st;
     switch (dt) {
         case GPTQ_BF16: st = launch_parts<ACT_BF16>(a, s); break;
