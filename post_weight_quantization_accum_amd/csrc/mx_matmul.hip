@@ -60,7 +60,7 @@ template <Act DT>
 constexpr int pieces_of() { return DT == ACT_F32 ? 8 : DT == ACT_FP8 ? 2 : DT == ACT_FP4 ? 1 : 4; }
 
 // Some consecutive activations of a token as they are in memory: N groups of
-// eight (N = 4, a block, for the microscaled kinds).
+// eight (N = 4, a block, for e2m1).
 template <Act DT, int N = 4>
 struct Raw {
     static constexpr int W = DT == ACT_F32 ? 2 * N : DT == ACT_FP8 ? (N + 1) / 2 : DT == ACT_FP4 ? 1 : N;
@@ -71,9 +71,8 @@ struct Raw {
     template <bool WHOLE>
     __device__ __forceinline__ void load(const MatArgs& a, int64_t t, int64_t k) {
         if constexpr (DT == ACT_FP4) {
-            const uint8_t* p = (const uint8_t*)a.X + t * a.ld_x + (k >> 1);
-            if constexpr (N == 4) w[0] = *(const u32x4_t*)p;
-            else w[0].x = *(const uint32_t*)p;
+            static_assert(N == 4, "whole blocks");
+            w[0] = *(const u32x4_t*)((const uint8_t*)a.X + t * a.ld_x + (k >> 1));
             s = a.XS[t * a.s_row + (k >> 5)];
         } else if constexpr (DT == ACT_FP8) {
             const uint8_t* p = (const uint8_t*)a.X + t * a.ld_x + k;
@@ -1015,17 +1014,18 @@ double rounds(const MatArgs& a, int64_t r, int64_t t) {
 // Which kernel, and which tile: the least of rounds x time per round, measured
 // in us at 4096 columns (they grow alike with the columns).  Few-token tiles of
 // 16 RT x 16 TT for (RT, TT) = (1,1) (2,1) (3,1) (4,1) (2,2) (4,2) (4,4), 0
-// where LDS does not hold two steps per wave; then the others: 16-bit 128 x 128
-// and 256 x 128 from LDS rings, and so e2m1 by e2m1; else 128 x 128 through
-// registers, where two (float32) or three workgroups share a compute unit.  For
-// example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256
+// where LDS does not hold two steps per wave, and for e2m1 (4,4), which took
+// 13.3 where 128 x 128 takes 13.0 and never has fewer workgroups; then the
+// others: 16-bit 128 x 128 and 256 x 128 from LDS rings, and so e2m1 by e2m1;
+// else 128 x 128 through registers, where two (float32) or three workgroups
+// share a compute unit.  For example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256
 // tokens (4,2) 20, 128 x 128 26; 2048 tokens 256 x 128 63, 128 x 128 72.  One
 // token 4096 -> 11008: (3,1) 8.5, (4,1) 9.9, (2,1) 11.3, (1,1) 13.0.
 constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // float32
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // float16
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // bfloat16
                                  {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
-                                 {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 13.3}};    // e2m1
+                                 {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 0}};      // e2m1
 static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
 constexpr int FEW_RT[7] = {1, 2, 3, 4, 2, 4, 4}, FEW_TT[7] = {1, 1, 1, 1, 2, 2, 4};
 
@@ -1062,7 +1062,8 @@ int choose(const MatArgs& a) {
 
 template <Act DT, int I>
 gptq_status launch_tile(const MatArgs& a, hipStream_t s) {
-    static_assert((FEW_US[DT][I] > 0) == FewTile<DT, FEW_RT[I], FEW_TT[I]>::FITS, "zeros where a tile does not fit");
+    static_assert((FEW_US[DT][I] > 0) == (FewTile<DT, FEW_RT[I], FEW_TT[I]>::FITS && !(DT == ACT_FP4 && I == 6)),
+                  "zeros where a tile does not fit, or is never the best");
     if constexpr (FEW_US[DT][I] > 0) return launch_few<DT, FEW_RT[I], FEW_TT[I]>(a, s);
     else return GPTQ_ERR_UNSUPPORTED;      // never chosen
 }
