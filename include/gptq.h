@@ -400,10 +400,14 @@ gptq_status gptq_mx_dequantize(const uint8_t* codes, const uint8_t* scales, gptq
 /* Y[t][r] = sum_{k < d_in} X[t][k] w[r][k], w the d_out x d_in e2m1 values of
  * (codes, scales).  X: n_tok x d_in of x_dtype, row stride ld_x; Y: float32,
  * n_tok x d_out, row stride ld_y, overwritten.  The weights enter the
- * matrix cores as bfloat16, which holds every one of them exactly; float32
- * activations enter as three bfloat16 parts that sum to them, float16 ones as
- * they are by float16 weights where the scales (2^-23 .. 2^13) allow it and as
- * two bfloat16 parts elsewhere.  So no product is rounded; sums are float32.
+ * matrix cores as bfloat16, which holds every one of them exactly (of scale
+ * bytes up to 252, the largest that gptq_mx_quantize writes: by 253 and 254
+ * the largest elements pass float32's range, and may count as infinite);
+ * float32 activations enter as three bfloat16 parts that sum to them, float16
+ * ones as they are by float16 weights where the scales (2^-23 .. 2^13) allow
+ * it and as two bfloat16 parts elsewhere.  So no product is rounded; sums are
+ * float32.  The exception are float32 activations below 2^-110, whose last
+ * part passes bfloat16's smallest step: each is off by less than 2^-133.
  * An infinity or NaN in X reaches its token's outputs as in float32
  * arithmetic, and no other's.  Which kernel runs, and so the order of a sum,
  * depends on the sizes, the type and X's alignment; the same call gives the
@@ -417,8 +421,10 @@ gptq_status gptq_mx_matmul(const void* X, gptq_dtype x_dtype, int64_t n_tok, int
 
 /* The same product with activations that are microscaled too (x_codes,
  * x_scales: n_tok x d_in as gptq_mx_quantize writes them, x_format e2m1 or
- * e4m3): e2m1 on the block-scaled matrix instructions, e4m3 as bfloat16
- * (which holds every value).  Errors as above, and GPTQ_ERR_INVALID_ARG for
+ * e4m3): e2m1 on the block-scaled matrix instructions or, for few tokens, as
+ * bfloat16; e4m3 as bfloat16, which holds every value (of scale bytes from 3
+ * on: the smallest elements of blocks below are rounded to its smallest step,
+ * and off by at most 2^-134).  Errors as above, and GPTQ_ERR_INVALID_ARG for
  * x_format GPTQ_MX_NONE. */
 gptq_status gptq_mx_matmul_quantized(const uint8_t* x_codes, const uint8_t* x_scales, gptq_mx_format x_format,
                                      int64_t n_tok, int64_t d_in, const uint8_t* codes, const uint8_t* scales,

@@ -27,8 +27,9 @@ __host__ __device__ __forceinline__ int64_t mx_scale_bytes(int64_t n_cols) {
 
 // Scale byte as the float operand of the conversion instructions, which take
 // its exponent field: byte 0 stands for 2^-127 although the float is 0, and
-// byte 255 makes every converted value NaN (both checked over all bytes and
-// codes by the tests).
+// byte 255 makes every converted value NaN.  (The tests check all codes and
+// all bytes in float32, and all up to the largest that the quantiser writes in
+// bfloat16 and float16.)
 __device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // One 16-bit type of activations and of the matrix cores.
@@ -305,7 +306,8 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
                                        float* Y, int64_t ld_y, hipStream_t s);
 int mx_matmul_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_in, int64_t d_out, bool aligned);
 
-// n / d for 32-bit n by a multiplication (d >= 1).
+// n / d for 32-bit n by a multiplication (d >= 1): division by invariant
+// integers after Granlund and Montgomery (1994).
 struct FastDiv {
     uint32_t d, mul, s1, s2;
 };

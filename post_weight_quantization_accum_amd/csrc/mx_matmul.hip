@@ -30,8 +30,9 @@ struct MatArgs {
 // ---------------------------------------------------------------------------
 // Activations as bfloat16 parts.  A float32 is the sum of three bfloat16 cut
 // off its top (8 + 8 + 8 of its 24 bits), a float16 of two: no rounding, and
-// no overflow.  The parts below an infinity or NaN are 0.  A microscaled value
-// is a bfloat16 as it is.  (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3
+// no overflow, down to bfloat16's smallest step, 2^-133 (float32 values below
+// 2^-110 lose what is under it).  The parts below an infinity or NaN are 0.  A
+// microscaled value is a bfloat16 as it is (e4m3 from scale byte 3 on).  (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3
 // codes directly, at twice the rate, but with an e4m3 operand it cuts products
 // off some 16 bits below the largest one of an instruction: an error of 1e-5
 // of sum |x w| and more, measured, where these sums keep 1e-7.)
@@ -54,10 +55,6 @@ __device__ __forceinline__ u32x4_t codes_if(bool keep, u32x4_t w) {
 }
 // codes that are not all zero
 __device__ __forceinline__ bool some(u32x4_t w) { return (w.x | w.y | w.z | w.w) != 0u; }
-
-// 16-byte pieces of 32 activations (one block of a token)
-template <Act DT>
-constexpr int pieces_of() { return DT == ACT_F32 ? 8 : DT == ACT_FP8 ? 2 : DT == ACT_FP4 ? 1 : 4; }
 
 // Some consecutive activations of a token as they are in memory: N groups of
 // eight (N = 4, a block, for e2m1).
