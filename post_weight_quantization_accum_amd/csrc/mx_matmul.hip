@@ -1023,6 +1023,13 @@ constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // fl
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // bfloat16
                                  {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
                                  {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 0}};      // e2m1
+// Where X's rows do not start on 16 bytes (or have no 128 columns), every step
+// is read by single elements, without the ring: one round of the tiles in the
+// same order, float32 and 16 bits (float32 (1,1): 29 for 13 tokens, 48 for 16).
+// Times of the general kernel there: float32 226 a round, 16 bits 250 for one
+// and 305 for two rounds.  64 tokens 4096 -> 4096 bf16: (4,1) 27 us, (2,2) 46,
+// which the ring's times would choose.
+constexpr double DIRECT_US[2][7] = {{40, 41, 43, 44, 81, 0, 0}, {21, 24, 26, 28, 52, 57, 0}};
 static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
 constexpr int FEW_RT[7] = {1, 2, 3, 4, 2, 4, 4}, FEW_TT[7] = {1, 1, 1, 1, 2, 2, 4};
 
@@ -1037,17 +1044,18 @@ int choose(const MatArgs& a) {
             best = id;
         }
     };
+    const double* us = a.full > 0 ? FEW_US[DT] : DIRECT_US[DT != ACT_F32];
     for (int i = 0; i < 7; ++i)
-        if (FEW_US[DT][i] > 0) offer(i, rounds(a, 16 * FEW_RT[i], 16 * FEW_TT[i]) * FEW_US[DT][i]);
+        if (us[i] > 0) offer(i, rounds(a, 16 * FEW_RT[i], 16 * FEW_TT[i]) * us[i]);
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
         if (a.full > 0) {
             offer(7, rounds(a, 128, MT) * 25.0);
             offer(8, rounds(a, 256, MT) * 43.0);
         } else {
-            offer(9, std::max(1.0, 0.8 * rounds(a, 128, MT)) * 75.0);
+            offer(9, std::max(1.0, 0.61 * rounds(a, 128, MT)) * 250.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(9, rounds(a, 128, MT) * 130.0);
+        offer(9, rounds(a, 128, MT) * (a.full > 0 ? 130.0 : 226.0));
     } else if constexpr (DT == ACT_FP8) {
         offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
     } else {

@@ -17,9 +17,9 @@ TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 # kernel -> (tokens, outputs); columns: 328 where rows are to start on 16 bytes, else 329
 FEW = {0: (3, 100), 1: (2, 4200), 2: (7, 8300), 3: (16, 12400)}
 HALF = {**FEW, 4: (30, 6300), 5: (25, 8300)}
-SIZES = {("f32", 1): {**FEW, 4: (96, 2700), 9: (1500, 2048)}, ("f32", 0): {**FEW, 4: (96, 2700), 9: (1500, 2048)},
+SIZES = {("f32", 1): {**FEW, 4: (96, 2700), 9: (1500, 2048)}, ("f32", 0): {**FEW, 4: (4100, 20), 9: (1500, 2048)},
          ("f16", 1): {**HALF, 7: (140, 8300), 8: (260, 16500)}, ("bf16", 1): {**HALF, 7: (140, 8300), 8: (260, 16500)},
-         ("f16", 0): {**HALF, 9: (2048, 2048)}, ("bf16", 0): {**HALF, 9: (2048, 2048)},
+         ("f16", 0): {**FEW, 9: (2048, 2048)}, ("bf16", 0): {**FEW, 9: (2048, 2048)},
          ("fp8", 1): {**HALF, 6: (60, 11000), 9: (4096, 2048)},
          ("fp4", 1): {**HALF, 7: (140, 8300), 8: (100, 33000)}}
 CASES = [(kind, aligned, k) for (kind, aligned), sizes in SIZES.items() for k in sizes]
