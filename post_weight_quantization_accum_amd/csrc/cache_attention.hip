@@ -31,12 +31,14 @@ namespace {
 constexpr int FEW_ROWS = 16, MANY_ROWS = 128;
 constexpr int FEW_WAVES = 8;                      // of a few-row workgroup, each with steps of its own
 // Sequences of at most this many rows go to the few-row kernel, which reads the
-// cache once per 16 rows: the fewer bytes a key has, the longer that pays (8
-// kv heads of 128 channels, pages of 16; few-row / many-row kernel, us: 32 x
-// 4096 e2m1 16 rows 30 / 113, 64 rows 86 / 123, 128 rows 130 / 130; 8 x 4096
-// 16 bits 16 rows 30 / 33, 32 rows 42 / 32, 64 rows 66 / 36; 1 x 32768 16 bits
-// 32 rows 45 / 46, 64 rows 71 / 48).
-constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == GPTQ_MX_FP8 ? 48 : 32; }
+// cache once per 16 rows: the fewer bytes a key has, the longer that pays.
+// Measured (8 kv heads of 128 channels, pages of 16; few-row / many-row kernel,
+// us, for 8 x 4096, 1 x 32768 and 32 x 4096 positions; the limit is where the
+// product of the three ratios passes 1):
+//   16 bits 16 rows 35 / 35, 35 / 46, 103 / 123; 32 rows 44 / 36, 44 / 47, 142 / 133
+//   e4m3    32 rows 31 / 34, 31 / 47,  87 / 114; 48 rows 42 / 38, 40 / 48, 126 / 96
+//   e2m1    64 rows 28 / 38, 30 / 43, 106 /  91; 96 rows 52 / 43, 42 / 45, 156 / 123
+constexpr int few_most(gptq_mx_format f) { return f == GPTQ_MX_FP4 ? 64 : f == GPTQ_MX_FP8 ? 32 : 16; }
 constexpr int FEW_KEYS = 64, MANY_KEYS = 64;      // keys per step
 constexpr int FEW_MIN = 4, MANY_MIN = 8;          // least steps per part
 // Positions from here on count as past the table: keys are fetched up to two

@@ -87,3 +87,16 @@ def test_starts_that_do_not_ascend_touch_nothing_else(starts):
             P.cache_attention(Q, p.cache, start, kv, wide, max_q=max_q, out=room[20: 20 + n])
             torch.cuda.synchronize()
             assert (room[:20] == 9.0).all() and (room[20 + n:] == 9.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp8", "fp4"])
+@pytest.mark.parametrize("q", [4, 5, 8, 9, 16, 17])
+def test_rows_at_each_limit(q, fmt):
+    """16, 32 and 64 rows and a token more: the last of the few-row kernel and the first of the other, whole and in parts."""
+    for kv in ([q + 3, 70, q], [2500, 40, q]):
+        p = Paged(q, kv, 1, 64, 16, fmt, "f16", garbage=True).write()
+        qs = [q, 3, q]
+        few, many, _ = plan(p, qs, 4, q)
+        assert (many > 0) == (4 * q > {"16bit": 16, "fp8": 32, "fp4": 64}[fmt])
+        out, Q, scale = attend(p, qs, 4, max_q=q)
+        check_tokens(out, Q, p, qs, scale, [range(n) for n in qs])

@@ -33,7 +33,7 @@ def test_plan_of_attention():
     assert st == _lib.OK and few > 1 and many == 0 and rows == 4 * 8 and ws == few * rows * (64 + 2) * 4
 
 
-@pytest.mark.parametrize("f,most", [(_lib.MX_NONE, 32), (_lib.MX_FP8, 48), (_lib.MX_FP4, 64)])
+@pytest.mark.parametrize("f,most", [(_lib.MX_NONE, 16), (_lib.MX_FP8, 32), (_lib.MX_FP4, 64)])
 def test_parts_beside_a_chunk_need_room_for_few_rows_only(f, most):
     """A decoded token in parts beside a chunk that is whole: the workspace holds what sequences of few rows can have."""
     c = _c(f=f, dt=_lib.BF16, n_pages=2048, page_size=64, n_kv=8, d=128)
