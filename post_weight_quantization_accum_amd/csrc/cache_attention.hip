@@ -394,7 +394,7 @@ __device__ __forceinline__ void patch(const AttnArgs& a, const Tile& t, int head
 // V passes through the wave's own LDS to be transposed, half a step at a time,
 // so that the waves never wait for each other before the join at the end.
 // Bound by the cache's bytes: 32 sequences of up to 4096 e2m1 positions, 8 kv
-// heads of 128 with 4 heads each, 26.6 us (90 MB, 3.4 TB/s: the longest of the
+// heads of 128 with 4 heads each, 27.3 us (90 MB, 3.3 TB/s: the longest of the
 // 256 workgroups has 1.5 times the mean); with 16 bits 85 us (4.0 TB/s); one
 // sequence of 65536 e4m3 positions 31 us in 32 parts (4.5 TB/s) and 4.5 us for
 // their join.  Steps of 32 keys on four waves took 43 and 77 us.
@@ -648,11 +648,14 @@ __global__ __launch_bounds__(64 * FEW_WAVES, (few_waves<F, D>())) void cache_few
 // that all of them share, in two LDS buffers (the next tile's keys and values
 // arrive in registers while this one is worked on, and are converted once for
 // 128 rows).  Bound by the matrix instructions and the weights' arithmetic,
-// which take about as long each and overlap only between the two waves of a
-// SIMD: 2048 tokens over 16384 16-bit positions, 8 kv heads of 128 with 4 heads
-// each, 562 to 580 us by card (890 to 917 TFLOP/s); e2m1 538 us.  Keys fetched two tiles ahead (no
-// faster), and softmax of one half of a tile beside the products of the other
-// (765 us: its registers spill), were tried and not kept.
+// which overlap only between the two waves of a SIMD: the matrix cores are busy
+// for 40 % of the time, LDS for 33 %, and the waves wait for 47 % of it.  2048
+// tokens over 16384 16-bit positions, 8 kv heads of 128 with 4 heads each, 560
+// to 610 us by card (845 to 920 TFLOP/s); e2m1 539 to 570.  Keys fetched two
+// tiles ahead (no faster), and softmax of one half of a tile beside the
+// products of the other (765 us: its registers spill), were tried and not kept.
+// Head sizes below D run in its tiles: 32 takes as long as 64 (384 and 375 us),
+// 96 as long as 128 (587 and 597), and every step of theirs mends its chunks.
 // ---------------------------------------------------------------------------
 template <gptq_mx_format F, bool BF, int D>
 __global__ __launch_bounds__(256, 2) void cache_many_kernel(AttnArgs a) {
@@ -985,8 +988,9 @@ Plan plan_of(const gptq_kv_cache& c, const AttentionShape& s) {
     // heads of 128: 1024 tokens in 1 part 477 us, 2 313, 3 391; 512 tokens in
     // 3 198, 4 170, 7 192; 2048 tokens in 1 567, 2 615.)  More than fill the chip
     // once are left whole, and the few-row kernel's parts fill it at most once:
-    // ragged sequences level out by themselves there (33 sequences of up to
-    // 4096 e2m1 positions, 8 kv heads: 1 part 37 us, 4 70).
+    // that suits sequences of like lengths (33 of up to 4096 e2m1 positions, 8 kv
+    // heads: 1 part 37 us, 4 70), not one long one among many short ones (65536
+    // e4m3 positions beside 31 of 300: 522 us, alone 32).
     int64_t keys = (int64_t)c.page_size * s.max_pages;
     if (s.window) keys = std::min(keys, s.window + s.max_q);
     const int64_t key_bytes = 2 * c.head_dim * (c.format == GPTQ_MX_NONE ? 32 : c.format == GPTQ_MX_FP8 ? 17 : 9) / 16;

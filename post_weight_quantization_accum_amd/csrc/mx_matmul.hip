@@ -202,9 +202,9 @@ __device__ __forceinline__ void store4(const MatArgs& a, int64_t t, int64_t r, f
 // bytes) come from memory directly.
 //
 // Measured: one bf16 token, 4096 -> 4096, 4.9 us (an empty launch is 2.6; the
-// codes 1.7 at the rate of a copy); 13 float16 tokens, 11008 -> 4096, 9.7 us
+// codes 1.7 at the rate of a copy); 13 float16 tokens, 11008 -> 4096, 9.8 us
 // (2.5 TB/s; every compute unit reads all 286 KB of activations, which L2
-// hands out at some 20 bytes a clock); 64 bf16 tokens, 4096 -> 4096, 8.0 us.
+// hands out at some 20 bytes a clock); 64 bf16 tokens, 4096 -> 4096, 8.1 us.
 // ---------------------------------------------------------------------------
 constexpr int LDS_BYTES = 160 * 1024;      // of a compute unit
 
@@ -417,8 +417,8 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
 // from memory into the lanes that multiply them: lane l holds row l % 32 and,
 // of every 64 columns, block l / 32.  Both are fetched a step ahead.  Bound by
 // the conversions (float32: three products for one as well).  Measured: 2048 x
-// 4096 -> 4096 with e4m3 activations 99 us (690 TFLOP/s), with float32 ones
-// 260 us (265 TFLOP/s; 328 with every part looking for infinities).
+// 4096 -> 4096 with e4m3 activations 99 us (695 TFLOP/s), with float32 ones
+// 257 us (267 TFLOP/s); 16-bit ones whose rows do not start on 16 bytes 306 us.
 // ---------------------------------------------------------------------------
 constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
@@ -586,10 +586,11 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
 // stages at once, a quarter of the rows with each stage (four lanes to the 16
 // bytes of a row), and held in registers from there.  Columns after the last
 // whole 128 come from memory directly, at the end.  Bound by the matrix
-// instructions and, beside them, the conversions of the codes (four per eight
-// products): 2048 x 4096 -> 11008 bf16 166 us (1110 TFLOP/s, where a large
-// library product of two bf16 matrices reaches 1600); through registers and
-// one LDS buffer per operand it took 258 us.
+// instructions (the matrix cores are busy for 69 % of the time) and, beside
+// them, the conversions of the codes (four per eight products): 2048 x 4096 ->
+// 11008 bf16 163 to 177 us by card (1043 to 1136 TFLOP/s, where a large library
+// product of two bf16 matrices reaches 1600); through registers and one LDS
+// buffer per operand it took 258 us.
 // ---------------------------------------------------------------------------
 template <int RG>
 struct WideTile {
@@ -794,8 +795,13 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
 // two stages at once (16 bytes of a row by four lanes: a request to the cache
 // per row, where a word per lane was 64 of them and took as long as the
 // codes), half of the rows with each stage, and held in registers from there.
-// Measured: 2048 x 11008 -> 4096 56 us (3270 TFLOP/s) with 256 x 128 tiles; 65
-// us with scales a word per lane, 102 us through registers and two LDS buffers.
+// Measured: 2048 x 11008 -> 4096 55 to 58 us (3200 to 3350 TFLOP/s) with 256 x
+// 128 tiles; 65 us with scales a word per lane, 102 us through registers and two
+// LDS buffers.  Bound by the codes' way to LDS, 21 bytes a clock and compute
+// unit, beside the matrix instructions: 42 to 48 us without fetching codes, 49
+// without reading operands from LDS, 56 without fetching scales, 39.5 with
+// matrix instructions alone (the chip runs at 1.8 GHz there).  The matrix cores
+// are busy for 44 % of the time, LDS reads for 18 %.
 // ---------------------------------------------------------------------------
 template <int RW>
 struct MxTile {

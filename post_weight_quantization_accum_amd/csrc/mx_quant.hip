@@ -6,7 +6,7 @@
 // field, and the elements come out of the conversion instructions, which
 // round half to even on v * 2^-e.  Both kernels are bound by memory: 4096 x
 // 11008 float32 to e2m1 and back to float32 take 46 and 33 us, 385 MB in 78 us
-// together (4.9 TB/s; a copy of 1 GiB reaches 5.2); 64 x 4096 bf16 takes 4.4 us
+// together (4.9 TB/s; a copy of 1 GiB reaches 5.2); 64 x 4096 bf16 takes 4.2 us
 // both ways, two launches.
 #include "mx.hpp"
 
