@@ -97,6 +97,10 @@ def load(path: str | None = None):
     p = path or LIB_PATH
     if not os.path.exists(p):
         raise OSError(f"{p} is missing: build it with `python -m post_weight_quantization_accum_amd.build`")
+    try:
+        import torch  # noqa: F401  its HIP runtime has to be the process's one: loaded after the library it is a second
+    except ImportError:
+        pass
     lib = ctypes.CDLL(p)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     cfgp = ctypes.POINTER(Config)
