@@ -505,11 +505,11 @@ gptq_status gptq_cache_read(const gptq_kv_cache* cache, const int32_t* table, in
  * zeros.  Keys and values at positions that a token does not attend to have
  * no influence on it, whatever they hold.  A page outside [0, n_pages), or a
  * position past the table (or from 2^31 - 4096 on), is not read and makes the
- * tokens that attend to it NaN.  Tokens outside q_start[0] .. q_start[n_seq] - 1 are left as they
- * were in O.
+ * tokens that attend to it NaN.  Tokens outside q_start[0] ..
+ * q_start[n_seq] - 1 are left as they were in O.
  * q_start: device int32[n_seq + 1], ascending (where it is not, the outputs of
- * the n_tok tokens are unspecified; nothing else is touched); kv_len: device int32[n_seq];
- * table: device int32[n_seq][max_pages].
+ * the n_tok tokens are unspecified; nothing else is touched); kv_len: device
+ * int32[n_seq]; table: device int32[n_seq][max_pages].
  * max_q: the largest number of new tokens of one sequence (a hint for the
  * choice of kernels: results depend on it, as on max_pages, only in the order
  * of float32 sums).

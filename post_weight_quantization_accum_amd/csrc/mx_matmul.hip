@@ -32,8 +32,8 @@ struct MatArgs {
 // off its top (8 + 8 + 8 of its 24 bits), a float16 of two: no rounding, and
 // no overflow, down to bfloat16's smallest step, 2^-133 (float32 values below
 // 2^-110 lose what is under it).  The parts below an infinity or NaN are 0.  A
-// microscaled value is a bfloat16 as it is (e4m3 from scale byte 3 on).  (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3
-// codes directly, at twice the rate, but with an e4m3 operand it cuts products
+// microscaled value is a bfloat16 as it is (e4m3 from scale byte 3 on).
+// (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3 codes directly, at twice the rate, but with an e4m3 operand it cuts products
 // off some 16 bits below the largest one of an instruction: an error of 1e-5
 // of sum |x w| and more, measured, where these sums keep 1e-7.)
 //
@@ -1021,9 +1021,10 @@ double rounds(const MatArgs& a, int64_t r, int64_t t) {
 // 13.3 where 128 x 128 takes 13.0 and never has fewer workgroups; then the
 // others: 16-bit 128 x 128 and 256 x 128 from LDS rings, and so e2m1 by e2m1;
 // else 128 x 128 through registers, where two (float32) or three workgroups
-// share a compute unit.  For example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us, (1,1) 9.0, (4,2) 9.0; 256
-// tokens (4,2) 20, 128 x 128 26; 2048 tokens 256 x 128 63, 128 x 128 72.  One
-// token 4096 -> 11008: (3,1) 8.5, (4,1) 9.9, (2,1) 11.3, (1,1) 13.0.
+// share a compute unit.  For example bf16 4096 -> 4096: 32 tokens (2,1) 6.6 us,
+// (1,1) 9.0, (4,2) 9.0; 256 tokens (4,2) 20, 128 x 128 26; 2048 tokens 256 x 128
+// 63, 128 x 128 72.  One token 4096 -> 11008: (3,1) 8.5, (4,1) 9.9, (2,1) 11.3,
+// (1,1) 13.0.
 constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // float32
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // float16
                                  {3.9, 5.0, 6.0, 6.9, 6.4, 9.4, 0},        // bfloat16

@@ -171,7 +171,7 @@ def cache_attention(Q, cache: KVCache, q_start, kv_len, table, *, max_q: int | N
     positions in all (int32 tensors on the GPU); its newest token stands last.
     max_q: the largest number of new tokens of a sequence, if known (decoding:
     1); it only chooses between kernels.  scale: head_dim ** -0.5 unless
-    given.  window > 0: only the last `window` positions.
+    given (2^-100 .. 2^100).  window > 0: only the last `window` positions.
     """
     lib, torch = load(), _torch()
     c, dev, _, d = _cache(cache)
