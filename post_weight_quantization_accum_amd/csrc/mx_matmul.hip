@@ -33,9 +33,10 @@ struct MatArgs {
 // no overflow, down to bfloat16's smallest step, 2^-133 (float32 values below
 // 2^-110 lose what is under it).  The parts below an infinity or NaN are 0.  A
 // microscaled value is a bfloat16 as it is (e4m3 from scale byte 3 on).
-// (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3 codes directly, at twice the rate, but with an e4m3 operand it cuts products
-// off some 16 bits below the largest one of an instruction: an error of 1e-5
-// of sum |x w| and more, measured, where these sums keep 1e-7.)
+// (v_mfma_scale_f32_32x32x64_f8f6f4 would take e4m3 codes directly, at twice
+// the rate, but with an e4m3 operand it cuts products off some 16 bits below the
+// largest one of an instruction: an error of 1e-5 of sum |x w| and more,
+// measured, where these sums keep 1e-7.)
 //
 // Float16 activations enter as they are, with weights as float16, for blocks
 // whose scale leaves them in float16's range (byte 104 .. 140: 2^-24 ..
