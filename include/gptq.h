@@ -536,6 +536,74 @@ gptq_status gptq_cache_attention(const gptq_kv_cache* cache, const void* Q, gptq
                                  float scale, int64_t window, void* O, int64_t ld_o, void* workspace,
                                  size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Norms around a block: the block's output joins the residual stream, and the
+ * stream is normalised for the next block.  Per token (row of d values):
+ *
+ *   p = B                     or, with post_weight, norm(B) * post_weight
+ *   h = residual_scale * x + gate * p           (without B: residual_scale * x)
+ *   y = norm(h) * weight + bias
+ *
+ *   norm(v) = v / sqrt(mean(v^2) + eps)                          GPTQ_NORM_RMS
+ *           = (v - mean(v)) / sqrt(var(v) + eps)                 GPTQ_NORM_LAYER
+ *
+ * Sums over a row are float64, all else float32; h and y are rounded once, to
+ * their types, and y is taken of h before its rounding.  An infinity or NaN
+ * reaches its own row's outputs, as in float32 arithmetic, and no other's.
+ * ------------------------------------------------------------------------ */
+typedef enum { GPTQ_NORM_RMS = 0, GPTQ_NORM_LAYER = 1 } gptq_norm_kind;
+
+typedef struct {
+    gptq_norm_kind kind;
+    float eps;                /* >= 0 */
+    float residual_scale;     /* finite */
+    gptq_dtype vec_dtype;     /* of the four vectors */
+    const void* weight;       /* d values; NULL: ones */
+    const void* bias;         /* d values; NULL: zeros */
+    const void* post_weight;  /* d values; NULL: the block's output is taken as it is */
+    const void* gate;         /* d values, or a row of them for each token; NULL: ones */
+    int64_t ld_gate;          /* row stride of the gate; 0: d values for all tokens */
+} gptq_norm;
+
+/* X, B, H, Y: n_tok x d, row strides ld_*, each of its own dtype (float32,
+ * float16, bfloat16), any alignment.  B may be NULL (without post_weight and
+ * gate then), H or Y too (not written).  H may be X, with its dtype and
+ * stride; otherwise an output overlaps nothing.
+ * Errors: GPTQ_ERR_INVALID_ARG for a bad kind, dtype, eps, scale, pointer or
+ * stride, n_tok outside [0, 2^20] or d outside [1, 2^20].  n_tok == 0: nothing
+ * is launched.  Asynchronous, no workspace. */
+gptq_status gptq_residual_norm(const gptq_norm* norm, int64_t n_tok, int64_t d, const void* X, gptq_dtype x_dtype,
+                               int64_t ld_x, const void* B, gptq_dtype b_dtype, int64_t ld_b, void* H, gptq_dtype h_dtype,
+                               int64_t ld_h, void* Y, gptq_dtype y_dtype, int64_t ld_y, hipStream_t stream);
+
+/* Its gradient: from dY, the gradient for y, and dH (may be NULL: none), that
+ * for h, with H and B as the forward call had and gave them (both are read
+ * again, nothing else is kept; B only where there is post_weight or gate):
+ *
+ *   D      = dH + the norm's gradient of dY * weight at H
+ *   dX     = residual_scale * D                     dP = gate * D
+ *   dB     = dP, or the norm's gradient of dP * post_weight at B
+ *   d_weight = sum dY * norm(H)    d_bias = sum dY    (sums over tokens)
+ *   d_post_weight = sum dP * norm(B)
+ *   d_gate = sum D * p, or with a gate for each token D * p
+ *
+ * Every output may be NULL.  dH and dX are of h_dtype, dB of b_dtype; the
+ * vectors' gradients are float32, d values, but a gate's for each token is
+ * n_tok x d of vec_dtype with row stride ld_dgate.  bias itself is not read.
+ * The sums are taken in float32 over up to n_tok / 512 rows (rounded up) and in
+ * float64 from there, in one order: the same call gives the same bits.
+ * Without tokens the sums are zeros.  Outputs overlap no input.
+ * workspace: gptq_residual_norm_backward_workspace(n_tok, d) bytes, 16-byte
+ * aligned, where a sum is asked for.  Errors as above and GPTQ_ERR_WORKSPACE.
+ * Asynchronous. */
+size_t gptq_residual_norm_backward_workspace(int64_t n_tok, int64_t d);
+gptq_status gptq_residual_norm_backward(const gptq_norm* norm, int64_t n_tok, int64_t d, const void* dY, gptq_dtype dy_dtype,
+                                        int64_t ld_dy, const void* H, gptq_dtype h_dtype, int64_t ld_h, const void* B,
+                                        gptq_dtype b_dtype, int64_t ld_b, const void* dH, int64_t ld_dh, void* dX,
+                                        int64_t ld_dx, void* dB, int64_t ld_db, float* d_weight, float* d_bias,
+                                        float* d_post_weight, void* d_gate, int64_t ld_dgate, void* workspace,
+                                        size_t ws_bytes, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* gptq_status_string(gptq_status status);
 

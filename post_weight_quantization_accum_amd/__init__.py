@@ -4,7 +4,8 @@ Python face of libgptq_mi355x.so.  The functions below mirror the C ABI of
 ``include/gptq.h`` one to one (same names without the ``gptq_`` prefix) and
 only marshal torch tensors (device memory) and the current HIP stream into
 the library; ``quantize`` chains the four calls for one layer.  The
-microscaled formats are in ``mx``, the paged cache in ``kv_cache``.
+microscaled formats are in ``mx``, the paged cache in ``kv_cache``, the norms
+around a block in ``norm``.
 
 Import is cheap: the shared library is loaded on first use, and a missing
 library raises instead of falling back to anything else.
@@ -23,11 +24,13 @@ from .kv_cache import KVCache, cache_attention, cache_read, cache_write, new_cac
 from .mx import (  # noqa: F401
     mx_codes_per_row, mx_dequantize, mx_matmul, mx_matmul_quantized, mx_quantize, mx_scales_per_row,
 )
+from .norm import residual_norm, residual_norm_backward  # noqa: F401
 
 __all__ = ["hessian_accumulate", "hessian_accumulate_timed", "hessian_accumulate_noalloc", "prepare_hinv", "quantize_layer", "prepare_hinv_factored", "quantize_layer_factored", "factored_supported", "pack", "quantize",
            "pack_permuted", "dequant_matmul", "dequant_max_groups", "gather_columns", "packed_words_per_row", "make_config",
            "mx_quantize", "mx_dequantize", "mx_matmul", "mx_matmul_quantized", "mx_codes_per_row", "mx_scales_per_row",
            "KVCache", "new_cache", "cache_write", "cache_read", "cache_attention",
+           "residual_norm", "residual_norm_backward",
            "Config", "load"]
 
 

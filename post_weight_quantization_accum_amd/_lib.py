@@ -19,6 +19,8 @@ OK, ERR_INVALID_ARG, ERR_NOT_PD, ERR_NONFINITE, ERR_WORKSPACE, ERR_HIP, ERR_UNSU
 F32, F16, BF16 = 0, 1, 2
 # gptq_mx_format
 MX_NONE, MX_FP8, MX_FP4 = 0, 1, 2
+# gptq_norm_kind
+NORM_RMS, NORM_LAYER = 0, 1
 
 # Every symbol include/gptq.h declares.
 EXPORTS = (
@@ -31,7 +33,8 @@ EXPORTS = (
     "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
     "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
     "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
-    "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_status_string", "gptq_version",
+    "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_residual_norm", "gptq_residual_norm_backward_workspace",
+    "gptq_residual_norm_backward", "gptq_status_string", "gptq_version",
 )
 
 
@@ -78,6 +81,13 @@ class Cache(ctypes.Structure):
                 ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class Norm(ctypes.Structure):
+    """gptq_norm."""
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("vec_dtype", ctypes.c_int), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64)]
 
 
 def make_config(bits=4, group_size=128, sym=False, act_order=False, block=128, damp=0.01,
@@ -176,6 +186,14 @@ def load(path: str | None = None):
     lib.gptq_cache_attention.argtypes = [cachep, vp, ci, i64, i64, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, i64,
                                          vp, i64, vp, sz, vp]
     lib.gptq_cache_attention.restype = ci
+    normp = ctypes.POINTER(Norm)
+    lib.gptq_residual_norm.argtypes = [normp, i64, i64, vp, ci, i64, vp, ci, i64, vp, ci, i64, vp, ci, i64, vp]
+    lib.gptq_residual_norm.restype = ci
+    lib.gptq_residual_norm_backward_workspace.argtypes = [i64, i64]
+    lib.gptq_residual_norm_backward_workspace.restype = sz
+    lib.gptq_residual_norm_backward.argtypes = [normp, i64, i64, vp, ci, i64, vp, ci, i64, vp, ci, i64, vp, i64, vp, i64,
+                                                vp, i64, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.gptq_residual_norm_backward.restype = ci
     _lib = lib
     return lib
 
