@@ -440,6 +440,78 @@ int32_t gptq_mx_matmul_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64
                               int32_t aligned);
 
 /* ------------------------------------------------------------------------
+ * A gated feed-forward layer's first half, with e2m1 weights of d_ff x d_in:
+ *
+ *   Y[t][r] = act(g) * u,   g = sum_k X[t][k] gate[r][k],   u = sum_k X[t][k] up[r][k]
+ *
+ *   act: SILU       v / (1 + exp(-v))
+ *        GELU       v * Phi(v), the normal distribution's function
+ *        GELU_TANH  v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
+ *        RELU       max(v, 0)
+ * ------------------------------------------------------------------------ */
+typedef enum { GPTQ_ACT_SILU = 0, GPTQ_ACT_GELU = 1, GPTQ_ACT_GELU_TANH = 2, GPTQ_ACT_RELU = 3 } gptq_activation;
+
+/* X: n_tok x d_in of x_dtype, row stride ld_x, as in gptq_mx_matmul, and g, u
+ * as precise as its products; act and the product of both in float32.  Y: of
+ * y_dtype (float32, float16, bfloat16), row stride ld_y.  G, U: both NULL, or
+ * n_tok x d_ff of y_dtype with row stride ld_gu that get g and u, as
+ * gptq_mx_gated_backward takes them.  Rows of the outputs may start anywhere.
+ * Errors as in gptq_mx_matmul, and GPTQ_ERR_INVALID_ARG for a bad activation or
+ * one of G and U alone.  Asynchronous, no workspace. */
+gptq_status gptq_mx_gated(const void* X, gptq_dtype x_dtype, int64_t n_tok, int64_t d_in, int64_t ld_x,
+                          const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                          const uint8_t* up_scales, int64_t d_ff, gptq_activation activation, void* Y, gptq_dtype y_dtype,
+                          int64_t ld_y, void* G, void* U, int64_t ld_gu, hipStream_t stream);
+
+/* The same with microscaled activations, as in gptq_mx_matmul_quantized. */
+gptq_status gptq_mx_gated_quantized(const uint8_t* x_codes, const uint8_t* x_scales, gptq_mx_format x_format, int64_t n_tok,
+                                    int64_t d_in, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                    const uint8_t* up_codes, const uint8_t* up_scales, int64_t d_ff,
+                                    gptq_activation activation, void* Y, gptq_dtype y_dtype, int64_t ld_y, void* G, void* U,
+                                    int64_t ld_gu, hipStream_t stream);
+
+/* The gradient of gptq_mx_matmul for its activations (the weights are codes
+ * and have none):  dX[t][k] = sum_{r < d_out} dY[t][r] w[r][k].
+ * dY: n_tok x d_out of dy_dtype, row stride ld_dy; codes, scales: d_out x d_in
+ * as in the product; dX: n_tok x d_in of dx_dtype, row stride ld_dx; any of
+ * the three dtypes, any alignment.  No product is rounded, as in
+ * gptq_mx_matmul (float32 dY: three bfloat16 parts, each below 2^-110 off by
+ * less than 2^-133); sums are float32, dX is rounded once.  An infinity or NaN
+ * in dY reaches its token's outputs as in float32 arithmetic, and no other's.
+ * workspace: gptq_mx_matmul_backward_workspace(...) bytes (may be 0), 16-byte
+ * aligned.  The same call gives the same bits.  d_out == 0: dX is zeros.
+ * Errors as in gptq_mx_matmul, and GPTQ_ERR_WORKSPACE.  Asynchronous. */
+size_t gptq_mx_matmul_backward_workspace(gptq_dtype dy_dtype, int64_t n_tok, int64_t d_in, int64_t d_out);
+gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t n_tok, int64_t d_out, int64_t ld_dy,
+                                    const uint8_t* codes, const uint8_t* scales, int64_t d_in, void* dX,
+                                    gptq_dtype dx_dtype, int64_t ld_dx, void* workspace, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/* The gradient of gptq_mx_gated for its activations, from dY and the G and U
+ * that it wrote (all three n_tok x d_ff of one dtype; row strides ld_dy,
+ * ld_gu):
+ *
+ *   dG = dY * U * act'(G),   dU = dY * act(G),   dX = dG gate + dU up
+ *
+ * dG and dU are computed in float32.  For the matrix cores they are rounded
+ * once: of 16-bit dtypes to float16 after each token's are scaled by a power of
+ * two of its own that brings the largest of them to 2^14 .. 2^15 (11 bits, down
+ * to 2^-29 of that); of float32 not at all.  Weights whose scales float16 does
+ * not hold (outside 2^-23 .. 2^13) are multiplied as bfloat16, by the same
+ * values in two parts.  Sums are float32.
+ * dG_out, dU_out: both NULL, or n_tok x d_ff of G's dtype with row stride ld_dgu
+ * that get dG and dU (for adapters beside the weights).  dX: as above.
+ * RELU's slope at 0 is 0.
+ * workspace: gptq_mx_gated_backward_workspace(...) bytes, 16-byte aligned.
+ * Errors as in gptq_mx_gated, and GPTQ_ERR_WORKSPACE.  Asynchronous. */
+size_t gptq_mx_gated_backward_workspace(gptq_dtype dtype, int64_t n_tok, int64_t d_in, int64_t d_ff);
+gptq_status gptq_mx_gated_backward(const void* dY, gptq_dtype dtype, int64_t n_tok, int64_t d_ff, int64_t ld_dy, const void* G,
+                                   const void* U, int64_t ld_gu, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                   const uint8_t* up_codes, const uint8_t* up_scales, int64_t d_in,
+                                   gptq_activation activation, void* dX, gptq_dtype dx_dtype, int64_t ld_dx, void* dG_out,
+                                   void* dU_out, int64_t ld_dgu, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * A paged cache of keys and values.
  *
  * k and v: [n_pages][n_kv_heads][page_size] rows of head_dim values: 16-bit

@@ -22,13 +22,15 @@ from ._lib import (  # noqa: F401
 )
 from .kv_cache import KVCache, cache_attention, cache_read, cache_write, new_cache  # noqa: F401
 from .mx import (  # noqa: F401
-    mx_codes_per_row, mx_dequantize, mx_matmul, mx_matmul_quantized, mx_quantize, mx_scales_per_row,
+    mx_codes_per_row, mx_dequantize, mx_gated, mx_gated_backward, mx_gated_quantized, mx_matmul, mx_matmul_backward,
+    mx_matmul_quantized, mx_quantize, mx_scales_per_row,
 )
 from .norm import residual_norm, residual_norm_backward  # noqa: F401
 
 __all__ = ["hessian_accumulate", "hessian_accumulate_timed", "hessian_accumulate_noalloc", "prepare_hinv", "quantize_layer", "prepare_hinv_factored", "quantize_layer_factored", "factored_supported", "pack", "quantize",
            "pack_permuted", "dequant_matmul", "dequant_max_groups", "gather_columns", "packed_words_per_row", "make_config",
-           "mx_quantize", "mx_dequantize", "mx_matmul", "mx_matmul_quantized", "mx_codes_per_row", "mx_scales_per_row",
+           "mx_quantize", "mx_dequantize", "mx_matmul", "mx_matmul_quantized", "mx_gated", "mx_gated_quantized",
+           "mx_matmul_backward", "mx_gated_backward", "mx_codes_per_row", "mx_scales_per_row",
            "KVCache", "new_cache", "cache_write", "cache_read", "cache_attention",
            "residual_norm", "residual_norm_backward",
            "Config", "load"]

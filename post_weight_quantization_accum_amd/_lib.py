@@ -19,6 +19,8 @@ OK, ERR_INVALID_ARG, ERR_NOT_PD, ERR_NONFINITE, ERR_WORKSPACE, ERR_HIP, ERR_UNSU
 F32, F16, BF16 = 0, 1, 2
 # gptq_mx_format
 MX_NONE, MX_FP8, MX_FP4 = 0, 1, 2
+# gptq_activation
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(4)
 # gptq_norm_kind
 NORM_RMS, NORM_LAYER = 0, 1
 
@@ -32,7 +34,9 @@ EXPORTS = (
     "gptq_packed_words_per_row", "gptq_pack", "gptq_pack_permuted",
     "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
     "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
-    "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
+    "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_mx_gated", "gptq_mx_gated_quantized",
+    "gptq_mx_matmul_backward_workspace", "gptq_mx_matmul_backward", "gptq_mx_gated_backward_workspace",
+    "gptq_mx_gated_backward", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
     "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_residual_norm", "gptq_residual_norm_backward_workspace",
     "gptq_residual_norm_backward", "gptq_status_string", "gptq_version",
 )
@@ -175,6 +179,19 @@ def load(path: str | None = None):
     lib.gptq_mx_matmul_quantized.restype = ci
     lib.gptq_mx_matmul_kernel.argtypes = [ci, ci, i64, i64, i64, ctypes.c_int32]
     lib.gptq_mx_matmul_kernel.restype = ctypes.c_int32
+    lib.gptq_mx_gated.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp, vp, i64, ci, vp, ci, i64, vp, vp, i64, vp]
+    lib.gptq_mx_gated.restype = ci
+    lib.gptq_mx_gated_quantized.argtypes = [vp, vp, ci, i64, i64, vp, vp, vp, vp, i64, ci, vp, ci, i64, vp, vp, i64, vp]
+    lib.gptq_mx_gated_quantized.restype = ci
+    lib.gptq_mx_matmul_backward_workspace.argtypes = [ci, i64, i64, i64]
+    lib.gptq_mx_matmul_backward_workspace.restype = sz
+    lib.gptq_mx_matmul_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, ci, i64, vp, sz, vp]
+    lib.gptq_mx_matmul_backward.restype = ci
+    lib.gptq_mx_gated_backward_workspace.argtypes = [ci, i64, i64, i64]
+    lib.gptq_mx_gated_backward_workspace.restype = sz
+    lib.gptq_mx_gated_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, ci, vp, ci, i64, vp, vp,
+                                           i64, vp, sz, vp]
+    lib.gptq_mx_gated_backward.restype = ci
     lib.gptq_cache_write.argtypes = [cachep, vp, vp, ci, i64, i64, i64, vp, vp]
     lib.gptq_cache_write.restype = ci
     lib.gptq_cache_read.argtypes = [cachep, vp, i64, i64, vp, i64, vp, vp, ci, i64, i64, vp]

@@ -1,6 +1,6 @@
 // C entry points of the microscaled operators: argument checks and dispatch.
 // Contracts are in include/gptq.h.
-#include "mx.hpp"
+#include "gated.hpp"
 
 using namespace gptq;
 
@@ -15,6 +15,8 @@ bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 bool on(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }
 // elements start on their own size
 bool elems(const void* p, gptq_dtype dt) { return on(p, dt == GPTQ_F32 ? 4 : 2); }
+bool matrix(const uint8_t* codes, const uint8_t* scales) { return on(codes, 16) && on(scales, 4); }
+bool is_act(gptq_activation a) { return a >= GPTQ_ACT_SILU && a <= GPTQ_ACT_RELU; }
 
 gptq_status check_cache(const gptq_kv_cache* c) {
     if (!c) return GPTQ_ERR_INVALID_ARG;
@@ -93,6 +95,114 @@ int32_t gptq_mx_matmul_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64
     if (x_format == GPTQ_MX_NONE ? !is_float(x_dtype) : !is_mx(x_format)) return -1;
     if (!in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 1, MAX_DIM)) return -1;
     return mx_matmul_kernel(x_dtype, x_format, n_tok, d_in, d_out, aligned != 0);
+}
+
+gptq_status gptq_mx_gated(const void* X, gptq_dtype x_dtype, int64_t n_tok, int64_t d_in, int64_t ld_x,
+                          const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                          const uint8_t* up_scales, int64_t d_ff, gptq_activation activation, void* Y, gptq_dtype y_dtype,
+                          int64_t ld_y, void* G, void* U, int64_t ld_gu, hipStream_t stream) {
+    if (!is_float(x_dtype) || !is_float(y_dtype) || !is_act(activation)) return GPTQ_ERR_INVALID_ARG;
+    if (!in(n_tok, 0, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_ff, 0, MAX_DIM)) return GPTQ_ERR_INVALID_ARG;
+    if (ld_x < d_in || ld_y < d_ff || !G != !U || (G && ld_gu < d_ff)) return GPTQ_ERR_INVALID_ARG;
+    if (n_tok == 0 || d_ff == 0) return GPTQ_OK;
+    if (!elems(X, x_dtype) || !matrix(gate_codes, gate_scales) || !matrix(up_codes, up_scales) || !elems(Y, y_dtype) ||
+        (G && (!elems(G, y_dtype) || !elems(U, y_dtype))))
+        return GPTQ_ERR_INVALID_ARG;
+    return mx_gated_launch(X, x_dtype, n_tok, d_in, ld_x, gate_codes, gate_scales, d_ff,
+                           GatedArgs{up_codes, up_scales, activation, Y, y_dtype, ld_y, G, U, ld_gu}, stream);
+}
+
+gptq_status gptq_mx_gated_quantized(const uint8_t* x_codes, const uint8_t* x_scales, gptq_mx_format x_format, int64_t n_tok,
+                                    int64_t d_in, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                    const uint8_t* up_codes, const uint8_t* up_scales, int64_t d_ff,
+                                    gptq_activation activation, void* Y, gptq_dtype y_dtype, int64_t ld_y, void* G, void* U,
+                                    int64_t ld_gu, hipStream_t stream) {
+    if (!is_mx(x_format) || !is_float(y_dtype) || !is_act(activation)) return GPTQ_ERR_INVALID_ARG;
+    if (!in(n_tok, 0, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_ff, 0, MAX_DIM)) return GPTQ_ERR_INVALID_ARG;
+    if (ld_y < d_ff || !G != !U || (G && ld_gu < d_ff)) return GPTQ_ERR_INVALID_ARG;
+    if (n_tok == 0 || d_ff == 0) return GPTQ_OK;
+    if (!matrix(x_codes, x_scales) || !matrix(gate_codes, gate_scales) || !matrix(up_codes, up_scales) || !elems(Y, y_dtype) ||
+        (G && (!elems(G, y_dtype) || !elems(U, y_dtype))))
+        return GPTQ_ERR_INVALID_ARG;
+    return mx_gated_quantized_launch(x_codes, x_scales, x_format, n_tok, d_in, gate_codes, gate_scales, d_ff,
+                                     GatedArgs{up_codes, up_scales, activation, Y, y_dtype, ld_y, G, U, ld_gu}, stream);
+}
+
+size_t gptq_mx_matmul_backward_workspace(gptq_dtype dy_dtype, int64_t n_tok, int64_t d_in, int64_t d_out) {
+    if (!is_float(dy_dtype) || !in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 1, MAX_DIM)) return 0;
+    return mx_backward_ws(dy_dtype, 1, n_tok, d_in, d_out);
+}
+
+gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t n_tok, int64_t d_out, int64_t ld_dy,
+                                    const uint8_t* codes, const uint8_t* scales, int64_t d_in, void* dX,
+                                    gptq_dtype dx_dtype, int64_t ld_dx, void* workspace, size_t ws_bytes,
+                                    hipStream_t stream) {
+    if (!is_float(dy_dtype) || !is_float(dx_dtype)) return GPTQ_ERR_INVALID_ARG;
+    if (!in(n_tok, 0, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 0, MAX_DIM)) return GPTQ_ERR_INVALID_ARG;
+    if (ld_dy < d_out || ld_dx < d_in) return GPTQ_ERR_INVALID_ARG;
+    if (n_tok == 0) return GPTQ_OK;
+    if (!elems(dX, dx_dtype) || (d_out > 0 && (!elems(dY, dy_dtype) || !matrix(codes, scales)))) return GPTQ_ERR_INVALID_ARG;
+    const size_t need = d_out > 0 ? mx_backward_ws(dy_dtype, 1, n_tok, d_in, d_out) : 0;
+    if (need && (!on(workspace, 16) || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+    BackArgs a{};
+    a.D = dY;
+    a.dt = dy_dtype;
+    a.n_tok = n_tok;
+    a.ld = ld_dy;
+    a.codes[0] = codes;
+    a.scales[0] = scales;
+    a.matrices = 1;
+    a.rows = d_out;
+    a.d_in = d_in;
+    a.dX = dX;
+    a.dx_dt = dx_dtype;
+    a.ld_dx = ld_dx;
+    return mx_backward_launch(a, workspace, stream);
+}
+
+size_t gptq_mx_gated_backward_workspace(gptq_dtype dtype, int64_t n_tok, int64_t d_in, int64_t d_ff) {
+    if (!is_float(dtype) || !in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_ff, 1, MAX_DIM)) return 0;
+    return mx_gated_backward_ws(dtype, n_tok, d_in, d_ff);
+}
+
+gptq_status gptq_mx_gated_backward(const void* dY, gptq_dtype dtype, int64_t n_tok, int64_t d_ff, int64_t ld_dy, const void* G,
+                                   const void* U, int64_t ld_gu, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                   const uint8_t* up_codes, const uint8_t* up_scales, int64_t d_in,
+                                   gptq_activation activation, void* dX, gptq_dtype dx_dtype, int64_t ld_dx, void* dG_out,
+                                   void* dU_out, int64_t ld_dgu, void* workspace, size_t ws_bytes, hipStream_t stream) {
+    if (!is_float(dtype) || !is_float(dx_dtype) || !is_act(activation)) return GPTQ_ERR_INVALID_ARG;
+    if (!in(n_tok, 0, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_ff, 0, MAX_DIM)) return GPTQ_ERR_INVALID_ARG;
+    if (ld_dy < d_ff || ld_gu < d_ff || ld_dx < d_in || !dG_out != !dU_out || (dG_out && ld_dgu < d_ff))
+        return GPTQ_ERR_INVALID_ARG;
+    if (n_tok == 0) return GPTQ_OK;
+    if (!elems(dX, dx_dtype)) return GPTQ_ERR_INVALID_ARG;
+    if (d_ff > 0 && (!elems(dY, dtype) || !elems(G, dtype) || !elems(U, dtype) || !matrix(gate_codes, gate_scales) ||
+                     !matrix(up_codes, up_scales) || (dG_out && (!elems(dG_out, dtype) || !elems(dU_out, dtype)))))
+        return GPTQ_ERR_INVALID_ARG;
+    const size_t need = d_ff > 0 ? mx_gated_backward_ws(dtype, n_tok, d_in, d_ff) : 0;
+    if (need && (!on(workspace, 16) || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+    GatedBackArgs a{};
+    a.dY = dY;
+    a.G = G;
+    a.U = U;
+    a.dt = dtype;
+    a.n_tok = n_tok;
+    a.d_ff = d_ff;
+    a.ld_dy = ld_dy;
+    a.ld_gu = ld_gu;
+    a.codes[0] = gate_codes;
+    a.codes[1] = up_codes;
+    a.scales[0] = gate_scales;
+    a.scales[1] = up_scales;
+    a.d_in = d_in;
+    a.act = activation;
+    a.dX = dX;
+    a.dx_dt = dx_dtype;
+    a.ld_dx = ld_dx;
+    a.dG = dG_out;
+    a.dU = dU_out;
+    a.ld_dgu = ld_dgu;
+    return mx_gated_backward_launch(a, workspace, stream);
 }
 
 gptq_status gptq_cache_write(const gptq_kv_cache* cache, const void* K, const void* V, gptq_dtype x_dtype,

@@ -4,7 +4,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "mx.hpp"
+#include "gated.hpp"
 
 namespace gptq {
 namespace {
@@ -24,7 +24,13 @@ struct MatArgs {
     int full;              // the first of them whose activations are read in whole 16-byte pieces
     int64_t d_out, ld_y;
     float* Y;
-    bool y_aligned;        // Y rows start on 16 bytes
+    bool y_aligned;        // Y rows start on 16 bytes (of gated products: all outputs' groups of four on their own size)
+    // gated products: W and S are the gate's, d_out rows of each
+    const uint8_t *W2, *S2;
+    gptq_activation act;
+    gptq_dtype y_dt;
+    void *YT, *G, *U;      // outputs of y_dt, G and U null if not asked for
+    int64_t ld_gu;
 };
 
 // ---------------------------------------------------------------------------
@@ -180,6 +186,34 @@ __device__ __forceinline__ void store4(const MatArgs& a, int64_t t, int64_t r, f
     }
 }
 
+// Four neighbouring outputs of a token, of a gated product.
+__device__ __forceinline__ void store_gated4(const MatArgs& a, int64_t t, int64_t r, const float (&g)[4], const float (&u)[4]) {
+    if (r >= a.d_out) return;
+    const int n = (int)min((int64_t)4, a.d_out - r);
+    const bool whole = a.y_aligned && n == 4;
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = activate(a.act, g[i]) * u[i];
+    put4(a.YT, a.y_dt, whole, t * a.ld_y + r, n, y);
+    if (a.G) {
+        put4(a.G, a.y_dt, whole, t * a.ld_gu + r, n, g);
+        put4(a.U, a.y_dt, whole, t * a.ld_gu + r, n, u);
+    }
+}
+
+// A lane's sixteen of a 32 x 32 tile.
+__device__ __forceinline__ void store_gated(const MatArgs& a, int64_t t, int64_t r, const f16_t& g, const f16_t& u) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const float gs[4] = {g[e], g[e + 1], g[e + 2], g[e + 3]}, us[4] = {u[e], u[e + 1], u[e + 2], u[e + 3]};
+        store_gated4(a, t, r + 2 * e, gs, us);
+    }
+}
+
+// Gated products run in the same kernels (GATED): of a wave's groups of weight
+// rows the first half are the gate's and the second half the same rows of up,
+// so that a lane ends with both products of its outputs.
+
 // ---------------------------------------------------------------------------
 // Few tokens: a workgroup computes 16 RT weight rows x 16 TT tokens; its waves
 // take a share of the 128-column steps each, and their sums meet in LDS.
@@ -223,16 +257,18 @@ struct FewTile {
 };
 constexpr uint32_t NOWHERE = 1u << 30;     // an offset past every tile's buffer, also with another added
 
-template <Act DT, int RT, int TT, int THREADS = 64 * FewTile<DT, RT, TT>::WAVES>
+template <Act DT, int RT, int TT, bool GATED = false, int THREADS = 64 * FewTile<DT, RT, TT>::WAVES>
 __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
+    static_assert(!GATED || RT % 2 == 0, "half of the rows are the gate's");
+    constexpr int RM = GATED ? RT / 2 : RT;                 // 16-row groups of one matrix
     using T = FewTile<DT, RT, TT>;
     constexpr int NP = parts_of<DT>(), CH = T::X_ROW / 16, PER = CH < 16 ? 16 / CH : 1, LOW = CH < 16 ? CH - 1 : 15;
     using Half = std::bool_constant<DT == ACT_F16>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i16 = lane & 15, g = lane >> 4;
-    const int64_t r0 = (int64_t)blockIdx.x * (16 * RT), t0 = (int64_t)blockIdx.y * (16 * TT);
-    const int64_t wn = min((int64_t)(16 * RT), a.d_out - r0), xn = min((int64_t)(16 * TT), a.n_tok - t0);
+    const int64_t r0 = (int64_t)blockIdx.x * (16 * RM), t0 = (int64_t)blockIdx.y * (16 * TT);
+    const int64_t wn = min((int64_t)(16 * RM), a.d_out - r0), xn = min((int64_t)(16 * TT), a.n_tok - t0);
     f32x4_t acc[RT][TT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -301,14 +337,16 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
     if (first < end) {
         constexpr int XB = T::XS ? 1 : DT == ACT_F32 ? 4 : 2;                    // bytes per element of ld_x
         const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), wsb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row);
+        const u32x4_t wb2 = GATED ? buffer_of(a.W2 + r0 * a.w_row, wn * a.w_row) : wb;
+        const u32x4_t wsb2 = GATED ? buffer_of(a.S2 + r0 * a.s_row, wn * a.s_row) : wsb;
         const u32x4_t xb = buffer_of((const char*)a.X + t0 * a.ld_x * XB, ((xn - 1) * a.ld_x + (T::XS ? a.ld_x : a.d_in)) * XB);
         const u32x4_t xsb = T::XS ? buffer_of(a.XS + t0 * a.s_row, xn * a.s_row) : wsb;
         uint32_t woff[T::W_DMA], xoff[T::X_DMA], wsoff[RT], xsoff[T::XS ? T::XS : 1];
 #pragma unroll
         for (int k = 0; k < RT; ++k) {
-            const int r = 16 * k + (lane >> 2);
+            const int r = 16 * (k % RM) + (lane >> 2);
             woff[k] = (uint32_t)(min((int64_t)r, wn - 1) * a.w_row + 16 * ((lane & 3) ^ (r >> 2 & 3)));
-            wsoff[k] = lane < 16 ? (uint32_t)(min((int64_t)(16 * k + lane), wn - 1) * a.s_row) : NOWHERE;
+            wsoff[k] = lane < 16 ? (uint32_t)(min((int64_t)(16 * (k % RM) + lane), wn - 1) * a.s_row) : NOWHERE;
         }
 #pragma unroll
         for (int k = 0; k < T::X_DMA; ++k) {
@@ -323,11 +361,11 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
             const bool is = st < end;
             const uint32_t wo = is ? 64u * st : NOWHERE, xo = is ? (uint32_t)T::X_ROW * st : NOWHERE, so = is ? 4u * st : NOWHERE;
 #pragma unroll
-            for (int k = 0; k < RT; ++k) dma_16(at + 1024 * k, woff[k] + wo, wb);
+            for (int k = 0; k < RT; ++k) dma_16(at + 1024 * k, woff[k] + wo, k < RM ? wb : wb2);
 #pragma unroll
             for (int k = 0; k < T::X_DMA; ++k) dma_16(at + 1024 * (RT + k), xoff[k] + xo, xb);
 #pragma unroll
-            for (int k = 0; k < RT; ++k) dma_4(at + T::S_AT + 256 * k, wsoff[k] + so, wsb);
+            for (int k = 0; k < RT; ++k) dma_4(at + T::S_AT + 256 * k, wsoff[k] + so, k < RM ? wsb : wsb2);
 #pragma unroll
             for (int k = 0; k < T::XS; ++k) dma_4(at + T::S_AT + 256 * (RT + k), xsoff[k] + so, xsb);
         };
@@ -367,9 +405,9 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
         Step d;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const int64_t row = min(r0 + 16 * i + i16, a.d_out - 1);
-            d.w[i] = *(const u32x4_t*)(a.W + row * a.w_row + 64 * (int64_t)st + 16 * g);
-            d.s[i] = a.S[row * a.s_row + 4 * (int64_t)st + g];
+            const int64_t row = min(r0 + 16 * (i % RM) + i16, a.d_out - 1);
+            d.w[i] = *(const u32x4_t*)((i < RM ? a.W : a.W2) + row * a.w_row + 64 * (int64_t)st + 16 * g);
+            d.s[i] = (i < RM ? a.S : a.S2)[row * a.s_row + 4 * (int64_t)st + g];
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j)
@@ -394,6 +432,36 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
     // the waves' sums, in the order of the waves, AT tiles at a time
     constexpr int AT = T::AT;
     f32x4_t* part = (f32x4_t*)lds;
+    if constexpr (GATED) {
+        // pairs of tiles, the gate's and up's of the same rows and tokens
+        constexpr int PAIRS = AT / 2;
+#pragma unroll
+        for (int b = 0; b < RM * TT; b += PAIRS) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e)
+                if (b + e < RM * TT)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        part[(wave * AT + 2 * e + m) * 64 + lane] = acc[m * RM + (b + e) / TT][(b + e) % TT];
+            __syncthreads();
+            for (int e = threadIdx.x; e < PAIRS * 64; e += 64 * T::WAVES) {
+                const int pair = b + (e >> 6), l = e & 63;
+                if (pair >= RM * TT) continue;
+                const f32x4_t* p = part + (e >> 6) * 128 + l;
+                f32x4_t v = p[0], w = p[64];
+#pragma unroll
+                for (int q = 1; q < T::WAVES; ++q) {
+                    v += p[q * AT * 64];
+                    w += p[q * AT * 64 + 64];
+                }
+                const int64_t t = t0 + 16 * (pair % TT) + (l & 15), r = r0 + 16 * (pair / TT) + 4 * (l >> 4);
+                const float gs[4] = {v[0], v[1], v[2], v[3]}, us[4] = {w[0], w[1], w[2], w[3]};
+                if (t < a.n_tok) store_gated4(a, t, r, gs, us);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int b = 0; b < RT * TT; b += AT) {
         __syncthreads();
@@ -423,9 +491,9 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
-template <Act DT>
+template <Act DT, bool GATED = false>
 __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
-    constexpr int RW = 2;
+    constexpr int RW = 2, RM = GATED ? 1 : RW;
     constexpr int NP = DT == ACT_F32 ? 3 : 1;           // planes in LDS
     constexpr int BUF = NP * MT * X_ROW;
     extern __shared__ __attribute__((aligned(16))) char xs[];   // two buffers
@@ -435,14 +503,14 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
     // tiles that share weight rows
     const uint32_t nt = (uint32_t)((a.n_tok + MT - 1) / MT), n = gridDim.x, per = n / 8;
     const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
-    const int64_t r0 = (int64_t)(id / nt) * (64 * RW) + 32 * RW * (wave >> 1), t0 = (int64_t)(id % nt) * MT;
+    const int64_t r0 = (int64_t)(id / nt) * (64 * RM) + 32 * RM * (wave >> 1), t0 = (int64_t)(id % nt) * MT;
     const int tw = 64 * (wave & 1);
     const uint8_t *wp[RW], *sp[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int64_t row = min(r0 + 32 * i + i32, a.d_out - 1);
-        wp[i] = a.W + row * a.w_row + 16 * h;
-        sp[i] = a.S + row * a.s_row + h;
+        const int64_t row = min(r0 + 32 * (i % RM) + i32, a.d_out - 1);
+        wp[i] = (i < RM ? a.W : a.W2) + row * a.w_row + 16 * h;
+        sp[i] = (i < RM ? a.S : a.S2) + row * a.s_row + h;
     }
     f16_t acc[RW][2];
 #pragma unroll
@@ -569,6 +637,10 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
+        if constexpr (GATED) {
+            store_gated(a, t, r0 + 4 * h, acc[0][j], acc[1][j]);
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -601,10 +673,10 @@ struct WideTile {
     static constexpr int LDS = RING * STAGE + 2 * SCALES;
 };
 
-template <Act DT, int RG>
+template <Act DT, int RG, bool GATED = false>
 __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
     using T = WideTile<RG>;
-    constexpr int RW = 2, NW = T::WAVES;
+    constexpr int RW = 2, RM = GATED ? 1 : RW, NW = T::WAVES;
     constexpr int DMA = T::W_DMA + T::X_DMA + 1;
     constexpr bool HALF = DT == ACT_F16;
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -612,18 +684,24 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
     const int i32 = lane & 31, h = lane >> 5;
     const uint32_t nt = (uint32_t)((a.n_tok + MT - 1) / MT), n = gridDim.x, per = n / 8;
     const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
-    const int64_t r0 = (int64_t)(id / nt) * T::WR, t0 = (int64_t)(id % nt) * MT;
+    const int64_t r0 = (int64_t)(id / nt) * (T::WR / RW * RM), t0 = (int64_t)(id % nt) * MT;
     const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
+    const int rm = 32 * RM * (wave >> 1);                   // the wave's first row of a matrix
+    // of a tile's rows: those of a matrix, and whether they are up's
+    const auto row_of = [](int r) { return GATED ? (r >> 6) * 32 + (r & 31) : r; };
+    const auto is_up = [](int group16) { return GATED && (group16 >> 1 & 1) != 0; };
 
     // buffers over the tile's rows: they end with the matrix
-    const int64_t wn = min((int64_t)T::WR, a.d_out - r0), xn = min((int64_t)MT, a.n_tok - t0);
+    const int64_t wn = min((int64_t)(T::WR / RW * RM), a.d_out - r0), xn = min((int64_t)MT, a.n_tok - t0);
     const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), sb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row);
+    const u32x4_t wb2 = GATED ? buffer_of(a.W2 + r0 * a.w_row, wn * a.w_row) : wb;
+    const u32x4_t sb2 = GATED ? buffer_of(a.S2 + r0 * a.s_row, wn * a.s_row) : sb;
     const u32x4_t xb = buffer_of((const uint16_t*)a.X + t0 * a.ld_x, 2 * ((xn - 1) * a.ld_x + a.d_in));
     uint32_t woff[T::W_DMA], xoff[T::X_DMA], soff[4];
 #pragma unroll
     for (int j = 0; j < T::W_DMA; ++j) {
         const int r = 16 * (wave + NW * j) + (lane >> 2), c = (lane & 3) ^ (r >> 2 & 3);
-        woff[j] = (uint32_t)(min((int64_t)r, wn - 1) * a.w_row + 16 * c);
+        woff[j] = (uint32_t)(min((int64_t)row_of(r), wn - 1) * a.w_row + 16 * c);
     }
 #pragma unroll
     for (int j = 0; j < T::X_DMA; ++j) {
@@ -633,14 +711,14 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
     // the waves bring some scales twice
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        soff[k] = (uint32_t)(min((int64_t)(16 * ((wave + NW * k) % (T::WR / 16)) + (lane >> 2)), wn - 1) * a.s_row + 4 * (lane & 3));
+        soff[k] = (uint32_t)(min((int64_t)row_of(16 * ((wave + NW * k) % (T::WR / 16)) + (lane >> 2)), wn - 1) * a.s_row + 4 * (lane & 3));
     const uint32_t base = (uint32_t)(uintptr_t)lds;
     const int stages = a.full, quads = (stages + 3) / 4;
     // stage f's codes and activations, and a quarter of the scales of the four
     // stages after its own four
     const auto fetch_scales = [&](int quad, int k) {
         dma_4(base + T::RING * T::STAGE + (quad & 1) * T::SCALES + 256 * ((wave + NW * k) % (T::WR / 16)),
-              soff[k] + __builtin_amdgcn_readfirstlane(16 * min(quad, quads - 1)), sb);
+              soff[k] + __builtin_amdgcn_readfirstlane(16 * min(quad, quads - 1)), is_up((wave + NW * k) % (T::WR / 16)) ? sb2 : sb);
     };
     // every eighth of a stage's pieces from e on
     constexpr int PIECES = T::W_DMA + T::X_DMA;
@@ -652,7 +730,8 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
             if (j < T::X_DMA)
                 dma_16(at + T::W_BYTES + 1024 * (wave + NW * j), xoff[j] + __builtin_amdgcn_readfirstlane(256 * st), xb);
             else
-                dma_16(at + 1024 * (wave + NW * (j - T::X_DMA)), woff[j - T::X_DMA] + __builtin_amdgcn_readfirstlane(64 * st), wb);
+                dma_16(at + 1024 * (wave + NW * (j - T::X_DMA)), woff[j - T::X_DMA] + __builtin_amdgcn_readfirstlane(64 * st),
+                       is_up(wave + NW * (j - T::X_DMA)) ? wb2 : wb);
         }
     };
 
@@ -762,9 +841,9 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
                 parts<true>(y, 0, p);
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
-                    const int64_t row = min(r0 + rw + 32 * i + i32, a.d_out - 1);
-                    const uint32_t code = *(const uint32_t*)(a.W + row * a.w_row + 32 * (int64_t)st + 16 * h + 4 * c);
-                    const u32x4_t v = fp4x8<true>(code, mx_scale(a.S[row * a.s_row + 2 * (int64_t)st + h]));
+                    const int64_t row = min(r0 + rm + 32 * (i % RM) + i32, a.d_out - 1);
+                    const uint32_t code = *(const uint32_t*)((i < RM ? a.W : a.W2) + row * a.w_row + 32 * (int64_t)st + 16 * h + 4 * c);
+                    const u32x4_t v = fp4x8<true>(code, mx_scale((i < RM ? a.S : a.S2)[row * a.s_row + 2 * (int64_t)st + h]));
 #pragma unroll
                     for (int k = 0; k < parts_of<DT>(); ++k) acc[i][j] = H16<true>::mfma32(v, p[k], acc[i][j]);
                 }
@@ -774,6 +853,10 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
+        if constexpr (GATED) {
+            store_gated(a, t, r0 + rm + 4 * h, acc[0][j], acc[1][j]);
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -819,30 +902,37 @@ __device__ __forceinline__ f16_t mfma_fp4(u32x4_t w, u32x4_t x, f16_t c, uint32_
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2 * (Q & 1), (int)ws, 2 * (Q & 1), (int)xs);
 }
 
-template <int RW>
+template <int RW, bool GATED = false>
 __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
     using T = MxTile<RW>;
+    constexpr int RM = GATED ? RW / 2 : RW;
     constexpr int DMA = T::C_DMA + T::S_DMA;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i32 = lane & 31, h = lane >> 5;
     const uint32_t nt = (uint32_t)((a.n_tok + 127) / 128), n = gridDim.x, per = n / 8;
     const uint32_t id = blockIdx.x < per * 8 ? (blockIdx.x % 8) * per + blockIdx.x / 8 : blockIdx.x;
-    const int64_t r0 = (int64_t)(id / nt) * T::WR, t0 = (int64_t)(id % nt) * 128;
+    const int64_t r0 = (int64_t)(id / nt) * (64 * RM), t0 = (int64_t)(id % nt) * 128;
     const int rw = 32 * RW * (wave >> 1), tw = 64 * (wave & 1);
+    const int rm = 32 * RM * (wave >> 1);               // the wave's first row of a matrix
+    // of a tile's rows: those of a matrix, and whether they are up's
+    const auto row_of = [](int r) { return GATED ? r / (32 * RW) * (32 * RM) + r % (32 * RM) : r; };
+    const auto is_up = [](int r) { return GATED && r % (32 * RW) >= 32 * RM; };
 
     // Buffers over the tile's rows (they end with the matrix; the last stage
     // may read past a row's end, into columns that are not multiplied).
-    const int64_t wn = min((int64_t)T::WR, a.d_out - r0), xn = min((int64_t)128, a.n_tok - t0);
+    const int64_t wn = min((int64_t)(64 * RM), a.d_out - r0), xn = min((int64_t)128, a.n_tok - t0);
     const u32x4_t wb = buffer_of(a.W + r0 * a.w_row, wn * a.w_row), xb = buffer_of((const uint8_t*)a.X + t0 * a.w_row, xn * a.w_row);
     const u32x4_t wsb = buffer_of(a.S + r0 * a.s_row, wn * a.s_row), xsb = buffer_of(a.XS + t0 * a.s_row, xn * a.s_row);
+    const u32x4_t wb2 = GATED ? buffer_of(a.W2 + r0 * a.w_row, wn * a.w_row) : wb;
+    const u32x4_t wsb2 = GATED ? buffer_of(a.S2 + r0 * a.s_row, wn * a.s_row) : wsb;
     // Codes: instruction j of wave w takes rows 8 (w + 4 j) .. + 7, lane l row
     // l / 8 and slot l % 8 of them.
     uint32_t coff[T::C_DMA];
 #pragma unroll
     for (int j = 0; j < T::C_DMA; ++j) {
         const int r = 8 * (wave + 4 * j) + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
-        const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
+        const int64_t row = r < T::WR ? min((int64_t)row_of(r), wn - 1) : min((int64_t)r - T::WR, xn - 1);
         coff[j] = (uint32_t)(row * a.w_row + 16 * c);
     }
     // Scales of two stages: instruction j of wave w takes rows 16 (w + 4 j) ..
@@ -852,7 +942,7 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
 #pragma unroll
     for (int j = 0; j < 2 * T::S_DMA; ++j) {
         const int r = 16 * (wave + 4 * j) + (lane >> 2);
-        const int64_t row = r < T::WR ? min((int64_t)r, wn - 1) : min((int64_t)r - T::WR, xn - 1);
+        const int64_t row = r < T::WR ? min((int64_t)row_of(r), wn - 1) : min((int64_t)r - T::WR, xn - 1);
         soff[j] = (uint32_t)(row * a.s_row + 4 * (lane & 3));
     }
     const uint32_t base = (uint32_t)(uintptr_t)lds;
@@ -863,7 +953,7 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
 #pragma unroll
         for (int i = 0; i < T::C_DMA / 4; ++i) {
             const int j = q * (T::C_DMA / 4) + i;
-            dma_16(at + 1024 * (wave + 4 * j), coff[j] + co, 32 * j < T::WR ? wb : xb);
+            dma_16(at + 1024 * (wave + 4 * j), coff[j] + co, 32 * j >= T::WR ? xb : is_up(8 * (wave + 4 * j)) ? wb2 : wb);
         }
     };
     const auto fetch_scales = [&](int pair, auto half) {
@@ -873,7 +963,8 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
         for (int i = 0; i < T::S_DMA; ++i) {
             constexpr int H = decltype(half)::value;
             const int j = H * T::S_DMA + i;
-            dma_4(at + 256 * (wave + 4 * j), soff[j] + so, 64 * j + 16 * wave < T::WR ? wsb : xsb);
+            dma_4(at + 256 * (wave + 4 * j), soff[j] + so,
+                  64 * j + 16 * wave >= T::WR ? xsb : is_up(64 * j + 16 * wave) ? wsb2 : wsb);
         }
     };
 
@@ -965,6 +1056,11 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
+        if constexpr (GATED) {
+#pragma unroll
+            for (int i = 0; i < RM; ++i) store_gated(a, t, r0 + rm + 32 * i + 4 * h, acc[i][j], acc[RM + i][j]);
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -973,45 +1069,48 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
     }
 }
 
-template <Act DT, int RT, int TT>
+template <Act DT, int RT, int TT, bool GATED = false>
 gptq_status launch_few(const MatArgs& a, hipStream_t s) {
     using T = FewTile<DT, RT, TT>;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_few_kernel<DT, RT, TT>, T::BYTES));
-    hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT>),
-                       dim3((unsigned)ceil_div(a.d_out, 16 * RT), (unsigned)ceil_div(a.n_tok, 16 * TT)),
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_few_kernel<DT, RT, TT, GATED>, T::BYTES));
+    hipLaunchKernelGGL((mx_few_kernel<DT, RT, TT, GATED>),
+                       dim3((unsigned)ceil_div(a.d_out, 16 * RT / (GATED ? 2 : 1)), (unsigned)ceil_div(a.n_tok, 16 * TT)),
                        dim3(64 * T::WAVES), T::BYTES, s, a);
     return GPTQ_OK;
 }
 
-template <Act DT>
+template <Act DT, bool GATED = false>
 gptq_status launch_many(const MatArgs& a, hipStream_t s) {
     constexpr int lds = 2 * (DT == ACT_F32 ? 3 : 1) * MT * X_ROW;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_many_kernel<DT>, lds));
-    hipLaunchKernelGGL(mx_many_kernel<DT>, dim3((unsigned)(ceil_div(a.d_out, 128) * ceil_div(a.n_tok, MT))), dim3(256), lds,
-                       s, a);
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_many_kernel<DT, GATED>, lds));
+    hipLaunchKernelGGL((mx_many_kernel<DT, GATED>),
+                       dim3((unsigned)(ceil_div(a.d_out, GATED ? 64 : 128) * ceil_div(a.n_tok, MT))), dim3(256), lds, s, a);
     return GPTQ_OK;
 }
 
-template <Act DT, int RG>
+template <Act DT, int RG, bool GATED = false>
 gptq_status launch_wide(const MatArgs& a, hipStream_t s) {
     constexpr int lds = WideTile<RG>::LDS;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_wide_kernel<DT, RG>, lds));
-    hipLaunchKernelGGL((mx_wide_kernel<DT, RG>), dim3((unsigned)(ceil_div(a.d_out, 64 * RG) * ceil_div(a.n_tok, MT))),
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_wide_kernel<DT, RG, GATED>, lds));
+    hipLaunchKernelGGL((mx_wide_kernel<DT, RG, GATED>),
+                       dim3((unsigned)(ceil_div(a.d_out, 64 * RG / (GATED ? 2 : 1)) * ceil_div(a.n_tok, MT))),
                        dim3(128 * RG), lds, s, a);
     return GPTQ_OK;
 }
 
-template <int RW>
+template <int RW, bool GATED = false>
 gptq_status launch_mx(const MatArgs& a, hipStream_t s) {
     constexpr int lds = MxTile<RW>::LDS;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW>, lds));
-    hipLaunchKernelGGL(mx_mx_kernel<RW>, dim3((unsigned)(ceil_div(a.d_out, 64 * RW) * ceil_div(a.n_tok, 128))),
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_mx_kernel<RW, GATED>, lds));
+    hipLaunchKernelGGL((mx_mx_kernel<RW, GATED>),
+                       dim3((unsigned)(ceil_div(a.d_out, 64 * RW / (GATED ? 2 : 1)) * ceil_div(a.n_tok, 128))),
                        dim3(256), lds, s, a);
     return GPTQ_OK;
 }
 
 // Workgroups of tiles of r rows x t tokens, in rounds of one per compute unit.
 double rounds(const MatArgs& a, int64_t r, int64_t t) {
+    if (a.W2) r /= 2;      // of each matrix
     return std::ceil((double)(ceil_div(a.d_out, r) * ceil_div(a.n_tok, t)) / 256.0);
 }
 
@@ -1102,6 +1201,51 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
     else return launch_many<DT>(a, s);
 }
 
+// Gated products.  Tiles of an odd number of row groups are out; of more rows:
+// (6,1) and (8,1).
+template <Act DT>
+gptq_status launch_gated(const MatArgs& a, hipStream_t s) {
+    constexpr const double* ring = FEW_US[DT];
+    const double* us = a.full > 0 ? ring : DIRECT_US[DT != ACT_F32];
+    int best = 9;
+    double least = 1e30;
+    const auto offer = [&](int id, double cost) {
+        if (cost < least) {
+            least = cost;
+            best = id;
+        }
+    };
+    for (int i : {1, 3, 4, 5})
+        if (us[i] > 0) offer(i, rounds(a, 16 * FEW_RT[i], 16 * FEW_TT[i]) * us[i]);
+    if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
+        if (a.full > 0) {
+            offer(7, rounds(a, 128, MT) * 25.0);
+            offer(8, rounds(a, 256, MT) * 43.0);
+        } else {
+            offer(9, std::max(1.0, 0.61 * rounds(a, 128, MT)) * 250.0);
+        }
+    } else if constexpr (DT == ACT_F32) {
+        offer(9, rounds(a, 128, MT) * (a.full > 0 ? 130.0 : 226.0));
+    } else if constexpr (DT == ACT_FP8) {
+        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
+    } else {
+        offer(7, rounds(a, 128, MT) * 13.0);
+        offer(8, rounds(a, 256, MT) * 25.0);
+    }
+    switch (best) {
+        case 1: return launch_few<DT, 2, 1, true>(a, s);
+        case 3: return launch_few<DT, 4, 1, true>(a, s);
+        case 4: return launch_few<DT, 2, 2, true>(a, s);
+        case 5: if constexpr (FEW_US[DT][5] > 0) return launch_few<DT, 4, 2, true>(a, s); break;
+        default: break;
+    }
+    if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
+        if (best == 7) return launch_wide<DT, 2, true>(a, s);
+        if (best == 8) return launch_wide<DT, 4, true>(a, s);
+    }
+    if constexpr (DT == ACT_FP4) return best == 7 ? launch_mx<2, true>(a, s) : launch_mx<4, true>(a, s);
+    else return launch_many<DT, true>(a, s);
+}
 
 MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int64_t d_in, int64_t d_out, float* Y,
                  int64_t ld_y) {
@@ -1122,13 +1266,41 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
     a.d_out = d_out;
     a.ld_y = ld_y;
     a.Y = Y;
+    a.W2 = a.S2 = nullptr;
+    a.act = GPTQ_ACT_SILU;
+    a.y_dt = GPTQ_F32;
+    a.YT = a.G = a.U = nullptr;
+    a.ld_gu = 0;
     return a;
+}
+
+// The gated product's second matrix and outputs.
+void gate_args(MatArgs& a, const GatedArgs& g) {
+    const size_t four = g.y_dt == GPTQ_F32 ? 16 : 8;
+    const auto fits = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * (int64_t)(four / 4))) % four == 0; };
+    a.W2 = g.up_codes;
+    a.S2 = g.up_scales;
+    a.act = g.act;
+    a.y_dt = g.y_dt;
+    a.YT = g.Y;
+    a.ld_y = g.ld_y;
+    a.G = g.G;
+    a.U = g.U;
+    a.ld_gu = g.ld_gu;
+    a.y_aligned = fits(g.Y, g.ld_y) && (!g.G || (fits(g.G, g.ld_gu) && fits(g.U, g.ld_gu)));
 }
 
 // Steps of 16-bit or float32 activations that are read in whole pieces: offsets
 // within a tile's tokens stay below 2^30.
 int whole_steps(bool aligned, int64_t d_in, int64_t ld_x) {
     return aligned && ld_x <= (int64_t(1) << 20) ? (int)(d_in / MX_PAD) : 0;
+}
+
+void activations(MatArgs& a, const void* X, gptq_dtype dt, int64_t ld_x) {
+    a.X = X;
+    a.ld_x = a.n_tok == 1 ? ceil_div(a.d_in, 8) * 8 : ld_x;      // of no use for one token
+    a.aligned = ((uintptr_t)X | (uintptr_t)(a.ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
+    a.full = whole_steps(a.aligned, a.d_in, a.ld_x);
 }
 
 }  // namespace
@@ -1145,11 +1317,7 @@ gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_
                              const uint8_t* codes, const uint8_t* scales, int64_t d_out, float* Y, int64_t ld_y,
                              hipStream_t s) {
     MatArgs a = mat_args(codes, scales, n_tok, d_in, d_out, Y, ld_y);
-    a.X = X;
-    a.ld_x = ld_x;
-    if (n_tok == 1) ld_x = a.ld_x = ceil_div(d_in, 8) * 8;   // of no use
-    a.aligned = ((uintptr_t)X | (uintptr_t)(ld_x * (dt == GPTQ_F32 ? 4 : 2))) % 16 == 0;
-    a.full = whole_steps(a.aligned, d_in, ld_x);
+    activations(a, X, dt, ld_x);
     gptq_status st;
     switch (dt) {
         case GPTQ_BF16: st = launch_parts<ACT_BF16>(a, s); break;
@@ -1169,6 +1337,36 @@ gptq_status mx_matmul_quantized_launch(const uint8_t* xc, const uint8_t* xs, gpt
     m.XS = xs;
     m.ld_x = mx_code_bytes(d_in, xf);
     const gptq_status st = xf == GPTQ_MX_FP8 ? launch_parts<ACT_FP8>(m, s) : launch_parts<ACT_FP4>(m, s);
+    if (st != GPTQ_OK) return st;
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+gptq_status mx_gated_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t ld_x, const uint8_t* codes,
+                            const uint8_t* scales, int64_t d_ff, const GatedArgs& g, hipStream_t s) {
+    MatArgs a = mat_args(codes, scales, n_tok, d_in, d_ff, nullptr, g.ld_y);
+    gate_args(a, g);
+    activations(a, X, dt, ld_x);
+    gptq_status st;
+    switch (dt) {
+        case GPTQ_BF16: st = launch_gated<ACT_BF16>(a, s); break;
+        case GPTQ_F16: st = launch_gated<ACT_F16>(a, s); break;
+        default: st = launch_gated<ACT_F32>(a, s); break;
+    }
+    if (st != GPTQ_OK) return st;
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+gptq_status mx_gated_quantized_launch(const uint8_t* xc, const uint8_t* xs, gptq_mx_format xf, int64_t n_tok, int64_t d_in,
+                                      const uint8_t* codes, const uint8_t* scales, int64_t d_ff, const GatedArgs& g,
+                                      hipStream_t s) {
+    MatArgs a = mat_args(codes, scales, n_tok, d_in, d_ff, nullptr, g.ld_y);
+    gate_args(a, g);
+    a.X = xc;
+    a.XS = xs;
+    a.ld_x = mx_code_bytes(d_in, xf);
+    const gptq_status st = xf == GPTQ_MX_FP8 ? launch_gated<ACT_FP8>(a, s) : launch_gated<ACT_FP4>(a, s);
     if (st != GPTQ_OK) return st;
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;

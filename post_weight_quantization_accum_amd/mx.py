@@ -14,6 +14,7 @@ from . import _lib
 from ._lib import load
 
 FORMATS = {"fp8": _lib.MX_FP8, "fp4": _lib.MX_FP4}
+ACTIVATIONS = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH, "relu": _lib.ACT_RELU}
 
 _t = None            # torch and the dtype codes, on first use
 _codes: dict = {}
@@ -201,4 +202,161 @@ def mx_matmul_quantized(x_codes, x_scales, codes, scales, x_fmt: str = "fp4", ou
     return out
 
 
-__all__ = ["mx_quantize", "mx_dequantize", "mx_matmul", "mx_matmul_quantized", "mx_codes_per_row", "mx_scales_per_row"]
+def _act(act: str) -> int:
+    a = ACTIVATIONS.get(act)
+    if a is None:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    return a
+
+
+def _weights(gate, up):
+    """(rows, padded columns) of a gate and up of one shape, each a pair of codes and scales."""
+    shape = _mx_pair(*gate, "fp4", "gate")
+    if _mx_pair(*up, "fp4", "up") != shape:
+        raise ValueError("gate and up differ in shape")
+    return shape
+
+
+def _rows_like(t, name, n, d, dtype=None):
+    """Row stride of a rows x d tensor."""
+    n_t, d_t, ld = _rows(t, name)
+    if (n_t, d_t) != (n, d) or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {n} x {d} with unit column stride, of the dtype the call names")
+    return ld
+
+
+def _gated_out(like, n, d_ff, dtype, pre, out):
+    """Outputs (Y[, G, U]) of a gated product and the row strides of Y and of G and U."""
+    if out is None:
+        new = [like.new_empty((n, d_ff), dtype=dtype) for _ in range(3 if pre else 1)]
+        return new, max(d_ff, 1), max(d_ff, 1)
+    out = list(out) if isinstance(out, (tuple, list)) else [out]
+    if len(out) != (3 if pre else 1):
+        raise TypeError("out must be Y, or Y, G and U with pre")
+    _gpu(like, *out)
+    dtype = dtype or out[0].dtype
+    lds = [_rows_like(t, "out", n, d_ff, dtype) for t in out]
+    if pre and lds[1] != lds[2]:
+        raise TypeError("out: G and U must have one row stride")
+    return out, lds[0], lds[-1]
+
+
+def mx_gated(X, gate, up, act: str = "silu", *, dtype=None, pre: bool = False, out=None, stream=None):
+    """Y = act(X gate^T) * (X up^T), tokens x d_ff; gate, up: the (codes, scales) of e2m1 matrices of d_ff rows.
+
+    X bf16 / f16 / f32; act: "silu", "gelu", "gelu_tanh" or "relu".  Y is of
+    dtype (X's unless given).  With pre, (Y, G, U): also the products with gate
+    and up, for mx_gated_backward.  out: Y, or (Y, G, U), to write to.
+    """
+    lib, a = load(), _act(act)
+    dev = _gpu(X, *gate, *up)
+    n, d, ld = _rows(X)
+    d_ff, padded = _weights(gate, up)
+    dt = _dtype_code(X)
+    if not padded - 128 < d <= padded:
+        raise ValueError("X and gate differ in columns")
+    with _on(dev, stream):
+        out, ld_y, ld_gu = _gated_out(X, n, d_ff, dtype or (X.dtype if out is None else None), pre, out)
+        G, U = (out[1].data_ptr(), out[2].data_ptr()) if pre else (None, None)
+        st = lib.gptq_mx_gated(X.data_ptr(), dt, n, d, ld, gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(),
+                               up[1].data_ptr(), d_ff, a, out[0].data_ptr(), _dtype_code(out[0]), ld_y, G, U, ld_gu,
+                               _current(dev))
+    if st:
+        _lib.check(st, "gptq_mx_gated")
+    return tuple(out) if pre else out[0]
+
+
+def mx_gated_quantized(x_codes, x_scales, gate, up, act: str = "silu", *, x_fmt: str = "fp4", dtype=None, pre: bool = False,
+                       out=None, stream=None):
+    """mx_gated with microscaled activations (x_codes, x_scales of x_fmt); dtype float32 unless given."""
+    lib, torch, a, f = load(), _torch(), _act(act), _format(x_fmt)
+    dev = _gpu(x_codes, x_scales, *gate, *up)
+    n, d = _mx_pair(x_codes, x_scales, x_fmt, "x_codes")
+    d_ff, padded = _weights(gate, up)
+    if d != padded:
+        raise ValueError("x_codes and gate differ in columns")
+    with _on(dev, stream):
+        out, ld_y, ld_gu = _gated_out(x_codes, n, d_ff, dtype or (torch.float32 if out is None else None), pre, out)
+        G, U = (out[1].data_ptr(), out[2].data_ptr()) if pre else (None, None)
+        st = lib.gptq_mx_gated_quantized(x_codes.data_ptr(), x_scales.data_ptr(), f, n, d, gate[0].data_ptr(),
+                                         gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), d_ff, a, out[0].data_ptr(),
+                                         _dtype_code(out[0]), ld_y, G, U, ld_gu, _current(dev))
+    if st:
+        _lib.check(st, "gptq_mx_gated_quantized")
+    return tuple(out) if pre else out[0]
+
+
+def _grad_out(like, n, d_in, dtype, out):
+    if out is None:
+        return like.new_empty((n, d_in), dtype=dtype), d_in
+    _gpu(like, out)
+    return out, _rows_like(out, "out", n, d_in, dtype)
+
+
+def _scratch(like, nws, workspace):
+    """(workspace or None, its bytes)"""
+    if workspace is None:
+        return (like.new_empty(nws, dtype=_torch().uint8) if nws else None), nws
+    _gpu(like, workspace)
+    if not workspace.is_contiguous():
+        raise TypeError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def mx_matmul_backward(dY, codes, scales, d_in: int, *, dtype=None, out=None, workspace=None, stream=None):
+    """dX = dY W, tokens x d_in: mx_matmul's gradient for its activations (W the e2m1 values of codes and scales).
+
+    dY bf16 / f16 / f32; dX of dtype (dY's unless given).
+    """
+    lib = load()
+    dev = _gpu(dY, codes, scales)
+    n, d_out, ld = _rows(dY, "dY")
+    rows, padded = _mx_pair(codes, scales, "fp4")
+    dt = _dtype_code(dY)
+    if rows != d_out or not padded - 128 < d_in <= padded:
+        raise ValueError("dY, codes and d_in do not match")
+    with _on(dev, stream):
+        out, ld_dx = _grad_out(dY, n, d_in, dtype, out)
+        ws, nws = _scratch(dY, lib.gptq_mx_matmul_backward_workspace(dt, n, d_in, d_out), workspace)
+        st = lib.gptq_mx_matmul_backward(dY.data_ptr(), dt, n, d_out, ld, codes.data_ptr(), scales.data_ptr(), d_in,
+                                         out.data_ptr(), _dtype_code(out), ld_dx, None if ws is None else ws.data_ptr(), nws,
+                                         _current(dev))
+    if st:
+        _lib.check(st, "gptq_mx_matmul_backward")
+    return out
+
+
+def mx_gated_backward(dY, G, U, gate, up, d_in: int, act: str = "silu", *, dtype=None, pre: bool = False, out=None,
+                      workspace=None, stream=None):
+    """dX = dG gate + dU up, tokens x d_in: mx_gated's gradient for its activations.
+
+    dY: Y's gradient; G, U: as mx_gated gave them with pre (all of one dtype).
+    dX is of dtype (dY's unless given).  With pre, (dX, dG, dU): also the
+    gradients of the products with gate and up, of dY's dtype.
+    """
+    lib, a = load(), _act(act)
+    dev = _gpu(dY, G, U, *gate, *up)
+    n, d_ff, ld = _rows(dY, "dY")
+    rows, padded = _weights(gate, up)
+    dt = _dtype_code(dY)
+    if rows != d_ff or not padded - 128 < d_in <= padded:
+        raise ValueError("dY, gate and d_in do not match")
+    ld_gu = _rows_like(G, "G", n, d_ff, dY.dtype)
+    if _rows_like(U, "U", n, d_ff, dY.dtype) != ld_gu:
+        raise TypeError("G and U must have one row stride")
+    with _on(dev, stream):
+        out, ld_dx = _grad_out(dY, n, d_in, dtype, out)
+        dG, dU = (dY.new_empty((n, d_ff)) for _ in range(2)) if pre else (None, None)
+        ws, nws = _scratch(dY, lib.gptq_mx_gated_backward_workspace(dt, n, d_in, d_ff), workspace)
+        st = lib.gptq_mx_gated_backward(dY.data_ptr(), dt, n, d_ff, ld, G.data_ptr(), U.data_ptr(), ld_gu, gate[0].data_ptr(),
+                                        gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), d_in, a, out.data_ptr(),
+                                        _dtype_code(out), ld_dx, None if dG is None else dG.data_ptr(),
+                                        None if dU is None else dU.data_ptr(), max(d_ff, 1),
+                                        None if ws is None else ws.data_ptr(), nws, _current(dev))
+    if st:
+        _lib.check(st, "gptq_mx_gated_backward")
+    return (out, dG, dU) if pre else out
+
+
+__all__ = ["mx_quantize", "mx_dequantize", "mx_matmul", "mx_matmul_quantized", "mx_gated", "mx_gated_quantized",
+           "mx_matmul_backward", "mx_gated_backward", "mx_codes_per_row", "mx_scales_per_row"]
