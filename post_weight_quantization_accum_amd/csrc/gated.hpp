@@ -93,22 +93,20 @@ gptq_status mx_gated_quantized_launch(const uint8_t* xc, const uint8_t* xs, gptq
                                       const uint8_t* codes, const uint8_t* scales, int64_t d_ff, const GatedArgs& g,
                                       hipStream_t s);
 
-// The gradient of products for their activations: one matrix of codes, or two
-// whose rows follow one another.
+// The gradient of products for their activations: one matrix of codes, or the
+// sum over two.
 struct BackArgs {
-    const void* D;                       // gradients, n_tok x rows of dt (of two matrices: the second's rows d2 further)
-    gptq_dtype dt;
-    int64_t n_tok, ld, d2;
-    const int32_t* exps;                 // null, or a power of two for each token, by which its sums are multiplied
+    gptq_dtype dt;                       // of the gradients
+    int64_t n_tok, rows, d_in;           // rows: of each matrix
     const uint8_t *codes[2], *scales[2];
     int matrices;
-    int64_t rows, d_in;
+    const int32_t* exps;                 // null, or a power of two for each token, by which its sums are multiplied
     void* dX;
     gptq_dtype dx_dt;
     int64_t ld_dx;
 };
-size_t mx_backward_ws(gptq_dtype dt, int matrices, int64_t n_tok, int64_t d_in, int64_t rows);
-gptq_status mx_backward_launch(const BackArgs& a, void* ws, hipStream_t s);
+size_t mx_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t rows);
+gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, void* ws, hipStream_t s);
 
 struct GatedBackArgs {
     const void *dY, *G, *U;

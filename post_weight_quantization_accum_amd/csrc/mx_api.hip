@@ -130,7 +130,7 @@ gptq_status gptq_mx_gated_quantized(const uint8_t* x_codes, const uint8_t* x_sca
 
 size_t gptq_mx_matmul_backward_workspace(gptq_dtype dy_dtype, int64_t n_tok, int64_t d_in, int64_t d_out) {
     if (!is_float(dy_dtype) || !in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 1, MAX_DIM)) return 0;
-    return mx_backward_ws(dy_dtype, 1, n_tok, d_in, d_out);
+    return mx_backward_ws(dy_dtype, n_tok, d_in, d_out);
 }
 
 gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t n_tok, int64_t d_out, int64_t ld_dy,
@@ -142,13 +142,11 @@ gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t
     if (ld_dy < d_out || ld_dx < d_in) return GPTQ_ERR_INVALID_ARG;
     if (n_tok == 0) return GPTQ_OK;
     if (!elems(dX, dx_dtype) || (d_out > 0 && (!elems(dY, dy_dtype) || !matrix(codes, scales)))) return GPTQ_ERR_INVALID_ARG;
-    const size_t need = d_out > 0 ? mx_backward_ws(dy_dtype, 1, n_tok, d_in, d_out) : 0;
+    const size_t need = d_out > 0 ? mx_backward_ws(dy_dtype, n_tok, d_in, d_out) : 0;
     if (need && (!on(workspace, 16) || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
     BackArgs a{};
-    a.D = dY;
     a.dt = dy_dtype;
     a.n_tok = n_tok;
-    a.ld = ld_dy;
     a.codes[0] = codes;
     a.scales[0] = scales;
     a.matrices = 1;
@@ -157,7 +155,7 @@ gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t
     a.dX = dX;
     a.dx_dt = dx_dtype;
     a.ld_dx = ld_dx;
-    return mx_backward_launch(a, workspace, stream);
+    return mx_backward_launch(a, dY, ld_dy, workspace, stream);
 }
 
 size_t gptq_mx_gated_backward_workspace(gptq_dtype dtype, int64_t n_tok, int64_t d_in, int64_t d_ff) {
