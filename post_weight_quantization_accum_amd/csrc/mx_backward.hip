@@ -2,6 +2,8 @@
 // dX = dY W (include/gptq.h, gptq_mx_matmul_backward), and of gated products,
 // dX = dG Wg + dU Wu (gptq_mx_gated_backward).
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "gated.hpp"
 
@@ -48,50 +50,84 @@ struct Call {
 };
 
 // ---------------------------------------------------------------------------
-// 256 columns x 64 TF tokens per workgroup of 2 x 2 waves, each 128 columns x
-// 32 TF tokens in v_mfma_f32_32x32x16, in stages of 64 rows of the matrix.
+// 256 columns x 32 TF TW tokens per workgroup of 2 x TW waves, each 128 columns
+// x 32 TF tokens in v_mfma_f32_32x32x16, in stages of 64 rows of the matrix.
 //
 // The weights' rows are the sum's index here, and a lane of the instruction
 // wants eight rows of one column, while memory holds a column's rows apart.  So
-// codes are turned once per workgroup, byte by byte: a thread takes eight rows
-// of eight columns (eight words), and stores for each of the four bytes of a
-// word (a pair of columns) its eight rows in a row.  A lane then reads the eight
-// rows of four neighbouring columns as 16 bytes, converts the two columns of a
-// byte with their row's scale in one instruction, and puts two rows' halves
-// together with a byte permute: five instructions for four values, of which each
-// wave's serve TF products.  Scale bytes are turned alike, and enter the
-// conversions shifted to a float's exponent (bits beside it are ignored).
+// a thread takes eight rows of four or eight columns, converts the two columns of
+// a byte with their row's scale in one instruction, puts two rows' halves together
+// with a byte permute, and stores eight rows of each column in a row: one
+// instruction a value, once a workgroup.
 //
-// Everything comes from memory to LDS without registers: gradients to a ring of
-// three slots two stages ahead (16-byte chunk c of a token at slot c ^ (token %
-// 8)), codes and scales as they are to another ring, three stages ahead, from
-// where they are turned during the stage before theirs.  A step's operands are
-// read from LDS, and its weights converted, while the one before multiplies;
-// the barrier of a stage stands before its last step, whose operands are in
+// Codes, scales and gradients come from memory to rings of LDS slots without
+// registers, some stages ahead; a stage's codes are converted during the stage
+// before.  A step's operands are read while the one before multiplies, and the
+// barrier of a stage stands before its last step, whose operands are in
 // registers by then, so that the matrix instructions run on behind it.
 //
-// Lane l ends with columns 4 m + c of its tokens (m the row of the instruction's
-// result, c the column of its four): sixteen neighbours at a time.
+// Tokens lie in LDS in order, column c at place (c % 4) 64 + c / 4; 16-byte chunk
+// q (eight rows) of place i at slot q ^ (i / 2 % 8), so that sixteen lanes' reads
+// of one chunk of neighbouring places hit all banks.  Lane l ends with columns 4 m + c of its tokens (m the row of
+// the instruction's result, c the column of its four): sixteen neighbours at a
+// time.
 // ---------------------------------------------------------------------------
 constexpr int BN = 256, SK = 64;
 constexpr int RAW = SK * BN / 2, RAW_S = SK * BN / 32;     // bytes of a stage's codes and scales
-template <int TF>
+constexpr int WT = SK * BN * 2;                            // and of its weights
+template <int TF, int TW>
 struct BackTile {
-    static constexpr int BT = 64 * TF, X = BT * SK * 2;
-    static constexpr int CODES = 3 * X, RAWS = CODES + 2 * RAW, SCALES = RAWS + 3 * RAW, RAW_SCALES = SCALES + 2 * RAW_S;
-    static constexpr int BYTES = RAW_SCALES + 3 * RAW_S;
-    static constexpr int X_DMA = X / 1024 / 4, W_DMA = RAW / 1024 / 4, DMA = X_DMA + W_DMA + 1;   // per wave and stage
+    static constexpr int BT = 32 * TF * TW, X = BT * SK * 2, WAVES = 2 * TW;
+    static constexpr int R = BT > 128 ? 2 : BT > 64 ? 3 : 4;                             // slots of a ring
+    static constexpr int W = R * X, RAWS = W + 2 * WT, RAW_SCALES = RAWS + R * RAW, BYTES = RAW_SCALES + R * RAW_S;
+    // per wave and stage; the scales are two instructions, which some waves repeat
+    static constexpr int X_DMA = X / 1024 / WAVES, W_DMA = RAW / 1024 / WAVES, DMA = X_DMA + W_DMA + 1;
+    // Behind the barrier of stage s - 1 the codes of s + R and the gradients of
+    // s + R - 1 are asked for, into the slots that it let go.  At that of s the codes
+    // of s + 2 and the gradients of s + 1 have landed if only what R - 2 stages
+    // asked for since is under way.
+    static constexpr int WAIT = (R - 2) * DMA;
+    static constexpr int PAIRS = 16 / WAVES;               // of columns that a thread converts: 4, or 2 of 8 waves
+    static_assert(BYTES <= 160 * 1024 - 1024 && WAIT < 64, "LDS and counters");
+    static_assert(WAVES == 4 || WAVES == 8, "threads of the conversion");
 };
 
-// A float whose exponent is byte E of w.
-template <int E>
-__device__ __forceinline__ float scale_of(uint32_t w) {
-    return __uint_as_float(E == 0 ? w << 23 : E == 1 ? w << 15 : E == 2 ? w << 7 : w >> 1);
+// As dma_16 of mx.hpp, with the address in LDS and that in memory each the sum of
+// a register and something the wave shares.
+__device__ __forceinline__ void dma_16_at(uint32_t to, int plus, uint32_t off, int at, u32x4_t buf) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+                 : : "s"(to), "n"(plus), "v"(off), "s"(buf), "s"(at) : "memory", "scc");
+}
+// A raw buffer from uniform values.
+__device__ __forceinline__ u32x4_t buffer_at(const void* p, uint32_t bytes) {
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    return u32x4_t{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
 
-template <bool HALF, int TF>
-__global__ __launch_bounds__(256, TF > 2 ? 1 : 2) void mx_back_kernel(Call c) {
-    using T = BackTile<TF>;
+// f(0), f(1), .. f(N - 1), each number a constant.
+template <class F, int... I>
+__device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+    for_each(f, std::make_integer_sequence<int, N>{});
+}
+
+// An address in LDS that stays in its register, for constants to be added by the
+// instructions (which have room for 16 bits of them).
+__device__ __forceinline__ uint32_t held(uint32_t at) {
+    asm volatile("" : "+v"(at));
+    return at;
+}
+template <class V>
+__device__ __forceinline__ __attribute__((address_space(3))) V& lds_at(uint32_t at, int plus) {
+    return *(__attribute__((address_space(3))) V*)(uintptr_t)(at + plus);
+}
+
+template <bool HALF, int TF, int TW>
+__global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
+    using T = BackTile<TF, TW>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const BackArgs& a = c.b;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -103,7 +139,7 @@ __global__ __launch_bounds__(256, TF > 2 ? 1 : 2) void mx_back_kernel(Call c) {
     const uint32_t id = blockIdx.x < each * 8 ? (blockIdx.x % 8) * each + blockIdx.x / 8 : blockIdx.x;
     const int part = (int)(id / (nt * nn));
     const int64_t n0 = (int64_t)(id / nt % nn) * BN, t0 = (int64_t)(id % nt) * T::BT;
-    const int nw = 128 * (wave >> 1), tw = 32 * TF * (wave & 1);
+    const int nw = 128 * (wave / TW), tw = 32 * TF * (wave % TW);
     const int first = part * c.per, end = min(first + c.per, c.stages * a.matrices * c.planes), S = end - first;
 
     // this thread's pieces
@@ -111,46 +147,62 @@ __global__ __launch_bounds__(256, TF > 2 ? 1 : 2) void mx_back_kernel(Call c) {
     uint32_t xoff[T::X_DMA], woff[T::W_DMA], soff;
 #pragma unroll
     for (int j = 0; j < T::X_DMA; ++j) {                  // eight tokens an instruction
-        const int t = 8 * (wave + 4 * j) + (lane >> 3), ch = (lane & 7) ^ (t & 7);
+        const int t = 8 * (wave + T::WAVES * j) + (lane >> 3), ch = (lane & 7) ^ (t >> 1 & 7);
         xoff[j] = (uint32_t)(min((int64_t)t, tn - 1) * c.ld * 2 + 16 * ch);
     }
 #pragma unroll
     for (int j = 0; j < T::W_DMA; ++j) {                  // eight rows an instruction
-        const int k = 8 * (wave + 4 * j) + (lane >> 3);
+        const int k = 8 * (wave + T::WAVES * j) + (lane >> 3);
         const int64_t at = n0 / 2 + 16 * (lane & 7);
         woff[j] = at < c.w_row ? (uint32_t)(k * c.w_row + at) : 1u << 31;
     }
-    {                                                     // 32 rows an instruction; waves 2, 3 as 0, 1
+    {                                                     // 32 rows an instruction
         const int k = 32 * (wave & 1) + (lane >> 1);
         const int64_t at = n0 / 32 + 4 * (lane & 1);
         soff = at < c.s_row ? (uint32_t)(k * c.s_row + at) : 1u << 31;
     }
     const uint32_t base = (uint32_t)(uintptr_t)lds;
-    // segment and first row of a stage
-    const auto place = [&](int f, int& seg, int64_t& k0) {
-        const int st = first + min(f, S - 1);
-        seg = __builtin_amdgcn_readfirstlane(st / c.stages);
-        k0 = (int64_t)(st - seg * c.stages) * SK;
-    };
-    const auto fetch_x = [&](int f, int slot, int from, int to) {
-        int seg;
-        int64_t k0;
-        place(f, seg, k0);
-        const u32x4_t b = buffer_of(c.D + t0 * c.ld + seg * c.pad + k0, ((tn - 1) * c.ld + SK) * 2);
+    // Stages come one after another in D's rows, over the segments.  Past the
+    // last one the fetches repeat it, into slots that nobody reads.
+    const u32x4_t xb = buffer_of(c.D + t0 * c.ld, ((tn - 1) * c.ld + (int64_t)c.stages * a.matrices * c.planes * SK) * 2);
+    int xcol = 2 * SK * first;
+    const int xlast = 2 * SK * (end - 1);
+    const auto fetch_x = [&](int slot, int from, int to) {
 #pragma unroll
-        for (int j = from; j < to; ++j) dma_16(base + slot * T::X + 1024 * (wave + 4 * j), xoff[j], b);
+        for (int j = from; j < to; ++j) dma_16_at(base + slot * T::X + 1024 * wave, 1024 * T::WAVES * j, xoff[j], xcol, xb);
+        if (to == T::X_DMA) xcol = min(xcol + 2 * SK, xlast);
     };
-    const auto fetch_w = [&](int f, int slot) {
-        int seg;
-        int64_t k0;
-        place(f, seg, k0);
-        const int m = seg / c.planes;
-        const int64_t rows = min((int64_t)SK, a.rows - k0);
-        const u32x4_t wb = buffer_of(a.codes[m] + k0 * c.w_row, rows * c.w_row);
-        const u32x4_t sb = buffer_of(a.scales[m] + k0 * c.s_row, rows * c.s_row);
-#pragma unroll
-        for (int j = 0; j < T::W_DMA; ++j) dma_16(base + T::RAWS + slot * RAW + 1024 * (wave + 4 * j), woff[j], wb);
+    // codes and scales from here on, and of the matrices
+    const uint8_t *wp, *sp, *wp0 = a.codes[0], *sp0 = a.scales[0], *wp1 = a.codes[1], *sp1 = a.scales[1];
+    int64_t wrows;                                                    // left of the segment
+    int wseg = first / c.stages, wleft = S;
+    {
+        const int64_t k0 = (int64_t)(first - wseg * c.stages) * SK;
+        const int m = wseg >= c.planes;
+        wp = a.codes[m] + k0 * c.w_row;
+        sp = a.scales[m] + k0 * c.s_row;
+        wrows = a.rows - k0;
+    }
+    u32x4_t wb, sb;
+    const auto fetch_w = [&](int slot, int piece) {
+        if (piece == 0) {
+            const uint32_t rows = (uint32_t)min((int64_t)SK, wrows);
+            wb = buffer_at(wp, rows * (uint32_t)c.w_row);
+            sb = buffer_at(sp, rows * (uint32_t)c.s_row);
+        }
+        if (piece < T::W_DMA) {
+            dma_16_at(base + T::RAWS + slot * RAW + 1024 * wave, 1024 * T::WAVES * piece, woff[piece], 0, wb);
+            return;
+        }
         dma_4(base + T::RAW_SCALES + slot * RAW_S + 256 * (wave & 1), soff, sb);
+        // on to the next rows, or the next segment's first (no branch: it would
+        // part the loop, and with it what is ordered among the products)
+        const bool more = --wleft > 0, turns = more && wrows <= SK;
+        wseg += turns;
+        const bool second = wseg >= c.planes;
+        wp = turns ? (second ? wp1 : wp0) : wp + (more ? SK * c.w_row : 0);
+        sp = turns ? (second ? sp1 : sp0) : sp + (more ? SK * c.s_row : 0);
+        wrows = turns ? a.rows : wrows - (more ? SK : 0);
     };
 
     f16_t acc[4][TF];
@@ -160,130 +212,168 @@ __global__ __launch_bounds__(256, TF > 2 ? 1 : 2) void mx_back_kernel(Call c) {
         for (int j = 0; j < TF; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    bool left = false;       // a block whose scale float16 lacks
+    uint32_t left = 0;       // not 0: codes whose scale float16 lacks
 
-    // turning: thread (q, o) has rows 8 q .. + 7 of column octet o
-    const int q8 = threadIdx.x >> 5, o8 = threadIdx.x & 31;
-    struct Turn {
+    // conversion: thread (q, o) has rows 8 q .. + 7 of the o-th group of 2 PAIRS
+    // columns, whose codes a word or half of one holds
+    constexpr int PC = T::PAIRS, GROUPS = BN / 2 / PC;
+    const int q8 = threadIdx.x / GROUPS, o8 = threadIdx.x % GROUPS;
+    struct Raw {
         uint32_t w[8], s[8];
     };
-    const auto turn_read = [&](int slot, Turn& r) {
-        const char* w = lds + T::RAWS + slot * RAW + 8 * q8 * (BN / 2) + 4 * o8;
-        const char* s = lds + T::RAW_SCALES + slot * RAW_S + 8 * q8 * (BN / 32) + (o8 >> 2);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            r.w[k] = *(const uint32_t*)(w + k * (BN / 2));
-            r.s[k] = *(const uint8_t*)(s + k * (BN / 32));
-        }
+    uint32_t code_at = held(base + T::RAWS + 8 * q8 * (BN / 2) + PC * o8);
+    uint32_t scale_at = held(base + T::RAW_SCALES + 8 * q8 * (BN / 32) + o8 / (16 / PC));
+    const auto raw_read = [&](Raw& r, int k) {
+        if constexpr (PC == 4) r.w[k] = lds_at<uint32_t>(code_at, k * (BN / 2));
+        else r.w[k] = lds_at<uint16_t>(code_at, k * (BN / 2));
+        r.s[k] = lds_at<uint8_t>(scale_at, k * (BN / 32));
     };
-    const auto turn_write = [&](int slot, const Turn& r) {
-        if constexpr (HALF) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) left |= r.s[k] - 104u > 36u && (r.w[k] != 0u || r.s[k] == 255u);
-        }
-        // byte b of four words
-        const auto four = [&](int k, auto b) {
-            constexpr uint32_t B = decltype(b)::value;
-            const uint32_t lo = __builtin_amdgcn_perm(r.w[k + 1], r.w[k], (4 + B) << 8 | B | 0x0C0C0000u);
-            const uint32_t hi = __builtin_amdgcn_perm(r.w[k + 3], r.w[k + 2], (4 + B) << 24 | B << 16 | 0x0C0Cu);
-            return lo | hi;
-        };
-        using B0 = std::integral_constant<uint32_t, 0>;
-        using B1 = std::integral_constant<uint32_t, 1>;
-        using B2 = std::integral_constant<uint32_t, 2>;
-        using B3 = std::integral_constant<uint32_t, 3>;
-        u32x4_t* to = (u32x4_t*)(lds + T::CODES + slot * RAW + q8 * (BN / 2 * 8) + 32 * o8);
-        to[0] = u32x4_t{four(0, B0{}), four(4, B0{}), four(0, B1{}), four(4, B1{})};
-        to[1] = u32x4_t{four(0, B2{}), four(4, B2{}), four(0, B3{}), four(4, B3{})};
-        if ((o8 & 3) == 0) {
-            u32x2_t v;
-            v.x = r.s[0] | r.s[1] << 8 | r.s[2] << 16 | r.s[3] << 24;
-            v.y = r.s[4] | r.s[5] << 8 | r.s[6] << 16 | r.s[7] << 24;
-            *(u32x2_t*)(lds + T::SCALES + slot * RAW_S + q8 * (BN / 32 * 8) + 8 * (o8 >> 2)) = v;
-        }
+    // codes that are not all zero with a scale byte outside 104 .. 140 (byte 255
+    // makes NaN of float16, too)
+    const auto look = [&](const Raw& r, int k) {
+        left |= min(__builtin_elementwise_sub_sat(r.s[k] - 104u, 36u), r.w[k]);
     };
+    // two rows of a pair of columns
+    const auto convert = [](const Raw& r, const float (&sc)[8], auto pair, int k, u32x4_t (&v)[2]) {
+        constexpr int P = decltype(pair)::value;
+        const uint32_t a = H16<!HALF>::template fp4<P>(r.w[2 * k], sc[2 * k]);
+        const uint32_t b = H16<!HALF>::template fp4<P>(r.w[2 * k + 1], sc[2 * k + 1]);
+        v[0][k] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+        v[1][k] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    };
+    // column c of the group: column 2 PC o + c of the tile, at place (c % 4) 64 + PC o / 2 + c / 4
+    uint32_t to = held(base + T::W + PC / 2 * o8 * (SK * 2) + 16 * ((q8 ^ PC * o8 / 4) & 7));
+    const auto write = [&](int c, u32x4_t v) { lds_at<u32x4_t>(to, ((c & 3) * 64 + (c >> 2)) * (SK * 2)) = v; };
 
-    // a step's operands as LDS holds them
+    // a step's operands
     struct Step {
-        u32x4_t x[TF], w;
-        u32x2_t s;
+        u32x4_t w[4], x[TF];
     };
-    const auto read = [&](int xslot, int wslot, int ks, Step& r) {
-        const int q = 2 * ks + h;
-        r.w = *(const u32x4_t*)(lds + T::CODES + wslot * RAW + q * (BN / 2 * 8) + 4 * nw + 16 * i32);
-        r.s = *(const u32x2_t*)(lds + T::SCALES + wslot * RAW_S + q * (BN / 32 * 8) + 8 * (nw / 32 + (i32 >> 3)));
-        const char* xp = lds + xslot * T::X + (tw + i32) * (SK * 2) + 16 * (q ^ (i32 & 7));
+    // in the order of their use: x0, the weights (columns 4 i32 + i), the other x
+    uint32_t x_at[4], w_at[4];
 #pragma unroll
-        for (int j = 0; j < TF; ++j) r.x[j] = *(const u32x4_t*)(xp + 32 * SK * 2 * j);
-    };
-    // its weights: four columns of eight rows
-    const auto convert = [](const Step& r, u32x4_t (&w)[4]) {
-        const float s[8] = {scale_of<0>(r.s.x), scale_of<1>(r.s.x), scale_of<2>(r.s.x), scale_of<3>(r.s.x),
-                            scale_of<0>(r.s.y), scale_of<1>(r.s.y), scale_of<2>(r.s.y), scale_of<3>(r.s.y)};
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {                 // rows 4 k .. + 3 of a pair of columns
-                const uint32_t v = r.w[2 * p + k];
-                const uint32_t v0 = H16<!HALF>::template fp4<0>(v, s[4 * k]), v1 = H16<!HALF>::template fp4<1>(v, s[4 * k + 1]);
-                const uint32_t v2 = H16<!HALF>::template fp4<2>(v, s[4 * k + 2]), v3 = H16<!HALF>::template fp4<3>(v, s[4 * k + 3]);
-                w[2 * p][2 * k] = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
-                w[2 * p + 1][2 * k] = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
-                w[2 * p][2 * k + 1] = __builtin_amdgcn_perm(v3, v2, 0x05040100u);
-                w[2 * p + 1][2 * k + 1] = __builtin_amdgcn_perm(v3, v2, 0x07060302u);
-            }
+    for (int ks = 0; ks < 4; ++ks) {
+        const int chunk = 16 * ((2 * ks + h) ^ (i32 >> 1 & 7));
+        x_at[ks] = held(base + (tw + i32) * (SK * 2) + chunk);
+        w_at[ks] = held(base + T::W + (nw / 4 + i32) * (SK * 2) + chunk);
+    }
+    const auto read = [&](uint32_t x, uint32_t w, Step& r, int n) {
+        if (n == 0 || n > 4) {
+            const int j = n == 0 ? 0 : n - 4;
+            r.x[j] = lds_at<u32x4_t>(x, 32 * j * (SK * 2));
+        } else {
+            r.w[n - 1] = lds_at<u32x4_t>(w, 64 * (n - 1) * (SK * 2));
+        }
     };
 
-    fetch_w(0, 0);
-    fetch_w(1, 1);
-    fetch_x(0, 0, 0, T::X_DMA);
-    fetch_w(2, 2);
-    fetch_x(1, 1, 0, T::X_DMA);
-    wait_vmem<T::DMA>();                                  // the last two are under way
+    const auto ask_w = [&](int slot) {
+#pragma unroll
+        for (int e = 0; e <= T::W_DMA; ++e) fetch_w(slot, e);
+    };
+    for_each<T::R>([&](auto f) { ask_w(f); });
+    for_each<T::R - 1>([&](auto f) { fetch_x(f, 0, T::X_DMA); });
+    wait_vmem<0>();
     meet();
-    {
-        Turn r;
-        turn_read(0, r);
-        turn_write(0, r);
-    }
+    Raw r;
+    float sc[8];
+    u32x4_t v[2][2];
+    for_each<8>([&](auto k) {
+        raw_read(r, k);
+        sc[k] = mx_scale(r.s[k]);
+    });
+    for_each<PC>([&](auto p) {
+        for_each<4>([&](auto k) { convert(r, sc, p, k, v[0]); });
+        write(2 * p, v[0][0]);
+        write(2 * p + 1, v[0][1]);
+    });
+    if constexpr (HALF) for_each<8>([&](auto k) { look(r, k); });
     meet();
-    Step d[2];
-    u32x4_t w[2][4];
-    read(0, 0, 0, d[0]);
-    convert(d[0], w[0]);
-    int xs = 0, rs = 1;          // s % 3, (s + 1) % 3
+    ask_w(0);
+    Step d0, d1;
+    for_each<4 + TF>([&](auto n) { read(x_at[0], w_at[0], d0, n); });
+
+    // The ring's slots of this stage, as scalars; the lanes' addresses point at the
+    // stage's gradients and weights, at the next one's codes and where its weights
+    // go, and move on with the stages.
+    int slot = 0, wslot = 0;
+    const auto onward = [](int at, int bytes) { return at == T::R - 1 ? -(T::R - 1) * bytes : bytes; };
+    code_at += RAW;
+    scale_at += RAW_S;
+    to += WT;
     for (int s = 0; s < S; ++s) {
-        const int x1 = xs == 2 ? 0 : xs + 1, x2 = x1 == 2 ? 0 : x1 + 1;
-        Turn r;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            if (ks == 3) {
-                // before the last step, whose operands are here: the next stage's
-                // gradients, and the codes after its own, have landed
-                wait_vmem<T::DMA>();
-                meet();
-            }
-            if (ks == 0) turn_read(rs, r);
-            if (ks < 3) read(xs, s & 1, ks + 1, d[(ks + 1) & 1]);
-            else read(x1, (s + 1) & 1, 0, d[0]);
-            if (ks == 0) fetch_x(s + 2, x2, 0, T::X_DMA / 2);
-            if (ks == 1) fetch_x(s + 2, x2, T::X_DMA / 2, T::X_DMA);
-            if (ks == 2) fetch_w(s + 3, xs);
-            if (ks == 1) turn_write((s + 1) & 1, r);
-#pragma unroll
-            for (int j = 0; j < TF; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i][j] = H16<!HALF>::mfma32(w[ks & 1][i], d[ks & 1].x[j], acc[i][j]);
-            convert(d[(ks + 1) & 1], w[(ks + 1) & 1]);
-        }
-        xs = x1;
-        rs = rs == 2 ? 0 : rs + 1;
+        const int next = slot == T::R - 1 ? 0 : slot + 1, last = slot == 0 ? T::R - 1 : slot - 1;
+        const int dx = onward(slot, T::X), dw = wslot ? -WT : WT;
+        // Sixteen slots of a step beside its products, so that none waits for
+        // another's: the first half of a product's 32 clocks issues it, and four
+        // instructions or so are free in the second.  Requests to LDS and memory
+        // come one to a slot, or the waves' would wait in line.
+        const auto step = [&](auto k, Step& d, Step& dn) {
+            constexpr int ks = decltype(k)::value;
+            const auto work = [&](auto at) {
+                constexpr int n = decltype(at)::value;
+                if constexpr (ks < 3) {
+                    if constexpr (n < 4 + TF) read(x_at[(ks + 1) % 4], w_at[(ks + 1) % 4], dn, n);
+                } else {
+                    if constexpr (n == 0) {
+                        // before the last step's other products, whose operands are
+                        // here: the next stage's gradients, and the codes after its
+                        // own, have landed
+                        wait_vmem<T::WAIT>();
+                        meet();
+                        for_each<4>([&](auto i) {
+                            x_at[i] = held(x_at[i] + dx);
+                            w_at[i] = held(w_at[i] + dw);
+                        });
+                    }
+                    if constexpr (n > 0 && n < 5 + TF) read(x_at[0], w_at[0], dn, n - 1);
+                    // the slot of the codes converted last
+                    if constexpr (n >= 10 && n % 2 == 0 && n / 2 - 5 <= T::W_DMA) fetch_w(next, n / 2 - 5);
+                    if constexpr (n == 15) {
+                        code_at = held(code_at + onward(next, RAW));
+                        scale_at = held(scale_at + onward(next, RAW_S));
+                        to = held(to - dw);
+                    }
+                }
+                if constexpr (ks == 0) {
+                    // that of the last stage's gradients, an eighth at a time
+                    constexpr int from = n / 2 * T::X_DMA / 8, end = (n / 2 + 1) * T::X_DMA / 8;
+                    if constexpr (n % 2 == 0 && end > from) fetch_x(last, from, end);
+                    if constexpr (n >= 7 && n < 15) raw_read(r, n - 7);
+                }
+                if constexpr (ks == 1) {
+                    if constexpr (n == 3) for_each<8>([&](auto e8) { sc[e8] = mx_scale(r.s[e8]); });
+                    if constexpr (HALF && n >= 8) look(r, n - 8);
+                }
+                // the conversion's units: eight to a step of four pairs, four of two
+                constexpr int at_unit = ks == 1 ? n - 4 : n;
+                if constexpr ((ks == 1 || ks == 2) && at_unit >= 0 && at_unit < 12 && at_unit % 3 < PC / 2) {
+                    constexpr int unit = (ks - 1) * 2 * PC + at_unit / 3 * (PC / 2) + at_unit % 3, pair = unit / 4;
+                    convert(r, sc, std::integral_constant<int, pair>{}, unit % 4, v[pair & 1]);
+                    if constexpr (unit % 4 == 3) {
+                        write(2 * pair, v[pair & 1][0]);
+                        write(2 * pair + 1, v[pair & 1][1]);
+                    }
+                }
+            };
+            for_each<4 * TF>([&](auto p) {
+                constexpr int P = decltype(p)::value, PER = 4 / TF;
+                acc[P % 4][P / 4] = H16<!HALF>::mfma32(d.w[P % 4], d.x[P / 4], acc[P % 4][P / 4]);
+                for_each<PER>([&](auto e) { work(std::integral_constant<int, P * PER + decltype(e)::value>{}); });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        step(std::integral_constant<int, 0>{}, d0, d1);
+        step(std::integral_constant<int, 1>{}, d1, d0);
+        step(std::integral_constant<int, 2>{}, d0, d1);
+        step(std::integral_constant<int, 3>{}, d1, d0);
+        slot = next;
+        wslot ^= 1;
     }
     wait_vmem<0>();              // nothing lands in LDS that is another's by then
 
     if constexpr (HALF) {
         // again with the gradients in two bfloat16 parts, from memory directly
-        if (__syncthreads_or(left)) {
+        if (__syncthreads_or(left != 0)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -331,29 +421,43 @@ __global__ __launch_bounds__(256, TF > 2 ? 1 : 2) void mx_back_kernel(Call c) {
         }
     }
 
+    // Out through LDS, 32 tokens of a wave at a time, in a region of its own: 128
+    // columns of a token in a row, which sixteen lanes read and store as eight each.
+    // (Straight from the registers, with all types and edges unrolled 32 times,
+    // the code alone took 17 us to come in.)  16-byte chunk q of token i at slot
+    // q ^ (i % 16).
+    meet();
+    char* const own = lds + wave * (32 * 512);
 #pragma unroll
     for (int j = 0; j < TF; ++j) {
-        const int64_t t = t0 + tw + 32 * j + i32;
-        if (t >= a.n_tok) continue;
-        const int e2 = a.exps && c.parts == 1 ? a.exps[t] : 0;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {                 // eight of a group's sixteen columns
-                const int64_t col = n0 + nw + 32 * g + 16 * h + 8 * o;
-                if (col >= a.d_in) continue;
-                const int m = (int)min((int64_t)8, a.d_in - col);
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = acc[e & 3][j][4 * g + 2 * o + (e >> 2)];
-                if (c.parts > 1) {
-                    store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * a.d_in + col, m, m == 8 && a.d_in % 4 == 0, v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
-                    store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, c.out8 && m == 8, v);
-                }
+            for (int e = 0; e < 4; ++e) {                 // columns 4 m .. + 3 of row m = 8 g + 4 h + e
+                const f32x4_t v = {acc[0][j][4 * g + e], acc[1][j][4 * g + e], acc[2][j][4 * g + e], acc[3][j][4 * g + e]};
+                *(f32x4_t*)(own + i32 * 512 + 16 * ((8 * g + 4 * h + e) ^ (i32 & 15))) = v;
             }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const int64_t col = n0 + nw + 8 * (lane & 15);
+        const int m = (int)max((int64_t)0, min((int64_t)8, a.d_in - col));
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+            const int i = 4 * q + (lane >> 4);
+            const int64_t t = t0 + tw + 32 * j + i;
+            const f32x4_t lo = *(const f32x4_t*)(own + i * 512 + 16 * ((2 * (lane & 15)) ^ (i & 15)));
+            const f32x4_t hi = *(const f32x4_t*)(own + i * 512 + 16 * ((2 * (lane & 15) + 1) ^ (i & 15)));
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (t >= a.n_tok || m == 0) continue;
+            if (c.parts > 1) {
+                store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * a.d_in + col, m, m == 8 && a.d_in % 4 == 0, v);
+            } else {
+                const int e2 = a.exps ? a.exps[t] : 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
+                store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, c.out8 && m == 8, v);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
@@ -388,8 +492,8 @@ __global__ __launch_bounds__(256) void mx_back_join_kernel(Call c) {
 struct Planes {
     const void* D;
     gptq_dtype dt;
-    int64_t n_tok, rows, ld, pad;
-    uint16_t* out;             // [token][plane][pad]
+    int64_t n_tok, rows, ld, pad, to;
+    uint16_t* out;             // [token][plane][pad], token to token `to` elements
     bool vec;
 };
 __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
@@ -403,14 +507,14 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
             u32x4_t p[3];
             cut(v, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.out + (t * 3 + j) * c.pad + k) = p[j];
+            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.out + t * c.to + j * c.pad + k) = p[j];
         } else {
             const uint16_t* d = (const uint16_t*)c.D + t * c.ld + k;
             u32x4_t w;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 w[i] = (2 * i < n ? d[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)d[2 * i + 1] : 0u) << 16;
-            *(u32x4_t*)(c.out + t * c.pad + k) = w;
+            *(u32x4_t*)(c.out + t * c.to + k) = w;
         }
     }
 }
@@ -423,7 +527,7 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 struct Gates {
     GatedBackArgs a;
     uint16_t* D;               // [token][2][pad] float16, or [token][2][3][pad] bfloat16 parts of float32 ones
-    int64_t pad;
+    int64_t pad, ld;           // token to token: ld elements
     int32_t* exps;             // null for float32
     bool vec, vec_out;
 };
@@ -483,16 +587,16 @@ __global__ __launch_bounds__(256) void mx_gates_kernel(Gates c) {
             u[i] = i < n ? ldexpf(u[i], e2) : 0.0f;
         }
         if (c.exps) {
-            store8(c.D, GPTQ_F16, t * 2 * c.pad + k, 8, true, g);
-            store8(c.D, GPTQ_F16, (t * 2 + 1) * c.pad + k, 8, true, u);
+            store8(c.D, GPTQ_F16, t * c.ld + k, 8, true, g);
+            store8(c.D, GPTQ_F16, t * c.ld + c.pad + k, 8, true, u);
         } else {
             u32x4_t p[3];
             cut(g, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + (t * 6 + j) * c.pad + k) = p[j];
+            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + t * c.ld + j * c.pad + k) = p[j];
             cut(u, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + (t * 6 + 3 + j) * c.pad + k) = p[j];
+            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + t * c.ld + (3 + j) * c.pad + k) = p[j];
         }
     }
 }
@@ -514,21 +618,25 @@ Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
 }
 
 int64_t padded(int64_t rows) { return ceil_div(rows, SK) * SK; }
+// Elements from token to token: an odd multiple of 256 bytes, so that one stage's
+// pieces of a tile's tokens lie on all channels of a cache (2 x 11008 rows apart
+// they hit a quarter of them).
+int64_t row_of(int64_t rows, int segments) { return (ceil_div(padded(rows) * segments, 128) | 1) * 128; }
 // bytes of the planes that a call makes of n_tok rows
 size_t planes_bytes(int64_t n_tok, int64_t rows, int segments) {
-    return align_up((size_t)n_tok * segments * padded(rows) * 2, 256);
+    return align_up((size_t)n_tok * row_of(rows, segments) * 2, 256);
 }
 size_t sums_bytes(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
     const Plan p = plan_of(segments, n_tok, d_in, rows);
     return p.parts > 1 ? (size_t)p.parts * n_tok * d_in * sizeof(float) : 0;
 }
 
-template <bool HALF, int TF>
+template <bool HALF, int TF, int TW>
 gptq_status launch_tile(const Call& c, hipStream_t s) {
-    using T = BackTile<TF>;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_back_kernel<HALF, TF>, T::BYTES));
+    using T = BackTile<TF, TW>;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_back_kernel<HALF, TF, TW>, T::BYTES));
     const int64_t tiles = ceil_div(c.b.d_in, BN) * ceil_div(c.b.n_tok, T::BT) * c.parts;
-    mx_back_kernel<HALF, TF><<<(unsigned)tiles, 256, T::BYTES, s>>>(c);
+    mx_back_kernel<HALF, TF, TW><<<(unsigned)tiles, 128 * TW, T::BYTES, s>>>(c);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -547,9 +655,9 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
     if (c.parts > 0) {
         const bool half = a.dt == GPTQ_F16;
         gptq_status st;
-        if (p.tf == 1) st = half ? launch_tile<true, 1>(c, s) : launch_tile<false, 1>(c, s);
-        else if (p.tf == 2) st = half ? launch_tile<true, 2>(c, s) : launch_tile<false, 2>(c, s);
-        else st = half ? launch_tile<true, 4>(c, s) : launch_tile<false, 4>(c, s);
+        if (p.tf == 1) st = half ? launch_tile<true, 1, 2>(c, s) : launch_tile<false, 1, 2>(c, s);
+        else if (p.tf == 2) st = half ? launch_tile<true, 1, 4>(c, s) : launch_tile<false, 1, 4>(c, s);
+        else st = half ? launch_tile<true, 4, 2>(c, s) : launch_tile<false, 4, 2>(c, s);
         if (st != GPTQ_OK) return st;
     }
     if (c.parts != 1) {
@@ -585,9 +693,9 @@ gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, voi
         c.ld = a.n_tok == 1 ? c.pad : ld;
     } else {
         c.D = (const uint16_t*)ws;
-        c.ld = planes * c.pad;
+        c.ld = row_of(a.rows, planes);
         if (a.rows > 0) {
-            Planes p{D, a.dt, a.n_tok, a.rows, ld, c.pad, (uint16_t*)ws, on16};
+            Planes p{D, a.dt, a.n_tok, a.rows, ld, c.pad, c.ld, (uint16_t*)ws, on16};
             mx_planes_kernel<<<dim3((unsigned)ceil_div(c.pad, 2048), (unsigned)std::min<int64_t>(a.n_tok, 65535)), 256, 0, s>>>(p);
             GPTQ_LAUNCH_CHECK();
         }
@@ -619,7 +727,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
     }
     c.D = (const uint16_t*)ws;
     c.pad = padded(a.d_ff);
-    c.ld = segments * c.pad;
+    c.ld = row_of(a.d_ff, segments);
     char* exps = (char*)ws + planes_bytes(a.n_tok, a.d_ff, segments);
     c.sums = (float*)(exps + align_up(4 * (size_t)a.n_tok, 256));
     if (a.d_ff > 0) {
@@ -627,6 +735,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         g.a = a;
         g.D = (uint16_t*)ws;
         g.pad = c.pad;
+        g.ld = c.ld;
         g.exps = wide ? nullptr : (int32_t*)exps;
         const auto fits = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * size)) % 16 == 0; };
         g.vec = fits(a.dY, a.ld_dy) && fits(a.G, a.ld_gu) && fits(a.U, a.ld_gu);
