@@ -6,16 +6,24 @@
 
 namespace gptq {
 
-// 1 / (1 + exp(-v)); 0 and 1 far out
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// exp(v), 1 / (1 + exp(-v)) (0 and 1 far out).  QUICK: for results of 16 bits, by
+// the hardware's power of two and reciprocal: off by some |v| + 3 roundings of
+// float32 (the product with log2 e is one), and by nothing that 16 bits see.
+template <bool QUICK>
+__device__ __forceinline__ float exp_of(float v) { return QUICK ? __builtin_amdgcn_exp2f(v * 1.44269504f) : expf(v); }
+template <bool QUICK>
+__device__ __forceinline__ float sigmoid(float v) {
+    return QUICK ? __builtin_amdgcn_rcpf(1.0f + exp_of<true>(-v)) : 1.0f / (1.0f + expf(-v));
+}
 
 constexpr float GELU_C = 0.7978845608028654f, GELU_A = 0.044715f;      // sqrt(2 / pi)
 
+template <bool QUICK>
 __device__ __forceinline__ float activate(gptq_activation act, float v) {
     switch (act) {
-        case GPTQ_ACT_SILU: return v * sigmoid(v);
+        case GPTQ_ACT_SILU: return v * sigmoid<QUICK>(v);
         case GPTQ_ACT_GELU: return v * (0.5f * erfcf(v * -0.70710678118654752f));      // no difference of near numbers below 0
-        case GPTQ_ACT_GELU_TANH: return v * sigmoid(2.0f * GELU_C * (v + GELU_A * v * v * v));
+        case GPTQ_ACT_GELU_TANH: return v * sigmoid<QUICK>(2.0f * GELU_C * (v + GELU_A * v * v * v));
         default: return v < 0.0f ? 0.0f : v;                                           // a NaN stays one
     }
 }
@@ -25,10 +33,11 @@ __device__ __forceinline__ float activate(gptq_activation act, float v) {
 __device__ __forceinline__ float within(float v) { return __builtin_amdgcn_fmed3f(v, -200.0f, 200.0f); }
 
 // The function's value and slope.
+template <bool QUICK>
 __device__ __forceinline__ void activate_with_slope(gptq_activation act, float v, float& value, float& slope) {
     switch (act) {
         case GPTQ_ACT_SILU: {
-            const float s = sigmoid(v);
+            const float s = sigmoid<QUICK>(v);
             value = v * s;
             slope = s * (1.0f + within(v) * (1.0f - s));
             break;
@@ -36,11 +45,11 @@ __device__ __forceinline__ void activate_with_slope(gptq_activation act, float v
         case GPTQ_ACT_GELU: {
             const float s = 0.5f * erfcf(v * -0.70710678118654752f);
             value = v * s;
-            slope = s + within(v) * (expf(-0.5f * within(v) * within(v)) * 0.3989422804014327f);      // 1 / sqrt(2 pi)
+            slope = s + within(v) * (exp_of<QUICK>(-0.5f * within(v) * within(v)) * 0.3989422804014327f);      // 1 / sqrt(2 pi)
             break;
         }
         case GPTQ_ACT_GELU_TANH: {
-            const float s = sigmoid(2.0f * GELU_C * (v + GELU_A * v * v * v));
+            const float s = sigmoid<QUICK>(2.0f * GELU_C * (v + GELU_A * v * v * v));
             value = v * s;
             slope = s + within(v) * s * (1.0f - s) * (2.0f * GELU_C * (1.0f + 3.0f * GELU_A * within(v) * within(v)));
             break;

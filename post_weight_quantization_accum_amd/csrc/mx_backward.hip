@@ -132,13 +132,15 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
     const BackArgs& a = c.b;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int i32 = lane & 31, h = lane >> 5;
-    // consecutive workgroups go to different dies: give each die a run of tiles
-    // that share columns
+    // Consecutive workgroups go to different dies: give each die a run of tiles,
+    // four of tokens by as many of columns (a stage's gradients are four times its
+    // codes: of 32 tiles 4 x 8 have the fewest bytes to share).
     const uint32_t nt = (uint32_t)((a.n_tok + T::BT - 1) / T::BT), nn = (uint32_t)((a.d_in + BN - 1) / BN);
     const uint32_t n = gridDim.x, each = n / 8;
     const uint32_t id = blockIdx.x < each * 8 ? (blockIdx.x % 8) * each + blockIdx.x / 8 : blockIdx.x;
     const int part = (int)(id / (nt * nn));
-    const int64_t n0 = (int64_t)(id / nt % nn) * BN, t0 = (int64_t)(id % nt) * T::BT;
+    const uint32_t tile = id % (nt * nn), rows4 = tile / (4 * nn) * 4, in4 = tile % (4 * nn), of4 = min(4u, nt - rows4);
+    const int64_t n0 = (int64_t)(in4 / of4) * BN, t0 = (int64_t)(rows4 + in4 % of4) * T::BT;
     const int nw = 128 * (wave / TW), tw = 32 * TF * (wave % TW);
     const int first = part * c.per, end = min(first + c.per, c.stages * a.matrices * c.planes), S = end - first;
 
@@ -356,9 +358,9 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
                 }
             };
             for_each<4 * TF>([&](auto p) {
-                constexpr int P = decltype(p)::value, PER = 4 / TF;
+                constexpr int P = decltype(p)::value, from = P * 4 / TF, end = (P + 1) * 4 / TF;
                 acc[P % 4][P / 4] = H16<!HALF>::mfma32(d.w[P % 4], d.x[P / 4], acc[P % 4][P / 4]);
-                for_each<PER>([&](auto e) { work(std::integral_constant<int, P * PER + decltype(e)::value>{}); });
+                for_each<end - from>([&](auto e) { work(std::integral_constant<int, from + decltype(e)::value>{}); });
                 __builtin_amdgcn_sched_barrier(0);
             });
         };
@@ -520,101 +522,180 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 }
 
 // ---------------------------------------------------------------------------
-// A token's dG and dU.  One workgroup a token, which looks for its largest
-// finite value first and scales by a power of two; float32 ones are kept as
-// they are.
+// dG and dU as planes: bfloat16 ones rounded to it; float32 ones in three parts;
+// float16 ones scaled by a power of two for each token, for which a workgroup
+// holds the token's values until it has seen the largest finite one.
 // ---------------------------------------------------------------------------
 struct Gates {
     GatedBackArgs a;
-    uint16_t* D;               // [token][2][pad] float16, or [token][2][3][pad] bfloat16 parts of float32 ones
-    int64_t pad, ld;           // token to token: ld elements
-    int32_t* exps;             // null for float32
+    uint16_t* D;               // [token][2][plane][pad], token to token ld elements
+    int64_t pad, ld;
+    int32_t* exps;             // of float16
     bool vec, vec_out;
 };
 
-__device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_t k, float (&g)[8], float (&u)[8]) {
+// Eight values from column k of a token on, of which n exist.
+template <gptq_dtype DT>
+__device__ __forceinline__ void load_eight(const void* p, int64_t at, int n, bool vec, float (&v)[8]) {
+    if (vec && n == 8) load8_f32(p, DT, at, 8, true, v);
+    else load8_f32(p, DT, at, n, false, v);
+}
+
+template <gptq_dtype DT, gptq_activation ACT>
+__device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_t k, int n, float (&g)[8], float (&u)[8]) {
     const GatedBackArgs& a = c.a;
-    const int n = (int)max((int64_t)0, min((int64_t)8, a.d_ff - k));
     float dy[8], gv[8], uv[8];
-    load8_f32(a.dY, a.dt, t * a.ld_dy + k, n, c.vec && n == 8, dy);
-    load8_f32(a.G, a.dt, t * a.ld_gu + k, n, c.vec && n == 8, gv);
-    load8_f32(a.U, a.dt, t * a.ld_gu + k, n, c.vec && n == 8, uv);
+    load_eight<DT>(a.dY, t * a.ld_dy + k, n, c.vec, dy);
+    load_eight<DT>(a.G, t * a.ld_gu + k, n, c.vec, gv);
+    load_eight<DT>(a.U, t * a.ld_gu + k, n, c.vec, uv);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float value, slope;
-        activate_with_slope(a.act, gv[i], value, slope);
-        g[i] = dy[i] * uv[i] * slope;
-        u[i] = dy[i] * value;
+        activate_with_slope<DT != GPTQ_F32>(ACT, gv[i], value, slope);
+        g[i] = i < n ? dy[i] * uv[i] * slope : 0.0f;      // zeros past d_ff, whatever act(0) is
+        u[i] = i < n ? dy[i] * value : 0.0f;
+    }
+    if (a.dG && n > 0) {
+        store8(a.dG, DT, t * a.ld_dgu + k, n, c.vec_out && n == 8, g);
+        store8(a.dU, DT, t * a.ld_dgu + k, n, c.vec_out && n == 8, u);
     }
 }
 
+template <gptq_dtype DT, gptq_activation ACT>
 __global__ __launch_bounds__(256) void mx_gates_kernel(Gates c) {
-    __shared__ float top[4];
-    const GatedBackArgs& a = c.a;
-    const int64_t t = blockIdx.x;
-    const auto finite_max = [](float m, float v) { return __builtin_isfinite(v) ? fmaxf(m, fabsf(v)) : m; };
-    int e2 = 0;
-    if (c.exps) {
-        float m = 0.0f;
-        for (int64_t k = 8 * threadIdx.x; k < a.d_ff; k += 2048) {
-            float g[8], u[8];
-            gate_gradients(c, t, k, g, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[i]), u[i]);
-        }
-#pragma unroll
-        for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
-        if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (m > 0.0f) {
-            frexpf(m, &e2);                      // m = f 2^e2, f in [1/2, 1)
-            e2 = 15 - e2;
-        }
-        if (threadIdx.x == 0) c.exps[t] = -e2;
-    }
-    for (int64_t k = 8 * threadIdx.x; k < c.pad; k += 2048) {
+    const int64_t k = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (k >= c.pad) return;
+    for (int64_t t = blockIdx.y; t < c.a.n_tok; t += gridDim.y) {
+        const int n = (int)max((int64_t)0, min((int64_t)8, c.a.d_ff - k));
         float g[8], u[8];
-        gate_gradients(c, t, k, g, u);
-        const int n = (int)max((int64_t)0, min((int64_t)8, a.d_ff - k));
-        if (a.dG) {
-            store8(a.dG, a.dt, t * a.ld_dgu + k, n, c.vec_out && n == 8, g);
-            store8(a.dU, a.dt, t * a.ld_dgu + k, n, c.vec_out && n == 8, u);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {            // past d_ff: zeros, whatever act(0) is
-            g[i] = i < n ? ldexpf(g[i], e2) : 0.0f;
-            u[i] = i < n ? ldexpf(u[i], e2) : 0.0f;
-        }
-        if (c.exps) {
-            store8(c.D, GPTQ_F16, t * c.ld + k, 8, true, g);
-            store8(c.D, GPTQ_F16, t * c.ld + c.pad + k, 8, true, u);
-        } else {
+        gate_gradients<DT, ACT>(c, t, k, n, g, u);
+        uint16_t* to = c.D + t * c.ld + k;
+        if constexpr (DT == GPTQ_F32) {
             u32x4_t p[3];
             cut(g, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + t * c.ld + j * c.pad + k) = p[j];
+            for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + j * c.pad) = p[j];
             cut(u, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(c.D + t * c.ld + (3 + j) * c.pad + k) = p[j];
+            for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + (3 + j) * c.pad) = p[j];
+        } else {
+            store8(to, GPTQ_BF16, 0, 8, true, g);
+            store8(to, GPTQ_BF16, c.pad, 8, true, u);
         }
     }
 }
 
-// How a call is computed: the tile's tokens, and the parts of the sum's stages.
+// A token by a workgroup, eight values P times a thread; P = 0: more than 2 x 1024
+// x 8, taken twice.
+template <gptq_activation ACT, int P>
+__global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
+    __shared__ float top[16];
+    const int64_t t = blockIdx.x, step = 8 * (int64_t)blockDim.x;
+    const auto finite_max = [](float m, float v) { return __builtin_isfinite(v) ? fmaxf(m, fabsf(v)) : m; };
+    const auto left = [&](int64_t k) { return (int)max((int64_t)0, min((int64_t)8, c.a.d_ff - k)); };
+    float g[P ? P : 1][8], u[P ? P : 1][8], m = 0.0f;
+    if constexpr (P > 0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int64_t k = 8 * threadIdx.x + p * step;
+            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), g[p], u[p]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[p][i]), u[p][i]);
+        }
+    } else {
+        for (int64_t k = 8 * threadIdx.x; k < c.a.d_ff; k += step) {
+            gate_gradients<GPTQ_F16, ACT>(c, t, k, left(k), g[0], u[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[0][i]), u[0][i]);
+        }
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) m = fmaxf(m, top[w]);
+    int e2 = 0;
+    if (m > 0.0f) {
+        frexpf(m, &e2);                          // m = f 2^e2, f in [1/2, 1)
+        e2 = 15 - e2;
+    }
+    if (threadIdx.x == 0) c.exps[t] = -e2;
+    const auto put = [&](int64_t k, float (&g)[8], float (&u)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[i] = ldexpf(g[i], e2);
+            u[i] = ldexpf(u[i], e2);
+        }
+        store8(c.D, GPTQ_F16, t * c.ld + k, 8, true, g);
+        store8(c.D, GPTQ_F16, t * c.ld + c.pad + k, 8, true, u);
+    };
+    if constexpr (P > 0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int64_t k = 8 * threadIdx.x + p * step;
+            if (k < c.pad) put(k, g[p], u[p]);
+        }
+    } else {
+        for (int64_t k = 8 * threadIdx.x; k < c.pad; k += step) {
+            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), g[0], u[0]);
+            put(k, g[0], u[0]);
+        }
+    }
+}
+
+template <gptq_activation ACT>
+void launch_gates(const Gates& c, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(c.pad, 2048), (unsigned)std::min<int64_t>(c.a.n_tok, 65535));
+    if (c.a.dt == GPTQ_BF16) mx_gates_kernel<GPTQ_BF16, ACT><<<grid, 256, 0, s>>>(c);
+    if (c.a.dt == GPTQ_F32) mx_gates_kernel<GPTQ_F32, ACT><<<grid, 256, 0, s>>>(c);
+    if (c.a.dt == GPTQ_F16) {
+        const int64_t pieces = c.pad / 8;
+        const unsigned n = (unsigned)c.a.n_tok;
+        if (pieces <= 1024) mx_gates_f16_kernel<ACT, 1><<<n, (unsigned)(ceil_div(pieces, 64) * 64), 0, s>>>(c);
+        else if (pieces <= 2048) mx_gates_f16_kernel<ACT, 2><<<n, (unsigned)(ceil_div(pieces, 128) * 64), 0, s>>>(c);
+        else mx_gates_f16_kernel<ACT, 0><<<n, 1024, 0, s>>>(c);
+    }
+}
+
+// How a call is computed: the tile's tokens (64 TF), and the parts of the sum's
+// stages, by the least of measured times.  A stage takes STAGE_US where one, half
+// and all of the compute units have a tile (the chip lowers its clock as they
+// run); a tile TILE_US besides, for its first stages' way in and its results' out;
+// parts 3 us for the join's launch and their sums at 4.5 TB/s.  For example 2048
+// tokens through 4096 rows of 11008 columns: 190 us in 473 tiles of 192 tokens
+// (two rounds, the second 85 % full), 211 in 344 of 256 (34 % full); through 2 x
+// 11008 rows of 4096 columns: 344 us in 128 tiles of 256 and two parts, with their
+// join, 443 in 176 of 192.
+constexpr double STAGE_US[4][3] = {{0.73, 0.81, 0.87}, {0.89, 1.00, 1.12}, {1.04, 1.17, 1.30}, {1.22, 1.31, 1.60}};
+constexpr double TILE_US[4] = {6, 9, 12, 15};
 struct Plan {
     int tf, stages, per, parts;
 };
 Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
-    Plan p;
-    p.tf = n_tok <= 64 ? 1 : n_tok <= 128 ? 2 : 4;
-    p.stages = (int)ceil_div(rows, SK);
-    const int64_t tiles = ceil_div(d_in, BN) * ceil_div(n_tok, 64 * p.tf), all = (int64_t)p.stages * segments;
-    const int64_t fill = p.tf < 4 ? 512 : 256;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(fill / tiles, all / 4));
-    p.per = (int)std::max<int64_t>(1, ceil_div(all, want));
-    p.parts = (int)ceil_div(all, p.per);
-    return p;
+    Plan best{1, (int)ceil_div(rows, SK), 1, 0};
+    const int64_t all = (int64_t)best.stages * segments;
+    if (all == 0) return best;
+    double least = 1e30;
+    for (int tf = 1; tf <= 4; ++tf) {
+        const int64_t tiles = ceil_div(d_in, BN) * ceil_div(n_tok, 64 * tf);
+        const double* us = STAGE_US[tf - 1];
+        // more parts than make two rounds of the chip cost a join and save nothing
+        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, all));
+        for (int64_t want = 1; want <= most; ++want) {
+            const int64_t per = ceil_div(all, want), parts = ceil_div(all, per);
+            const int64_t full = tiles * parts / 256, rest = tiles * parts % 256;
+            const double fill = rest / 256.0, stage = fill < 0.5 ? us[0] + 2 * fill * (us[1] - us[0]) : us[1] + (2 * fill - 1) * (us[2] - us[1]);
+            const double cost = full * (per * us[2] + TILE_US[tf - 1]) + (rest ? per * stage + TILE_US[tf - 1] : 0) +
+                                (parts > 1 ? 3 + 4e-6 * parts * n_tok * d_in / 4.5 : 0);
+            if (cost < least) {
+                least = cost;
+                best.tf = tf;
+                best.per = (int)per;
+                best.parts = (int)parts;
+            }
+        }
+    }
+    return best;
 }
 
 int64_t padded(int64_t rows) { return ceil_div(rows, SK) * SK; }
@@ -656,7 +737,8 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
         const bool half = a.dt == GPTQ_F16;
         gptq_status st;
         if (p.tf == 1) st = half ? launch_tile<true, 1, 2>(c, s) : launch_tile<false, 1, 2>(c, s);
-        else if (p.tf == 2) st = half ? launch_tile<true, 1, 4>(c, s) : launch_tile<false, 1, 4>(c, s);
+        else if (p.tf == 2) st = half ? launch_tile<true, 2, 2>(c, s) : launch_tile<false, 2, 2>(c, s);
+        else if (p.tf == 3) st = half ? launch_tile<true, 3, 2>(c, s) : launch_tile<false, 3, 2>(c, s);
         else st = half ? launch_tile<true, 4, 2>(c, s) : launch_tile<false, 4, 2>(c, s);
         if (st != GPTQ_OK) return st;
     }
@@ -713,7 +795,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
     const int size = wide ? 4 : 2, segments = wide ? 6 : 2;
     Call c{};
     BackArgs& b = c.b;
-    b.dt = wide ? GPTQ_F32 : GPTQ_F16;
+    b.dt = a.dt;
     b.n_tok = a.n_tok;
     b.matrices = 2;
     b.rows = a.d_ff;
@@ -736,11 +818,16 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         g.D = (uint16_t*)ws;
         g.pad = c.pad;
         g.ld = c.ld;
-        g.exps = wide ? nullptr : (int32_t*)exps;
+        g.exps = a.dt == GPTQ_F16 ? (int32_t*)exps : nullptr;
         const auto fits = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * size)) % 16 == 0; };
         g.vec = fits(a.dY, a.ld_dy) && fits(a.G, a.ld_gu) && fits(a.U, a.ld_gu);
         g.vec_out = a.dG && fits(a.dG, a.ld_dgu) && fits(a.dU, a.ld_dgu);
-        mx_gates_kernel<<<(unsigned)a.n_tok, 256, 0, s>>>(g);
+        switch (a.act) {
+            case GPTQ_ACT_SILU: launch_gates<GPTQ_ACT_SILU>(g, s); break;
+            case GPTQ_ACT_GELU: launch_gates<GPTQ_ACT_GELU>(g, s); break;
+            case GPTQ_ACT_GELU_TANH: launch_gates<GPTQ_ACT_GELU_TANH>(g, s); break;
+            default: launch_gates<GPTQ_ACT_RELU>(g, s); break;
+        }
         GPTQ_LAUNCH_CHECK();
         b.exps = g.exps;
     }

@@ -193,7 +193,7 @@ __device__ __forceinline__ void store_gated4(const MatArgs& a, int64_t t, int64_
     const bool whole = a.y_aligned && n == 4;
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = activate(a.act, g[i]) * u[i];
+    for (int i = 0; i < 4; ++i) y[i] = activate<false>(a.act, g[i]) * u[i];
     put4(a.YT, a.y_dt, whole, t * a.ld_y + r, n, y);
     if (a.G) {
         put4(a.G, a.y_dt, whole, t * a.ld_gu + r, n, g);

@@ -8,8 +8,9 @@ or of erfc adds to it (its rounding times the function's relative slope: v^2 for
 GELU_TANH), act(v) is off by at most R(v) u |act(v)|, R = 16 + 4 v^2 + 8 (|v| + 0.05 |v|^3), and its slope by at
 most 64 u (1 + |v|); |act'| < 1.2.
 
-Gradients: D = dG or dU of 16-bit types is rounded to 11 bits (2^-12 of the value, or 2^-39 of the token's
-largest); float32 ones are not.  Results of type t are rounded once: half a step.
+Gradients: D = dG or dU of 16-bit types is rounded for the matrix instructions: bfloat16 to itself (half a step: 2^-8
+of the value), float16 to 11 bits (2^-11, or half of float16's smallest number, 2^-25, after the token's largest
+has been brought to 2^14: 2^-39 of it); float32 ones are not.  Results of type t are rounded once: half a step.
 """
 import math
 
@@ -227,6 +228,13 @@ def test_product_gradient_odd_values_and_places():
         assert P.mx_matmul_backward(dy[:0], codes, scales, d).shape == (0, d)
 
 
+def rounded_error(eG, eU, dG, dU, kind):
+    """With the rounding of dG and dU for the matrix instructions."""
+    top = torch.maximum(dG.abs().amax(1), dU.abs().amax(1))[:, None] * 2.0 ** -39
+    step, low = (2.0 ** -8, 2.0 ** -134) if kind == "bf16" else (2.0 ** -11, top)
+    return eG + dG.abs() * step + low, eU + dU.abs() * step + low
+
+
 def gated_gradients(dy, g, u, act):
     g = g.double().requires_grad_()
     a = act64(g, act)
@@ -252,8 +260,7 @@ def test_gated_gradient(n, d, ff, kind):
         assert bool(((gg.double() - dG).abs() <= eG + half_step(dG, gg.dtype)).all())
         assert bool(((gu.double() - dU).abs() <= eU + half_step(dU, gu.dtype)).all())
         if kind != "f32":
-            top = torch.maximum(dG.abs().amax(1), dU.abs().amax(1))[:, None] * 2.0 ** -39
-            eG, eU = eG + dG.abs() * 2.0 ** -12 + top, eU + dU.abs() * 2.0 ** -12 + top
+            eG, eU = rounded_error(eG, eU, dG, dU, kind)
         check_back(dx, torch.cat((dG, dU), 1), torch.cat((wg, wu)), eG @ wg.abs() + eU @ wu.abs())
         assert torch.equal(dx, P.mx_gated_backward(dy, g, u, gate, up, d, act=act))
 
@@ -275,8 +282,7 @@ def test_gated_gradient_ranges(kind):
         eG = 64 * U * (dy.double() * u.double()).abs() * (1 + v.abs()) + 1e-44
         eU = dy.double().abs() * act_error(v, act) + U * dU.abs() + 1e-44
         if kind != "f32":
-            top = torch.maximum(dG.abs().amax(1), dU.abs().amax(1))[:, None] * 2.0 ** -39
-            eG, eU = eG + dG.abs() * 2.0 ** -12 + top, eU + dU.abs() * 2.0 ** -12 + top
+            eG, eU = rounded_error(eG, eU, dG, dU, kind)
         else:                                              # parts below bfloat16's smallest step
             eG, eU = eG + 2.0 ** -133, eU + 2.0 ** -133
         wg, wu = values(gate, d), values(up, d)
