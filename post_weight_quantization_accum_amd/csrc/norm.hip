@@ -11,6 +11,7 @@
 #include "norm.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gptq {
 namespace {
@@ -27,19 +28,26 @@ struct Piece {
 };
 
 template <bool VEC>
-__device__ __forceinline__ int64_t column(int64_t v, int e, int T, int t) {
+__device__ __forceinline__ int column(int v, int e, int T, int t) {
     return VEC ? (v * T + t) * 8 + e : (v * 8 + e) * T + t;
 }
 
+// Where a row starts: the same for all its lanes.
+template <class P>
+__device__ __forceinline__ P* row_at(P* p, gptq_dtype dt, int64_t elements) {
+    using Byte = std::conditional_t<std::is_const_v<P>, const char, char>;
+    return (P*)((Byte*)p + elements * (dt == GPTQ_F32 ? 4 : 2));
+}
+
 template <bool VEC>
-__device__ __forceinline__ Piece load(const void* p, gptq_dtype dt, int64_t at, int64_t v, int T, int t, int64_t d) {
+__device__ __forceinline__ Piece load(const void* row, gptq_dtype dt, int v, int T, int t, int d) {
     Piece r;
 #pragma unroll
     for (int e = 0; e < 8; ++e) r.w[e] = 0u;
     if constexpr (VEC) {
-        const int64_t c = column<true>(v, 0, T, t);
+        const int c = column<true>(v, 0, T, t);
         if (c < d) {
-            const uint4* q = (const uint4*)((const char*)p + (at + c) * (dt == GPTQ_F32 ? 4 : 2));
+            const uint4* q = (const uint4*)((const char*)row + (uint32_t)c * (dt == GPTQ_F32 ? 4u : 2u));
             const uint4 a = q[0];
             r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
             if (dt == GPTQ_F32) {
@@ -50,8 +58,8 @@ __device__ __forceinline__ Piece load(const void* p, gptq_dtype dt, int64_t at, 
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<false>(v, e, T, t);
-            if (c < d) r.w[e] = dt == GPTQ_F32 ? ((const uint32_t*)p)[at + c] : ((const uint16_t*)p)[at + c];
+            const int c = column<false>(v, e, T, t);
+            if (c < d) r.w[e] = dt == GPTQ_F32 ? ((const uint32_t*)row)[c] : ((const uint16_t*)row)[c];
         }
     }
     return r;
@@ -59,39 +67,51 @@ __device__ __forceinline__ Piece load(const void* p, gptq_dtype dt, int64_t at, 
 
 template <bool VEC>
 __device__ __forceinline__ void values(const Piece& r, gptq_dtype dt, float (&x)[8]) {
+    const auto half = [&](int e) { return VEC ? r.w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu : r.w[e]; };
     if (dt == GPTQ_F32) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r.w[e]);
+    } else if (dt == GPTQ_BF16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = H16<true>::to_f32((uint16_t)half(e));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t b = VEC ? (r.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu : r.w[e];
-            x[e] = dt == GPTQ_BF16 ? H16<true>::to_f32((uint16_t)b) : H16<false>::to_f32((uint16_t)b);
-        }
+        for (int e = 0; e < 8; ++e) x[e] = H16<false>::to_f32((uint16_t)half(e));
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store(void* p, gptq_dtype dt, int64_t at, int64_t v, int T, int t, int64_t d, const float (&x)[8]) {
+__device__ __forceinline__ void store(void* row, gptq_dtype dt, int v, int T, int t, int d, const float (&x)[8]) {
     if constexpr (VEC) {
-        const int64_t c = column<true>(v, 0, T, t);
-        if (c < d) store8(p, dt, at + c, 8, true, x);
+        const int c = column<true>(v, 0, T, t);
+        if (c >= d) return;
+        char* p = (char*)row + (uint32_t)c * (dt == GPTQ_F32 ? 4u : 2u);
+        if (dt == GPTQ_F32) {
+            ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else if (dt == GPTQ_BF16) {
+            *(uint4*)p = make_uint4(H16<true>::pack(x[0], x[1]), H16<true>::pack(x[2], x[3]), H16<true>::pack(x[4], x[5]),
+                                    H16<true>::pack(x[6], x[7]));
+        } else {
+            *(uint4*)p = make_uint4(H16<false>::pack(x[0], x[1]), H16<false>::pack(x[2], x[3]), H16<false>::pack(x[4], x[5]),
+                                    H16<false>::pack(x[6], x[7]));
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<false>(v, e, T, t);
+            const int c = column<false>(v, e, T, t);
             if (c >= d) continue;
-            if (dt == GPTQ_F32) ((float*)p)[at + c] = x[e];
-            else ((uint16_t*)p)[at + c] = (uint16_t)(dt == GPTQ_BF16 ? H16<true>::pack(x[e], 0.f) : H16<false>::pack(x[e], 0.f));
+            if (dt == GPTQ_F32) ((float*)row)[c] = x[e];
+            else ((uint16_t*)row)[c] = (uint16_t)(dt == GPTQ_BF16 ? H16<true>::pack(x[e], 0.f) : H16<false>::pack(x[e], 0.f));
         }
     }
 }
 
 // A vector of d values, or `none` of them.
 template <bool VEC>
-__device__ __forceinline__ void vector(const void* p, gptq_dtype dt, int64_t v, int T, int t, int64_t d, float none, float (&x)[8]) {
+__device__ __forceinline__ void vector(const void* p, gptq_dtype dt, int v, int T, int t, int d, float none, float (&x)[8]) {
     if (p) {
-        values<VEC>(load<VEC>(p, dt, 0, v, T, t, d), dt, x);
+        values<VEC>(load<VEC>(p, dt, v, T, t, d), dt, x);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = none;
@@ -108,11 +128,15 @@ __device__ __forceinline__ double moved(double v) {
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ double wave_sum(double v) {
+__device__ __forceinline__ double sum_of_16(double v) {
     v += moved<0xB1>(v);         // the neighbour's
     v += moved<0x4E>(v);         // the other pair's of four
     v += moved<0x141>(v);        // the other four's of eight
-    v += moved<0x140>(v);        // the other eight's of sixteen
+    v += moved<0x140>(v);        // the other eight's
+    return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = sum_of_16(v);
     v += __shfl_xor(v, 16, 64);
     v += __shfl_xor(v, 32, 64);
     return v;
@@ -124,7 +148,9 @@ using Sums = double[2][MAX_WAVES][K];
 // Of K sums over the workgroup (over the wave where it has the row).  `turn`
 // alternates, so that one barrier a sum is enough: who writes a half again has
 // passed the barrier of the other in between, which nobody reaches before
-// having read.
+// having read.  The barrier waits for LDS alone: rows asked for ahead and results
+// on their way out stay under way (with __syncthreads() 8000 rows of 5120 took
+// half as long again).
 template <bool WAVE, int K, int KMAX>
 __device__ __forceinline__ void row_sums(double (&v)[K], Sums<KMAX>& lds, int& turn) {
 #pragma unroll
@@ -136,13 +162,12 @@ __device__ __forceinline__ void row_sums(double (&v)[K], Sums<KMAX>& lds, int& t
 #pragma unroll
             for (int k = 0; k < K; ++k) lds[turn][threadIdx.x >> 6][k] = v[k];
         }
-        __syncthreads();
+        meet();
+        const int w = threadIdx.x & 15;
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = lds[turn][0][k];
-        for (int w = 1; w < waves; ++w) {
+        for (int k = 0; k < K; ++k) v[k] = w < waves ? lds[turn][w][k] : 0.0;
 #pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += lds[turn][w][k];
-        }
+        for (int k = 0; k < K; ++k) v[k] = sum_of_16(v[k]);
         turn ^= 1;
     }
 }
@@ -153,14 +178,16 @@ struct Stat {
 };
 __device__ __forceinline__ Stat stat(const NormArgs& a, double sum, double sq) {
     const double m = a.layer ? sum * a.inv_d : 0.0;
-    const double var = sq * a.inv_d - m * m;
-    const double r = 1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps);        // a NaN stays one
-    return Stat{(float)m, (float)r};
+    const double var = sq * a.inv_d - m * m, x = (var < 0.0 ? 0.0 : var) + (double)a.eps;        // a NaN stays one
+    // the hardware's estimate and one step of Newton's: far beyond float32
+    const double r = __builtin_amdgcn_rsq(x);
+    const bool inside = x > 0.0 && x < __builtin_inf();
+    return Stat{(float)m, (float)(inside ? r * fma(-0.5 * x * r, r, 1.5) : r)};
 }
 
 // One piece of h = scale x + gate p, p the block's output (normalised).
 template <bool VEC>
-__device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int64_t v, int T, int t, Stat sb, const Piece& xr,
+__device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int v, int T, int t, Stat sb, const Piece& xr,
                                              const Piece& br, float (&h)[8]) {
     float p[8];
     values<VEC>(xr, a.x_dt, h);
@@ -176,7 +203,7 @@ __device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int
     }
     if (a.gate) {
         float g[8];
-        values<VEC>(load<VEC>(a.gate, a.v_dt, row * a.ld_gate, v, T, t, a.d), a.v_dt, g);
+        values<VEC>(load<VEC>(row_at(a.gate, a.v_dt, row * a.ld_gate), a.v_dt, v, T, t, a.d), a.v_dt, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = fmaf(g[e], p[e], h[e]);
     } else {
@@ -186,66 +213,81 @@ __device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int
 }
 
 template <bool VEC>
-__device__ __forceinline__ void write_y(const NormArgs& a, int64_t row, int64_t v, int T, int t, Stat s, const float (&h)[8]) {
+__device__ __forceinline__ void write_y(const NormArgs& a, int64_t row, int v, int T, int t, Stat s, const float (&h)[8]) {
     float w[8], c[8];
     vector<VEC>(a.weight, a.v_dt, v, T, t, a.d, 1.0f, w);
     vector<VEC>(a.bias, a.v_dt, v, T, t, a.d, 0.0f, c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = fmaf((h[e] - s.mean) * s.rstd, w[e], c[e]);
-    store<VEC>(a.Y, a.y_dt, row * a.ld_y, v, T, t, a.d, w);
+    store<VEC>(row_at(a.Y, a.y_dt, row * a.ld_y), a.y_dt, v, T, t, a.d, w);
 }
 
-// Lanes past the row's end hold zeros, which add nothing to sums.
+// A workgroup (a wave) takes every ROWS-th row and asks for the next one before it
+// works on its own.  Lanes past the row's end hold zeros, which add nothing to
+// sums.
 template <int V, bool VEC, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
     __shared__ Sums<2> lds;
     const int T = WAVE ? 64 : blockDim.x, t = WAVE ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    if (WAVE && row >= a.n_tok) return;
-    Piece x[V], b[V];
+    const int64_t first = WAVE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : blockIdx.x;
+    const int64_t rows = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
+    if (WAVE && first >= a.n_tok) return;
+    Piece nx[V], nb[V];
+    const auto ask = [&](int64_t row) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = load<VEC>(a.X, a.x_dt, row * a.ld_x, v, T, t, a.d);
-    if (a.B) {
+        for (int v = 0; v < V; ++v) nx[v] = load<VEC>(row_at(a.X, a.x_dt, row * a.ld_x), a.x_dt, v, T, t, a.d);
+        if (a.B) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[v] = load<VEC>(a.B, a.b_dt, row * a.ld_b, v, T, t, a.d);
-    }
+            for (int v = 0; v < V; ++v) nb[v] = load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d);
+        }
+    };
+    ask(first);
     int turn = 0;
-    Stat sb{0.f, 0.f};
-    if (a.post) {
+    for (int64_t row = first; row < a.n_tok; row += rows) {
+        Piece x[V], b[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = nx[v];
+            b[v] = nb[v];
+        }
+        if (row + rows < a.n_tok) ask(row + rows);
+        Stat sb{0.f, 0.f};
+        if (a.post) {
+            double s[2] = {0.0, 0.0};
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float p[8];
+                values<VEC>(b[v], a.b_dt, p);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[0] += (double)p[e];
+                    s[1] = fma((double)p[e], (double)p[e], s[1]);
+                }
+            }
+            row_sums<WAVE, 2, 2>(s, lds, turn);
+            sb = stat(a, s[0], s[1]);
+        }
+        float h[V][8];
         double s[2] = {0.0, 0.0};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float p[8];
-            values<VEC>(b[v], a.b_dt, p);
+            stream_value<VEC>(a, row, v, T, t, sb, x[v], b[v], h[v]);
+            if (a.H) store<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.d, h[v]);
+            if (!a.Y) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s[0] += (double)p[e];
-                s[1] = fma((double)p[e], (double)p[e], s[1]);
+                const bool is = column<VEC>(v, e, T, t) < a.d;   // a layer norm's p of a lane past the end is not 0
+                const double q = is ? (double)h[v][e] : 0.0;
+                s[0] += q;
+                s[1] = fma(q, q, s[1]);
             }
         }
-        row_sums<WAVE, 2, 2>(s, lds, turn);
-        sb = stat(a, s[0], s[1]);
-    }
-    float h[V][8];
-    double s[2] = {0.0, 0.0};
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        stream_value<VEC>(a, row, v, T, t, sb, x[v], b[v], h[v]);
-        if (a.H) store<VEC>(a.H, a.h_dt, row * a.ld_h, v, T, t, a.d, h[v]);
         if (!a.Y) continue;
+        row_sums<WAVE, 2, 2>(s, lds, turn);
+        const Stat sh = stat(a, s[0], s[1]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool is = column<VEC>(v, e, T, t) < a.d;       // a layer norm's p of a lane past the end is not 0
-            const double q = is ? (double)h[v][e] : 0.0;
-            s[0] += q;
-            s[1] = fma(q, q, s[1]);
-        }
+        for (int v = 0; v < V; ++v) write_y<VEC>(a, row, v, T, t, sh, h[v]);
     }
-    if (!a.Y) return;
-    row_sums<WAVE, 2, 2>(s, lds, turn);
-    const Stat sh = stat(a, s[0], s[1]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) write_y<VEC>(a, row, v, T, t, sh, h[v]);
 }
 
 // Rows that registers do not hold: sums in one pass over them, values in the next.
@@ -253,14 +295,15 @@ template <bool VEC>
 __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
     __shared__ Sums<2> lds;
     const int T = blockDim.x, t = threadIdx.x;
-    const int64_t row = blockIdx.x, n = (a.d + 8 * T - 1) / (8 * T);
+    const int64_t row = blockIdx.x;
+    const int n = (int)((a.d + 8 * T - 1) / (8 * T));
     int turn = 0;
     Stat sb{0.f, 0.f};
     if (a.post) {
         double s[2] = {0.0, 0.0};
-        for (int64_t v = 0; v < n; ++v) {
+        for (int v = 0; v < n; ++v) {
             float p[8];
-            values<VEC>(load<VEC>(a.B, a.b_dt, row * a.ld_b, v, T, t, a.d), a.b_dt, p);
+            values<VEC>(load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d), a.b_dt, p);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s[0] += (double)p[e];
@@ -270,16 +313,16 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
         row_sums<false, 2, 2>(s, lds, turn);
         sb = stat(a, s[0], s[1]);
     }
-    const auto value = [&](int64_t v, float (&h)[8]) {
-        const Piece x = load<VEC>(a.X, a.x_dt, row * a.ld_x, v, T, t, a.d);
+    const auto value = [&](int v, float (&h)[8]) {
+        const Piece x = load<VEC>(row_at(a.X, a.x_dt, row * a.ld_x), a.x_dt, v, T, t, a.d);
         Piece b = x;
-        if (a.B) b = load<VEC>(a.B, a.b_dt, row * a.ld_b, v, T, t, a.d);
+        if (a.B) b = load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d);
         stream_value<VEC>(a, row, v, T, t, sb, x, b, h);
     };
     Stat sh{0.f, 0.f};
     if (a.Y) {
         double s[2] = {0.0, 0.0};
-        for (int64_t v = 0; v < n; ++v) {
+        for (int v = 0; v < n; ++v) {
             float h[8];
             value(v, h);
 #pragma unroll
@@ -292,10 +335,10 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
         row_sums<false, 2, 2>(s, lds, turn);
         sh = stat(a, s[0], s[1]);
     }
-    for (int64_t v = 0; v < n; ++v) {
+    for (int v = 0; v < n; ++v) {
         float h[8];
         value(v, h);
-        if (a.H) store<VEC>(a.H, a.h_dt, row * a.ld_h, v, T, t, a.d, h);      // may be X: its values are read
+        if (a.H) store<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.d, h);      // may be X: its values are read
         if (a.Y) write_y<VEC>(a, row, v, T, t, sh, h);
     }
 }
@@ -332,7 +375,7 @@ __device__ __forceinline__ RowSums first_round(const NormGradArgs& a, const doub
 }
 
 template <bool VEC>
-__device__ __forceinline__ void first_sums(const NormGradArgs& a, const Piece& hr, const Piece& yr, const Piece& br, int64_t v,
+__device__ __forceinline__ void first_sums(const NormGradArgs& a, const Piece& hr, const Piece& yr, const Piece& br, int v,
                                            int T, int t, double (&s)[6]) {
     float h[8], dy[8], w[8], b[8];
     values<VEC>(hr, a.h_dt, h);
@@ -359,7 +402,7 @@ __device__ __forceinline__ void first_sums(const NormGradArgs& a, const Piece& h
 // the vectors' gradients, and what the output's gradient is before its norm
 // (q), with the output's normalised values (nb).
 template <bool VEC>
-__device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t row, int64_t v, int T, int t, const RowSums& r,
+__device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t row, int v, int T, int t, const RowSums& r,
                                                 const Piece& hr, const Piece& yr, const Piece& br, const Piece& ghr,
                                                 float (&sum)[N_VEC][8], float (&q)[8], float (&nb)[8]) {
     float h[8], dy[8], w[8], D[8];
@@ -383,7 +426,7 @@ __device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t r
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = D[e] * a.f.scale;
-        store<VEC>(a.dX, a.h_dt, row * a.ld_dx, v, T, t, a.f.d, x);
+        store<VEC>(row_at(a.dX, a.h_dt, row * a.ld_dx), a.h_dt, v, T, t, a.f.d, x);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -398,14 +441,14 @@ __device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t r
     for (int e = 0; e < 8; ++e) nb[e] = a.f.post ? (p[e] - r.b.mean) * r.b.rstd : p[e];
     if (a.f.gate) {
         float g[8], each[8];
-        values<VEC>(load<VEC>(a.f.gate, a.f.v_dt, row * a.f.ld_gate, v, T, t, a.f.d), a.f.v_dt, g);
+        values<VEC>(load<VEC>(row_at(a.f.gate, a.f.v_dt, row * a.f.ld_gate), a.f.v_dt, v, T, t, a.f.d), a.f.v_dt, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             each[e] = D[e] * (nb[e] * pw[e]);
             sum[V_GATE][e] += each[e];
             q[e] = D[e] * g[e];
         }
-        if (a.d_gate_rows) store<VEC>(a.d_gate_rows, a.f.v_dt, row * a.ld_dgate, v, T, t, a.f.d, each);
+        if (a.d_gate_rows) store<VEC>(row_at(a.d_gate_rows, a.f.v_dt, row * a.ld_dgate), a.f.v_dt, v, T, t, a.f.d, each);
     }
     if (a.f.post) {
 #pragma unroll
@@ -417,7 +460,7 @@ __device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t r
 }
 
 template <bool VEC>
-__device__ __forceinline__ void second_sums(const NormGradArgs& a, int64_t v, int T, int t, const float (&q)[8], const float (&nb)[8],
+__device__ __forceinline__ void second_sums(const NormGradArgs& a, int v, int T, int t, const float (&q)[8], const float (&nb)[8],
                                             double (&s)[2]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -429,27 +472,27 @@ __device__ __forceinline__ void second_sums(const NormGradArgs& a, int64_t v, in
 }
 
 template <bool VEC>
-__device__ __forceinline__ void write_db(const NormGradArgs& a, int64_t row, int64_t v, int T, int t, Stat sb, float mq, float mqn,
+__device__ __forceinline__ void write_db(const NormGradArgs& a, int64_t row, int v, int T, int t, Stat sb, float mq, float mqn,
                                          float (&q)[8], const float (&nb)[8]) {
     if (a.f.post) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = through(q[e], nb[e], sb.rstd, mq, mqn);
     }
-    store<VEC>(a.dB, a.f.b_dt, row * a.ld_db, v, T, t, a.f.d, q);
+    store<VEC>(row_at(a.dB, a.f.b_dt, row * a.ld_db), a.f.b_dt, v, T, t, a.f.d, q);
 }
 
 // One part's sums of vector k, if it is asked for.
 template <bool VEC>
-__device__ __forceinline__ void write_part(const NormGradArgs& a, int64_t part, int k, int64_t v, int T, int t, const float (&x)[8]) {
+__device__ __forceinline__ void write_part(const NormGradArgs& a, int64_t part, int k, int v, int T, int t, const float (&x)[8]) {
     if (a.slot[k] < 0) return;
-    store<VEC>(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part, v, T, t, a.f.d, x);
+    store<VEC>(row_at(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part), GPTQ_F32, v, T, t, a.f.d, x);
 }
 
 template <int V, bool VEC, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArgs a) {
     __shared__ Sums<6> lds;
     const int T = WAVE ? 64 : blockDim.x, t = WAVE ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t part = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int64_t part = WAVE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : blockIdx.x;
     const int64_t parts = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
     float sum[V][N_VEC][8];
 #pragma unroll
@@ -459,15 +502,27 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[v][k][e] = 0.0f;
     int turn = 0;
+    Piece nh[V], ny[V], nb_[V], ng[V];
+    const auto ask = [&](int64_t row) {          // the next row, before this one is worked on
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nh[v] = load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
+            ny[v] = load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
+            if (a.has_b) nb_[v] = load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
+            if (a.dH) ng[v] = load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
+        }
+    };
+    if (part < a.f.n_tok) ask(part);
     for (int64_t row = part; row < a.f.n_tok; row += parts) {
         Piece h[V], y[V], b[V], g[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h[v] = load<VEC>(a.H, a.h_dt, row * a.ld_h, v, T, t, a.f.d);
-            y[v] = load<VEC>(a.dY, a.dy_dt, row * a.ld_dy, v, T, t, a.f.d);
-            if (a.has_b) b[v] = load<VEC>(a.f.B, a.f.b_dt, row * a.f.ld_b, v, T, t, a.f.d);
-            if (a.dH) g[v] = load<VEC>(a.dH, a.h_dt, row * a.ld_dh, v, T, t, a.f.d);
+            h[v] = nh[v];
+            y[v] = ny[v];
+            b[v] = nb_[v];
+            g[v] = ng[v];
         }
+        if (row + parts < a.f.n_tok) ask(row + parts);
         double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
         for (int v = 0; v < V; ++v) first_sums<VEC>(a, h[v], y[v], b[v], v, T, t, s);
@@ -501,20 +556,21 @@ template <bool VEC>
 __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
     __shared__ Sums<6> lds;
     const int T = blockDim.x, t = threadIdx.x;
-    const int64_t n = (a.f.d + 8 * T - 1) / (8 * T), part = blockIdx.x;
+    const int64_t part = blockIdx.x;
+    const int n = (int)((a.f.d + 8 * T - 1) / (8 * T));
     int turn = 0;
     bool first = true;
     for (int64_t row = part; row < a.f.n_tok; row += gridDim.x) {
         Piece h, y, b, g;
-        const auto read = [&](int64_t v) {
-            h = load<VEC>(a.H, a.h_dt, row * a.ld_h, v, T, t, a.f.d);
-            y = load<VEC>(a.dY, a.dy_dt, row * a.ld_dy, v, T, t, a.f.d);
+        const auto read = [&](int v) {
+            h = load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
+            y = load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
             b = g = h;
-            if (a.has_b) b = load<VEC>(a.f.B, a.f.b_dt, row * a.f.ld_b, v, T, t, a.f.d);
-            if (a.dH) g = load<VEC>(a.dH, a.h_dt, row * a.ld_dh, v, T, t, a.f.d);
+            if (a.has_b) b = load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
+            if (a.dH) g = load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
         };
         double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-        for (int64_t v = 0; v < n; ++v) {
+        for (int v = 0; v < n; ++v) {
             read(v);
             first_sums<VEC>(a, h, y, b, v, T, t, s);
         }
@@ -528,7 +584,7 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
         quiet.dX = nullptr;
         quiet.d_gate_rows = nullptr;
         if (a.dB && a.f.post) {
-            for (int64_t v = 0; v < n; ++v) {
+            for (int v = 0; v < n; ++v) {
                 float sum[N_VEC][8], q[8], nb[8];
 #pragma unroll
                 for (int k = 0; k < N_VEC; ++k)
@@ -542,14 +598,14 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
             mq = a.f.layer ? (float)(u[0] * a.f.inv_d) : 0.0f;
             mqn = (float)(u[1] * a.f.inv_d);
         }
-        for (int64_t v = 0; v < n; ++v) {
+        for (int v = 0; v < n; ++v) {
             float sum[N_VEC][8], q[8], nb[8];
 #pragma unroll
             for (int k = 0; k < N_VEC; ++k) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[k][e] = 0.0f;
                 if (!first && a.slot[k] >= 0)
-                    values<VEC>(load<VEC>(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part, v, T, t, a.f.d), GPTQ_F32,
+                    values<VEC>(load<VEC>(row_at(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part), GPTQ_F32, v, T, t, a.f.d), GPTQ_F32,
                                 sum[k]);
             }
             read(v);
@@ -572,7 +628,16 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* parts, int
     double s = 0.0;
     if (c < d) {
         const float* p = parts + slot * ld + c;
-        for (int64_t i = n_parts * share / 16; i < n_parts * (share + 1) / 16; ++i) s += (double)p[i * n_slots * ld];
+        const int64_t end = n_parts * (share + 1) / 16;
+        int64_t i = n_parts * share / 16;
+        for (; i + 8 <= end; i += 8) {           // eight on their way at once
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = p[(i + e) * n_slots * ld];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (double)v[e];
+        }
+        for (; i < end; ++i) s += (double)p[i * n_slots * ld];
     }
     lds[share][lane] = s;
     __syncthreads();
@@ -593,11 +658,13 @@ unsigned threads_for(int64_t d, int pieces) { return (unsigned)(ceil_div(ceil_di
 
 template <bool VEC>
 void launch_norm(const NormArgs& a, hipStream_t s) {
-    const unsigned n = (unsigned)a.n_tok, four = (unsigned)ceil_div(a.n_tok, 4);
+    // as many workgroups as the chip holds at once (2048 threads a compute unit)
+    const auto groups = [&](int64_t rows, unsigned threads) { return (unsigned)std::min<int64_t>(rows, 256 * (2048 / threads)); };
+    const unsigned n = (unsigned)a.n_tok, four = groups(ceil_div(a.n_tok, 4), 256), t1 = threads_for(a.d, 1), t2 = threads_for(a.d, 2);
     if (a.d <= 512) norm_kernel<1, VEC, true><<<four, 256, 0, s>>>(a);
     else if (a.d <= 1024) norm_kernel<2, VEC, true><<<four, 256, 0, s>>>(a);
-    else if (a.d <= 8192) norm_kernel<1, VEC, false><<<n, threads_for(a.d, 1), 0, s>>>(a);
-    else if (a.d <= 16384) norm_kernel<2, VEC, false><<<n, threads_for(a.d, 2), 0, s>>>(a);
+    else if (a.d <= 8192) norm_kernel<1, VEC, false><<<groups(n, t1), t1, 0, s>>>(a);
+    else if (a.d <= 16384) norm_kernel<2, VEC, false><<<groups(n, t2), t2, 0, s>>>(a);
     else norm_wide_kernel<VEC><<<n, 1024, 0, s>>>(a);
 }
 
