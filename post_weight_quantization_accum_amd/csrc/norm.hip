@@ -23,9 +23,11 @@ constexpr int MAX_WAVES = 16;
 // multiple of 8): eight in a row; else every T-th, so that neighbouring lanes
 // read neighbouring values all the same.
 // ---------------------------------------------------------------------------
-struct Piece {
-    uint32_t w[8];
+template <bool NARROW = false>
+struct Raw8 {
+    uint32_t w[NARROW ? 4 : 8];           // NARROW: eight values of 16 bits in a row
 };
+using Piece = Raw8<>;
 
 template <bool VEC>
 __device__ __forceinline__ int column(int v, int e, int T, int t) {
@@ -65,13 +67,27 @@ __device__ __forceinline__ Piece load(const void* row, gptq_dtype dt, int v, int
     return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void values(const Piece& r, gptq_dtype dt, float (&x)[8]) {
+__device__ __forceinline__ Raw8<true> load_narrow(const void* row, int v, int T, int t, int d) {
+    Raw8<true> r = {{0u, 0u, 0u, 0u}};
+    const int c = column<true>(v, 0, T, t);
+    if (c < d) {
+        const uint4 a = *(const uint4*)((const char*)row + 2u * (uint32_t)c);
+        r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    }
+    return r;
+}
+
+template <bool VEC, bool NARROW>
+__device__ __forceinline__ void values(const Raw8<NARROW>& r, gptq_dtype dt, float (&x)[8]) {
     const auto half = [&](int e) { return VEC ? r.w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu : r.w[e]; };
-    if (dt == GPTQ_F32) {
+    if constexpr (!NARROW) {
+        if (dt == GPTQ_F32) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r.w[e]);
-    } else if (dt == GPTQ_BF16) {
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r.w[e]);
+            return;
+        }
+    }
+    if (dt == GPTQ_BF16) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = H16<true>::to_f32((uint16_t)half(e));
     } else {
@@ -172,12 +188,25 @@ __device__ __forceinline__ void row_sums(double (&v)[K], Sums<KMAX>& lds, int& t
     }
 }
 
+// A row's sum of squares and, for a layer norm, its sum.
+template <bool LAYER>
+constexpr int STATS = LAYER ? 2 : 1;
+template <bool LAYER>
+__device__ __forceinline__ void add_stats(const float (&x)[8], double (&s)[STATS<LAYER>]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const double q = (double)x[e];
+        s[0] = fma(q, q, s[0]);
+        if constexpr (LAYER) s[1] += q;
+    }
+}
 // Mean (0 of an rms norm) and reciprocal deviation from a row's sum and sum of squares.
 struct Stat {
     float mean, rstd;
 };
-__device__ __forceinline__ Stat stat(const NormArgs& a, double sum, double sq) {
-    const double m = a.layer ? sum * a.inv_d : 0.0;
+template <bool LAYER>
+__device__ __forceinline__ Stat stat(const NormArgs& a, double sq, double sum) {
+    const double m = LAYER ? sum * a.inv_d : 0.0;
     const double var = sq * a.inv_d - m * m, x = (var < 0.0 ? 0.0 : var) + (double)a.eps;        // a NaN stays one
     // the hardware's estimate and one step of Newton's: far beyond float32
     const double r = __builtin_amdgcn_rsq(x);
@@ -185,16 +214,14 @@ __device__ __forceinline__ Stat stat(const NormArgs& a, double sum, double sq) {
     return Stat{(float)m, (float)(inside ? r * fma(-0.5 * x * r, r, 1.5) : r)};
 }
 
-// One piece of h = scale x + gate p, p the block's output (normalised).
+// One piece of h = scale x + gate p from x in h, p the block's output (here to be
+// normalised).
 template <bool VEC>
-__device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int v, int T, int t, Stat sb, const Piece& xr,
-                                             const Piece& br, float (&h)[8]) {
-    float p[8];
-    values<VEC>(xr, a.x_dt, h);
+__device__ __forceinline__ void stream_value(const NormArgs& a, int64_t row, int v, int T, int t, Stat sb, float (&p)[8],
+                                             float (&h)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] *= a.scale;
     if (!a.B) return;
-    values<VEC>(br, a.b_dt, p);
     if (a.post) {
         float w[8];
         vector<VEC>(a.post, a.v_dt, v, T, t, a.d, 1.0f, w);
@@ -223,76 +250,68 @@ __device__ __forceinline__ void write_y(const NormArgs& a, int64_t row, int v, i
 }
 
 // A workgroup (a wave) takes every ROWS-th row and asks for the next one before it
-// works on its own.  Lanes past the row's end hold zeros, which add nothing to
-// sums.
-template <int V, bool VEC, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
+// works on its own.  Lanes past the row's end read zeros, weights too, so that
+// their values are zeros throughout and add nothing to sums.
+template <int V, bool VEC, bool WAVE, bool LAYER, bool NARROW = false>
+__global__ __launch_bounds__(WAVE ? 256 : V == 1 ? 1024 : 512) void norm_kernel(NormArgs a) {
+    static_assert(VEC || !NARROW, "pieces in a row");
+    constexpr int K = STATS<LAYER>;
     __shared__ Sums<2> lds;
     const int T = WAVE ? 64 : blockDim.x, t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int64_t first = WAVE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : blockIdx.x;
     const int64_t rows = WAVE ? (int64_t)gridDim.x * 4 : gridDim.x;
     if (WAVE && first >= a.n_tok) return;
-    Piece nx[V], nb[V];
+    Raw8<NARROW> x[V], b[V];
     const auto ask = [&](int64_t row) {
+        const void *xr = row_at(a.X, a.x_dt, row * a.ld_x), *br = row_at(a.B, a.b_dt, row * a.ld_b);
 #pragma unroll
-        for (int v = 0; v < V; ++v) nx[v] = load<VEC>(row_at(a.X, a.x_dt, row * a.ld_x), a.x_dt, v, T, t, a.d);
-        if (a.B) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) nb[v] = load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d);
+        for (int v = 0; v < V; ++v) {
+            if constexpr (NARROW) {
+                x[v] = load_narrow(xr, v, T, t, a.d);
+                if (a.B) b[v] = load_narrow(br, v, T, t, a.d);
+            } else {
+                x[v] = load<VEC>(xr, a.x_dt, v, T, t, a.d);
+                if (a.B) b[v] = load<VEC>(br, a.b_dt, v, T, t, a.d);
+            }
         }
     };
     ask(first);
     int turn = 0;
     for (int64_t row = first; row < a.n_tok; row += rows) {
-        Piece x[V], b[V];
+        float h[V][8], p[V][8];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x[v] = nx[v];
-            b[v] = nb[v];
+            if (a.B) values<VEC>(b[v], a.b_dt, p[v]);
+            values<VEC>(x[v], a.x_dt, h[v]);
         }
         if (row + rows < a.n_tok) ask(row + rows);
         Stat sb{0.f, 0.f};
         if (a.post) {
-            double s[2] = {0.0, 0.0};
+            double s[K] = {};
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float p[8];
-                values<VEC>(b[v], a.b_dt, p);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s[0] += (double)p[e];
-                    s[1] = fma((double)p[e], (double)p[e], s[1]);
-                }
-            }
-            row_sums<WAVE, 2, 2>(s, lds, turn);
-            sb = stat(a, s[0], s[1]);
+            for (int v = 0; v < V; ++v) add_stats<LAYER>(p[v], s);
+            row_sums<WAVE, K, 2>(s, lds, turn);
+            sb = stat<LAYER>(a, s[0], s[K - 1]);
         }
-        float h[V][8];
-        double s[2] = {0.0, 0.0};
+        double s[K] = {};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            stream_value<VEC>(a, row, v, T, t, sb, x[v], b[v], h[v]);
+            stream_value<VEC>(a, row, v, T, t, sb, p[v], h[v]);
             if (a.H) store<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.d, h[v]);
-            if (!a.Y) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const bool is = column<VEC>(v, e, T, t) < a.d;   // a layer norm's p of a lane past the end is not 0
-                const double q = is ? (double)h[v][e] : 0.0;
-                s[0] += q;
-                s[1] = fma(q, q, s[1]);
-            }
+            add_stats<LAYER>(h[v], s);
         }
         if (!a.Y) continue;
-        row_sums<WAVE, 2, 2>(s, lds, turn);
-        const Stat sh = stat(a, s[0], s[1]);
+        row_sums<WAVE, K, 2>(s, lds, turn);
+        const Stat sh = stat<LAYER>(a, s[0], s[K - 1]);
 #pragma unroll
         for (int v = 0; v < V; ++v) write_y<VEC>(a, row, v, T, t, sh, h[v]);
     }
 }
 
 // Rows that registers do not hold: sums in one pass over them, values in the next.
-template <bool VEC>
+template <bool VEC, bool LAYER>
 __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
+    constexpr int K = STATS<LAYER>;
     __shared__ Sums<2> lds;
     const int T = blockDim.x, t = threadIdx.x;
     const int64_t row = blockIdx.x;
@@ -300,40 +319,31 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
     int turn = 0;
     Stat sb{0.f, 0.f};
     if (a.post) {
-        double s[2] = {0.0, 0.0};
+        double s[K] = {};
         for (int v = 0; v < n; ++v) {
             float p[8];
             values<VEC>(load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d), a.b_dt, p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[0] += (double)p[e];
-                s[1] = fma((double)p[e], (double)p[e], s[1]);
-            }
+            add_stats<LAYER>(p, s);
         }
-        row_sums<false, 2, 2>(s, lds, turn);
-        sb = stat(a, s[0], s[1]);
+        row_sums<false, K, 2>(s, lds, turn);
+        sb = stat<LAYER>(a, s[0], s[K - 1]);
     }
     const auto value = [&](int v, float (&h)[8]) {
-        const Piece x = load<VEC>(row_at(a.X, a.x_dt, row * a.ld_x), a.x_dt, v, T, t, a.d);
-        Piece b = x;
-        if (a.B) b = load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d);
-        stream_value<VEC>(a, row, v, T, t, sb, x, b, h);
+        float p[8];
+        values<VEC>(load<VEC>(row_at(a.X, a.x_dt, row * a.ld_x), a.x_dt, v, T, t, a.d), a.x_dt, h);
+        if (a.B) values<VEC>(load<VEC>(row_at(a.B, a.b_dt, row * a.ld_b), a.b_dt, v, T, t, a.d), a.b_dt, p);
+        stream_value<VEC>(a, row, v, T, t, sb, p, h);
     };
     Stat sh{0.f, 0.f};
     if (a.Y) {
-        double s[2] = {0.0, 0.0};
+        double s[K] = {};
         for (int v = 0; v < n; ++v) {
             float h[8];
             value(v, h);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double q = column<VEC>(v, e, T, t) < a.d ? (double)h[e] : 0.0;
-                s[0] += q;
-                s[1] = fma(q, q, s[1]);
-            }
+            add_stats<LAYER>(h, s);
         }
-        row_sums<false, 2, 2>(s, lds, turn);
-        sh = stat(a, s[0], s[1]);
+        row_sums<false, K, 2>(s, lds, turn);
+        sh = stat<LAYER>(a, s[0], s[K - 1]);
     }
     for (int v = 0; v < n; ++v) {
         float h[8];
@@ -365,109 +375,98 @@ struct RowSums {
     Stat h, b;
     float mt, mtn;
 };
-__device__ __forceinline__ RowSums first_round(const NormGradArgs& a, const double (&s)[6]) {
+// of h^2, t h, b^2, and for layer norms of h, t, b
+template <bool LAYER>
+constexpr int FIRST = LAYER ? 6 : 3;
+template <bool LAYER>
+__device__ __forceinline__ RowSums first_round(const NormGradArgs& a, const double (&s)[FIRST<LAYER>]) {
+    constexpr int L = LAYER ? 3 : 0;
     RowSums r;
-    r.h = stat(a.f, s[0], s[1]);
-    r.b = a.f.post ? stat(a.f, s[4], s[5]) : Stat{0.f, 0.f};
-    r.mt = a.f.layer ? (float)(s[2] * a.f.inv_d) : 0.0f;
-    r.mtn = (float)((s[3] - (double)r.h.mean * s[2]) * (double)r.h.rstd * a.f.inv_d);
+    r.h = stat<LAYER>(a.f, s[0], s[L]);
+    r.b = a.f.post ? stat<LAYER>(a.f, s[2], s[L + 2]) : Stat{0.f, 0.f};
+    r.mt = LAYER ? (float)(s[L + 1] * a.f.inv_d) : 0.0f;
+    r.mtn = (float)((LAYER ? s[1] - (double)r.h.mean * s[L + 1] : s[1]) * (double)r.h.rstd * a.f.inv_d);
     return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void first_sums(const NormGradArgs& a, const Piece& hr, const Piece& yr, const Piece& br, int v,
-                                           int T, int t, double (&s)[6]) {
-    float h[8], dy[8], w[8], b[8];
-    values<VEC>(hr, a.h_dt, h);
-    values<VEC>(yr, a.dy_dt, dy);
+template <bool VEC, bool LAYER>
+__device__ __forceinline__ void first_sums(const NormGradArgs& a, const float (&h)[8], const float (&dy)[8], const float (&b)[8],
+                                           int v, int T, int t, double (&s)[FIRST<LAYER>]) {
+    float w[8];
     vector<VEC>(a.f.weight, a.f.v_dt, v, T, t, a.f.d, 1.0f, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const double x = (double)h[e], g = (double)(dy[e] * w[e]);       // both 0 past the end
-        s[0] += x;
-        s[1] = fma(x, x, s[1]);
-        s[2] += g;
-        s[3] = fma(g, x, s[3]);
+        s[0] = fma(x, x, s[0]);
+        s[1] = fma(g, x, s[1]);
+        if constexpr (LAYER) {
+            s[3] += x;
+            s[4] += g;
+        }
     }
     if (!a.f.post) return;
-    values<VEC>(br, a.f.b_dt, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        s[4] += (double)b[e];
-        s[5] = fma((double)b[e], (double)b[e], s[5]);
+        s[2] = fma((double)b[e], (double)b[e], s[2]);
+        if constexpr (LAYER) s[5] += (double)b[e];
     }
 }
 
 // Of one piece: the gradient of the stream (also stored for x), the terms of
-// the vectors' gradients, and what the output's gradient is before its norm
-// (q), with the output's normalised values (nb).
+// the vectors' gradients, and what the output's gradient is before its norm,
+// with the output's normalised values.  In: h, dy, b, dH; out: q in g and nb in b.
 template <bool VEC>
 __device__ __forceinline__ void stream_gradient(const NormGradArgs& a, int64_t row, int v, int T, int t, const RowSums& r,
-                                                const Piece& hr, const Piece& yr, const Piece& br, const Piece& ghr,
-                                                float (&sum)[N_VEC][8], float (&q)[8], float (&nb)[8]) {
-    float h[8], dy[8], w[8], D[8];
-    values<VEC>(hr, a.h_dt, h);
-    values<VEC>(yr, a.dy_dt, dy);
+                                                const float (&h)[8], const float (&dy)[8], float (&b)[8], float (&g)[8],
+                                                float (&sum)[N_VEC][8]) {
+    float w[8];
     vector<VEC>(a.f.weight, a.f.v_dt, v, T, t, a.f.d, 1.0f, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float n = (h[e] - r.h.mean) * r.h.rstd;
-        D[e] = through(dy[e] * w[e], n, r.h.rstd, r.mt, r.mtn);
+        const float D = through(dy[e] * w[e], n, r.h.rstd, r.mt, r.mtn);
         sum[V_WEIGHT][e] = fmaf(dy[e], n, sum[V_WEIGHT][e]);
         sum[V_BIAS][e] += dy[e];
-    }
-    if (a.dH) {
-        float g[8];
-        values<VEC>(ghr, a.h_dt, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) D[e] += g[e];
+        g[e] = a.dH ? D + g[e] : D;
     }
     if (a.dX) {
-        float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = D[e] * a.f.scale;
-        store<VEC>(row_at(a.dX, a.h_dt, row * a.ld_dx), a.h_dt, v, T, t, a.f.d, x);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        q[e] = D[e];
-        nb[e] = 0.0f;
+        for (int e = 0; e < 8; ++e) w[e] = g[e] * a.f.scale;
+        store<VEC>(row_at(a.dX, a.h_dt, row * a.ld_dx), a.h_dt, v, T, t, a.f.d, w);
     }
     if (!a.has_b) return;
-    float p[8], pw[8];
-    values<VEC>(br, a.f.b_dt, p);
-    vector<VEC>(a.f.post, a.f.v_dt, v, T, t, a.f.d, 1.0f, pw);
+    vector<VEC>(a.f.post, a.f.v_dt, v, T, t, a.f.d, 1.0f, w);
+    if (a.f.post) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) nb[e] = a.f.post ? (p[e] - r.b.mean) * r.b.rstd : p[e];
+        for (int e = 0; e < 8; ++e) b[e] = (b[e] - r.b.mean) * r.b.rstd;
+    }
     if (a.f.gate) {
-        float g[8], each[8];
-        values<VEC>(load<VEC>(row_at(a.f.gate, a.f.v_dt, row * a.f.ld_gate), a.f.v_dt, v, T, t, a.f.d), a.f.v_dt, g);
+        float gate[8], each[8];
+        values<VEC>(load<VEC>(row_at(a.f.gate, a.f.v_dt, row * a.f.ld_gate), a.f.v_dt, v, T, t, a.f.d), a.f.v_dt, gate);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            each[e] = D[e] * (nb[e] * pw[e]);
+            each[e] = g[e] * (b[e] * w[e]);
             sum[V_GATE][e] += each[e];
-            q[e] = D[e] * g[e];
+            g[e] *= gate[e];
         }
         if (a.d_gate_rows) store<VEC>(row_at(a.d_gate_rows, a.f.v_dt, row * a.ld_dgate), a.f.v_dt, v, T, t, a.f.d, each);
     }
     if (a.f.post) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sum[V_POST][e] = fmaf(q[e], nb[e], sum[V_POST][e]);
-            q[e] *= pw[e];
+            sum[V_POST][e] = fmaf(g[e], b[e], sum[V_POST][e]);
+            g[e] *= w[e];
         }
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void second_sums(const NormGradArgs& a, int v, int T, int t, const float (&q)[8], const float (&nb)[8],
-                                            double (&s)[2]) {
+// of q nb and, for layer norms, q (0 past the end, where post_weight reads as 0)
+template <bool LAYER>
+__device__ __forceinline__ void second_sums(const float (&q)[8], const float (&nb)[8], double (&s)[STATS<LAYER>]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const bool is = column<VEC>(v, e, T, t) < a.f.d;
-        const double x = is ? (double)q[e] : 0.0;
-        s[0] += x;
-        s[1] = fma(x, (double)nb[e], s[1]);
+        s[0] = fma((double)q[e], (double)nb[e], s[0]);
+        if constexpr (LAYER) s[1] += (double)q[e];
     }
 }
 
@@ -488,8 +487,9 @@ __device__ __forceinline__ void write_part(const NormGradArgs& a, int64_t part, 
     store<VEC>(row_at(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part), GPTQ_F32, v, T, t, a.f.d, x);
 }
 
-template <int V, bool VEC, bool WAVE>
+template <int V, bool VEC, bool WAVE, bool LAYER>
 __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArgs a) {
+    constexpr int F = FIRST<LAYER>, K = STATS<LAYER>;
     __shared__ Sums<6> lds;
     const int T = WAVE ? 64 : blockDim.x, t = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int64_t part = WAVE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : blockIdx.x;
@@ -502,47 +502,46 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[v][k][e] = 0.0f;
     int turn = 0;
-    Piece nh[V], ny[V], nb_[V], ng[V];
+    Piece hr[V], yr[V], br[V], gr[V];
     const auto ask = [&](int64_t row) {          // the next row, before this one is worked on
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nh[v] = load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
-            ny[v] = load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
-            if (a.has_b) nb_[v] = load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
-            if (a.dH) ng[v] = load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
+            hr[v] = load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
+            yr[v] = load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
+            if (a.has_b) br[v] = load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
+            if (a.dH) gr[v] = load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
         }
     };
     if (part < a.f.n_tok) ask(part);
     for (int64_t row = part; row < a.f.n_tok; row += parts) {
-        Piece h[V], y[V], b[V], g[V];
+        float h[V][8], y[V][8], b[V][8], g[V][8];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h[v] = nh[v];
-            y[v] = ny[v];
-            b[v] = nb_[v];
-            g[v] = ng[v];
+            values<VEC>(hr[v], a.h_dt, h[v]);
+            values<VEC>(yr[v], a.dy_dt, y[v]);
+            if (a.has_b) values<VEC>(br[v], a.f.b_dt, b[v]);
+            if (a.dH) values<VEC>(gr[v], a.h_dt, g[v]);
         }
         if (row + parts < a.f.n_tok) ask(row + parts);
-        double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+        double s[F] = {};
 #pragma unroll
-        for (int v = 0; v < V; ++v) first_sums<VEC>(a, h[v], y[v], b[v], v, T, t, s);
-        row_sums<WAVE, 6, 6>(s, lds, turn);
-        const RowSums r = first_round(a, s);
-        float q[V][8], nb[V][8];
+        for (int v = 0; v < V; ++v) first_sums<VEC, LAYER>(a, h[v], y[v], b[v], v, T, t, s);
+        row_sums<WAVE, F, 6>(s, lds, turn);
+        const RowSums r = first_round<LAYER>(a, s);
 #pragma unroll
-        for (int v = 0; v < V; ++v) stream_gradient<VEC>(a, row, v, T, t, r, h[v], y[v], b[v], g[v], sum[v], q[v], nb[v]);
+        for (int v = 0; v < V; ++v) stream_gradient<VEC>(a, row, v, T, t, r, h[v], y[v], b[v], g[v], sum[v]);
         if (!a.dB) continue;
         float mq = 0.f, mqn = 0.f;
         if (a.f.post) {
-            double u[2] = {0.0, 0.0};
+            double u[K] = {};
 #pragma unroll
-            for (int v = 0; v < V; ++v) second_sums<VEC>(a, v, T, t, q[v], nb[v], u);
-            row_sums<WAVE, 2, 6>(u, lds, turn);
-            mq = a.f.layer ? (float)(u[0] * a.f.inv_d) : 0.0f;
-            mqn = (float)(u[1] * a.f.inv_d);
+            for (int v = 0; v < V; ++v) second_sums<LAYER>(g[v], b[v], u);
+            row_sums<WAVE, K, 6>(u, lds, turn);
+            mq = LAYER ? (float)(u[K - 1] * a.f.inv_d) : 0.0f;
+            mqn = (float)(u[0] * a.f.inv_d);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) write_db<VEC>(a, row, v, T, t, r.b, mq, mqn, q[v], nb[v]);
+        for (int v = 0; v < V; ++v) write_db<VEC>(a, row, v, T, t, r.b, mq, mqn, g[v], b[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -552,8 +551,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArg
 
 // Rows that registers do not hold: each pass over them reads them again, and
 // the vectors' sums live in the part itself (every value a lane's own).
-template <bool VEC>
+template <bool VEC, bool LAYER>
 __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
+    constexpr int F = FIRST<LAYER>, K = STATS<LAYER>;
     __shared__ Sums<6> lds;
     const int T = blockDim.x, t = threadIdx.x;
     const int64_t part = blockIdx.x;
@@ -561,22 +561,21 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
     int turn = 0;
     bool first = true;
     for (int64_t row = part; row < a.f.n_tok; row += gridDim.x) {
-        Piece h, y, b, g;
+        float h[8], y[8], b[8], g[8];
         const auto read = [&](int v) {
-            h = load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
-            y = load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
-            b = g = h;
-            if (a.has_b) b = load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
-            if (a.dH) g = load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
+            values<VEC>(load<VEC>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d), a.h_dt, h);
+            values<VEC>(load<VEC>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d), a.dy_dt, y);
+            if (a.has_b) values<VEC>(load<VEC>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d), a.f.b_dt, b);
+            if (a.dH) values<VEC>(load<VEC>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d), a.h_dt, g);
         };
-        double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+        double s[F] = {};
         for (int v = 0; v < n; ++v) {
             read(v);
-            first_sums<VEC>(a, h, y, b, v, T, t, s);
+            first_sums<VEC, LAYER>(a, h, y, b, v, T, t, s);
         }
-        row_sums<false, 6, 6>(s, lds, turn);
-        const RowSums r = first_round(a, s);
-        double u[2] = {0.0, 0.0};
+        row_sums<false, F, 6>(s, lds, turn);
+        const RowSums r = first_round<LAYER>(a, s);
+        double u[K] = {};
         float mq = 0.f, mqn = 0.f;
         // the output's gradient needs the stream's first: a pass that stores
         // nothing, where there is a norm to go through
@@ -585,21 +584,21 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
         quiet.d_gate_rows = nullptr;
         if (a.dB && a.f.post) {
             for (int v = 0; v < n; ++v) {
-                float sum[N_VEC][8], q[8], nb[8];
+                float sum[N_VEC][8];
 #pragma unroll
                 for (int k = 0; k < N_VEC; ++k)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sum[k][e] = 0.0f;
                 read(v);
-                stream_gradient<VEC>(quiet, row, v, T, t, r, h, y, b, g, sum, q, nb);
-                second_sums<VEC>(a, v, T, t, q, nb, u);
+                stream_gradient<VEC>(quiet, row, v, T, t, r, h, y, b, g, sum);
+                second_sums<LAYER>(g, b, u);
             }
-            row_sums<false, 2, 6>(u, lds, turn);
-            mq = a.f.layer ? (float)(u[0] * a.f.inv_d) : 0.0f;
-            mqn = (float)(u[1] * a.f.inv_d);
+            row_sums<false, K, 6>(u, lds, turn);
+            mq = LAYER ? (float)(u[K - 1] * a.f.inv_d) : 0.0f;
+            mqn = (float)(u[0] * a.f.inv_d);
         }
         for (int v = 0; v < n; ++v) {
-            float sum[N_VEC][8], q[8], nb[8];
+            float sum[N_VEC][8];
 #pragma unroll
             for (int k = 0; k < N_VEC; ++k) {
 #pragma unroll
@@ -609,8 +608,8 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a) {
                                 sum[k]);
             }
             read(v);
-            stream_gradient<VEC>(a, row, v, T, t, r, h, y, b, g, sum, q, nb);
-            if (a.dB) write_db<VEC>(a, row, v, T, t, r.b, mq, mqn, q, nb);
+            stream_gradient<VEC>(a, row, v, T, t, r, h, y, b, g, sum);
+            if (a.dB) write_db<VEC>(a, row, v, T, t, r.b, mq, mqn, g, b);
 #pragma unroll
             for (int k = 0; k < N_VEC; ++k) write_part<VEC>(a, part, k, v, T, t, sum[k]);
         }
@@ -656,16 +655,16 @@ bool rows_on_16(const void* p, gptq_dtype dt, int64_t ld) {
 // Threads of a workgroup for rows of d values, eight or sixteen or 32 a lane.
 unsigned threads_for(int64_t d, int pieces) { return (unsigned)(ceil_div(ceil_div(d, 8 * pieces), 64) * 64); }
 
-template <bool VEC>
+template <bool VEC, bool LAYER, bool NARROW>
 void launch_norm(const NormArgs& a, hipStream_t s) {
     // as many workgroups as the chip holds at once (2048 threads a compute unit)
     const auto groups = [&](int64_t rows, unsigned threads) { return (unsigned)std::min<int64_t>(rows, 256 * (2048 / threads)); };
-    const unsigned n = (unsigned)a.n_tok, four = groups(ceil_div(a.n_tok, 4), 256), t1 = threads_for(a.d, 1), t2 = threads_for(a.d, 2);
-    if (a.d <= 512) norm_kernel<1, VEC, true><<<four, 256, 0, s>>>(a);
-    else if (a.d <= 1024) norm_kernel<2, VEC, true><<<four, 256, 0, s>>>(a);
-    else if (a.d <= 8192) norm_kernel<1, VEC, false><<<groups(n, t1), t1, 0, s>>>(a);
-    else if (a.d <= 16384) norm_kernel<2, VEC, false><<<groups(n, t2), t2, 0, s>>>(a);
-    else norm_wide_kernel<VEC><<<n, 1024, 0, s>>>(a);
+    const unsigned four = groups(ceil_div(a.n_tok, 4), 256), t1 = threads_for(a.d, 1), t4 = threads_for(a.d, 4);
+    if (a.d <= 512) norm_kernel<1, VEC, true, LAYER, NARROW><<<four, 256, 0, s>>>(a);
+    else if (a.d <= 1024) norm_kernel<2, VEC, true, LAYER, NARROW><<<four, 256, 0, s>>>(a);
+    else if (a.d <= 8192) norm_kernel<1, VEC, false, LAYER, NARROW><<<groups(a.n_tok, t1), t1, 0, s>>>(a);
+    else if (a.d <= 16384) norm_kernel<4, VEC, false, LAYER, NARROW><<<groups(a.n_tok, t4), t4, 0, s>>>(a);
+    else norm_wide_kernel<VEC, LAYER><<<(unsigned)a.n_tok, 1024, 0, s>>>(a);
 }
 
 // Parts of the sums over tokens, and with them workgroups of the gradient.
@@ -674,16 +673,16 @@ int64_t grad_parts(int64_t n_tok, int64_t d) {
     return std::min<int64_t>(n_tok, 512);
 }
 
-template <bool VEC>
+template <bool VEC, bool LAYER>
 void launch_grad(const NormGradArgs& a, hipStream_t s) {
     const int64_t d = a.f.d;
     const unsigned n = (unsigned)grad_parts(a.f.n_tok, d);
-    if (d <= 512) norm_grad_kernel<1, VEC, true><<<n / 4, 256, 0, s>>>(a);
-    else if (d <= 1024) norm_grad_kernel<2, VEC, true><<<n / 4, 256, 0, s>>>(a);
-    else if (d <= 4096) norm_grad_kernel<1, VEC, false><<<n, threads_for(d, 1), 0, s>>>(a);
-    else if (d <= 8192) norm_grad_kernel<2, VEC, false><<<n, threads_for(d, 2), 0, s>>>(a);
-    else if (d <= 16384) norm_grad_kernel<4, VEC, false><<<n, threads_for(d, 4), 0, s>>>(a);
-    else norm_grad_wide_kernel<VEC><<<n, 512, 0, s>>>(a);
+    if (d <= 512) norm_grad_kernel<1, VEC, true, LAYER><<<n / 4, 256, 0, s>>>(a);
+    else if (d <= 1024) norm_grad_kernel<2, VEC, true, LAYER><<<n / 4, 256, 0, s>>>(a);
+    else if (d <= 4096) norm_grad_kernel<1, VEC, false, LAYER><<<n, threads_for(d, 1), 0, s>>>(a);
+    else if (d <= 8192) norm_grad_kernel<2, VEC, false, LAYER><<<n, threads_for(d, 2), 0, s>>>(a);
+    else if (d <= 16384) norm_grad_kernel<4, VEC, false, LAYER><<<n, threads_for(d, 4), 0, s>>>(a);
+    else norm_grad_wide_kernel<VEC, LAYER><<<n, 512, 0, s>>>(a);
 }
 
 }  // namespace
@@ -692,8 +691,9 @@ gptq_status norm_launch(const NormArgs& a, hipStream_t s) {
     const bool vec = a.d % 8 == 0 && rows_on_16(a.X, a.x_dt, a.ld_x) && rows_on_16(a.B, a.b_dt, a.ld_b) &&
                      rows_on_16(a.H, a.h_dt, a.ld_h) && rows_on_16(a.Y, a.y_dt, a.ld_y) && rows_on_16(a.weight, a.v_dt, 0) &&
                      rows_on_16(a.bias, a.v_dt, 0) && rows_on_16(a.post, a.v_dt, 0) && rows_on_16(a.gate, a.v_dt, a.ld_gate);
-    if (vec) launch_norm<true>(a, s);
-    else launch_norm<false>(a, s);
+    const bool narrow = vec && a.x_dt != GPTQ_F32 && (!a.B || a.b_dt != GPTQ_F32);
+    if (a.layer) narrow ? launch_norm<true, true, true>(a, s) : vec ? launch_norm<true, true, false>(a, s) : launch_norm<false, true, false>(a, s);
+    else narrow ? launch_norm<true, false, true>(a, s) : vec ? launch_norm<true, false, false>(a, s) : launch_norm<false, false, false>(a, s);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -718,8 +718,8 @@ gptq_status norm_grad_launch(NormGradArgs a, float* d_weight, float* d_bias, flo
         if (outs[k]) o[a.n_slots++] = outs[k];
     }
     if (a.f.n_tok > 0) {
-        if (vec) launch_grad<true>(a, s);
-        else launch_grad<false>(a, s);
+        if (a.f.layer) vec ? launch_grad<true, true>(a, s) : launch_grad<false, true>(a, s);
+        else vec ? launch_grad<true, false>(a, s) : launch_grad<false, false>(a, s);
         GPTQ_LAUNCH_CHECK();
     }
     if (a.n_slots) {       // without tokens: zeros
