@@ -2,6 +2,8 @@
 // functions, arguments and launchers (checked in mx_api.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "mx.hpp"
 
 namespace gptq {
@@ -25,6 +27,22 @@ __device__ __forceinline__ float activate(gptq_activation act, float v) {
         case GPTQ_ACT_GELU: return v * (0.5f * erfcf(v * -0.70710678118654752f));      // no difference of near numbers below 0
         case GPTQ_ACT_GELU_TANH: return v * sigmoid<QUICK>(2.0f * GELU_C * (v + GELU_A * v * v * v));
         default: return v < 0.0f ? 0.0f : v;                                           // a NaN stays one
+    }
+}
+
+// y = act(g) u of eight values.  The function is chosen once, not for each value:
+// code that is unrolled with all four takes longer to come in than to run.
+template <bool QUICK>
+__device__ __forceinline__ void gate8(gptq_activation act, const float (&g)[8], const float (&u)[8], float (&y)[8]) {
+    const auto all = [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = activate<QUICK>(decltype(a)::value, g[i]) * u[i];
+    };
+    switch (act) {
+        case GPTQ_ACT_SILU: all(std::integral_constant<gptq_activation, GPTQ_ACT_SILU>{}); break;
+        case GPTQ_ACT_GELU: all(std::integral_constant<gptq_activation, GPTQ_ACT_GELU>{}); break;
+        case GPTQ_ACT_GELU_TANH: all(std::integral_constant<gptq_activation, GPTQ_ACT_GELU_TANH>{}); break;
+        default: all(std::integral_constant<gptq_activation, GPTQ_ACT_RELU>{}); break;
     }
 }
 

@@ -25,6 +25,7 @@ struct MatArgs {
     int64_t d_out, ld_y;
     float* Y;
     bool y_aligned;        // Y rows start on 16 bytes (of gated products: all outputs' groups of four on their own size)
+    bool y_aligned8;       // of gated products: their groups of eight on 16 bytes
     // gated products: W and S are the gate's, d_out rows of each
     const uint8_t *W2, *S2;
     gptq_activation act;
@@ -201,12 +202,51 @@ __device__ __forceinline__ void store_gated4(const MatArgs& a, int64_t t, int64_
     }
 }
 
-// A lane's sixteen of a 32 x 32 tile.
-__device__ __forceinline__ void store_gated(const MatArgs& a, int64_t t, int64_t r, const f16_t& g, const f16_t& u) {
+// A wave's results, 32 RM rows of both matrices by 32 TJ tokens in tiles of 32 x
+// 32, out through LDS (8192 RM TJ bytes of the wave's own at `own`): a lane reads
+// eight rows of a token back.  16-byte chunk c of a token's 128 bytes lies at slot
+// c ^ (token / 2 % 8).
+template <int RM, int TJ, int RW>
+__device__ __forceinline__ void gated_out(const MatArgs& a, char* own, const f16_t (&acc)[RW][TJ], int64_t t0, int64_t r0) {
+    static_assert(RW == 2 * RM, "the gate's rows, then up's");
+    const int lane = threadIdx.x & 63, i32 = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-        const float gs[4] = {g[e], g[e + 1], g[e + 2], g[e + 3]}, us[4] = {u[e], u[e + 1], u[e + 2], u[e + 3]};
-        store_gated4(a, t, r + 2 * e, gs, us);
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {                  // rows 8 q + 4 h .. + 3
+                const f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                *(f32x4_t*)(own + (j * RW + i) * 4096 + i32 * 128 + 16 * ((2 * q + h) ^ (i32 >> 1 & 7))) = v;
+            }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int c = lane & 3;
+    const bool all8 = a.y_aligned8;
+#pragma unroll 1
+    for (int n = 0; n < 2 * RM * TJ; ++n) {
+        const int j = n / (2 * RM), i = n / 2 % RM, token = 16 * (n & 1) + (lane >> 2);
+        const int64_t t = t0 + 32 * j + token, r = r0 + 32 * i + 8 * c;
+        const int m = (int)max((int64_t)0, min((int64_t)8, a.d_out - r));
+        if (t >= a.n_tok || m == 0) continue;
+        float g[8], u[8], y[8];
+        const char* p = own + (j * RW + i) * 4096 + token * 128;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int at = 16 * ((2 * c + e) ^ (token >> 1 & 7));
+            const f32x4_t gv = *(const f32x4_t*)(p + at), uv = *(const f32x4_t*)(p + RM * 4096 + at);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[4 * e + k] = gv[k];
+                u[4 * e + k] = uv[k];
+            }
+        }
+        if (a.y_dt == GPTQ_F32) gate8<false>(a.act, g, u, y);
+        else gate8<true>(a.act, g, u, y);
+        store8(a.YT, a.y_dt, t * a.ld_y + r, m, all8 && m == 8, y);
+        if (a.G) {
+            store8(a.G, a.y_dt, t * a.ld_gu + r, m, all8 && m == 8, g);
+            store8(a.U, a.y_dt, t * a.ld_gu + r, m, all8 && m == 8, u);
+        }
     }
 }
 
@@ -633,14 +673,19 @@ __global__ __launch_bounds__(256, 2) void mx_many_kernel(MatArgs a) {
                 }
         }
     }
+    if constexpr (GATED) {
+        // 32 tokens at a time: the buffers hold that much for every wave
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f16_t half[2][1] = {{acc[0][j]}, {acc[1][j]}};
+            gated_out<1, 1, 2>(a, xs + 8192 * wave, half, t0 + tw + 32 * j, r0);
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
-        if constexpr (GATED) {
-            store_gated(a, t, r0 + 4 * h, acc[0][j], acc[1][j]);
-            continue;
-        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -849,14 +894,15 @@ __global__ __launch_bounds__(128 * RG, 2) void mx_wide_kernel(MatArgs a) {
                 }
             }
     }
+    if constexpr (GATED) {
+        meet();                                             // the ring's readers are done
+        gated_out<1, 2, 2>(a, lds + 16384 * wave, acc, t0 + tw, r0 + rm);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
-        if constexpr (GATED) {
-            store_gated(a, t, r0 + rm + 4 * h, acc[0][j], acc[1][j]);
-            continue;
-        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -1052,15 +1098,15 @@ __global__ __launch_bounds__(256, 1) void mx_mx_kernel(MatArgs a) {
         if (st + 1 < stages) multiply(st + 1, Second{});
     }
     wait_vmem<0>();                                     // nothing lands in LDS that is another's by then
+    if constexpr (GATED) {
+        meet();                                         // the ring's readers are done
+        gated_out<RM, 2, RW>(a, lds + 8192 * RW * wave, acc, t0 + tw, r0 + rm);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t t = t0 + tw + 32 * j + i32;
         if (t >= a.n_tok) continue;
-        if constexpr (GATED) {
-#pragma unroll
-            for (int i = 0; i < RM; ++i) store_gated(a, t, r0 + rm + 32 * i + 4 * h, acc[i][j], acc[RM + i][j]);
-            continue;
-        }
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
@@ -1267,6 +1313,7 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
     a.ld_y = ld_y;
     a.Y = Y;
     a.W2 = a.S2 = nullptr;
+    a.y_aligned8 = false;
     a.act = GPTQ_ACT_SILU;
     a.y_dt = GPTQ_F32;
     a.YT = a.G = a.U = nullptr;
@@ -1288,6 +1335,8 @@ void gate_args(MatArgs& a, const GatedArgs& g) {
     a.U = g.U;
     a.ld_gu = g.ld_gu;
     a.y_aligned = fits(g.Y, g.ld_y) && (!g.G || (fits(g.G, g.ld_gu) && fits(g.U, g.ld_gu)));
+    const auto on16 = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * (int64_t)(four / 4))) % 16 == 0; };
+    a.y_aligned8 = on16(g.Y, g.ld_y) && (!g.G || (on16(g.G, g.ld_gu) && on16(g.U, g.ld_gu)));
 }
 
 // Steps of 16-bit or float32 activations that are read in whole pieces: offsets
