@@ -470,6 +470,12 @@ gptq_status gptq_mx_gated_quantized(const uint8_t* x_codes, const uint8_t* x_sca
                                     gptq_activation activation, void* Y, gptq_dtype y_dtype, int64_t ld_y, void* G, void* U,
                                     int64_t ld_gu, hipStream_t stream);
 
+/* Which kernel a gated product of these sizes takes, for profiles and tests, as
+ * gptq_mx_matmul_kernel says it (rows: of both matrices together); 10, 11: a
+ * tile of 96, 128 rows x 16 tokens. */
+int32_t gptq_mx_gated_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64_t n_tok, int64_t d_in, int64_t d_ff,
+                             int32_t aligned);
+
 /* The gradient of gptq_mx_matmul for its activations (the weights are codes
  * and have none):  dX[t][k] = sum_{r < d_out} dY[t][r] w[r][k].
  * dY: n_tok x d_out of dy_dtype, row stride ld_dy; codes, scales: d_out x d_in
@@ -487,6 +493,12 @@ gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t
                                     gptq_dtype dx_dtype, int64_t ld_dx, void* workspace, size_t ws_bytes,
                                     hipStream_t stream);
 
+/* How a gradient of these sizes is computed, for profiles and tests: plan[0]
+ * (host memory) gets the tokens of a tile, plan[1] the parts that the sum over the
+ * rows is cut into.  matrices: 1, or 2 for gptq_mx_gated_backward. */
+gptq_status gptq_mx_backward_plan(gptq_dtype dy_dtype, int32_t matrices, int64_t n_tok, int64_t d_in, int64_t d_out,
+                                  int64_t* plan);
+
 /* The gradient of gptq_mx_gated for its activations, from dY and the G and U
  * that it wrote (all three n_tok x d_ff of one dtype; row strides ld_dy,
  * ld_gu):
@@ -494,11 +506,11 @@ gptq_status gptq_mx_matmul_backward(const void* dY, gptq_dtype dy_dtype, int64_t
  *   dG = dY * U * act'(G),   dU = dY * act(G),   dX = dG gate + dU up
  *
  * dG and dU are computed in float32.  For the matrix cores they are rounded
- * once: of 16-bit dtypes to float16 after each token's are scaled by a power of
- * two of its own that brings the largest of them to 2^14 .. 2^15 (11 bits, down
- * to 2^-29 of that); of float32 not at all.  Weights whose scales float16 does
- * not hold (outside 2^-23 .. 2^13) are multiplied as bfloat16, by the same
- * values in two parts.  Sums are float32.
+ * once: of bfloat16 to bfloat16; of float16 to float16 after each token's are
+ * scaled by a power of two of its own that brings the largest of them to 2^14 ..
+ * 2^15 (11 bits, down to 2^-29 of that); of float32 not at all.  With float16,
+ * weights whose scales it does not hold (outside 2^-23 .. 2^13) are multiplied as
+ * bfloat16, by the same values in two parts.  Sums are float32.
  * dG_out, dU_out: both NULL, or n_tok x d_ff of G's dtype with row stride ld_dgu
  * that get dG and dU (for adapters beside the weights).  dX: as above.
  * RELU's slope at 0 is 0.

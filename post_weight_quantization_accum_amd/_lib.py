@@ -34,7 +34,7 @@ EXPORTS = (
     "gptq_packed_words_per_row", "gptq_pack", "gptq_pack_permuted",
     "gptq_dequant_max_groups", "gptq_dequant_matmul", "gptq_gather_columns",
     "gptq_mx_codes_per_row", "gptq_mx_scales_per_row", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
-    "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_mx_gated", "gptq_mx_gated_quantized",
+    "gptq_mx_matmul_quantized", "gptq_mx_matmul_kernel", "gptq_mx_gated", "gptq_mx_gated_quantized", "gptq_mx_gated_kernel", "gptq_mx_backward_plan",
     "gptq_mx_matmul_backward_workspace", "gptq_mx_matmul_backward", "gptq_mx_gated_backward_workspace",
     "gptq_mx_gated_backward", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention_workspace",
     "gptq_cache_attention_plan", "gptq_cache_attention", "gptq_residual_norm", "gptq_residual_norm_backward_workspace",
@@ -183,6 +183,10 @@ def load(path: str | None = None):
     lib.gptq_mx_gated.restype = ci
     lib.gptq_mx_gated_quantized.argtypes = [vp, vp, ci, i64, i64, vp, vp, vp, vp, i64, ci, vp, ci, i64, vp, vp, i64, vp]
     lib.gptq_mx_gated_quantized.restype = ci
+    lib.gptq_mx_gated_kernel.argtypes = [ci, ci, i64, i64, i64, ctypes.c_int32]
+    lib.gptq_mx_gated_kernel.restype = ctypes.c_int32
+    lib.gptq_mx_backward_plan.argtypes = [ci, ctypes.c_int32, i64, i64, i64, ctypes.POINTER(i64)]
+    lib.gptq_mx_backward_plan.restype = ci
     lib.gptq_mx_matmul_backward_workspace.argtypes = [ci, i64, i64, i64]
     lib.gptq_mx_matmul_backward_workspace.restype = sz
     lib.gptq_mx_matmul_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, ci, i64, vp, sz, vp]

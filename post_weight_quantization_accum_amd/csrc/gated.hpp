@@ -120,6 +120,8 @@ gptq_status mx_gated_quantized_launch(const uint8_t* xc, const uint8_t* xs, gptq
                                       const uint8_t* codes, const uint8_t* scales, int64_t d_ff, const GatedArgs& g,
                                       hipStream_t s);
 
+int mx_gated_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_in, int64_t d_ff, bool aligned);
+
 // The gradient of products for their activations: one matrix of codes, or the
 // sum over two.
 struct BackArgs {
@@ -133,6 +135,7 @@ struct BackArgs {
     int64_t ld_dx;
 };
 size_t mx_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t rows);
+void mx_backward_plan(gptq_dtype dt, int matrices, int64_t n_tok, int64_t d_in, int64_t rows, int64_t* plan);
 gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, void* ws, hipStream_t s);
 
 struct GatedBackArgs {

@@ -128,6 +128,22 @@ gptq_status gptq_mx_gated_quantized(const uint8_t* x_codes, const uint8_t* x_sca
                                      GatedArgs{up_codes, up_scales, activation, Y, y_dtype, ld_y, G, U, ld_gu}, stream);
 }
 
+int32_t gptq_mx_gated_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64_t n_tok, int64_t d_in, int64_t d_ff,
+                             int32_t aligned) {
+    if (x_format == GPTQ_MX_NONE ? !is_float(x_dtype) : !is_mx(x_format)) return -1;
+    if (!in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_ff, 1, MAX_DIM)) return -1;
+    return mx_gated_kernel(x_dtype, x_format, n_tok, d_in, d_ff, aligned != 0);
+}
+
+gptq_status gptq_mx_backward_plan(gptq_dtype dy_dtype, int32_t matrices, int64_t n_tok, int64_t d_in, int64_t d_out,
+                                  int64_t* plan) {
+    if (!plan || !is_float(dy_dtype) || (matrices != 1 && matrices != 2) || !in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) ||
+        !in(d_out, 1, MAX_DIM))
+        return GPTQ_ERR_INVALID_ARG;
+    mx_backward_plan(dy_dtype, matrices, n_tok, d_in, d_out, plan);
+    return GPTQ_OK;
+}
+
 size_t gptq_mx_matmul_backward_workspace(gptq_dtype dy_dtype, int64_t n_tok, int64_t d_in, int64_t d_out) {
     if (!is_float(dy_dtype) || !in(n_tok, 1, MAX_DIM) || !in(d_in, 1, MAX_DIM) || !in(d_out, 1, MAX_DIM)) return 0;
     return mx_backward_ws(dy_dtype, n_tok, d_in, d_out);

@@ -463,25 +463,38 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
     }
 }
 
-// dX from the parts' sums, in the order of the parts (zeros of none).
+// dX from the parts' sums, in the order of the parts (zeros of none): four columns
+// of a token by a thread.
 __global__ __launch_bounds__(256) void mx_back_join_kernel(Call c) {
     const BackArgs& a = c.b;
     const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
     if (n >= a.d_in) return;
     const int m = (int)min((int64_t)4, a.d_in - n);
     const bool whole = m == 4 && a.d_in % 4 == 0;
+    const int64_t part = a.n_tok * a.d_in;
+    const float* s = c.sums + t * a.d_in + n;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < c.parts; ++p) {
-        const float* s = c.sums + ((int64_t)p * a.n_tok + t) * a.d_in + n;
-        if (whole) {
-            const f32x4_t x = *(const f32x4_t*)s;
+    int p = 0;
+    if (whole) {
+        for (; p + 8 <= c.parts; p += 8) {       // eight on their way at once
+            f32x4_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = *(const f32x4_t*)(s + (p + e) * part);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += x[e][q];
+        }
+        for (; p < c.parts; ++p) {
+            const f32x4_t x = *(const f32x4_t*)(s + p * part);
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] += x[q];
-        } else {
+        }
+    } else {
+        for (; p < c.parts; ++p)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (q < m) v[q] += s[q];
-        }
+                if (q < m) v[q] += s[p * part + q];
     }
     const int e2 = a.exps ? a.exps[t] : 0;
 #pragma unroll
@@ -757,6 +770,12 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
 }
 
 }  // namespace
+
+void mx_backward_plan(gptq_dtype dt, int matrices, int64_t n_tok, int64_t d_in, int64_t rows, int64_t* plan) {
+    const Plan p = plan_of(matrices * (dt == GPTQ_F32 ? 3 : 1), n_tok, d_in, rows);
+    plan[0] = 64 * p.tf;
+    plan[1] = p.parts;
+}
 
 size_t mx_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t rows) {
     const int planes = dt == GPTQ_F32 ? 3 : 1;

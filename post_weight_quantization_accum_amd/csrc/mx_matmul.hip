@@ -1247,12 +1247,22 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
     else return launch_many<DT>(a, s);
 }
 
-// Gated products.  Tiles of an odd number of row groups are out; of more rows:
-// (6,1) and (8,1).
+// Gated products: the same rule with times of their own (they write 16 bits
+// through an activation, and a tile has half as many rows of each matrix).  Tiles
+// of an odd number of row groups are out; two of more rows are in, (6,1) and
+// (8,1): by 16 RT x 16 TT in the order of GATED_TILE, us a round at 4096 columns.
+// One bf16 token 4096 -> 2 x 11008: (6,1) 14.9 us in one round, (8,1) 17.1, (4,1)
+// 18.9, (2,1) 19.1; 13 f16 tokens 5120 -> 2 x 13824: (8,1) 23.7, (4,1) 25.8, (2,1)
+// 31.4, (6,1) 34.9 (two rounds).  1500 e2m1 tokens: 256 x 128 120 us, 128 x 128 129.
+constexpr int GATED_TILE[6] = {1, 3, 4, 5, 10, 11}, GATED_RT[6] = {2, 4, 2, 4, 6, 8}, GATED_TT[6] = {1, 1, 2, 2, 1, 1};
+constexpr double GATED_US[5][6] = {{11, 15, 19, 0, 20, 25},                // float32
+                                   {6.9, 10.3, 7.4, 11.9, 14.5, 17.5},     // float16
+                                   {6.9, 10.3, 7.4, 11.9, 14.5, 17.5},     // bfloat16
+                                   {5.9, 9.0, 7.4, 11.5, 15.0, 17.0},      // e4m3
+                                   {5.7, 9.0, 7.3, 11.2, 14.0, 17.0}};     // e2m1
+
 template <Act DT>
-gptq_status launch_gated(const MatArgs& a, hipStream_t s) {
-    constexpr const double* ring = FEW_US[DT];
-    const double* us = a.full > 0 ? ring : DIRECT_US[DT != ACT_F32];
+int choose_gated(const MatArgs& a) {
     int best = 9;
     double least = 1e30;
     const auto offer = [&](int id, double cost) {
@@ -1261,28 +1271,39 @@ gptq_status launch_gated(const MatArgs& a, hipStream_t s) {
             best = id;
         }
     };
-    for (int i : {1, 3, 4, 5})
-        if (us[i] > 0) offer(i, rounds(a, 16 * FEW_RT[i], 16 * FEW_TT[i]) * us[i]);
+    for (int i = 0; i < 6; ++i) {
+        // by single elements (DIRECT_US): without the ring more rows gain nothing
+        const double us = a.full > 0 ? GATED_US[DT][i] : i < 4 && GATED_US[DT][i] > 0 ? DIRECT_US[DT != ACT_F32][GATED_TILE[i]] : 0;
+        if (us > 0) offer(GATED_TILE[i], rounds(a, 16 * GATED_RT[i], 16 * GATED_TT[i]) * us);
+    }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
         if (a.full > 0) {
-            offer(7, rounds(a, 128, MT) * 25.0);
-            offer(8, rounds(a, 256, MT) * 43.0);
+            offer(7, rounds(a, 128, MT) * 30.0);
+            offer(8, rounds(a, 256, MT) * 48.0);
         } else {
             offer(9, std::max(1.0, 0.61 * rounds(a, 128, MT)) * 250.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(9, rounds(a, 128, MT) * (a.full > 0 ? 130.0 : 226.0));
+        offer(9, rounds(a, 128, MT) * (a.full > 0 ? 129.0 : 226.0));
     } else if constexpr (DT == ACT_FP8) {
-        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 69.0);
+        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 72.0);
     } else {
-        offer(7, rounds(a, 128, MT) * 13.0);
-        offer(8, rounds(a, 256, MT) * 25.0);
+        offer(7, rounds(a, 128, MT) * 14.5);
+        offer(8, rounds(a, 256, MT) * 23.5);
     }
+    return best;
+}
+
+template <Act DT>
+gptq_status launch_gated(const MatArgs& a, hipStream_t s) {
+    const int best = choose_gated<DT>(a);
     switch (best) {
         case 1: return launch_few<DT, 2, 1, true>(a, s);
         case 3: return launch_few<DT, 4, 1, true>(a, s);
         case 4: return launch_few<DT, 2, 2, true>(a, s);
-        case 5: if constexpr (FEW_US[DT][5] > 0) return launch_few<DT, 4, 2, true>(a, s); break;
+        case 5: if constexpr (GATED_US[DT][3] > 0) return launch_few<DT, 4, 2, true>(a, s); break;
+        case 10: return launch_few<DT, 6, 1, true>(a, s);
+        case 11: return launch_few<DT, 8, 1, true>(a, s);
         default: break;
     }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
@@ -1360,6 +1381,15 @@ int mx_matmul_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_
     if (xf == GPTQ_MX_FP4) return choose<ACT_FP4>(a);
     a.full = whole_steps(aligned, d_in, d_in);
     return dt == GPTQ_BF16 ? choose<ACT_BF16>(a) : dt == GPTQ_F16 ? choose<ACT_F16>(a) : choose<ACT_F32>(a);
+}
+
+int mx_gated_kernel(gptq_dtype dt, gptq_mx_format xf, int64_t n_tok, int64_t d_in, int64_t d_ff, bool aligned) {
+    MatArgs a = mat_args(nullptr, nullptr, n_tok, d_in, d_ff, nullptr, d_ff);
+    a.W2 = (const uint8_t*)&a;             // two matrices, for the count of rows; not read
+    if (xf == GPTQ_MX_FP8) return choose_gated<ACT_FP8>(a);
+    if (xf == GPTQ_MX_FP4) return choose_gated<ACT_FP4>(a);
+    a.full = whole_steps(aligned, d_in, d_in);
+    return dt == GPTQ_BF16 ? choose_gated<ACT_BF16>(a) : dt == GPTQ_F16 ? choose_gated<ACT_F16>(a) : choose_gated<ACT_F32>(a);
 }
 
 gptq_status mx_matmul_launch(const void* X, gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t ld_x,
