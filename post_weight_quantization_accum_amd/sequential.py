@@ -23,6 +23,16 @@ cache_attention from there.
 
     A  = attention(X W_q^T, cache of X W_k^T and X W_v^T)
 
+With norms in its blocks (Block.norm1 and norm2, optionally biases and norms of
+the outputs; norms=Norms(...) says of which kind) the stream is normalised in
+front of q, k, v and fc1, by residual_norm, which also takes the blocks' outputs
+into it:
+
+    n1 = norm(X) norm1 + bias1             q, k, v <- H(n1)
+    h1 = s X + p(A W_out^T)                (p: norm() post1 where there is one)
+    n2 = norm(h1) norm2 + bias2            fc1 <- H(n2)
+    X' = s h1 + p(relu(n2 W_fc1^T) W_fc2^T)
+
 Every product uses the already-quantized weights, computed by
 gptq_dequant_matmul from the packed words (with act-order: packed in
 quantization order, activations gathered into that order first).  Products come out
@@ -37,8 +47,9 @@ import dataclasses
 
 from . import (cache_attention, cache_write, dequant_matmul, factored_supported, gather_columns, hessian_accumulate,
                load, new_cache, pack, pack_permuted, prepare_hinv, prepare_hinv_factored, quantize_layer,
-               quantize_layer_factored)
+               quantize_layer_factored, residual_norm)
 from .kv_cache import FORMATS
+from .norm import KINDS
 
 LAYERS = ("q", "k", "v", "out", "fc1", "fc2")
 
@@ -47,13 +58,22 @@ LAYERS = ("q", "k", "v", "out", "fc1", "fc2")
 class Block:
     """Weights of one block (device tensors, d_out x d_in, fp16/bf16/fp32):
     q, k, v, out: hidden x hidden; fc1: ffn x hidden; fc2: hidden x ffn.
-    With attention of fewer kv heads, k and v have kv_heads * head_dim rows."""
+    With attention of fewer kv heads, k and v have kv_heads * head_dim rows.
+    norm1, norm2 (both or neither): the norms' weights in front of q, k, v and
+    of fc1, with bias1, bias2 if there are; post1, post2: those of the norms of
+    out's and fc2's products, if there are (all of hidden values, one dtype)."""
     q: object
     k: object
     v: object
     out: object
     fc1: object
     fc2: object
+    norm1: object = None
+    bias1: object = None
+    post1: object = None
+    norm2: object = None
+    bias2: object = None
+    post2: object = None
 
 
 @dataclasses.dataclass
@@ -70,9 +90,38 @@ class Attention:
     window: int = 0
 
 
+@dataclasses.dataclass
+class Norms:
+    """The norms of blocks that have some, as in residual_norm."""
+    kind: str = "rms"
+    eps: float = 1e-6
+    residual_scale: float = 1.0
+
+
 def _torch():
     import torch
     return torch
+
+
+def _norms(block: Block, X, norms: Norms | None):
+    """The block's norms (None: it has none), checked against its tokens before any work."""
+    vectors = {k: getattr(block, k) for k in ("norm1", "bias1", "post1", "norm2", "bias2", "post2")}
+    given = {k: v for k, v in vectors.items() if v is not None}
+    if not given:
+        if norms is not None:
+            raise ValueError("norms were given, but the block has no norm1 and norm2")
+        return None
+    if block.norm1 is None or block.norm2 is None:
+        raise ValueError("a block with norms has norm1 and norm2")
+    for name, v in given.items():
+        if tuple(v.shape) != (X.shape[1],) or v.dtype != block.norm1.dtype or (X.shape[1] > 1 and v.stride(0) != 1):
+            raise ValueError(f"{name} must have as many values as a token, all norms of one dtype")
+    norms = norms or Norms()
+    if norms.kind not in KINDS:
+        raise ValueError(f"norms.kind must be one of {', '.join(KINDS)}")
+    if not (0 <= norms.eps < float("inf")) or not abs(norms.residual_scale) < float("inf"):
+        raise ValueError("norms.eps must be 0 or more, and norms.eps and residual_scale finite")
+    return norms
 
 
 def _hessian(X):
@@ -188,15 +237,20 @@ def _attend(X, res, cfg, attention: Attention, shape, stats: dict | None):
 
 
 def quantize_block(block: Block, X, cfg, stats: dict | None = None, want_w_hat: bool = True,
-                   attention: Attention | None = None):
+                   attention: Attention | None = None, norms: Norms | None = None):
     """Quantize one block from its input activations X (tokens x hidden,
     device, fp16/bf16).  Returns (per-layer outputs of quantize_layer plus
     perm and packed, the activations each layer was quantized on, the next
     block's input X').  want_w_hat=False skips the float32 reconstructions
     (4 bytes per weight).  attention: identity unless given (stats then gets
-    attention_ms)."""
+    attention_ms).  norms: of blocks that have norms (Norms() unless given)."""
     dt = X.dtype
     shape = None if attention is None else _attention_shape(block, X, attention)
+    norms = _norms(block, X, norms)
+    kw = {} if norms is None else dataclasses.asdict(norms)
+    X_in = X
+    if norms is not None:
+        _, X = residual_norm(X, weight=block.norm1, bias=block.bias1, kind=norms.kind, eps=norms.eps)
     res, inputs = {}, {}
     res.update(_quantize_shared({"q": block.q, "k": block.k, "v": block.v}, X, cfg, stats, want_w_hat))
     for n in ("q", "k", "v"):
@@ -204,19 +258,27 @@ def quantize_block(block: Block, X, cfg, stats: dict | None = None, want_w_hat: 
     A = _product(X, res["v"], cfg, stats).to(dt) if attention is None else _attend(X, res, cfg, attention, shape, stats)
     inputs["out"] = A
     res.update(_quantize_shared({"out": block.out}, A, cfg, stats, want_w_hat))
-    h1f = X.float() + _product(A, res["out"], cfg, stats)
-    h1 = h1f.to(dt)
+    if norms is None:
+        h1f = X.float() + _product(A, res["out"], cfg, stats)
+        h1 = h1f.to(dt)
+    else:
+        h1f, h1 = residual_norm(X_in, _product(A, res["out"], cfg, stats), weight=block.norm2, bias=block.bias2,
+                                post_weight=block.post1, h_dtype=_torch().float32, dtype=dt, **kw)
     inputs["fc1"] = h1
     res.update(_quantize_shared({"fc1": block.fc1}, h1, cfg, stats, want_w_hat))
     r = _torch().relu(_product(h1, res["fc1"], cfg, stats)).to(dt)
     inputs["fc2"] = r
     res.update(_quantize_shared({"fc2": block.fc2}, r, cfg, stats, want_w_hat))
-    X_next = (h1f + _product(r, res["fc2"], cfg, stats)).to(dt)
+    if norms is None:
+        X_next = (h1f + _product(r, res["fc2"], cfg, stats)).to(dt)
+    else:
+        X_next = _torch().empty_like(X_in, memory_format=_torch().contiguous_format)
+        residual_norm(h1f, _product(r, res["fc2"], cfg, stats), post_weight=block.post2, out=(X_next, None), **kw)
     return res, inputs, X_next
 
 
 def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool = True,
-                   attention: Attention | None = None):
+                   attention: Attention | None = None, norms: Norms | None = None):
     """Quantize the blocks in order; block b+1 is calibrated on the output of
     the already-quantized block b.  Returns a list of (outputs, inputs) per
     block and the stack's output activations."""
@@ -224,7 +286,7 @@ def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool 
     out = []
     X = X0
     for b in blocks:
-        res, inputs, X = quantize_block(b, X, cfg, stats, want_w_hat, attention)
+        res, inputs, X = quantize_block(b, X, cfg, stats, want_w_hat, attention, norms)
         out.append((res, inputs))
     return out, X
 
@@ -233,4 +295,4 @@ def new_stats() -> dict:
     return {"hessian_ms": 0.0, "solver_ms": 0.0, "product_ms": 0.0}
 
 
-__all__ = ["Attention", "Block", "LAYERS", "quantize_block", "quantize_stack", "new_stats"]
+__all__ = ["Attention", "Block", "LAYERS", "Norms", "quantize_block", "quantize_stack", "new_stats"]
