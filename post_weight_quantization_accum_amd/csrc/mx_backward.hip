@@ -694,8 +694,9 @@ Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
         const double* us = STAGE_US[tf - 1];
         // more parts than make two rounds of the chip cost a join and save nothing
         const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, all));
-        for (int64_t want = 1; want <= most; ++want) {
-            const int64_t per = ceil_div(all, want), parts = ceil_div(all, per);
+        for (int64_t want = 1, per; want <= most; want = per > 1 ? ceil_div(all, per - 1) : most + 1) {
+            per = ceil_div(all, want);
+            const int64_t parts = ceil_div(all, per);
             const int64_t full = tiles * parts / 256, rest = tiles * parts % 256;
             const double fill = rest / 256.0, stage = fill < 0.5 ? us[0] + 2 * fill * (us[1] - us[0]) : us[1] + (2 * fill - 1) * (us[2] - us[1]);
             const double cost = full * (per * us[2] + TILE_US[tf - 1]) + (rest ? per * stage + TILE_US[tf - 1] : 0) +
@@ -712,10 +713,8 @@ Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
 }
 
 int64_t padded(int64_t rows) { return ceil_div(rows, SK) * SK; }
-// Elements from token to token: an odd multiple of 256 bytes, so that one stage's
-// pieces of a tile's tokens lie on all channels of a cache (2 x 11008 rows apart
-// they hit a quarter of them).
-int64_t row_of(int64_t rows, int segments) { return (ceil_div(padded(rows) * segments, 128) | 1) * 128; }
+// elements from token to token in the planes
+int64_t row_of(int64_t rows, int segments) { return padded(rows) * segments; }
 // bytes of the planes that a call makes of n_tok rows
 size_t planes_bytes(int64_t n_tok, int64_t rows, int segments) {
     return align_up((size_t)n_tok * row_of(rows, segments) * 2, 256);
