@@ -119,13 +119,22 @@ __device__ __forceinline__ u32x4_t fp8x8(uint32_t w0, uint32_t w1, float s) {
     return r;
 }
 
+// 16 and 8 bytes in memory that start where an element may: gfx950 takes wide
+// accesses at any address (one row more of a cache for a wave of them; eight
+// accesses by single elements cost five times as much).
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_any_t __attribute__((aligned(2)));
+typedef float f32x2_any_t __attribute__((ext_vector_type(2), aligned(4)));
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+
 // Eight consecutive elements of a row as float32; n of them exist (0..8),
-// the others are 0.  vec: the whole 8 exist and p is 16-byte aligned.
+// the others are 0.  vec: the whole 8 exist.
 __device__ __forceinline__ void load8_f32(const void* X, gptq_dtype dt, int64_t at, int n, bool vec, float (&v)[8]) {
     if (dt == GPTQ_F32) {
         const float* p = (const float*)X + at;
         if (vec) {
-            const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+            const f32x4_any_t a = *(const f32x4_any_t*)p, b = *(const f32x4_any_t*)(p + 4);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
@@ -137,7 +146,7 @@ __device__ __forceinline__ void load8_f32(const void* X, gptq_dtype dt, int64_t 
     const uint16_t* p = (const uint16_t*)X + at;
     uint32_t w[4];
     if (vec) {
-        const uint4 a = *(const uint4*)p;
+        const u32x4_any_t a = *(const u32x4_any_t*)p;
         w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     } else {
 #pragma unroll
@@ -163,8 +172,8 @@ __device__ __forceinline__ void store8(void* Y, gptq_dtype dt, int64_t at, int n
     if (dt == GPTQ_F32) {
         float* p = (float*)Y + at;
         if (vec) {
-            *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-            *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *(f32x4_any_t*)p = f32x4_any_t{v[0], v[1], v[2], v[3]};
+            *(f32x4_any_t*)(p + 4) = f32x4_any_t{v[4], v[5], v[6], v[7]};
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -178,7 +187,7 @@ __device__ __forceinline__ void store8(void* Y, gptq_dtype dt, int64_t at, int n
     for (int i = 0; i < 4; ++i)
         w[i] = dt == GPTQ_BF16 ? H16<true>::pack(v[2 * i], v[2 * i + 1]) : H16<false>::pack(v[2 * i], v[2 * i + 1]);
     if (vec) {
-        *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+        *(u32x4_any_t*)p = u32x4_any_t{w[0], w[1], w[2], w[3]};
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
