@@ -79,12 +79,13 @@ __device__ __forceinline__ void activate_with_slope(gptq_activation act, float v
     }
 }
 
-// Four neighbouring outputs, n of which exist; whole: all, and on their own size.
-__device__ __forceinline__ void put4(void* Y, gptq_dtype dt, bool whole, int64_t at, int n, const float (&v)[4]) {
+// Four neighbouring outputs, n of which exist.
+__device__ __forceinline__ void put4(void* Y, gptq_dtype dt, int64_t at, int n, const float (&v)[4]) {
+    const bool whole = n >= 4;
     if (dt == GPTQ_F32) {
         float* y = (float*)Y + at;
         if (whole) {
-            *(f32x4_t*)y = f32x4_t{v[0], v[1], v[2], v[3]};
+            *(f32x4_any_t*)y = f32x4_any_t{v[0], v[1], v[2], v[3]};
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -97,7 +98,7 @@ __device__ __forceinline__ void put4(void* Y, gptq_dtype dt, bool whole, int64_t
     w.x = dt == GPTQ_BF16 ? H16<true>::pack(v[0], v[1]) : H16<false>::pack(v[0], v[1]);
     w.y = dt == GPTQ_BF16 ? H16<true>::pack(v[2], v[3]) : H16<false>::pack(v[2], v[3]);
     if (whole) {
-        *(u32x2_t*)y = w;
+        *(u32x2_any_t*)y = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -45,8 +45,8 @@ struct Call {
     int64_t w_row, s_row;      // bytes per row
     int stages, per;           // stages of one segment; stages of one part
     int parts;
-    float* sums;               // [part][token][d_in], of more than one part
-    bool out8;                 // dX's groups of eight start on 16 bytes
+    float* sums;               // [part][token][pitch], of more than one part
+    int64_t pitch;             // d_in, to whole groups of eight
 };
 
 // ---------------------------------------------------------------------------
@@ -451,55 +451,64 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
             float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             if (t >= a.n_tok || m == 0) continue;
             if (c.parts > 1) {
-                store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * a.d_in + col, m, m == 8 && a.d_in % 4 == 0, v);
+                store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * c.pitch + col, 8, true, v);
             } else {
                 const int e2 = a.exps ? a.exps[t] : 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
-                store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, c.out8 && m == 8, v);
+                store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, m == 8, v);
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
-// dX from the parts' sums, in the order of the parts (zeros of none): four columns
-// of a token by a thread.
+// dX from the parts' sums (zeros of none): four columns of a token by S threads,
+// each a share of the parts, in their order, eight on their way at once; their
+// sums meet in LDS.  218 parts of one token's 249 columns: 105 us by one thread
+// one part after the other, 4 so.
+template <int S>
 __global__ __launch_bounds__(256) void mx_back_join_kernel(Call c) {
+    constexpr int Q = 256 / S;
+    __shared__ f32x4_t lds[S][Q];
     const BackArgs& a = c.b;
-    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
-    if (n >= a.d_in) return;
-    const int m = (int)min((int64_t)4, a.d_in - n);
-    const bool whole = m == 4 && a.d_in % 4 == 0;
-    const int64_t part = a.n_tok * a.d_in;
-    const float* s = c.sums + t * a.d_in + n;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    int p = 0;
-    if (whole) {
-        for (; p + 8 <= c.parts; p += 8) {       // eight on their way at once
-            f32x4_t x[8];
+    const int64_t row = c.pitch / 4, all = a.n_tok * row;
+    const int lane = threadIdx.x % Q, share = threadIdx.x / Q;
+    const int first = (int)((int64_t)c.parts * share / S), end = (int)((int64_t)c.parts * (share + 1) / S);
+    for (int64_t q0 = (int64_t)blockIdx.x * Q; q0 < all; q0 += (int64_t)gridDim.x * Q) {
+        const int64_t q = q0 + lane;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (q < all) {
+            const f32x4_t* s = (const f32x4_t*)c.sums + q;
+            for (int p = first; p < end; p += 8) {
+                f32x4_t x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = *(const f32x4_t*)(s + (p + e) * part);
+                for (int e = 0; e < 8; ++e) x[e] = s[min(p + e, end - 1) * all];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 8; ++e)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += x[e][q];
+                    for (int i = 0; i < 4; ++i) v[i] += p + e < end ? x[e][i] : 0.0f;
+            }
         }
-        for (; p < c.parts; ++p) {
-            const f32x4_t x = *(const f32x4_t*)(s + p * part);
+        if constexpr (S > 1) {
+            lds[share][lane] = f32x4_t{v[0], v[1], v[2], v[3]};
+            __syncthreads();
+            if (share == 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] += x[q];
+                for (int k = 1; k < S; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += lds[k][lane][i];
+            }
+            __syncthreads();
         }
-    } else {
-        for (; p < c.parts; ++p)
+        if (share != 0 || q >= all) continue;
+        const int64_t t = q / row, n = 4 * (q - t * row);
+        if (n >= a.d_in) continue;
+        const int e2 = a.exps ? a.exps[t] : 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (q < m) v[q] += s[p * part + q];
+        for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], e2);
+        put4(a.dX, a.dx_dt, t * a.ld_dx + n, (int)min((int64_t)4, a.d_in - n), v);
     }
-    const int e2 = a.exps ? a.exps[t] : 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], e2);
-    put4(a.dX, a.dx_dt, c.out8 && m == 4, t * a.ld_dx + n, m, v);
 }
 
 // The caller's gradients as planes: padded to whole stages, on 16 bytes, and
@@ -509,7 +518,6 @@ struct Planes {
     gptq_dtype dt;
     int64_t n_tok, rows, ld, pad, to;
     uint16_t* out;             // [token][plane][pad], token to token `to` elements
-    bool vec;
 };
 __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
     const int64_t k = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
@@ -518,7 +526,7 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
         const int n = (int)max((int64_t)0, min((int64_t)8, c.rows - k));
         if (c.dt == GPTQ_F32) {
             float v[8];
-            load8_f32(c.D, GPTQ_F32, t * c.ld + k, n, c.vec && n == 8, v);
+            load8_f32(c.D, GPTQ_F32, t * c.ld + k, n, n == 8, v);
             u32x4_t p[3];
             cut(v, p);
 #pragma unroll
@@ -526,9 +534,13 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
         } else {
             const uint16_t* d = (const uint16_t*)c.D + t * c.ld + k;
             u32x4_t w;
+            if (n == 8) {
+                w = *(const u32x4_any_t*)d;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (2 * i < n ? d[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)d[2 * i + 1] : 0u) << 16;
+                for (int i = 0; i < 4; ++i)
+                    w[i] = (2 * i < n ? d[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)d[2 * i + 1] : 0u) << 16;
+            }
             *(u32x4_t*)(c.out + t * c.to + k) = w;
         }
     }
@@ -544,23 +556,16 @@ struct Gates {
     uint16_t* D;               // [token][2][plane][pad], token to token ld elements
     int64_t pad, ld;
     int32_t* exps;             // of float16
-    bool vec, vec_out;
 };
 
-// Eight values from column k of a token on, of which n exist.
-template <gptq_dtype DT>
-__device__ __forceinline__ void load_eight(const void* p, int64_t at, int n, bool vec, float (&v)[8]) {
-    if (vec && n == 8) load8_f32(p, DT, at, 8, true, v);
-    else load8_f32(p, DT, at, n, false, v);
-}
-
+// Eight values of both gradients from column k of a token on, of which n exist.
 template <gptq_dtype DT, gptq_activation ACT>
 __device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_t k, int n, float (&g)[8], float (&u)[8]) {
     const GatedBackArgs& a = c.a;
     float dy[8], gv[8], uv[8];
-    load_eight<DT>(a.dY, t * a.ld_dy + k, n, c.vec, dy);
-    load_eight<DT>(a.G, t * a.ld_gu + k, n, c.vec, gv);
-    load_eight<DT>(a.U, t * a.ld_gu + k, n, c.vec, uv);
+    load8_f32(a.dY, DT, t * a.ld_dy + k, n, n == 8, dy);
+    load8_f32(a.G, DT, t * a.ld_gu + k, n, n == 8, gv);
+    load8_f32(a.U, DT, t * a.ld_gu + k, n, n == 8, uv);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float value, slope;
@@ -569,8 +574,8 @@ __device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_
         u[i] = i < n ? dy[i] * value : 0.0f;
     }
     if (a.dG && n > 0) {
-        store8(a.dG, DT, t * a.ld_dgu + k, n, c.vec_out && n == 8, g);
-        store8(a.dU, DT, t * a.ld_dgu + k, n, c.vec_out && n == 8, u);
+        store8(a.dG, DT, t * a.ld_dgu + k, n, n == 8, g);
+        store8(a.dU, DT, t * a.ld_dgu + k, n, n == 8, u);
     }
 }
 
@@ -715,13 +720,14 @@ Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
 int64_t padded(int64_t rows) { return ceil_div(rows, SK) * SK; }
 // elements from token to token in the planes
 int64_t row_of(int64_t rows, int segments) { return padded(rows) * segments; }
+int64_t pitch_of(int64_t d_in) { return ceil_div(d_in, 8) * 8; }
 // bytes of the planes that a call makes of n_tok rows
 size_t planes_bytes(int64_t n_tok, int64_t rows, int segments) {
     return align_up((size_t)n_tok * row_of(rows, segments) * 2, 256);
 }
 size_t sums_bytes(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
     const Plan p = plan_of(segments, n_tok, d_in, rows);
-    return p.parts > 1 ? (size_t)p.parts * n_tok * d_in * sizeof(float) : 0;
+    return p.parts > 1 ? (size_t)p.parts * n_tok * pitch_of(d_in) * sizeof(float) : 0;
 }
 
 template <bool HALF, int TF, int TW>
@@ -737,14 +743,13 @@ gptq_status launch_tile(const Call& c, hipStream_t s) {
 gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
     const BackArgs& a = c.b;
     const Plan p = plan_of(segments, a.n_tok, a.d_in, a.rows);
-    const int size = a.dx_dt == GPTQ_F32 ? 4 : 2;
     c.planes = segments / a.matrices;
     c.w_row = mx_code_bytes(a.d_in, GPTQ_MX_FP4);
     c.s_row = mx_scale_bytes(a.d_in);
     c.stages = p.stages;
     c.per = p.per;
     c.parts = p.parts;
-    c.out8 = ((uintptr_t)a.dX | (uintptr_t)(a.ld_dx * size)) % 16 == 0;
+    c.pitch = pitch_of(a.d_in);
     if (c.parts > 0) {
         const bool half = a.dt == GPTQ_F16;
         gptq_status st;
@@ -755,15 +760,11 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
         if (st != GPTQ_OK) return st;
     }
     if (c.parts != 1) {
-        for (int64_t t = 0; t < a.n_tok; t += 65535) {
-            Call j = c;
-            const int64_t n = std::min<int64_t>(65535, a.n_tok - t);
-            j.b.dX = (char*)a.dX + t * a.ld_dx * size;
-            if (j.sums) j.sums += t * a.d_in;
-            if (a.exps) j.b.exps += t;
-            mx_back_join_kernel<<<dim3((unsigned)ceil_div(a.d_in, 1024), (unsigned)n), 256, 0, s>>>(j);
-            GPTQ_LAUNCH_CHECK();
-        }
+        const auto groups = [&](int shares) { return (unsigned)std::min<int64_t>(ceil_div(a.n_tok * c.pitch / 4, 256 / shares), 1 << 20); };
+        if (c.parts <= 8) mx_back_join_kernel<1><<<groups(1), 256, 0, s>>>(c);
+        else if (c.parts <= 32) mx_back_join_kernel<4><<<groups(4), 256, 0, s>>>(c);
+        else mx_back_join_kernel<16><<<groups(16), 256, 0, s>>>(c);
+        GPTQ_LAUNCH_CHECK();
     }
     return GPTQ_OK;
 }
@@ -795,7 +796,7 @@ gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, voi
         c.D = (const uint16_t*)ws;
         c.ld = row_of(a.rows, planes);
         if (a.rows > 0) {
-            Planes p{D, a.dt, a.n_tok, a.rows, ld, c.pad, c.ld, (uint16_t*)ws, on16};
+            Planes p{D, a.dt, a.n_tok, a.rows, ld, c.pad, c.ld, (uint16_t*)ws};
             mx_planes_kernel<<<dim3((unsigned)ceil_div(c.pad, 2048), (unsigned)std::min<int64_t>(a.n_tok, 65535)), 256, 0, s>>>(p);
             GPTQ_LAUNCH_CHECK();
         }
@@ -810,7 +811,7 @@ size_t mx_gated_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t 
 
 gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream_t s) {
     const bool wide = a.dt == GPTQ_F32;
-    const int size = wide ? 4 : 2, segments = wide ? 6 : 2;
+    const int segments = wide ? 6 : 2;
     Call c{};
     BackArgs& b = c.b;
     b.dt = a.dt;
@@ -837,9 +838,6 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         g.pad = c.pad;
         g.ld = c.ld;
         g.exps = a.dt == GPTQ_F16 ? (int32_t*)exps : nullptr;
-        const auto fits = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * size)) % 16 == 0; };
-        g.vec = fits(a.dY, a.ld_dy) && fits(a.G, a.ld_gu) && fits(a.U, a.ld_gu);
-        g.vec_out = a.dG && fits(a.dG, a.ld_dgu) && fits(a.dU, a.ld_dgu);
         switch (a.act) {
             case GPTQ_ACT_SILU: launch_gates<GPTQ_ACT_SILU>(g, s); break;
             case GPTQ_ACT_GELU: launch_gates<GPTQ_ACT_GELU>(g, s); break;

@@ -24,8 +24,7 @@ struct MatArgs {
     int full;              // the first of them whose activations are read in whole 16-byte pieces
     int64_t d_out, ld_y;
     float* Y;
-    bool y_aligned;        // Y rows start on 16 bytes (of gated products: all outputs' groups of four on their own size)
-    bool y_aligned8;       // of gated products: their groups of eight on 16 bytes
+    bool y_aligned;        // Y rows start on 16 bytes
     // gated products: W and S are the gate's, d_out rows of each
     const uint8_t *W2, *S2;
     gptq_activation act;
@@ -96,7 +95,11 @@ struct Raw {
             for (int i = 0; i < W; ++i) w[i] = p[i];
         } else {
             const int n = (int)max((int64_t)0, min((int64_t)(8 * N), a.d_in - k));
-            if constexpr (DT == ACT_F32) {
+            if (n == 8 * N) {
+                const u32x4_any_t* p = (const u32x4_any_t*)((const char*)a.X + (t * a.ld_x + k) * (DT == ACT_F32 ? 4 : 2));
+#pragma unroll
+                for (int i = 0; i < W; ++i) w[i] = p[i];
+            } else if constexpr (DT == ACT_F32) {
                 const uint32_t* p = (const uint32_t*)a.X + t * a.ld_x + k;
 #pragma unroll
                 for (int i = 0; i < 8 * N; ++i) w[i >> 2][i & 3] = i < n ? p[i] : 0u;
@@ -191,14 +194,13 @@ __device__ __forceinline__ void store4(const MatArgs& a, int64_t t, int64_t r, f
 __device__ __forceinline__ void store_gated4(const MatArgs& a, int64_t t, int64_t r, const float (&g)[4], const float (&u)[4]) {
     if (r >= a.d_out) return;
     const int n = (int)min((int64_t)4, a.d_out - r);
-    const bool whole = a.y_aligned && n == 4;
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = activate<false>(a.act, g[i]) * u[i];
-    put4(a.YT, a.y_dt, whole, t * a.ld_y + r, n, y);
+    put4(a.YT, a.y_dt, t * a.ld_y + r, n, y);
     if (a.G) {
-        put4(a.G, a.y_dt, whole, t * a.ld_gu + r, n, g);
-        put4(a.U, a.y_dt, whole, t * a.ld_gu + r, n, u);
+        put4(a.G, a.y_dt, t * a.ld_gu + r, n, g);
+        put4(a.U, a.y_dt, t * a.ld_gu + r, n, u);
     }
 }
 
@@ -221,7 +223,6 @@ __device__ __forceinline__ void gated_out(const MatArgs& a, char* own, const f16
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int c = lane & 3;
-    const bool all8 = a.y_aligned8;
 #pragma unroll 1
     for (int n = 0; n < 2 * RM * TJ; ++n) {
         const int j = n / (2 * RM), i = n / 2 % RM, token = 16 * (n & 1) + (lane >> 2);
@@ -242,10 +243,10 @@ __device__ __forceinline__ void gated_out(const MatArgs& a, char* own, const f16
         }
         if (a.y_dt == GPTQ_F32) gate8<false>(a.act, g, u, y);
         else gate8<true>(a.act, g, u, y);
-        store8(a.YT, a.y_dt, t * a.ld_y + r, m, all8 && m == 8, y);
+        store8(a.YT, a.y_dt, t * a.ld_y + r, m, m == 8, y);
         if (a.G) {
-            store8(a.G, a.y_dt, t * a.ld_gu + r, m, all8 && m == 8, g);
-            store8(a.U, a.y_dt, t * a.ld_gu + r, m, all8 && m == 8, u);
+            store8(a.G, a.y_dt, t * a.ld_gu + r, m, m == 8, g);
+            store8(a.U, a.y_dt, t * a.ld_gu + r, m, m == 8, u);
         }
     }
 }
@@ -1177,8 +1178,10 @@ constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // fl
                                  {3.5, 4.8, 5.7, 6.6, 5.9, 9.1, 13.4},     // e4m3
                                  {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 0}};      // e2m1
 // Where X's rows do not start on 16 bytes (or have no 128 columns), every step
-// is read by single elements, without the ring: one round of the tiles in the
-// same order, float32 and 16 bits (float32 (1,1): 29 for 13 tokens, 48 for 16).
+// is read from memory directly, without the ring: one round of the tiles in the
+// same order, float32 and 16 bits (float32 (1,1): 29 for 13 tokens, 48 for 16), as
+// measured with reads by single elements.  Whole pieces are read at once since;
+// the rule, and with it the order of the results' sums, is as it was.
 // Times of the general kernel there: float32 226 a round, 16 bits 250 for one
 // and 305 for two rounds.  64 tokens 4096 -> 4096 bf16: (4,1) 27 us, (2,2) 46,
 // which the ring's times would choose.
@@ -1254,42 +1257,49 @@ gptq_status launch_parts(const MatArgs& a, hipStream_t s) {
 // One bf16 token 4096 -> 2 x 11008: (6,1) 14.9 us in one round, (8,1) 17.1, (4,1)
 // 18.9, (2,1) 19.1; 13 f16 tokens 5120 -> 2 x 13824: (8,1) 23.7, (4,1) 25.8, (2,1)
 // 31.4, (6,1) 34.9 (two rounds).  1500 e2m1 tokens: 256 x 128 120 us, 128 x 128 129.
+// Part of a round does not grow with the columns (FIXED_US, from 128 columns): 463
+// e4m3 tokens 140 -> 2 x 2102 take 9.1 us by 128 x 128, 20 by (4,2).  Rows of X that
+// do not start on 16 bytes, 512 tokens 4090 -> 2 x 2048 bf16: 128 x 128 69 us, (4,2)
+// 69, (2,2) 97, (4,1) 98 (a round for 18, 12 and 13).
 constexpr int GATED_TILE[6] = {1, 3, 4, 5, 10, 11}, GATED_RT[6] = {2, 4, 2, 4, 6, 8}, GATED_TT[6] = {1, 1, 2, 2, 1, 1};
-constexpr double GATED_US[5][6] = {{11, 15, 19, 0, 20, 25},                // float32
+constexpr double GATED_US[5][6] = {{11, 15, 0, 0, 20, 25},                 // float32
                                    {6.9, 10.3, 7.4, 11.9, 14.5, 17.5},     // float16
                                    {6.9, 10.3, 7.4, 11.9, 14.5, 17.5},     // bfloat16
                                    {5.9, 9.0, 7.4, 11.5, 15.0, 17.0},      // e4m3
                                    {5.7, 9.0, 7.3, 11.2, 14.0, 17.0}};     // e2m1
+constexpr double GATED_DIRECT_US[2][4] = {{13, 17, 0, 0}, {8.5, 12.5, 12.2, 17.5}};
+constexpr double FIXED_US[6] = {2.2, 2.7, 2.7, 4.4, 3.8, 4.2};
 
 template <Act DT>
 int choose_gated(const MatArgs& a) {
     int best = 9;
     double least = 1e30;
-    const auto offer = [&](int id, double cost) {
+    const auto offer = [&](int id, double n, double fixed, double us) {
+        const double cost = n * (fixed + (us - fixed) * a.d_in / 4096.0);
         if (cost < least) {
             least = cost;
             best = id;
         }
     };
     for (int i = 0; i < 6; ++i) {
-        // by single elements (DIRECT_US): without the ring more rows gain nothing
-        const double us = a.full > 0 ? GATED_US[DT][i] : i < 4 && GATED_US[DT][i] > 0 ? DIRECT_US[DT != ACT_F32][GATED_TILE[i]] : 0;
-        if (us > 0) offer(GATED_TILE[i], rounds(a, 16 * GATED_RT[i], 16 * GATED_TT[i]) * us);
+        // without the ring more rows gain nothing
+        const double us = a.full > 0 ? GATED_US[DT][i] : i < 4 ? GATED_DIRECT_US[DT != ACT_F32][i] : 0;
+        if (us > 0) offer(GATED_TILE[i], rounds(a, 16 * GATED_RT[i], 16 * GATED_TT[i]), FIXED_US[i], us);
     }
     if constexpr (DT == ACT_BF16 || DT == ACT_F16) {
         if (a.full > 0) {
-            offer(7, rounds(a, 128, MT) * 30.0);
-            offer(8, rounds(a, 256, MT) * 48.0);
+            offer(7, rounds(a, 128, MT), 6.0, 30.0);
+            offer(8, rounds(a, 256, MT), 7.5, 48.0);
         } else {
-            offer(9, std::max(1.0, 0.61 * rounds(a, 128, MT)) * 250.0);
+            offer(9, std::max(1.0, 0.8 * rounds(a, 128, MT)), 7.0, 67.0);
         }
     } else if constexpr (DT == ACT_F32) {
-        offer(9, rounds(a, 128, MT) * (a.full > 0 ? 129.0 : 226.0));
+        offer(9, rounds(a, 128, MT), 6.0, a.full > 0 ? 129.0 : 136.0);
     } else if constexpr (DT == ACT_FP8) {
-        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)) * 72.0);
+        offer(9, std::max(1.0, 0.68 * rounds(a, 128, MT)), 6.0, 72.0);
     } else {
-        offer(7, rounds(a, 128, MT) * 14.5);
-        offer(8, rounds(a, 256, MT) * 23.5);
+        offer(7, rounds(a, 128, MT), 6.0, 14.5);
+        offer(8, rounds(a, 256, MT), 9.0, 23.5);
     }
     return best;
 }
@@ -1300,7 +1310,7 @@ gptq_status launch_gated(const MatArgs& a, hipStream_t s) {
     switch (best) {
         case 1: return launch_few<DT, 2, 1, true>(a, s);
         case 3: return launch_few<DT, 4, 1, true>(a, s);
-        case 4: return launch_few<DT, 2, 2, true>(a, s);
+        case 4: if constexpr (GATED_US[DT][2] > 0) return launch_few<DT, 2, 2, true>(a, s); break;
         case 5: if constexpr (GATED_US[DT][3] > 0) return launch_few<DT, 4, 2, true>(a, s); break;
         case 10: return launch_few<DT, 6, 1, true>(a, s);
         case 11: return launch_few<DT, 8, 1, true>(a, s);
@@ -1334,7 +1344,6 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
     a.ld_y = ld_y;
     a.Y = Y;
     a.W2 = a.S2 = nullptr;
-    a.y_aligned8 = false;
     a.act = GPTQ_ACT_SILU;
     a.y_dt = GPTQ_F32;
     a.YT = a.G = a.U = nullptr;
@@ -1344,8 +1353,6 @@ MatArgs mat_args(const uint8_t* codes, const uint8_t* scales, int64_t n_tok, int
 
 // The gated product's second matrix and outputs.
 void gate_args(MatArgs& a, const GatedArgs& g) {
-    const size_t four = g.y_dt == GPTQ_F32 ? 16 : 8;
-    const auto fits = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * (int64_t)(four / 4))) % four == 0; };
     a.W2 = g.up_codes;
     a.S2 = g.up_scales;
     a.act = g.act;
@@ -1355,9 +1362,6 @@ void gate_args(MatArgs& a, const GatedArgs& g) {
     a.G = g.G;
     a.U = g.U;
     a.ld_gu = g.ld_gu;
-    a.y_aligned = fits(g.Y, g.ld_y) && (!g.G || (fits(g.G, g.ld_gu) && fits(g.U, g.ld_gu)));
-    const auto on16 = [&](const void* p, int64_t ld) { return ((uintptr_t)p | (uintptr_t)(ld * (int64_t)(four / 4))) % 16 == 0; };
-    a.y_aligned8 = on16(g.Y, g.ld_y) && (!g.G || (on16(g.G, g.ld_gu) && on16(g.U, g.ld_gu)));
 }
 
 // Steps of 16-bit or float32 activations that are read in whole pieces: offsets

@@ -68,12 +68,11 @@ def test_gradient_refusals():
 
 # kernel -> (tokens, d_ff); columns: 328 where rows are to start on 16 bytes, else 329
 FEW = {1: (3, 100), 3: (1, 4200), 10: (1, 8250), 11: (7, 12300)}
-HALF = {**FEW, 4: (17, 2100), 5: (18, 4200)}
-SIXTEEN = {**HALF, 7: (33, 8250), 8: (34, 16500)}
-ODD = {1: (3, 100), 3: (2, 4200), 9: (65, 13200)}
-SIZES = {("f32", 1): {**FEW, 9: (4200, 260), 4: (1 << 20, 8)}, ("f32", 0): {**ODD, 4: (1 << 14, 8)},
-         ("f16", 1): SIXTEEN, ("bf16", 1): SIXTEEN, ("f16", 0): ODD, ("bf16", 0): ODD,
-         ("fp8", 1): {**HALF, 9: (100, 12300)}, ("fp4", 1): {k: v for k, v in {**SIXTEEN, 7: (2, 12300), 8: (3, 16500)}.items() if k != 11}}
+HALF = {**FEW, 4: (17, 2100), 5: (4200, 20)}
+SIXTEEN = {**HALF, 7: (17, 8250), 8: (18, 16500)}
+ODD = {1: (3, 100), 3: (2, 4200), 4: (17, 2100), 5: (18, 4200), 9: (33, 8250)}
+SIZES = {("f32", 1): {**FEW, 9: (33, 12300)}, ("f32", 0): {1: (3, 100), 3: (2, 4200), 9: (33, 10950)}, ("f16", 1): SIXTEEN,
+         ("bf16", 1): SIXTEEN, ("f16", 0): ODD, ("bf16", 0): ODD, ("fp8", 1): {**HALF, 9: (33, 10950)}, ("fp4", 1): SIXTEEN}
 KINDS = {"f32": (_lib.F32, 0), "f16": (_lib.F16, 0), "bf16": (_lib.BF16, 0), "fp8": (0, _lib.MX_FP8), "fp4": (0, _lib.MX_FP4)}
 
 
