@@ -303,3 +303,18 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         kept = [t.clone() for t in got]
         assert all(torch.equal(a, b) for a, b in zip(kept, both()))
+
+
+@pytest.mark.parametrize("n,d", [(3, 5), (40, 89), (700, 1003), (600, 5117), (300, 8191), (600, 9001), (600, 16386)])
+@pytest.mark.parametrize("post", [False, True])
+def test_stream_in_place_of_any_width(n, d, post):
+    """h over X, whose last values two lanes read."""
+    c = case(n, d, b="bf16", post=post, seed=d)
+    h, y = P.residual_norm(c["X"], c["B"], **c["kw"])
+    X = c["X"].clone()
+    y2 = torch.empty_like(y)
+    P.residual_norm(X, c["B"], out=(X, y2), **c["kw"])
+    assert torch.equal(X, h) and torch.equal(y2, y)
+    X = c["X"].clone()
+    P.residual_norm(X, c["B"], out=(X, None), **c["kw"])
+    assert torch.equal(X, h)
