@@ -3,7 +3,7 @@
 //
 // A row is read once into registers, by one wave where it is short and by a
 // workgroup otherwise, and everything about it is computed from there: no
-// value is read twice but by rows of more than 16384 values (wide kernels).
+// value is read twice but by rows of more than 16384 values, of gradients 8192 (wide kernels).
 // Sums over a row are float64: the squares of float32 values leave float32's
 // range, and mean and variance come from one pass (sum and sum of squares)
 // without the loss that float32 would have there.  They cost a few percent of
@@ -525,7 +525,7 @@ __device__ __forceinline__ void write_part(const NormGradArgs& a, int64_t part, 
     store<D>(row_at(a.parts, GPTQ_F32, (part * a.n_slots + a.slot[k]) * a.ld_part), GPTQ_F32, v, T, t, a.f.d, x);
 }
 
-template <int V, Width D, bool WAVE, bool LAYER>
+template <int V, Width D, bool WAVE, bool LAYER, bool NARROW>
 __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArgs a) {
     constexpr int F = FIRST<LAYER>, K = STATS<LAYER>;
     __shared__ Sums<6> lds;
@@ -540,14 +540,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void norm_grad_kernel(NormGradArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[v][k][e] = 0.0f;
     int turn = 0;
-    Piece hr[V], yr[V], br[V], gr[V];
+    Raw8<NARROW> hr[V], yr[V], br[V], gr[V];
     const auto ask = [&](int64_t row) {          // the next row, before this one is worked on
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            hr[v] = load<D>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
-            yr[v] = load<D>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
-            if (a.has_b) br[v] = load<D>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
-            if (a.dH) gr[v] = load<D>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
+            hr[v] = load_as<D, NARROW>(row_at(a.H, a.h_dt, row * a.ld_h), a.h_dt, v, T, t, a.f.d);
+            yr[v] = load_as<D, NARROW>(row_at(a.dY, a.dy_dt, row * a.ld_dy), a.dy_dt, v, T, t, a.f.d);
+            if (a.has_b) br[v] = load_as<D, NARROW>(row_at(a.f.B, a.f.b_dt, row * a.f.ld_b), a.f.b_dt, v, T, t, a.f.d);
+            if (a.dH) gr[v] = load_as<D, NARROW>(row_at(a.dH, a.h_dt, row * a.ld_dh), a.h_dt, v, T, t, a.f.d);
         }
     };
     if (part < a.f.n_tok) ask(part);
@@ -709,16 +709,15 @@ int64_t grad_parts(int64_t n_tok, int64_t d) {
     return std::min<int64_t>(n_tok, 512);
 }
 
-template <Width D, bool LAYER>
+template <Width D, bool LAYER, bool NARROW>
 void launch_grad(const NormGradArgs& a, hipStream_t s) {
     const int64_t d = a.f.d;
     const unsigned n = (unsigned)grad_parts(a.f.n_tok, d);
-    if (D == TINY || d <= 512) norm_grad_kernel<1, D, true, LAYER><<<n / 4, 256, 0, s>>>(a);
+    if (D == TINY || d <= 512) norm_grad_kernel<1, D, true, LAYER, NARROW><<<n / 4, 256, 0, s>>>(a);
     else if constexpr (D == TINY) return;
-    else if (d <= 1024) norm_grad_kernel<2, D, true, LAYER><<<n / 4, 256, 0, s>>>(a);
-    else if (d <= 4096) norm_grad_kernel<1, D, false, LAYER><<<n, threads_for(d, 1), 0, s>>>(a);
-    else if (d <= 8192) norm_grad_kernel<2, D, false, LAYER><<<n, threads_for(d, 2), 0, s>>>(a);
-    else if (d <= 16384) norm_grad_kernel<4, D, false, LAYER><<<n, threads_for(d, 4), 0, s>>>(a);
+    else if (d <= 1024) norm_grad_kernel<2, D, true, LAYER, NARROW><<<n / 4, 256, 0, s>>>(a);
+    else if (d <= 4096) norm_grad_kernel<1, D, false, LAYER, NARROW><<<n, threads_for(d, 1), 0, s>>>(a);
+    else if (d <= 8192) norm_grad_kernel<2, D, false, LAYER, NARROW><<<n, threads_for(d, 2), 0, s>>>(a);
     else norm_grad_wide_kernel<D, LAYER><<<n, 512, 0, s>>>(a);
 }
 
@@ -752,9 +751,12 @@ gptq_status norm_grad_launch(NormGradArgs a, float* d_weight, float* d_bias, flo
         if (outs[k]) o[a.n_slots++] = outs[k];
     }
     if (a.f.n_tok > 0) {
+        const bool narrow = a.h_dt != GPTQ_F32 && a.dy_dt != GPTQ_F32 && (!a.has_b || a.f.b_dt != GPTQ_F32);
         const auto go = [&](auto layer) {
             constexpr bool L = decltype(layer)::value;
-            d < 8 ? launch_grad<TINY, L>(a, s) : d % 8 == 0 ? launch_grad<EIGHTS, L>(a, s) : launch_grad<OTHER, L>(a, s);
+            if (d < 8) launch_grad<TINY, L, false>(a, s);
+            else if (d % 8 == 0) narrow ? launch_grad<EIGHTS, L, true>(a, s) : launch_grad<EIGHTS, L, false>(a, s);
+            else narrow ? launch_grad<OTHER, L, true>(a, s) : launch_grad<OTHER, L, false>(a, s);
         };
         a.f.layer ? go(std::true_type{}) : go(std::false_type{});
         GPTQ_LAUNCH_CHECK();
