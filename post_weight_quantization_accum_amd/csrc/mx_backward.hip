@@ -66,6 +66,11 @@ struct Call {
 // barrier of a stage stands before its last step, whose operands are in
 // registers by then, so that the matrix instructions run on behind it.
 //
+// 2048 tokens through 4096 rows of 11008 bf16: 190 us (980 TFLOP/s; matrix
+// instructions busy 52 % of the clocks, on a chip that lowers its clock as they run:
+// alone they would take 1180 of a stage's 1600 ns), through 2 x 11008 rows of 4096
+// 328 us (1130).  24 tokens, 4096 x 4096: 12 us.
+//
 // Tokens lie in LDS in order, column c at place (c % 4) 64 + c / 4; 16-byte chunk
 // q (eight rows) of place i at slot q ^ (i / 2 % 8), so that sixteen lanes' reads
 // of one chunk of neighbouring places hit all banks.  Lane l ends with columns 4 m + c of its tokens (m the row of
@@ -549,7 +554,8 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 // ---------------------------------------------------------------------------
 // dG and dU as planes: bfloat16 ones rounded to it; float32 ones in three parts;
 // float16 ones scaled by a power of two for each token, for which a workgroup
-// holds the token's values until it has seen the largest finite one.
+// holds the token's values until it has seen the largest finite one.  Bound by
+// memory: 2048 x 11008 bf16 35 us (6.4 TB/s, part of it in the caches).
 // ---------------------------------------------------------------------------
 struct Gates {
     GatedBackArgs a;
