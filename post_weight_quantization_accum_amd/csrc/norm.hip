@@ -401,7 +401,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
 // a second kernel adds the parts in order, in float64.  No atomics: the same
 // call gives the same bits.  The sums' registers leave a compute unit eight waves,
 // which bound it: 8192 x 4096 with a float32 stream 165 us (3.7 TB/s), 16 bits 115;
-// 500 x 768 9.5 and 6 for the parts.
+// 500 x 768 8.9 and 6 for the parts.
 // ---------------------------------------------------------------------------
 enum Vec : int { V_WEIGHT = 0, V_BIAS, V_POST, V_GATE, N_VEC };
 
