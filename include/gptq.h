@@ -455,7 +455,8 @@ typedef enum { GPTQ_ACT_SILU = 0, GPTQ_ACT_GELU = 1, GPTQ_ACT_GELU_TANH = 2, GPT
  * as precise as its products; act and the product of both in float32.  Y: of
  * y_dtype (float32, float16, bfloat16), row stride ld_y.  G, U: both NULL, or
  * n_tok x d_ff of y_dtype with row stride ld_gu that get g and u, as
- * gptq_mx_gated_backward takes them.  Rows of the outputs may start anywhere.
+ * gptq_mx_gated_backward takes them.  Rows of the outputs may start anywhere;
+ * outputs overlap nothing.
  * Errors as in gptq_mx_matmul, and GPTQ_ERR_INVALID_ARG for a bad activation or
  * one of G and U alone.  Asynchronous, no workspace. */
 gptq_status gptq_mx_gated(const void* X, gptq_dtype x_dtype, int64_t n_tok, int64_t d_in, int64_t ld_x,
@@ -484,6 +485,7 @@ int32_t gptq_mx_gated_kernel(gptq_dtype x_dtype, gptq_mx_format x_format, int64_
  * gptq_mx_matmul (float32 dY: three bfloat16 parts, each below 2^-110 off by
  * less than 2^-133); sums are float32, dX is rounded once.  An infinity or NaN
  * in dY reaches its token's outputs as in float32 arithmetic, and no other's.
+ * dX and workspace overlap nothing.
  * workspace: gptq_mx_matmul_backward_workspace(...) bytes (may be 0), 16-byte
  * aligned.  The same call gives the same bits.  d_out == 0: dX is zeros.
  * Errors as in gptq_mx_matmul, and GPTQ_ERR_WORKSPACE.  Asynchronous. */
@@ -512,7 +514,8 @@ gptq_status gptq_mx_backward_plan(gptq_dtype dy_dtype, int32_t matrices, int64_t
  * weights whose scales it does not hold (outside 2^-23 .. 2^13) are multiplied as
  * bfloat16, by the same values in two parts.  Sums are float32.
  * dG_out, dU_out: both NULL, or n_tok x d_ff of G's dtype with row stride ld_dgu
- * that get dG and dU (for adapters beside the weights).  dX: as above.
+ * that get dG and dU (for adapters beside the weights); they may be G and U, with
+ * their stride.  dX: as above.  Otherwise outputs and workspace overlap nothing.
  * RELU's slope at 0 is 0.
  * workspace: gptq_mx_gated_backward_workspace(...) bytes, 16-byte aligned.
  * Errors as in gptq_mx_gated, and GPTQ_ERR_WORKSPACE.  Asynchronous. */

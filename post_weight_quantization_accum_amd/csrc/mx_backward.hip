@@ -564,9 +564,10 @@ struct Gates {
     int32_t* exps;             // of float16
 };
 
-// Eight values of both gradients from column k of a token on, of which n exist.
+// Eight values of both gradients from column k of a token on, of which n exist; to
+// dG and dU, which may be G and U, with `out`: the last time that they are computed.
 template <gptq_dtype DT, gptq_activation ACT>
-__device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_t k, int n, float (&g)[8], float (&u)[8]) {
+__device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_t k, int n, bool out, float (&g)[8], float (&u)[8]) {
     const GatedBackArgs& a = c.a;
     float dy[8], gv[8], uv[8];
     load8_f32(a.dY, DT, t * a.ld_dy + k, n, n == 8, dy);
@@ -579,7 +580,7 @@ __device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_
         g[i] = i < n ? dy[i] * uv[i] * slope : 0.0f;      // zeros past d_ff, whatever act(0) is
         u[i] = i < n ? dy[i] * value : 0.0f;
     }
-    if (a.dG && n > 0) {
+    if (out && a.dG && n > 0) {
         store8(a.dG, DT, t * a.ld_dgu + k, n, n == 8, g);
         store8(a.dU, DT, t * a.ld_dgu + k, n, n == 8, u);
     }
@@ -592,7 +593,7 @@ __global__ __launch_bounds__(256) void mx_gates_kernel(Gates c) {
     for (int64_t t = blockIdx.y; t < c.a.n_tok; t += gridDim.y) {
         const int n = (int)max((int64_t)0, min((int64_t)8, c.a.d_ff - k));
         float g[8], u[8];
-        gate_gradients<DT, ACT>(c, t, k, n, g, u);
+        gate_gradients<DT, ACT>(c, t, k, n, true, g, u);
         uint16_t* to = c.D + t * c.ld + k;
         if constexpr (DT == GPTQ_F32) {
             u32x4_t p[3];
@@ -622,13 +623,13 @@ __global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int64_t k = 8 * threadIdx.x + p * step;
-            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), g[p], u[p]);
+            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[p], u[p]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[p][i]), u[p][i]);
         }
     } else {
         for (int64_t k = 8 * threadIdx.x; k < c.a.d_ff; k += step) {
-            gate_gradients<GPTQ_F16, ACT>(c, t, k, left(k), g[0], u[0]);
+            gate_gradients<GPTQ_F16, ACT>(c, t, k, left(k), false, g[0], u[0]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[0][i]), u[0][i]);
         }
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
         }
     } else {
         for (int64_t k = 8 * threadIdx.x; k < c.pad; k += step) {
-            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), g[0], u[0]);
+            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[0], u[0]);
             put(k, g[0], u[0]);
         }
     }
