@@ -130,7 +130,7 @@ struct BackArgs {
     int64_t n_tok, rows, d_in;           // rows: of each matrix
     const uint8_t *codes[2], *scales[2];
     int matrices;
-    const int32_t* exps;                 // null, or a power of two for each token, by which its sums are multiplied
+    const int32_t* exps;                 // null, or for each token the exponent of the power of two that its gradients lack
     void* dX;
     gptq_dtype dx_dt;
     int64_t ld_dx;

@@ -378,9 +378,13 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
     }
     wait_vmem<0>();              // nothing lands in LDS that is another's by then
 
+    const int32_t* exps = a.exps;
     if constexpr (HALF) {
-        // again with the gradients in two bfloat16 parts, from memory directly
+        // The whole tile again with the gradients in two bfloat16 parts, from memory
+        // directly, and as large as they are: with a token's power of two the
+        // products of large weights would pass float32's range.
         if (__syncthreads_or(left != 0)) {
+            exps = nullptr;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -416,6 +420,11 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = H16<false>::to_f32((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
+                    if (a.exps) {
+                        const int e2 = a.exps[t];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = ldexpf(f[e], e2);
+                    }
                     u32x4_t p[2];
                     cut(f, p);
 #pragma unroll
@@ -455,14 +464,11 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
             const f32x4_t hi = *(const f32x4_t*)(own + i * 512 + 16 * ((2 * (lane & 15) + 1) ^ (i & 15)));
             float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             if (t >= a.n_tok || m == 0) continue;
-            if (c.parts > 1) {
-                store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * c.pitch + col, 8, true, v);
-            } else {
-                const int e2 = a.exps ? a.exps[t] : 0;
+            const int e2 = exps ? exps[t] : 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
-                store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, m == 8, v);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
+            if (c.parts > 1) store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * c.pitch + col, 8, true, v);
+            else store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, m == 8, v);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -509,9 +515,6 @@ __global__ __launch_bounds__(256) void mx_back_join_kernel(Call c) {
         if (share != 0 || q >= all) continue;
         const int64_t t = q / row, n = 4 * (q - t * row);
         if (n >= a.d_in) continue;
-        const int e2 = a.exps ? a.exps[t] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], e2);
         put4(a.dX, a.dx_dt, t * a.ld_dx + n, (int)min((int64_t)4, a.d_in - n), v);
     }
 }
