@@ -508,11 +508,12 @@ gptq_status gptq_mx_backward_plan(gptq_dtype dy_dtype, int32_t matrices, int64_t
  *   dG = dY * U * act'(G),   dU = dY * act(G),   dX = dG gate + dU up
  *
  * dG and dU are computed in float32.  For the matrix cores they are rounded
- * once: of bfloat16 to bfloat16; of float16 to float16 after each token's are
- * scaled by a power of two of its own that brings the largest of them to 2^14 ..
- * 2^15 (11 bits, down to 2^-29 of that); of float32 not at all.  With float16,
- * weights whose scales it does not hold (outside 2^-23 .. 2^13) are multiplied as
- * bfloat16, by the same values in two parts.  Sums are float32.
+ * once, to at least three bits more than G's type has: of bfloat16 to 11 bits, of
+ * float16 to 22, each down to 2^-39 of the token's largest; of float32 not at all.
+ * A token's own power of two brings them into float16's range for that; weights
+ * whose scales float16 does not hold (outside 2^-23 .. 2^13) are multiplied as
+ * bfloat16, by the same values in two parts (each below 2^-110 off by less than
+ * 2^-133).  Sums are float32.
  * dG_out, dU_out: both NULL, or n_tok x d_ff of G's dtype with row stride ld_dgu
  * that get dG and dU (for adapters beside the weights); they may be G and U, with
  * their stride.  dX: as above.  Otherwise outputs and workspace overlap nothing.

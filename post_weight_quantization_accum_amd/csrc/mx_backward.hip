@@ -10,6 +10,11 @@
 namespace gptq {
 namespace {
 
+// 16-bit planes that a call's gradients are given to the matrix cores in: dY is
+// taken as it is, dG and dU as below.
+constexpr int planes_of(gptq_dtype dt) { return dt == GPTQ_F32 ? 3 : 1; }
+constexpr int gate_planes(gptq_dtype dt) { return dt == GPTQ_F32 ? 3 : dt == GPTQ_F16 ? 2 : 1; }
+
 // float32 as three bfloat16 parts that sum to it (two: of values that two hold,
 // as float16 ones); below an infinity or NaN the others are 0.
 template <int NP>
@@ -35,12 +40,13 @@ __device__ __forceinline__ void cut(const float (&v)[8], u32x4_t (&p)[NP]) {
 }
 
 // One call, as the kernels see it.  The sum runs over segments: a matrix's rows
-// with one plane of the gradients (three planes where they are float32), each
+// with one plane of the gradients (one to three, planes_of and gate_planes), each
 // in stages of 64 rows; rows past a segment's end are zeros in both operands.
 struct Call {
     BackArgs b;
     const uint16_t* D;         // planes of 16-bit values: [token][segment][pad]
     int64_t ld, pad;           // of D: token to token, segment to segment (elements, 16-byte multiples)
+    bool half;                 // the planes hold float16, not bfloat16
     int planes;                // segments of one matrix
     int64_t w_row, s_row;      // bytes per row
     int stages, per;           // stages of one segment; stages of one part
@@ -555,16 +561,21 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 }
 
 // ---------------------------------------------------------------------------
-// dG and dU as planes: bfloat16 ones rounded to it; float32 ones in three parts;
-// float16 ones scaled by a power of two for each token, for which a workgroup
-// holds the token's values until it has seen the largest finite one.  Bound by
-// memory: 2048 x 11008 bf16 35 us (6.4 TB/s, part of it in the caches).
+// dG and dU as planes.  They are products that have more bits than their factors'
+// type, and the result is not to show that they were rounded: it should be off by
+// its own rounding alone.  So float32 ones are kept whole, in three bfloat16
+// parts; bfloat16's in a float16 value (11 bits: 0.00171 of the result's norm, as
+// of float32 ones, where bfloat16 has 0.0023), float16's in two (22 bits: 0.00021
+// against 0.00029 with one).  Float16 values lack range, so each token's are
+// scaled by a power of two that brings the largest finite one to 2^14 .. 2^15, for
+// which a workgroup holds the token's values until it has seen them all.  Bound
+// by memory.
 // ---------------------------------------------------------------------------
 struct Gates {
     GatedBackArgs a;
     uint16_t* D;               // [token][2][plane][pad], token to token ld elements
     int64_t pad, ld;
-    int32_t* exps;             // of float16
+    int32_t* exps;             // of 16-bit types
 };
 
 // Eight values of both gradients from column k of a token on, of which n exist; to
@@ -589,34 +600,30 @@ __device__ __forceinline__ void gate_gradients(const Gates& c, int64_t t, int64_
     }
 }
 
-template <gptq_dtype DT, gptq_activation ACT>
-__global__ __launch_bounds__(256) void mx_gates_kernel(Gates c) {
+template <gptq_activation ACT>
+__global__ __launch_bounds__(256) void mx_gates_f32_kernel(Gates c) {
     const int64_t k = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (k >= c.pad) return;
     for (int64_t t = blockIdx.y; t < c.a.n_tok; t += gridDim.y) {
         const int n = (int)max((int64_t)0, min((int64_t)8, c.a.d_ff - k));
         float g[8], u[8];
-        gate_gradients<DT, ACT>(c, t, k, n, true, g, u);
+        gate_gradients<GPTQ_F32, ACT>(c, t, k, n, true, g, u);
         uint16_t* to = c.D + t * c.ld + k;
-        if constexpr (DT == GPTQ_F32) {
-            u32x4_t p[3];
-            cut(g, p);
+        u32x4_t p[3];
+        cut(g, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + j * c.pad) = p[j];
-            cut(u, p);
+        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + j * c.pad) = p[j];
+        cut(u, p);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + (3 + j) * c.pad) = p[j];
-        } else {
-            store8(to, GPTQ_BF16, 0, 8, true, g);
-            store8(to, GPTQ_BF16, c.pad, 8, true, u);
-        }
+        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + (3 + j) * c.pad) = p[j];
     }
 }
 
 // A token by a workgroup, eight values P times a thread; P = 0: more than 2 x 1024
 // x 8, taken twice.
-template <gptq_activation ACT, int P>
-__global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
+template <gptq_dtype DT, gptq_activation ACT, int P>
+__global__ __launch_bounds__(1024) void mx_gates_kernel(Gates c) {
+    constexpr int PLANES = gate_planes(DT);
     __shared__ float top[16];
     const int64_t t = blockIdx.x, step = 8 * (int64_t)blockDim.x;
     const auto finite_max = [](float m, float v) { return __builtin_isfinite(v) ? fmaxf(m, fabsf(v)) : m; };
@@ -626,13 +633,13 @@ __global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int64_t k = 8 * threadIdx.x + p * step;
-            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[p], u[p]);
+            gate_gradients<DT, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[p], u[p]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[p][i]), u[p][i]);
         }
     } else {
         for (int64_t k = 8 * threadIdx.x; k < c.a.d_ff; k += step) {
-            gate_gradients<GPTQ_F16, ACT>(c, t, k, left(k), false, g[0], u[0]);
+            gate_gradients<DT, ACT>(c, t, k, left(k), false, g[0], u[0]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = finite_max(finite_max(m, g[0][i]), u[0][i]);
         }
@@ -648,41 +655,49 @@ __global__ __launch_bounds__(1024) void mx_gates_f16_kernel(Gates c) {
         e2 = 15 - e2;
     }
     if (threadIdx.x == 0) c.exps[t] = -e2;
-    const auto put = [&](int64_t k, float (&g)[8], float (&u)[8]) {
+    const auto put = [&](int64_t at, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            g[i] = ldexpf(g[i], e2);
-            u[i] = ldexpf(u[i], e2);
+        for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e2);
+#pragma unroll
+        for (int j = 0; j < PLANES; ++j) {
+            store8(c.D, GPTQ_F16, t * c.ld + at + j * c.pad, 8, true, x);
+            if (j + 1 < PLANES) {                // what the value lacks; nothing beside an infinity or NaN
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __builtin_isfinite(x[i]) ? x[i] - (float)(_Float16)x[i] : 0.0f;
+            }
         }
-        store8(c.D, GPTQ_F16, t * c.ld + k, 8, true, g);
-        store8(c.D, GPTQ_F16, t * c.ld + c.pad + k, 8, true, u);
     };
     if constexpr (P > 0) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int64_t k = 8 * threadIdx.x + p * step;
-            if (k < c.pad) put(k, g[p], u[p]);
+            if (k >= c.pad) continue;
+            put(k, g[p]);
+            put(k + PLANES * c.pad, u[p]);
         }
     } else {
         for (int64_t k = 8 * threadIdx.x; k < c.pad; k += step) {
-            gate_gradients<GPTQ_F16, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[0], u[0]);
-            put(k, g[0], u[0]);
+            gate_gradients<DT, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[0], u[0]);
+            put(k, g[0]);
+            put(k + PLANES * c.pad, u[0]);
         }
     }
 }
 
+template <gptq_dtype DT, gptq_activation ACT>
+void launch_gates_of(const Gates& c, hipStream_t s) {
+    const int64_t pieces = c.pad / 8;
+    const unsigned n = (unsigned)c.a.n_tok;
+    if (pieces <= 1024) mx_gates_kernel<DT, ACT, 1><<<n, (unsigned)(ceil_div(pieces, 64) * 64), 0, s>>>(c);
+    else if (pieces <= 2048) mx_gates_kernel<DT, ACT, 2><<<n, (unsigned)(ceil_div(pieces, 128) * 64), 0, s>>>(c);
+    else mx_gates_kernel<DT, ACT, 0><<<n, 1024, 0, s>>>(c);
+}
 template <gptq_activation ACT>
 void launch_gates(const Gates& c, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(c.pad, 2048), (unsigned)std::min<int64_t>(c.a.n_tok, 65535));
-    if (c.a.dt == GPTQ_BF16) mx_gates_kernel<GPTQ_BF16, ACT><<<grid, 256, 0, s>>>(c);
-    if (c.a.dt == GPTQ_F32) mx_gates_kernel<GPTQ_F32, ACT><<<grid, 256, 0, s>>>(c);
-    if (c.a.dt == GPTQ_F16) {
-        const int64_t pieces = c.pad / 8;
-        const unsigned n = (unsigned)c.a.n_tok;
-        if (pieces <= 1024) mx_gates_f16_kernel<ACT, 1><<<n, (unsigned)(ceil_div(pieces, 64) * 64), 0, s>>>(c);
-        else if (pieces <= 2048) mx_gates_f16_kernel<ACT, 2><<<n, (unsigned)(ceil_div(pieces, 128) * 64), 0, s>>>(c);
-        else mx_gates_f16_kernel<ACT, 0><<<n, 1024, 0, s>>>(c);
-    }
+    if (c.a.dt == GPTQ_F32) mx_gates_f32_kernel<ACT><<<grid, 256, 0, s>>>(c);
+    else if (c.a.dt == GPTQ_F16) launch_gates_of<GPTQ_F16, ACT>(c, s);
+    else launch_gates_of<GPTQ_BF16, ACT>(c, s);
 }
 
 // How a call is computed: the tile's tokens (64 TF), and the parts of the sum's
@@ -699,7 +714,8 @@ constexpr double TILE_US[4] = {6, 9, 12, 15};
 struct Plan {
     int tf, stages, per, parts;
 };
-Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
+Plan plan_of(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows) {
+    const int segments = matrices * planes;
     Plan best{1, (int)ceil_div(rows, SK), 1, 0};
     const int64_t all = (int64_t)best.stages * segments;
     if (all == 0) return best;
@@ -707,8 +723,9 @@ Plan plan_of(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
     for (int tf = 1; tf <= 4; ++tf) {
         const int64_t tiles = ceil_div(d_in, BN) * ceil_div(n_tok, 64 * tf);
         const double* us = STAGE_US[tf - 1];
-        // more parts than make two rounds of the chip cost a join and save nothing
-        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, all));
+        // more parts than make two rounds of the chip cost a join and save nothing,
+        // nor do float16's of one stage, half of what its rows have
+        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, planes == 2 ? all / 2 : all));
         for (int64_t want = 1, per; want <= most; want = per > 1 ? ceil_div(all, per - 1) : most + 1) {
             per = ceil_div(all, want);
             const int64_t parts = ceil_div(all, per);
@@ -735,8 +752,8 @@ int64_t pitch_of(int64_t d_in) { return ceil_div(d_in, 8) * 8; }
 size_t planes_bytes(int64_t n_tok, int64_t rows, int segments) {
     return align_up((size_t)n_tok * row_of(rows, segments) * 2, 256);
 }
-size_t sums_bytes(int segments, int64_t n_tok, int64_t d_in, int64_t rows) {
-    const Plan p = plan_of(segments, n_tok, d_in, rows);
+size_t sums_bytes(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows) {
+    const Plan p = plan_of(matrices, planes, n_tok, d_in, rows);
     return p.parts > 1 ? (size_t)p.parts * n_tok * pitch_of(d_in) * sizeof(float) : 0;
 }
 
@@ -750,10 +767,9 @@ gptq_status launch_tile(const Call& c, hipStream_t s) {
     return GPTQ_OK;
 }
 
-gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
+gptq_status launch_sum(Call& c, hipStream_t s) {
     const BackArgs& a = c.b;
-    const Plan p = plan_of(segments, a.n_tok, a.d_in, a.rows);
-    c.planes = segments / a.matrices;
+    const Plan p = plan_of(a.matrices, c.planes, a.n_tok, a.d_in, a.rows);
     c.w_row = mx_code_bytes(a.d_in, GPTQ_MX_FP4);
     c.s_row = mx_scale_bytes(a.d_in);
     c.stages = p.stages;
@@ -761,7 +777,7 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
     c.parts = p.parts;
     c.pitch = pitch_of(a.d_in);
     if (c.parts > 0) {
-        const bool half = a.dt == GPTQ_F16;
+        const bool half = c.half;
         gptq_status st;
         if (p.tf == 1) st = half ? launch_tile<true, 1, 2>(c, s) : launch_tile<false, 1, 2>(c, s);
         else if (p.tf == 2) st = half ? launch_tile<true, 2, 2>(c, s) : launch_tile<false, 2, 2>(c, s);
@@ -782,20 +798,21 @@ gptq_status launch_sum(Call& c, int segments, hipStream_t s) {
 }  // namespace
 
 void mx_backward_plan(gptq_dtype dt, int matrices, int64_t n_tok, int64_t d_in, int64_t rows, int64_t* plan) {
-    const Plan p = plan_of(matrices * (dt == GPTQ_F32 ? 3 : 1), n_tok, d_in, rows);
+    const Plan p = plan_of(matrices, matrices == 2 ? gate_planes(dt) : planes_of(dt), n_tok, d_in, rows);
     plan[0] = 64 * p.tf;
     plan[1] = p.parts;
 }
 
 size_t mx_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t rows) {
-    const int planes = dt == GPTQ_F32 ? 3 : 1;
-    return planes_bytes(n_tok, rows, planes) + sums_bytes(planes, n_tok, d_in, rows);
+    const int planes = planes_of(dt);
+    return planes_bytes(n_tok, rows, planes) + sums_bytes(1, planes, n_tok, d_in, rows);
 }
 
 gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, void* ws, hipStream_t s) {
     Call c{};
     c.b = a;
-    const int planes = a.dt == GPTQ_F32 ? 3 : 1, size = a.dt == GPTQ_F32 ? 4 : 2;
+    const int planes = c.planes = planes_of(a.dt), size = a.dt == GPTQ_F32 ? 4 : 2;
+    c.half = a.dt == GPTQ_F16;
     c.pad = padded(a.rows);
     c.sums = (float*)((char*)ws + planes_bytes(a.n_tok, a.rows, planes));
     const bool on16 = ((uintptr_t)D | (uintptr_t)(ld * size)) % 16 == 0;
@@ -811,18 +828,19 @@ gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, voi
             GPTQ_LAUNCH_CHECK();
         }
     }
-    return launch_sum(c, planes, s);
+    return launch_sum(c, s);
 }
 
 size_t mx_gated_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t d_ff) {
-    const int segments = dt == GPTQ_F32 ? 6 : 2;
-    return planes_bytes(n_tok, d_ff, segments) + align_up(4 * (size_t)n_tok, 256) + sums_bytes(segments, n_tok, d_in, d_ff);
+    const int planes = gate_planes(dt);
+    return planes_bytes(n_tok, d_ff, 2 * planes) + align_up(4 * (size_t)n_tok, 256) + sums_bytes(2, planes, n_tok, d_in, d_ff);
 }
 
 gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream_t s) {
-    const bool wide = a.dt == GPTQ_F32;
-    const int segments = wide ? 6 : 2;
     Call c{};
+    c.planes = gate_planes(a.dt);
+    c.half = a.dt != GPTQ_F32;
+    const int segments = 2 * c.planes;
     BackArgs& b = c.b;
     b.dt = a.dt;
     b.n_tok = a.n_tok;
@@ -847,7 +865,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         g.D = (uint16_t*)ws;
         g.pad = c.pad;
         g.ld = c.ld;
-        g.exps = a.dt == GPTQ_F16 ? (int32_t*)exps : nullptr;
+        g.exps = c.half ? (int32_t*)exps : nullptr;
         switch (a.act) {
             case GPTQ_ACT_SILU: launch_gates<GPTQ_ACT_SILU>(g, s); break;
             case GPTQ_ACT_GELU: launch_gates<GPTQ_ACT_GELU>(g, s); break;
@@ -857,7 +875,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         GPTQ_LAUNCH_CHECK();
         b.exps = g.exps;
     }
-    return launch_sum(c, segments, s);
+    return launch_sum(c, s);
 }
 
 }  // namespace gptq
