@@ -56,12 +56,12 @@ struct Call {
 };
 
 // ---------------------------------------------------------------------------
-// 256 columns x 32 TF TW tokens per workgroup of 2 x TW waves, each 128 columns
-// x 32 TF tokens in v_mfma_f32_32x32x16, in stages of 64 rows of the matrix.
+// 256 columns x 64 TF tokens per workgroup of 2 x 2 waves, each 128 columns x 32
+// TF tokens in v_mfma_f32_32x32x16, in stages of 64 rows of the matrix.
 //
 // The weights' rows are the sum's index here, and a lane of the instruction
 // wants eight rows of one column, while memory holds a column's rows apart.  So
-// a thread takes eight rows of four or eight columns, converts the two columns of
+// a thread takes eight rows of eight columns, converts the two columns of
 // a byte with their row's scale in one instruction, puts two rows' halves together
 // with a byte permute, and stores eight rows of each column in a row: one
 // instruction a value, once a workgroup.
@@ -86,9 +86,9 @@ struct Call {
 constexpr int BN = 256, SK = 64;
 constexpr int RAW = SK * BN / 2, RAW_S = SK * BN / 32;     // bytes of a stage's codes and scales
 constexpr int WT = SK * BN * 2;                            // and of its weights
-template <int TF, int TW>
+template <int TF>
 struct BackTile {
-    static constexpr int BT = 32 * TF * TW, X = BT * SK * 2, WAVES = 2 * TW;
+    static constexpr int BT = 64 * TF, X = BT * SK * 2, WAVES = 4;
     static constexpr int R = BT > 128 ? 2 : BT > 64 ? 3 : 4;                             // slots of a ring
     static constexpr int W = R * X, RAWS = W + 2 * WT, RAW_SCALES = RAWS + R * RAW, BYTES = RAW_SCALES + R * RAW_S;
     // per wave and stage; the scales are two instructions, which some waves repeat
@@ -98,9 +98,7 @@ struct BackTile {
     // of s + 2 and the gradients of s + 1 have landed if only what R - 2 stages
     // asked for since is under way.
     static constexpr int WAIT = (R - 2) * DMA;
-    static constexpr int PAIRS = 16 / WAVES;               // of columns that a thread converts: 4, or 2 of 8 waves
     static_assert(BYTES <= 160 * 1024 - 1024 && WAIT < 64, "LDS and counters");
-    static_assert(WAVES == 4 || WAVES == 8, "threads of the conversion");
 };
 
 // As dma_16 of mx.hpp, with the address in LDS and that in memory each the sum of
@@ -136,9 +134,9 @@ __device__ __forceinline__ __attribute__((address_space(3))) V& lds_at(uint32_t 
     return *(__attribute__((address_space(3))) V*)(uintptr_t)(at + plus);
 }
 
-template <bool HALF, int TF, int TW>
-__global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
-    using T = BackTile<TF, TW>;
+template <bool HALF, int TF>
+__global__ __launch_bounds__(256, 1) void mx_back_kernel(Call c) {
+    using T = BackTile<TF>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const BackArgs& a = c.b;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -152,7 +150,7 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
     const int part = (int)(id / (nt * nn));
     const uint32_t tile = id % (nt * nn), rows4 = tile / (4 * nn) * 4, in4 = tile % (4 * nn), of4 = min(4u, nt - rows4);
     const int64_t n0 = (int64_t)(in4 / of4) * BN, t0 = (int64_t)(rows4 + in4 % of4) * T::BT;
-    const int nw = 128 * (wave / TW), tw = 32 * TF * (wave % TW);
+    const int nw = 128 * (wave / 2), tw = 32 * TF * (wave % 2);
     const int first = part * c.per, end = min(first + c.per, c.stages * a.matrices * c.planes), S = end - first;
 
     // this thread's pieces
@@ -227,18 +225,16 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     uint32_t left = 0;       // not 0: codes whose scale float16 lacks
 
-    // conversion: thread (q, o) has rows 8 q .. + 7 of the o-th group of 2 PAIRS
-    // columns, whose codes a word or half of one holds
-    constexpr int PC = T::PAIRS, GROUPS = BN / 2 / PC;
-    const int q8 = threadIdx.x / GROUPS, o8 = threadIdx.x % GROUPS;
+    // conversion: thread (q, o) has rows 8 q .. + 7 of the o-th group of eight columns,
+    // whose codes a word holds
+    const int q8 = threadIdx.x / 32, o8 = threadIdx.x % 32;
     struct Raw {
         uint32_t w[8], s[8];
     };
-    uint32_t code_at = held(base + T::RAWS + 8 * q8 * (BN / 2) + PC * o8);
-    uint32_t scale_at = held(base + T::RAW_SCALES + 8 * q8 * (BN / 32) + o8 / (16 / PC));
+    uint32_t code_at = held(base + T::RAWS + 8 * q8 * (BN / 2) + 4 * o8);
+    uint32_t scale_at = held(base + T::RAW_SCALES + 8 * q8 * (BN / 32) + o8 / 4);
     const auto raw_read = [&](Raw& r, int k) {
-        if constexpr (PC == 4) r.w[k] = lds_at<uint32_t>(code_at, k * (BN / 2));
-        else r.w[k] = lds_at<uint16_t>(code_at, k * (BN / 2));
+        r.w[k] = lds_at<uint32_t>(code_at, k * (BN / 2));
         r.s[k] = lds_at<uint8_t>(scale_at, k * (BN / 32));
     };
     // codes that are not all zero with a scale byte outside 104 .. 140 (byte 255
@@ -254,8 +250,8 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
         v[0][k] = __builtin_amdgcn_perm(b, a, 0x05040100u);
         v[1][k] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     };
-    // column c of the group: column 2 PC o + c of the tile, at place (c % 4) 64 + PC o / 2 + c / 4
-    uint32_t to = held(base + T::W + PC / 2 * o8 * (SK * 2) + 16 * ((q8 ^ PC * o8 / 4) & 7));
+    // column c of the group: column 8 o + c of the tile, at place (c % 4) 64 + 2 o + c / 4
+    uint32_t to = held(base + T::W + 2 * o8 * (SK * 2) + 16 * ((q8 ^ o8) & 7));
     const auto write = [&](int c, u32x4_t v) { lds_at<u32x4_t>(to, ((c & 3) * 64 + (c >> 2)) * (SK * 2)) = v; };
 
     // a step's operands
@@ -294,7 +290,7 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
         raw_read(r, k);
         sc[k] = mx_scale(r.s[k]);
     });
-    for_each<PC>([&](auto p) {
+    for_each<4>([&](auto p) {
         for_each<4>([&](auto k) { convert(r, sc, p, k, v[0]); });
         write(2 * p, v[0][0]);
         write(2 * p + 1, v[0][1]);
@@ -357,10 +353,10 @@ __global__ __launch_bounds__(128 * TW, TW / 2) void mx_back_kernel(Call c) {
                     if constexpr (n == 3) for_each<8>([&](auto e8) { sc[e8] = mx_scale(r.s[e8]); });
                     if constexpr (HALF && n >= 8) look(r, n - 8);
                 }
-                // the conversion's units: eight to a step of four pairs, four of two
+                // the conversion's units, of four pairs of columns four each: eight to a step
                 constexpr int at_unit = ks == 1 ? n - 4 : n;
-                if constexpr ((ks == 1 || ks == 2) && at_unit >= 0 && at_unit < 12 && at_unit % 3 < PC / 2) {
-                    constexpr int unit = (ks - 1) * 2 * PC + at_unit / 3 * (PC / 2) + at_unit % 3, pair = unit / 4;
+                if constexpr ((ks == 1 || ks == 2) && at_unit >= 0 && at_unit < 12 && at_unit % 3 < 2) {
+                    constexpr int unit = (ks - 1) * 8 + at_unit / 3 * 2 + at_unit % 3, pair = unit / 4;
                     convert(r, sc, std::integral_constant<int, pair>{}, unit % 4, v[pair & 1]);
                     if constexpr (unit % 4 == 3) {
                         write(2 * pair, v[pair & 1][0]);
@@ -757,12 +753,12 @@ size_t sums_bytes(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t
     return p.parts > 1 ? (size_t)p.parts * n_tok * pitch_of(d_in) * sizeof(float) : 0;
 }
 
-template <bool HALF, int TF, int TW>
+template <bool HALF, int TF>
 gptq_status launch_tile(const Call& c, hipStream_t s) {
-    using T = BackTile<TF, TW>;
-    GPTQ_HIP(ensure_lds_limit((const void*)mx_back_kernel<HALF, TF, TW>, T::BYTES));
+    using T = BackTile<TF>;
+    GPTQ_HIP(ensure_lds_limit((const void*)mx_back_kernel<HALF, TF>, T::BYTES));
     const int64_t tiles = ceil_div(c.b.d_in, BN) * ceil_div(c.b.n_tok, T::BT) * c.parts;
-    mx_back_kernel<HALF, TF, TW><<<(unsigned)tiles, 128 * TW, T::BYTES, s>>>(c);
+    mx_back_kernel<HALF, TF><<<(unsigned)tiles, 256, T::BYTES, s>>>(c);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -779,10 +775,10 @@ gptq_status launch_sum(Call& c, hipStream_t s) {
     if (c.parts > 0) {
         const bool half = c.half;
         gptq_status st;
-        if (p.tf == 1) st = half ? launch_tile<true, 1, 2>(c, s) : launch_tile<false, 1, 2>(c, s);
-        else if (p.tf == 2) st = half ? launch_tile<true, 2, 2>(c, s) : launch_tile<false, 2, 2>(c, s);
-        else if (p.tf == 3) st = half ? launch_tile<true, 3, 2>(c, s) : launch_tile<false, 3, 2>(c, s);
-        else st = half ? launch_tile<true, 4, 2>(c, s) : launch_tile<false, 4, 2>(c, s);
+        if (p.tf == 1) st = half ? launch_tile<true, 1>(c, s) : launch_tile<false, 1>(c, s);
+        else if (p.tf == 2) st = half ? launch_tile<true, 2>(c, s) : launch_tile<false, 2>(c, s);
+        else if (p.tf == 3) st = half ? launch_tile<true, 3>(c, s) : launch_tile<false, 3>(c, s);
+        else st = half ? launch_tile<true, 4>(c, s) : launch_tile<false, 4>(c, s);
         if (st != GPTQ_OK) return st;
     }
     if (c.parts != 1) {
