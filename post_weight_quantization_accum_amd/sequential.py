@@ -116,6 +116,8 @@ def _norms(block: Block, X, norms: Norms | None):
     for name, v in given.items():
         if tuple(v.shape) != (X.shape[1],) or v.dtype != block.norm1.dtype or (X.shape[1] > 1 and v.stride(0) != 1):
             raise ValueError(f"{name} must have as many values as a token, all norms of one dtype")
+        if v.device != X.device:
+            raise ValueError(f"{name} must live where the tokens do")
     norms = norms or Norms()
     if norms.kind not in KINDS:
         raise ValueError(f"norms.kind must be one of {', '.join(KINDS)}")
@@ -281,8 +283,14 @@ def quantize_stack(blocks, X0, cfg, stats: dict | None = None, want_w_hat: bool 
                    attention: Attention | None = None, norms: Norms | None = None):
     """Quantize the blocks in order; block b+1 is calibrated on the output of
     the already-quantized block b.  Returns a list of (outputs, inputs) per
-    block and the stack's output activations."""
+    block and the stack's output activations.  Of blocks in a list or tuple what
+    a later one lacks is refused before the first is quantized."""
     load()
+    if isinstance(blocks, (list, tuple)):
+        for b in blocks:
+            if attention is not None:
+                _attention_shape(b, X0, attention)
+            _norms(b, X0, norms)
     out = []
     X = X0
     for b in blocks:
