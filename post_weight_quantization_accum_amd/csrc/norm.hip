@@ -3,7 +3,8 @@
 //
 // A row is read once into registers, by one wave where it is short and by a
 // workgroup otherwise, and everything about it is computed from there: no
-// value is read twice but by rows of more than 16384 values, of gradients 8192 (wide kernels).
+// value is read twice but by rows of more than 16384 values, with float32 ones and of
+// gradients 8192 (wide kernels).
 // Sums over a row are float64: the squares of float32 values leave float32's
 // range, and mean and variance come from one pass (sum and sum of squares)
 // without the loss that float32 would have there.  They cost a few percent of
@@ -695,6 +696,10 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* parts, int
 // Threads of a workgroup for rows of d values, eight or sixteen or 32 a lane.
 unsigned threads_for(int64_t d, int pieces) { return (unsigned)(ceil_div(ceil_div(d, 8 * pieces), 64) * 64); }
 
+// Rows of 8193 to 16384 values in registers, 32 a lane, where all are of 16 bits
+// (4096 rows with two norms, of 8200 97 us against 105 in passes, of 11008 112 and 135,
+// of 16384 137 and 150); float32 ones leave the registers (4096 x 8200 float32 stream
+// 145 against 106 in passes, x 16384 219 and 179).
 template <Width D, bool LAYER, bool NARROW>
 void launch_norm(const NormArgs& a, hipStream_t s) {
     // as many workgroups as the chip holds at once (six waves a SIMD, by their registers)
@@ -704,8 +709,8 @@ void launch_norm(const NormArgs& a, hipStream_t s) {
     else if constexpr (D == TINY) return;
     else if (a.d <= 1024) norm_kernel<2, D, true, LAYER, NARROW><<<four, 256, 0, s>>>(a);
     else if (a.d <= 8192) norm_kernel<1, D, false, LAYER, NARROW><<<groups(a.n_tok, t1), t1, 0, s>>>(a);
-    else if (a.d <= 16384) norm_kernel<4, D, false, LAYER, NARROW><<<groups(a.n_tok, t4), t4, 0, s>>>(a);
-    else norm_wide_kernel<D, LAYER><<<(unsigned)a.n_tok, 1024, 0, s>>>(a);
+    else if (!NARROW || a.d > 16384) norm_wide_kernel<D, LAYER><<<(unsigned)a.n_tok, 1024, 0, s>>>(a);
+    else if constexpr (NARROW) norm_kernel<4, D, false, LAYER, true><<<groups(a.n_tok, t4), t4, 0, s>>>(a);
 }
 
 // Parts of the sums over tokens, and with them workgroups of the gradient.
@@ -716,7 +721,10 @@ int64_t grad_parts(int64_t n_tok, int64_t d) {
 
 // Sixteen values a lane where registers hold them (16-bit rows: two workgroups of
 // four waves a compute unit do better than one of eight, 8192 x 4096 115 us against
-// 127; with float32 rows they spill, 237 against 167).
+// 127).  With float32 rows they do not, and some go to memory: eight a lane are better
+// as long as a workgroup has them (8192 x 4096 167 us, sixteen 237), and past that
+// sixteen are still better than passes (4096 x 5120 float32 stream 198 against 251,
+// x 8192 233 and 338).
 template <Width D, bool LAYER, bool NARROW>
 void launch_grad(const NormGradArgs& a, hipStream_t s) {
     const int64_t d = a.f.d;
