@@ -134,311 +134,305 @@ __device__ __forceinline__ __attribute__((address_space(3))) V& lds_at(uint32_t 
     return *(__attribute__((address_space(3))) V*)(uintptr_t)(at + plus);
 }
 
-template <bool HALF, int TF>
-__global__ __launch_bounds__(256, 1) void mx_back_kernel(Call c) {
-    using T = BackTile<TF>;
-    extern __shared__ __attribute__((aligned(16))) char lds[];
-    const BackArgs& a = c.b;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int i32 = lane & 31, h = lane >> 5;
-    // Consecutive workgroups go to different dies: give each die a run of tiles,
-    // four of tokens by as many of columns (a stage's gradients are four times its
-    // codes: of 32 tiles 4 x 8 have the fewest bytes to share).
-    const uint32_t nt = (uint32_t)((a.n_tok + T::BT - 1) / T::BT), nn = (uint32_t)((a.d_in + BN - 1) / BN);
+// A workgroup's tile: columns n0 .. and tokens t0 .., and its stages of the sum.
+// Consecutive workgroups go to different dies: give each die a run of tiles,
+// four of tokens by as many of columns (a stage's gradients are four times its
+// codes: of 32 tiles 4 x 8 have the fewest bytes to share).
+struct Place {
+    int64_t n0, t0;
+    int part, first, end;
+};
+template <int BT, class C>
+__device__ __forceinline__ Place place_of(const C& c) {
+    const uint32_t nt = (uint32_t)((c.b.n_tok + BT - 1) / BT), nn = (uint32_t)((c.b.d_in + BN - 1) / BN);
     const uint32_t n = gridDim.x, each = n / 8;
     const uint32_t id = blockIdx.x < each * 8 ? (blockIdx.x % 8) * each + blockIdx.x / 8 : blockIdx.x;
     const int part = (int)(id / (nt * nn));
     const uint32_t tile = id % (nt * nn), rows4 = tile / (4 * nn) * 4, in4 = tile % (4 * nn), of4 = min(4u, nt - rows4);
-    const int64_t n0 = (int64_t)(in4 / of4) * BN, t0 = (int64_t)(rows4 + in4 % of4) * T::BT;
-    const int nw = 128 * (wave / 2), tw = 32 * TF * (wave % 2);
-    const int first = part * c.per, end = min(first + c.per, c.stages * a.matrices * c.planes), S = end - first;
+    const int first = part * c.per;
+    return Place{(int64_t)(in4 / of4) * BN, (int64_t)(rows4 + in4 % of4) * BT, part, first,
+                 min(first + c.per, c.stages * c.b.matrices * c.planes)};
+}
 
-    // this thread's pieces
-    const int64_t tn = min((int64_t)T::BT, a.n_tok - t0);
-    uint32_t xoff[T::X_DMA], woff[T::W_DMA], soff;
-#pragma unroll
-    for (int j = 0; j < T::X_DMA; ++j) {                  // eight tokens an instruction
-        const int t = 8 * (wave + T::WAVES * j) + (lane >> 3), ch = (lane & 7) ^ (t >> 1 & 7);
-        xoff[j] = (uint32_t)(min((int64_t)t, tn - 1) * c.ld * 2 + 16 * ch);
-    }
-#pragma unroll
-    for (int j = 0; j < T::W_DMA; ++j) {                  // eight rows an instruction
-        const int k = 8 * (wave + T::WAVES * j) + (lane >> 3);
-        const int64_t at = n0 / 2 + 16 * (lane & 7);
-        woff[j] = at < c.w_row ? (uint32_t)(k * c.w_row + at) : 1u << 31;
-    }
-    {                                                     // 32 rows an instruction
-        const int k = 32 * (wave & 1) + (lane >> 1);
-        const int64_t at = n0 / 32 + 4 * (lane & 1);
-        soff = at < c.s_row ? (uint32_t)(k * c.s_row + at) : 1u << 31;
-    }
-    const uint32_t base = (uint32_t)(uintptr_t)lds;
-    // Stages come one after another in D's rows, over the segments.  Past the
-    // last one the fetches repeat it, into slots that nobody reads.
-    const u32x4_t xb = buffer_of(c.D + t0 * c.ld, ((tn - 1) * c.ld + (int64_t)c.stages * a.matrices * c.planes * SK) * 2);
-    int xcol = 2 * SK * first;
-    const int xlast = 2 * SK * (end - 1);
-    const auto fetch_x = [&](int slot, int from, int to) {
-#pragma unroll
-        for (int j = from; j < to; ++j) dma_16_at(base + slot * T::X + 1024 * wave, 1024 * T::WAVES * j, xoff[j], xcol, xb);
-        if (to == T::X_DMA) xcol = min(xcol + 2 * SK, xlast);
-    };
-    // codes and scales from here on, and of the matrices
-    const uint8_t *wp, *sp, *wp0 = a.codes[0], *sp0 = a.scales[0], *wp1 = a.codes[1], *sp1 = a.scales[1];
-    int64_t wrows;                                                    // left of the segment
-    int wseg = first / c.stages, wleft = S;
-    {
-        const int64_t k0 = (int64_t)(first - wseg * c.stages) * SK;
-        const int m = wseg >= c.planes;
-        wp = a.codes[m] + k0 * c.w_row;
-        sp = a.scales[m] + k0 * c.s_row;
-        wrows = a.rows - k0;
-    }
-    u32x4_t wb, sb;
-    const auto fetch_w = [&](int slot, int piece) {
-        if (piece == 0) {
-            const uint32_t rows = (uint32_t)min((int64_t)SK, wrows);
-            wb = buffer_at(wp, rows * (uint32_t)c.w_row);
-            sb = buffer_at(sp, rows * (uint32_t)c.s_row);
-        }
-        if (piece < T::W_DMA) {
-            dma_16_at(base + T::RAWS + slot * RAW + 1024 * wave, 1024 * T::WAVES * piece, woff[piece], 0, wb);
-            return;
-        }
-        dma_4(base + T::RAW_SCALES + slot * RAW_S + 256 * (wave & 1), soff, sb);
-        // on to the next rows, or the next segment's first (no branch: it would
-        // part the loop, and with it what is ordered among the products)
-        const bool more = --wleft > 0, turns = more && wrows <= SK;
-        wseg += turns;
-        const bool second = wseg >= c.planes;
-        wp = turns ? (second ? wp1 : wp0) : wp + (more ? SK * c.w_row : 0);
-        sp = turns ? (second ? sp1 : sp0) : sp + (more ? SK * c.s_row : 0);
-        wrows = turns ? a.rows : wrows - (more ? SK : 0);
-    };
-
+template <bool HALF, int TF>
+__global__ __launch_bounds__(256, 1) void mx_back_kernel(Call c) {
+    using T = BackTile<TF>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int i32 = lane & 31, h = lane >> 5, nw = 128 * (wave / 2), tw = 32 * TF * (wave % 2);
     f16_t acc[4][TF];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < TF; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     uint32_t left = 0;       // not 0: codes whose scale float16 lacks
+    // The tile's sums.  FAR: of float16 gradients beside such weights.
+    const auto sum = [&](auto far, const auto& c) __attribute__((always_inline)) {
+        constexpr bool FAR = decltype(far)::value, F16 = HALF && !FAR;
+        const auto& a = c.b;
+        const auto [n0, t0, part, first, end] = place_of<T::BT>(c);
+        const int S = end - first;
 
-    // conversion: thread (q, o) has rows 8 q .. + 7 of the o-th group of eight columns,
-    // whose codes a word holds
-    const int q8 = threadIdx.x / 32, o8 = threadIdx.x % 32;
-    struct Raw {
-        uint32_t w[8], s[8];
-    };
-    uint32_t code_at = held(base + T::RAWS + 8 * q8 * (BN / 2) + 4 * o8);
-    uint32_t scale_at = held(base + T::RAW_SCALES + 8 * q8 * (BN / 32) + o8 / 4);
-    const auto raw_read = [&](Raw& r, int k) {
-        r.w[k] = lds_at<uint32_t>(code_at, k * (BN / 2));
-        r.s[k] = lds_at<uint8_t>(scale_at, k * (BN / 32));
-    };
-    // codes that are not all zero with a scale byte outside 104 .. 140 (byte 255
-    // makes NaN of float16, too)
-    const auto look = [&](const Raw& r, int k) {
-        left |= min(__builtin_elementwise_sub_sat(r.s[k] - 104u, 36u), r.w[k]);
-    };
-    // two rows of a pair of columns
-    const auto convert = [](const Raw& r, const float (&sc)[8], auto pair, int k, u32x4_t (&v)[2]) {
-        constexpr int P = decltype(pair)::value;
-        const uint32_t a = H16<!HALF>::template fp4<P>(r.w[2 * k], sc[2 * k]);
-        const uint32_t b = H16<!HALF>::template fp4<P>(r.w[2 * k + 1], sc[2 * k + 1]);
-        v[0][k] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-        v[1][k] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-    };
-    // column c of the group: column 8 o + c of the tile, at place (c % 4) 64 + 2 o + c / 4
-    uint32_t to = held(base + T::W + 2 * o8 * (SK * 2) + 16 * ((q8 ^ o8) & 7));
-    const auto write = [&](int c, u32x4_t v) { lds_at<u32x4_t>(to, ((c & 3) * 64 + (c >> 2)) * (SK * 2)) = v; };
-
-    // a step's operands
-    struct Step {
-        u32x4_t w[4], x[TF];
-    };
-    // in the order of their use: x0, the weights (columns 4 i32 + i), the other x
-    uint32_t x_at[4], w_at[4];
+        // this thread's pieces
+        const int64_t tn = min((int64_t)T::BT, a.n_tok - t0);
+        uint32_t xoff[T::X_DMA], woff[T::W_DMA], soff;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-        const int chunk = 16 * ((2 * ks + h) ^ (i32 >> 1 & 7));
-        x_at[ks] = held(base + (tw + i32) * (SK * 2) + chunk);
-        w_at[ks] = held(base + T::W + (nw / 4 + i32) * (SK * 2) + chunk);
-    }
-    const auto read = [&](uint32_t x, uint32_t w, Step& r, int n) {
-        if (n == 0 || n > 4) {
-            const int j = n == 0 ? 0 : n - 4;
-            r.x[j] = lds_at<u32x4_t>(x, 32 * j * (SK * 2));
-        } else {
-            r.w[n - 1] = lds_at<u32x4_t>(w, 64 * (n - 1) * (SK * 2));
+        for (int j = 0; j < T::X_DMA; ++j) {                  // eight tokens an instruction
+            const int t = 8 * (wave + T::WAVES * j) + (lane >> 3), ch = (lane & 7) ^ (t >> 1 & 7);
+            xoff[j] = (uint32_t)(min((int64_t)t, tn - 1) * c.ld * 2 + 16 * ch);
         }
-    };
-
-    const auto ask_w = [&](int slot) {
 #pragma unroll
-        for (int e = 0; e <= T::W_DMA; ++e) fetch_w(slot, e);
-    };
-    for_each<T::R>([&](auto f) { ask_w(f); });
-    for_each<T::R - 1>([&](auto f) { fetch_x(f, 0, T::X_DMA); });
-    wait_vmem<0>();
-    meet();
-    Raw r;
-    float sc[8];
-    u32x4_t v[2][2];
-    for_each<8>([&](auto k) {
-        raw_read(r, k);
-        sc[k] = mx_scale(r.s[k]);
-    });
-    for_each<4>([&](auto p) {
-        for_each<4>([&](auto k) { convert(r, sc, p, k, v[0]); });
-        write(2 * p, v[0][0]);
-        write(2 * p + 1, v[0][1]);
-    });
-    if constexpr (HALF) for_each<8>([&](auto k) { look(r, k); });
-    meet();
-    ask_w(0);
-    Step d0, d1;
-    for_each<4 + TF>([&](auto n) { read(x_at[0], w_at[0], d0, n); });
-
-    // The ring's slots of this stage, as scalars; the lanes' addresses point at the
-    // stage's gradients and weights, at the next one's codes and where its weights
-    // go, and move on with the stages.
-    int slot = 0, wslot = 0;
-    const auto onward = [](int at, int bytes) { return at == T::R - 1 ? -(T::R - 1) * bytes : bytes; };
-    code_at += RAW;
-    scale_at += RAW_S;
-    to += WT;
-    for (int s = 0; s < S; ++s) {
-        const int next = slot == T::R - 1 ? 0 : slot + 1, last = slot == 0 ? T::R - 1 : slot - 1;
-        const int dx = onward(slot, T::X), dw = wslot ? -WT : WT;
-        // Sixteen slots of a step beside its products, so that none waits for
-        // another's: the first half of a product's 32 clocks issues it, and four
-        // instructions or so are free in the second.  Requests to LDS and memory
-        // come one to a slot, or the waves' would wait in line.
-        const auto step = [&](auto k, Step& d, Step& dn) {
-            constexpr int ks = decltype(k)::value;
-            const auto work = [&](auto at) {
-                constexpr int n = decltype(at)::value;
-                if constexpr (ks < 3) {
-                    if constexpr (n < 4 + TF) read(x_at[(ks + 1) % 4], w_at[(ks + 1) % 4], dn, n);
-                } else {
-                    if constexpr (n == 0) {
-                        // before the last step's other products, whose operands are
-                        // here: the next stage's gradients, and the codes after its
-                        // own, have landed
-                        wait_vmem<T::WAIT>();
-                        meet();
-                        for_each<4>([&](auto i) {
-                            x_at[i] = held(x_at[i] + dx);
-                            w_at[i] = held(w_at[i] + dw);
-                        });
-                    }
-                    if constexpr (n > 0 && n < 5 + TF) read(x_at[0], w_at[0], dn, n - 1);
-                    // the slot of the codes converted last
-                    if constexpr (n >= 10 && n % 2 == 0 && n / 2 - 5 <= T::W_DMA) fetch_w(next, n / 2 - 5);
-                    if constexpr (n == 15) {
-                        code_at = held(code_at + onward(next, RAW));
-                        scale_at = held(scale_at + onward(next, RAW_S));
-                        to = held(to - dw);
-                    }
-                }
-                if constexpr (ks == 0) {
-                    // that of the last stage's gradients, an eighth at a time
-                    constexpr int from = n / 2 * T::X_DMA / 8, end = (n / 2 + 1) * T::X_DMA / 8;
-                    if constexpr (n % 2 == 0 && end > from) fetch_x(last, from, end);
-                    if constexpr (n >= 7 && n < 15) raw_read(r, n - 7);
-                }
-                if constexpr (ks == 1) {
-                    if constexpr (n == 3) for_each<8>([&](auto e8) { sc[e8] = mx_scale(r.s[e8]); });
-                    if constexpr (HALF && n >= 8) look(r, n - 8);
-                }
-                // the conversion's units, of four pairs of columns four each: eight to a step
-                constexpr int at_unit = ks == 1 ? n - 4 : n;
-                if constexpr ((ks == 1 || ks == 2) && at_unit >= 0 && at_unit < 12 && at_unit % 3 < 2) {
-                    constexpr int unit = (ks - 1) * 8 + at_unit / 3 * 2 + at_unit % 3, pair = unit / 4;
-                    convert(r, sc, std::integral_constant<int, pair>{}, unit % 4, v[pair & 1]);
-                    if constexpr (unit % 4 == 3) {
-                        write(2 * pair, v[pair & 1][0]);
-                        write(2 * pair + 1, v[pair & 1][1]);
-                    }
-                }
-            };
-            for_each<4 * TF>([&](auto p) {
-                constexpr int P = decltype(p)::value, from = P * 4 / TF, end = (P + 1) * 4 / TF;
-                acc[P % 4][P / 4] = H16<!HALF>::mfma32(d.w[P % 4], d.x[P / 4], acc[P % 4][P / 4]);
-                for_each<end - from>([&](auto e) { work(std::integral_constant<int, from + decltype(e)::value>{}); });
-                __builtin_amdgcn_sched_barrier(0);
-            });
+        for (int j = 0; j < T::W_DMA; ++j) {                  // eight rows an instruction
+            const int k = 8 * (wave + T::WAVES * j) + (lane >> 3);
+            const int64_t at = n0 / 2 + 16 * (lane & 7);
+            woff[j] = at < c.w_row ? (uint32_t)(k * c.w_row + at) : 1u << 31;
+        }
+        {                                                     // 32 rows an instruction
+            const int k = 32 * (wave & 1) + (lane >> 1);
+            const int64_t at = n0 / 32 + 4 * (lane & 1);
+            soff = at < c.s_row ? (uint32_t)(k * c.s_row + at) : 1u << 31;
+        }
+        const uint32_t base = (uint32_t)(uintptr_t)lds;
+        // Stages come one after another in D's rows, over the segments.  Past the
+        // last one the fetches repeat it, into slots that nobody reads.
+        const u32x4_t xb = buffer_of(c.D + t0 * c.ld, ((tn - 1) * c.ld + (int64_t)c.stages * a.matrices * c.planes * SK) * 2);
+        int xcol = 2 * SK * first;
+        const int xlast = 2 * SK * (end - 1);
+        const auto fetch_x = [&](int slot, int from, int to) {
+#pragma unroll
+            for (int j = from; j < to; ++j) dma_16_at(base + slot * T::X + 1024 * wave, 1024 * T::WAVES * j, xoff[j], xcol, xb);
+            if (to == T::X_DMA) xcol = min(xcol + 2 * SK, xlast);
         };
-        step(std::integral_constant<int, 0>{}, d0, d1);
-        step(std::integral_constant<int, 1>{}, d1, d0);
-        step(std::integral_constant<int, 2>{}, d0, d1);
-        step(std::integral_constant<int, 3>{}, d1, d0);
-        slot = next;
-        wslot ^= 1;
-    }
-    wait_vmem<0>();              // nothing lands in LDS that is another's by then
+        // codes and scales from here on, and of the matrices
+        const uint8_t *wp, *sp, *wp0 = a.codes[0], *sp0 = a.scales[0], *wp1 = a.codes[1], *sp1 = a.scales[1];
+        int64_t wrows;                                                    // left of the segment
+        int wseg = first / c.stages, wleft = S;
+        {
+            const int64_t k0 = (int64_t)(first - wseg * c.stages) * SK;
+            const int m = wseg >= c.planes;
+            wp = a.codes[m] + k0 * c.w_row;
+            sp = a.scales[m] + k0 * c.s_row;
+            wrows = a.rows - k0;
+        }
+        u32x4_t wb, sb;
+        const auto fetch_w = [&](int slot, int piece) {
+            if (piece == 0) {
+                const uint32_t rows = (uint32_t)min((int64_t)SK, wrows);
+                wb = buffer_at(wp, rows * (uint32_t)c.w_row);
+                sb = buffer_at(sp, rows * (uint32_t)c.s_row);
+            }
+            if (piece < T::W_DMA) {
+                dma_16_at(base + T::RAWS + slot * RAW + 1024 * wave, 1024 * T::WAVES * piece, woff[piece], 0, wb);
+                return;
+            }
+            dma_4(base + T::RAW_SCALES + slot * RAW_S + 256 * (wave & 1), soff, sb);
+            // on to the next rows, or the next segment's first (no branch: it would
+            // part the loop, and with it what is ordered among the products)
+            const bool more = --wleft > 0, turns = more && wrows <= SK;
+            wseg += turns;
+            const bool second = wseg >= c.planes;
+            wp = turns ? (second ? wp1 : wp0) : wp + (more ? SK * c.w_row : 0);
+            sp = turns ? (second ? sp1 : sp0) : sp + (more ? SK * c.s_row : 0);
+            wrows = turns ? a.rows : wrows - (more ? SK : 0);
+        };
 
-    const int32_t* exps = a.exps;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < TF; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+        // conversion: thread (q, o) has rows 8 q .. + 7 of the o-th group of eight columns,
+        // whose codes a word holds
+        const int q8 = threadIdx.x / 32, o8 = threadIdx.x % 32;
+        struct Raw {
+            uint32_t w[8], s[8];
+        };
+        uint32_t code_at = held(base + T::RAWS + 8 * q8 * (BN / 2) + 4 * o8);
+        uint32_t scale_at = held(base + T::RAW_SCALES + 8 * q8 * (BN / 32) + o8 / 4);
+        const auto raw_read = [&](Raw& r, int k) {
+            r.w[k] = lds_at<uint32_t>(code_at, k * (BN / 2));
+            r.s[k] = lds_at<uint8_t>(scale_at, k * (BN / 32));
+        };
+        // codes that are not all zero with a scale byte outside 104 .. 140 (byte 255
+        // makes NaN of float16, too)
+        const auto look = [&](const Raw& r, int k) {
+            left |= min(__builtin_elementwise_sub_sat(r.s[k] - 104u, 36u), r.w[k]);
+        };
+        // two rows of a pair of columns
+        const auto convert = [](const Raw& r, const float (&sc)[8], auto pair, int k, u32x4_t (&v)[2]) {
+            constexpr int P = decltype(pair)::value;
+            const uint32_t a = H16<!F16>::template fp4<P>(r.w[2 * k], sc[2 * k]);
+            const uint32_t b = H16<!F16>::template fp4<P>(r.w[2 * k + 1], sc[2 * k + 1]);
+            v[0][k] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            v[1][k] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        };
+        // column c of the group: column 8 o + c of the tile, at place (c % 4) 64 + 2 o + c / 4
+        uint32_t to = held(base + T::W + 2 * o8 * (SK * 2) + 16 * ((q8 ^ o8) & 7));
+        const auto write = [&](int c, u32x4_t v) { lds_at<u32x4_t>(to, ((c & 3) * 64 + (c >> 2)) * (SK * 2)) = v; };
+
+        // a step's operands
+        struct Step {
+            u32x4_t w[4], x[TF];
+        };
+        // in the order of their use: x0, the weights (columns 4 i32 + i), the other x
+        uint32_t x_at[4], w_at[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const int chunk = 16 * ((2 * ks + h) ^ (i32 >> 1 & 7));
+            x_at[ks] = held(base + (tw + i32) * (SK * 2) + chunk);
+            w_at[ks] = held(base + T::W + (nw / 4 + i32) * (SK * 2) + chunk);
+        }
+        const auto read = [&](uint32_t x, uint32_t w, Step& r, int n) {
+            if (n == 0 || n > 4) {
+                const int j = n == 0 ? 0 : n - 4;
+                r.x[j] = lds_at<u32x4_t>(x, 32 * j * (SK * 2));
+            } else {
+                r.w[n - 1] = lds_at<u32x4_t>(w, 64 * (n - 1) * (SK * 2));
+            }
+        };
+
+        // float16 gradients in two bfloat16 parts
+        int e2[TF];
+        u32x4_t xp[2];
+        if constexpr (FAR) {
+#pragma unroll
+            for (int j = 0; j < TF; ++j) e2[j] = a.exps ? a.exps[min(t0 + tw + 32 * j + i32, a.n_tok - 1)] : 0;
+        }
+        const auto parts = [](u32x4_t x, int e2, u32x4_t (&p)[2]) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = ldexpf(H16<false>::to_f32((uint16_t)(x[e >> 1] >> (16 * (e & 1)))), e2);
+            cut(f, p);
+        };
+
+        const auto ask_w = [&](int slot) {
+#pragma unroll
+            for (int e = 0; e <= T::W_DMA; ++e) fetch_w(slot, e);
+        };
+        for_each<T::R>([&](auto f) { ask_w(f); });
+        for_each<T::R - 1>([&](auto f) { fetch_x(f, 0, T::X_DMA); });
+        wait_vmem<0>();
+        meet();
+        Raw r;
+        float sc[8];
+        u32x4_t v[2][2];
+        for_each<8>([&](auto k) {
+            raw_read(r, k);
+            sc[k] = mx_scale(r.s[k]);
+        });
+        for_each<4>([&](auto p) {
+            for_each<4>([&](auto k) { convert(r, sc, p, k, v[0]); });
+            write(2 * p, v[0][0]);
+            write(2 * p + 1, v[0][1]);
+        });
+        if constexpr (F16) for_each<8>([&](auto k) { look(r, k); });
+        meet();
+        ask_w(0);
+        Step d0, d1;
+        for_each<4 + TF>([&](auto n) { read(x_at[0], w_at[0], d0, n); });
+
+        // The ring's slots of this stage, as scalars; the lanes' addresses point at the
+        // stage's gradients and weights, at the next one's codes and where its weights
+        // go, and move on with the stages.
+        int slot = 0, wslot = 0;
+        const auto onward = [](int at, int bytes) { return at == T::R - 1 ? -(T::R - 1) * bytes : bytes; };
+        code_at += RAW;
+        scale_at += RAW_S;
+        to += WT;
+        for (int s = 0; s < S; ++s) {
+            const int next = slot == T::R - 1 ? 0 : slot + 1, last = slot == 0 ? T::R - 1 : slot - 1;
+            const int dx = onward(slot, T::X), dw = wslot ? -WT : WT;
+            // Sixteen slots of a step beside its products, so that none waits for
+            // another's: the first half of a product's 32 clocks issues it, and four
+            // instructions or so are free in the second.  Requests to LDS and memory
+            // come one to a slot, or the waves' would wait in line.
+            const auto step = [&](auto k, Step& d, Step& dn) {
+                constexpr int ks = decltype(k)::value;
+                const auto work = [&](auto at) {
+                    constexpr int n = decltype(at)::value;
+                    if constexpr (ks < 3) {
+                        if constexpr (n < 4 + TF) read(x_at[(ks + 1) % 4], w_at[(ks + 1) % 4], dn, n);
+                    } else {
+                        if constexpr (n == 0) {
+                            // before the last step's other products, whose operands are
+                            // here: the next stage's gradients, and the codes after its
+                            // own, have landed
+                            wait_vmem<T::WAIT>();
+                            meet();
+                            for_each<4>([&](auto i) {
+                                x_at[i] = held(x_at[i] + dx);
+                                w_at[i] = held(w_at[i] + dw);
+                            });
+                        }
+                        if constexpr (n > 0 && n < 5 + TF) read(x_at[0], w_at[0], dn, n - 1);
+                        // the slot of the codes converted last
+                        if constexpr (n >= 10 && n % 2 == 0 && n / 2 - 5 <= T::W_DMA) fetch_w(next, n / 2 - 5);
+                        if constexpr (n == 15) {
+                            code_at = held(code_at + onward(next, RAW));
+                            scale_at = held(scale_at + onward(next, RAW_S));
+                            to = held(to - dw);
+                        }
+                    }
+                    if constexpr (ks == 0) {
+                        // that of the last stage's gradients, an eighth at a time
+                        constexpr int from = n / 2 * T::X_DMA / 8, end = (n / 2 + 1) * T::X_DMA / 8;
+                        if constexpr (n % 2 == 0 && end > from) fetch_x(last, from, end);
+                        if constexpr (n >= 7 && n < 15) raw_read(r, n - 7);
+                    }
+                    if constexpr (ks == 1) {
+                        if constexpr (n == 3) for_each<8>([&](auto e8) { sc[e8] = mx_scale(r.s[e8]); });
+                        if constexpr (F16 && n >= 8) look(r, n - 8);
+                    }
+                    // the conversion's units, of four pairs of columns four each: eight to a step
+                    constexpr int at_unit = ks == 1 ? n - 4 : n;
+                    if constexpr ((ks == 1 || ks == 2) && at_unit >= 0 && at_unit < 12 && at_unit % 3 < 2) {
+                        constexpr int unit = (ks - 1) * 8 + at_unit / 3 * 2 + at_unit % 3, pair = unit / 4;
+                        convert(r, sc, std::integral_constant<int, pair>{}, unit % 4, v[pair & 1]);
+                        if constexpr (unit % 4 == 3) {
+                            write(2 * pair, v[pair & 1][0]);
+                            write(2 * pair + 1, v[pair & 1][1]);
+                        }
+                    }
+                };
+                for_each<4 * TF>([&](auto p) {
+                    constexpr int P = decltype(p)::value, from = P * 4 / TF, end = (P + 1) * 4 / TF;
+                    if constexpr (FAR) {
+                        if constexpr (P % 4 == 0) parts(d.x[P / 4], e2[P / 4], xp);
+                        acc[P % 4][P / 4] = H16<true>::mfma32(d.w[P % 4], xp[0], acc[P % 4][P / 4]);
+                        acc[P % 4][P / 4] = H16<true>::mfma32(d.w[P % 4], xp[1], acc[P % 4][P / 4]);
+                    } else {
+                        acc[P % 4][P / 4] = H16<!F16>::mfma32(d.w[P % 4], d.x[P / 4], acc[P % 4][P / 4]);
+                    }
+                    for_each<end - from>([&](auto e) { work(std::integral_constant<int, from + decltype(e)::value>{}); });
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            };
+            step(std::integral_constant<int, 0>{}, d0, d1);
+            step(std::integral_constant<int, 1>{}, d1, d0);
+            step(std::integral_constant<int, 2>{}, d0, d1);
+            step(std::integral_constant<int, 3>{}, d1, d0);
+            slot = next;
+            wslot ^= 1;
+        }
+        wait_vmem<0>();              // nothing lands in LDS that is another's by then
+    };
+    const int32_t* exps = c.b.exps;
+    sum(std::false_type{}, c);
     if constexpr (HALF) {
-        // The whole tile again with the gradients in two bfloat16 parts, from memory
-        // directly, and as large as they are: with a token's power of two the
-        // products of large weights would pass float32's range.
+        // Again in bfloat16, with the gradients in two parts and as large as they are:
+        // with a token's power of two the products of large weights would pass
+        // float32's range.  One such block among 2 x 11008 rows of 4096, 2048 bfloat16
+        // tokens: 1330 us for 390 (3780 by loads of operands straight from memory).
         if (__syncthreads_or(left != 0)) {
             exps = nullptr;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < TF; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-            const int64_t col = n0 + nw + 4 * i32;
-            for (int st = 4 * first; st < 4 * end; ++st) {
-                const int seg = st / (4 * c.stages), m = seg / c.planes;
-                const int64_t k0 = (int64_t)(st - seg * 4 * c.stages) * 16 + 8 * h;
-                u32x4_t v[4];
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    uint32_t u[2][2] = {{0u, 0u}, {0u, 0u}};
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (k0 + k + e < a.rows && col < 2 * c.w_row) {
-                            const uint32_t code = *(const uint16_t*)(a.codes[m] + (k0 + k + e) * c.w_row + col / 2);
-                            const float sc = mx_scale(a.scales[m][(k0 + k + e) * c.s_row + col / 32]);
-                            u[e][0] = H16<true>::fp4<0>(code, sc);
-                            u[e][1] = H16<true>::fp4<1>(code, sc);
-                        }
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        v[2 * p][k / 2] = __builtin_amdgcn_perm(u[1][p], u[0][p], 0x05040100u);
-                        v[2 * p + 1][k / 2] = __builtin_amdgcn_perm(u[1][p], u[0][p], 0x07060302u);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < TF; ++j) {
-                    const int64_t t = min(t0 + tw + 32 * j + i32, a.n_tok - 1);
-                    const u32x4_t x = *(const u32x4_t*)(c.D + t * c.ld + seg * c.pad + k0);
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = H16<false>::to_f32((uint16_t)(x[e >> 1] >> (16 * (e & 1))));
-                    if (a.exps) {
-                        const int e2 = a.exps[t];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = ldexpf(f[e], e2);
-                    }
-                    u32x4_t p[2];
-                    cut(f, p);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[i][j] = H16<true>::mfma32(v[i], p[0], acc[i][j]);
-                        acc[i][j] = H16<true>::mfma32(v[i], p[1], acc[i][j]);
-                    }
-                }
-            }
+            // the arguments are read anew: kept in registers meanwhile, scalars would
+            // spill, into lanes that the loads to LDS cannot take them from in time
+            const auto* again = (const __attribute__((address_space(4))) Call*)__builtin_amdgcn_kernarg_segment_ptr();
+            asm volatile("" : "+s"(again));
+            sum(std::true_type{}, *again);
         }
     }
 
+    const BackArgs& a = c.b;
+    const auto [n0, t0, part, first, end] = place_of<T::BT>(c);
     // Out through LDS, 32 tokens of a wave at a time, in a region of its own: 128
     // columns of a token in a row, which sixteen lanes read and store as eight each.
     // (Straight from the registers, with all types and edges unrolled 32 times,
