@@ -51,7 +51,8 @@ struct Call {
     int64_t w_row, s_row;      // bytes per row
     int stages, per;           // stages of one segment; stages of one part
     int parts;
-    float* sums;               // [part][token][pitch], of more than one part
+    bool joined;               // to sums, not to dX
+    float* sums;               // [part][token][pitch]
     int64_t pitch;             // d_in, to whole groups of eight
 };
 
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(256, 1) void mx_back_kernel(Call c) {
             const int e2 = exps ? exps[t] : 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
-            if (c.parts > 1) store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * c.pitch + col, 8, true, v);
+            if (c.joined) store8(c.sums, GPTQ_F32, ((int64_t)part * a.n_tok + t) * c.pitch + col, 8, true, v);
             else store8(a.dX, a.dx_dt, t * a.ld_dx + col, m, m == 8, v);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -563,9 +564,11 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 // ---------------------------------------------------------------------------
 struct Gates {
     GatedBackArgs a;
-    uint16_t* D;               // [token][2][plane][pad], token to token ld elements
-    int64_t pad, ld;
-    int32_t* exps;             // of 16-bit types
+    uint16_t* D;               // [token][matrix][plane][pad], or [plane][token][matrix][pad]
+    int64_t pad, ld;           // token to token ld elements,
+    int64_t matrix, plane;     // matrix to matrix and plane to plane as many as these
+    int rows;                  // planes that are rows of their own
+    int32_t* exps;             // of 16-bit types, for each row
 };
 
 // Eight values of both gradients from column k of a token on, of which n exist; to
@@ -602,10 +605,10 @@ __global__ __launch_bounds__(256) void mx_gates_f32_kernel(Gates c) {
         u32x4_t p[3];
         cut(g, p);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + j * c.pad) = p[j];
+        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + j * c.plane) = p[j];
         cut(u, p);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + (3 + j) * c.pad) = p[j];
+        for (int j = 0; j < 3; ++j) *(u32x4_t*)(to + c.matrix + j * c.plane) = p[j];
     }
 }
 
@@ -644,13 +647,13 @@ __global__ __launch_bounds__(1024) void mx_gates_kernel(Gates c) {
         frexpf(m, &e2);                          // m = f 2^e2, f in [1/2, 1)
         e2 = 15 - e2;
     }
-    if (threadIdx.x == 0) c.exps[t] = -e2;
+    if (threadIdx.x < c.rows) c.exps[threadIdx.x * c.a.n_tok + t] = -e2;
     const auto put = [&](int64_t at, float (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e2);
 #pragma unroll
         for (int j = 0; j < PLANES; ++j) {
-            store8(c.D, GPTQ_F16, t * c.ld + at + j * c.pad, 8, true, x);
+            store8(c.D, GPTQ_F16, t * c.ld + at + j * c.plane, 8, true, x);
             if (j + 1 < PLANES) {                // what the value lacks; nothing beside an infinity or NaN
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = __builtin_isfinite(x[i]) ? x[i] - (float)(_Float16)x[i] : 0.0f;
@@ -663,13 +666,13 @@ __global__ __launch_bounds__(1024) void mx_gates_kernel(Gates c) {
             const int64_t k = 8 * threadIdx.x + p * step;
             if (k >= c.pad) continue;
             put(k, g[p]);
-            put(k + PLANES * c.pad, u[p]);
+            put(k + c.matrix, u[p]);
         }
     } else {
         for (int64_t k = 8 * threadIdx.x; k < c.pad; k += step) {
             gate_gradients<DT, ACT>(c, t, min(k, c.a.d_ff), left(k), true, g[0], u[0]);
             put(k, g[0]);
-            put(k + PLANES * c.pad, u[0]);
+            put(k + c.matrix, u[0]);
         }
     }
 }
@@ -701,20 +704,20 @@ void launch_gates(const Gates& c, hipStream_t s) {
 // join, 443 in 176 of 192.
 constexpr double STAGE_US[4][3] = {{0.73, 0.81, 0.87}, {0.89, 1.00, 1.12}, {1.04, 1.17, 1.30}, {1.22, 1.31, 1.60}};
 constexpr double TILE_US[4] = {6, 9, 12, 15};
+// Where float16's gradients have a second value, it is a segment of its own, or a
+// token of its own behind all others (`rows` for each token), whose sums the join
+// adds: free where a tile has room (24 tokens, 2 x 11008 rows of 4096: 41 us against 57).
 struct Plan {
     int tf, stages, per, parts;
+    int planes, rows;          // segments of one matrix; rows of D and of the sums for each token
 };
-Plan plan_of(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows) {
-    const int segments = matrices * planes;
-    Plan best{1, (int)ceil_div(rows, SK), 1, 0};
-    const int64_t all = (int64_t)best.stages * segments;
-    if (all == 0) return best;
-    double least = 1e30;
+void offer_plans(Plan& best, double& least, int matrices, int planes, int rows, int64_t tokens, int64_t d_in) {
+    const int64_t all = (int64_t)best.stages * matrices * planes, n_tok = tokens * rows;
     for (int tf = 1; tf <= 4; ++tf) {
         const int64_t tiles = ceil_div(d_in, BN) * ceil_div(n_tok, 64 * tf);
         const double* us = STAGE_US[tf - 1];
         // more parts than make two rounds of the chip cost a join and save nothing,
-        // nor do float16's of one stage, half of what its rows have
+        // nor do those of one stage with half of its values' bits
         const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, planes == 2 ? all / 2 : all));
         for (int64_t want = 1, per; want <= most; want = per > 1 ? ceil_div(all, per - 1) : most + 1) {
             per = ceil_div(all, want);
@@ -722,15 +725,24 @@ Plan plan_of(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows
             const int64_t full = tiles * parts / 256, rest = tiles * parts % 256;
             const double fill = rest / 256.0, stage = fill < 0.5 ? us[0] + 2 * fill * (us[1] - us[0]) : us[1] + (2 * fill - 1) * (us[2] - us[1]);
             const double cost = full * (per * us[2] + TILE_US[tf - 1]) + (rest ? per * stage + TILE_US[tf - 1] : 0) +
-                                (parts > 1 ? 3 + 4e-6 * parts * n_tok * d_in / 4.5 : 0);
+                                (parts * rows > 1 ? 3 + 4e-6 * parts * n_tok * d_in / 4.5 : 0);
             if (cost < least) {
                 least = cost;
                 best.tf = tf;
                 best.per = (int)per;
                 best.parts = (int)parts;
+                best.planes = planes;
+                best.rows = rows;
             }
         }
     }
+}
+Plan plan_of(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows) {
+    Plan best{1, (int)ceil_div(rows, SK), 1, 0, planes, 1};
+    if (rows == 0) return best;
+    double least = 1e30;
+    offer_plans(best, least, matrices, planes, 1, n_tok, d_in);
+    if (planes == 2) offer_plans(best, least, matrices, 1, 2, n_tok, d_in);
     return best;
 }
 
@@ -744,7 +756,7 @@ size_t planes_bytes(int64_t n_tok, int64_t rows, int segments) {
 }
 size_t sums_bytes(int matrices, int planes, int64_t n_tok, int64_t d_in, int64_t rows) {
     const Plan p = plan_of(matrices, planes, n_tok, d_in, rows);
-    return p.parts > 1 ? (size_t)p.parts * n_tok * pitch_of(d_in) * sizeof(float) : 0;
+    return p.parts * p.rows > 1 ? (size_t)p.parts * p.rows * n_tok * pitch_of(d_in) * sizeof(float) : 0;
 }
 
 template <bool HALF, int TF>
@@ -757,23 +769,26 @@ gptq_status launch_tile(const Call& c, hipStream_t s) {
     return GPTQ_OK;
 }
 
-gptq_status launch_sum(Call& c, hipStream_t s) {
-    const BackArgs& a = c.b;
-    const Plan p = plan_of(a.matrices, c.planes, a.n_tok, a.d_in, a.rows);
+gptq_status launch_sum(Call& c, const Plan& p, hipStream_t s) {
+    BackArgs& a = c.b;
     c.w_row = mx_code_bytes(a.d_in, GPTQ_MX_FP4);
     c.s_row = mx_scale_bytes(a.d_in);
+    c.planes = p.planes;
     c.stages = p.stages;
     c.per = p.per;
     c.parts = p.parts;
+    c.joined = p.parts * p.rows > 1;
     c.pitch = pitch_of(a.d_in);
     if (c.parts > 0) {
-        const bool half = c.half;
         gptq_status st;
-        if (p.tf == 1) st = half ? launch_tile<true, 1>(c, s) : launch_tile<false, 1>(c, s);
-        else if (p.tf == 2) st = half ? launch_tile<true, 2>(c, s) : launch_tile<false, 2>(c, s);
-        else if (p.tf == 3) st = half ? launch_tile<true, 3>(c, s) : launch_tile<false, 3>(c, s);
-        else st = half ? launch_tile<true, 4>(c, s) : launch_tile<false, 4>(c, s);
+        a.n_tok *= p.rows;
+        if (p.tf == 1) st = c.half ? launch_tile<true, 1>(c, s) : launch_tile<false, 1>(c, s);
+        else if (p.tf == 2) st = c.half ? launch_tile<true, 2>(c, s) : launch_tile<false, 2>(c, s);
+        else if (p.tf == 3) st = c.half ? launch_tile<true, 3>(c, s) : launch_tile<false, 3>(c, s);
+        else st = c.half ? launch_tile<true, 4>(c, s) : launch_tile<false, 4>(c, s);
         if (st != GPTQ_OK) return st;
+        a.n_tok /= p.rows;
+        c.parts *= p.rows;       // the second values' sums are parts as well
     }
     if (c.parts != 1) {
         const auto groups = [&](int shares) { return (unsigned)std::min<int64_t>(ceil_div(a.n_tok * c.pitch / 4, 256 / shares), 1 << 20); };
@@ -801,7 +816,7 @@ size_t mx_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t rows) 
 gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, void* ws, hipStream_t s) {
     Call c{};
     c.b = a;
-    const int planes = c.planes = planes_of(a.dt), size = a.dt == GPTQ_F32 ? 4 : 2;
+    const int planes = planes_of(a.dt), size = a.dt == GPTQ_F32 ? 4 : 2;
     c.half = a.dt == GPTQ_F16;
     c.pad = padded(a.rows);
     c.sums = (float*)((char*)ws + planes_bytes(a.n_tok, a.rows, planes));
@@ -818,19 +833,22 @@ gptq_status mx_backward_launch(const BackArgs& a, const void* D, int64_t ld, voi
             GPTQ_LAUNCH_CHECK();
         }
     }
-    return launch_sum(c, s);
+    return launch_sum(c, plan_of(1, planes, a.n_tok, a.d_in, a.rows), s);
 }
+
+// bytes of the tokens' exponents, for each of D's rows
+size_t exps_bytes(gptq_dtype dt, int64_t n_tok) { return align_up(4 * (size_t)n_tok * gate_planes(dt), 256); }
 
 size_t mx_gated_backward_ws(gptq_dtype dt, int64_t n_tok, int64_t d_in, int64_t d_ff) {
     const int planes = gate_planes(dt);
-    return planes_bytes(n_tok, d_ff, 2 * planes) + align_up(4 * (size_t)n_tok, 256) + sums_bytes(2, planes, n_tok, d_in, d_ff);
+    return planes_bytes(n_tok, d_ff, 2 * planes) + exps_bytes(dt, n_tok) + sums_bytes(2, planes, n_tok, d_in, d_ff);
 }
 
 gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream_t s) {
     Call c{};
-    c.planes = gate_planes(a.dt);
     c.half = a.dt != GPTQ_F32;
-    const int segments = 2 * c.planes;
+    const int planes = gate_planes(a.dt);
+    const Plan p = plan_of(2, planes, a.n_tok, a.d_in, a.d_ff);
     BackArgs& b = c.b;
     b.dt = a.dt;
     b.n_tok = a.n_tok;
@@ -846,15 +864,18 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
     }
     c.D = (const uint16_t*)ws;
     c.pad = padded(a.d_ff);
-    c.ld = row_of(a.d_ff, segments);
-    char* exps = (char*)ws + planes_bytes(a.n_tok, a.d_ff, segments);
-    c.sums = (float*)(exps + align_up(4 * (size_t)a.n_tok, 256));
+    c.ld = row_of(a.d_ff, 2 * p.planes);
+    char* exps = (char*)ws + planes_bytes(a.n_tok, a.d_ff, 2 * planes);
+    c.sums = (float*)(exps + exps_bytes(a.dt, a.n_tok));
     if (a.d_ff > 0) {
         Gates g{};
         g.a = a;
         g.D = (uint16_t*)ws;
         g.pad = c.pad;
         g.ld = c.ld;
+        g.matrix = p.planes * c.pad;
+        g.plane = p.rows > 1 ? a.n_tok * c.ld : c.pad;
+        g.rows = p.rows;
         g.exps = c.half ? (int32_t*)exps : nullptr;
         switch (a.act) {
             case GPTQ_ACT_SILU: launch_gates<GPTQ_ACT_SILU>(g, s); break;
@@ -865,7 +886,7 @@ gptq_status mx_gated_backward_launch(const GatedBackArgs& a, void* ws, hipStream
         GPTQ_LAUNCH_CHECK();
         b.exps = g.exps;
     }
-    return launch_sum(c, s);
+    return launch_sum(c, p, s);
 }
 
 }  // namespace gptq
