@@ -73,10 +73,11 @@ struct Call {
 // barrier of a stage stands before its last step, whose operands are in
 // registers by then, so that the matrix instructions run on behind it.
 //
-// 2048 tokens through 4096 rows of 11008 bf16: 190 us (980 TFLOP/s; matrix
+// 2048 tokens through 4096 rows of 11008 bf16: 192 us (960 TFLOP/s; matrix
 // instructions busy 52 % of the clocks, on a chip that lowers its clock as they run:
-// alone they would take 1180 of a stage's 1600 ns), through 2 x 11008 rows of 4096
-// 328 us (1130).  24 tokens, 4096 x 4096: 12 us.
+// alone they would take 1180 of a stage's 1600 ns), through 2 x 11008 rows of 4096, in
+// float16 values, 345 us (1070; busy 60 %).  24 tokens, 4096 x 4096: 13 us, of which
+// the four stages of each part take some 4 and the way in and out the rest.
 //
 // Tokens lie in LDS in order, column c at place (c % 4) 64 + c / 4; 16-byte chunk
 // q (eight rows) of place i at slot q ^ (i / 2 % 8), so that sixteen lanes' reads
@@ -560,7 +561,7 @@ __global__ __launch_bounds__(256) void mx_planes_kernel(Planes c) {
 // against 0.00029 with one).  Float16 values lack range, so each token's are
 // scaled by a power of two that brings the largest finite one to 2^14 .. 2^15, for
 // which a workgroup holds the token's values until it has seen them all.  Bound
-// by memory.
+// by memory: 2048 x 11008 bf16 45 us (5.0 TB/s), 300 x 2050 f16 8.6.
 // ---------------------------------------------------------------------------
 struct Gates {
     GatedBackArgs a;
@@ -700,8 +701,8 @@ void launch_gates(const Gates& c, hipStream_t s) {
 // parts 3 us for the join's launch and their sums at 4.5 TB/s.  For example 2048
 // tokens through 4096 rows of 11008 columns: 190 us in 473 tiles of 192 tokens
 // (two rounds, the second 85 % full), 211 in 344 of 256 (34 % full); through 2 x
-// 11008 rows of 4096 columns: 344 us in 128 tiles of 256 and two parts, with their
-// join, 443 in 176 of 192.
+// 11008 rows of 4096 columns, in bfloat16: 344 us in 128 tiles of 256 and two parts,
+// with their join, 443 in 176 of 192 (float16 values 360 in the former).
 constexpr double STAGE_US[4][3] = {{0.73, 0.81, 0.87}, {0.89, 1.00, 1.12}, {1.04, 1.17, 1.30}, {1.22, 1.31, 1.60}};
 constexpr double TILE_US[4] = {6, 9, 12, 15};
 // Where float16's gradients have a second value, it is a segment of its own, or a

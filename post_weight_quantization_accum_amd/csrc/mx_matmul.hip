@@ -528,7 +528,7 @@ __global__ __launch_bounds__(THREADS) void mx_few_kernel(MatArgs a) {
 // of every 64 columns, block l / 32.  Both are fetched a step ahead.  Bound by
 // the conversions (float32: three products for one as well).  Measured: 2048 x
 // 4096 -> 4096 with e4m3 activations 99 us (695 TFLOP/s), with float32 ones
-// 257 us (267 TFLOP/s); 16-bit ones whose rows do not start on 16 bytes 306 us.
+// 257 us (267 TFLOP/s); 16-bit ones whose rows do not start on 16 bytes 126 to 139 us.
 // ---------------------------------------------------------------------------
 constexpr int MT = 128, MK = 64, X_ROW = MK * 2 + 16;   // 16 bytes further in the banks with each row
 
@@ -1179,12 +1179,15 @@ constexpr double FEW_US[5][7] = {{7.8, 10.5, 12.0, 13.5, 20, 0, 0},        // fl
                                  {2.1, 4.1, 5.4, 6.6, 5.9, 8.7, 0}};      // e2m1
 // Where X's rows do not start on 16 bytes (or have no 128 columns), every step
 // is read from memory directly, without the ring: one round of the tiles in the
-// same order, float32 and 16 bits (float32 (1,1): 29 for 13 tokens, 48 for 16), as
-// measured with reads by single elements.  Whole pieces are read at once since;
-// the rule, and with it the order of the results' sums, is as it was.
-// Times of the general kernel there: float32 226 a round, 16 bits 250 for one
-// and 305 for two rounds.  64 tokens 4096 -> 4096 bf16: (4,1) 27 us, (2,2) 46,
-// which the ring's times would choose.
+// same order, float32 and 16 bits, as measured when they were read by single
+// elements; of the general kernel float32 226 a round, 16 bits 250.  Whole pieces are
+// read at once since, and all take a half to a quarter of that: 4096 -> 4096 bf16 the
+// first six, in one round, 12, 12, 13, 15, 21 and 22 us, the general kernel 63 (two
+// rounds 126); float32 the first five 9, 12, 14, 16 and 20, the general 114 (two 269).
+// The rule, and with it the order of the results' sums, is as it was.  It takes the
+// least of them but in between: 128 tokens bf16 (4,1) 29 us, (4,2) 24; 256 55 and 46;
+// 512 (4,1) 104, general 78; 128 tokens 4090 -> 11008 (4,1) 142, general 78, float32
+// general 131, (4,1) 104.
 constexpr double DIRECT_US[2][7] = {{40, 41, 43, 44, 81, 0, 0}, {21, 24, 26, 28, 52, 57, 0}};
 static_assert(ACT_F32 == 0 && ACT_F16 == 1 && ACT_BF16 == 2 && ACT_FP8 == 3 && ACT_FP4 == 4, "rows of the table");
 constexpr int FEW_RT[7] = {1, 2, 3, 4, 2, 4, 4}, FEW_TT[7] = {1, 1, 1, 1, 2, 2, 4};

@@ -286,8 +286,9 @@ __device__ __forceinline__ void write_y(const NormArgs& a, int64_t row, int v, i
 
 // A workgroup (a wave) takes every ROWS-th row and asks for the next one before it
 // works on its own.  Bound by memory: 8000 rows of 5120 bf16, two norms, stream and
-// norm written, 75 us (4.4 TB/s; a copy has 5.2); one token 2.9, a launch.  Lanes past the row's end read zeros, weights too, so that
-// their values are zeros throughout and add nothing to sums.
+// norm written, 76 us (4.3 TB/s; a copy has 5.1), with a float32 stream and output of
+// the block 116 (4.9); one token 2.9, a launch.  Lanes past the row's end read zeros,
+// weights too, so that their values are zeros throughout and add nothing to sums.
 template <int V, Width D, bool WAVE, bool LAYER, bool NARROW = false>
 __global__ __launch_bounds__(WAVE ? 256 : V == 1 ? 1024 : 512) void norm_kernel(NormArgs a) {
     constexpr int K = STATS<LAYER>;
@@ -344,7 +345,8 @@ __global__ __launch_bounds__(WAVE ? 256 : V == 1 ? 1024 : 512) void norm_kernel(
 }
 
 // Rows that registers do not hold: sums in one pass over them, values in the next
-// (from the caches: 2048 x 20000 bf16 112 us, 2.9 TB/s of the bytes that it must move).
+// (from the caches: 2048 x 20000 bf16 112 us, 2.9 TB/s of the bytes that it must move,
+// with a float32 stream and output of the block 165, 3.5 TB/s).
 template <Width D, bool LAYER>
 __global__ __launch_bounds__(1024) void norm_wide_kernel(NormArgs a) {
     constexpr int K = STATS<LAYER>;
