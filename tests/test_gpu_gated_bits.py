@@ -143,3 +143,24 @@ def test_products_are_far_inside_their_bound(n, d, out, kind):
     wg, wu = x.double() @ w.t(), x.double() @ w2.t()
     for got, want in ((g, wg), (u, wu), (y, G.act64(wg, "silu") * wu)):
         assert float((got.double() - want).norm()) <= 1e-5 * float(want.norm())
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("n,d,ff", [(1, 300, 2050), (20, 140000, 300), (32, 1000, 700), (33, 1000, 700), (64, 600, 4100), (65, 300, 1000),
+                                    (130, 140000, 130)])
+def test_second_values_beside_the_tokens(n, d, ff, kind):
+    """Few tokens, whose second values may share a tile with them; one part and several, weights near and far from float16."""
+    rnd = G.gen(n + ff)
+    dy, g, u = ((rnd(n, ff) * s).to(T[kind]) for s in (2e-3, 1.5, 1.0))
+    dy[0] *= 2.0 ** -10                                    # another power of two
+    dG, dU = G.gated_gradients(dy, g, u, "silu")
+    eG, eU = (a + b + 2.0 ** -133 for a, b in zip(arithmetic_error(dy, g, u, dU, "silu"), rounded(kind, dG, dU)))
+    for scale in (None, 2.0 ** -30):
+        gate, up = G.weights(rnd, ff, d), G.weights(rnd, ff, d, scale)
+        w = torch.cat((G.values(gate, d), G.values(up, d)))
+        for dtype in (torch.float32, T[kind]):
+            wide = torch.full((n, d + 5), 7.0, device=DEV, dtype=dtype)
+            dx = wide[:, 2: 2 + d]
+            P.mx_gated_backward(dy, g, u, gate, up, d, out=dx)
+            G.check_back(dx, torch.cat((dG, dU), 1), w, torch.cat((eG, eU), 1) @ w.abs())
+            assert bool((wide[:, :2] == 7).all()) and bool((wide[:, 2 + d:] == 7).all())

@@ -29,3 +29,18 @@ def test_written_over_the_products(ff, kind):
     assert st == 0
     for a, b in zip((dx, g, u), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", list(T))
+@pytest.mark.parametrize("n,d,ff", [(1, 40, 33), (20, 600, 700), (24, 4096, 2000), (20, 140000, 70), (200, 300, 4100), (700, 2050, 300)])
+def test_workspaces_are_as_large_as_they_say(n, d, ff, kind):
+    """Nothing behind the bytes that the size's entry names is written, and nothing in them is read before it is."""
+    rnd = G.gen(n + d)
+    gate, up = G.weights(rnd, ff, d), G.weights(rnd, ff, d)
+    dy, g, u = (rnd(n, ff).to(T[kind]) for _ in range(3))
+    lib, code = P.load(), {"f32": 0, "f16": 1, "bf16": 2}[kind]
+    for need, call in ((lib.gptq_mx_gated_backward_workspace(code, n, d, ff), lambda **kw: P.mx_gated_backward(dy, g, u, gate, up, d, **kw)),
+                       (lib.gptq_mx_matmul_backward_workspace(code, n, d, ff), lambda **kw: P.mx_matmul_backward(dy, *gate, d, **kw))):
+        ws = torch.full((need + (1 << 20),), 255, dtype=torch.uint8, device=DEV)      # NaN in every type
+        assert torch.equal(call(workspace=ws), call())
+        assert bool((ws[need:] == 255).all())
