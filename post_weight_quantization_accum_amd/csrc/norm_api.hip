@@ -56,6 +56,8 @@ gptq_status gptq_residual_norm(const gptq_norm* norm, int64_t n_tok, int64_t d, 
     if (n_tok == 0) return GPTQ_OK;
     if (!elems(X, x_dtype) || !starts(B, b_dtype) || !starts(H, h_dtype) || !starts(Y, y_dtype)) return GPTQ_ERR_INVALID_ARG;
     if (!B && (norm->post_weight || norm->gate)) return GPTQ_ERR_INVALID_ARG;
+    // in place, a lane writes where it has read
+    if (H == X && (h_dtype != x_dtype || (n_tok > 1 && ld_h != ld_x))) return GPTQ_ERR_INVALID_ARG;
     if (!H && !Y) return GPTQ_OK;
     NormArgs a = base(norm, n_tok, d);
     a.X = X;
